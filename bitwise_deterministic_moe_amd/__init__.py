@@ -7,6 +7,8 @@ The functions carry the names of the C ABI (include/moedet.h).  There is no
 fallback: a missing library raises ``MoeLibraryMissing``.
 """
 import ctypes
+import functools
+import math
 import os
 from dataclasses import dataclass, replace
 from typing import Optional
@@ -20,7 +22,8 @@ __all__ = [
     "moe_router_bwd", "moe_router_fwd", "moe_sgd_step", "moe_mx_quantize", "moe_mx_dgrad_fc1",
     "moe_bwd_dgrad_dprob_noalloc", "moe_mx_quantize_t", "moe_mx_fwd_fc1", "moe_mx_fwd_fc2", "EXPORTED_SYMBOLS",
     "moe_mx_wgrad_rows", "moe_mx_quantize_wgrad", "moe_mx_wgrad", "MXW_TOKEN", "MXW_ROW", "MXW_ACT_P",
-    "moe_route",
+    "moe_route", "moe_layernorm_fwd", "moe_layernorm_bwd", "moe_linear_fwd", "moe_linear_bwd", "moe_glu_fwd",
+    "moe_glu_bwd", "moe_layernorm_workspace_size", "moe_linear_workspace_size", "moe_glu_workspace_size", "ACTIVATIONS",
 ]
 
 DETERMINISTIC = 0
@@ -35,7 +38,11 @@ EXPORTED_SYMBOLS = ("moe_abi_version", "moe_status_string", "moe_rows_cap", "moe
                     "moe_mx_quantize", "moe_mx_dgrad_fc1", "moe_mx_dgrad_fc2",
                     "moe_nvfp4_quantize", "moe_bwd_dgrad_dprob_noalloc", "moe_mx_quantize_t", "moe_mx_fwd_fc1",
                     "moe_mx_fwd_fc2", "moe_mx_wgrad_rows", "moe_mx_quantize_wgrad", "moe_mx_wgrad", "moe_route",
-                    "moe_source_hash")
+                    "moe_source_hash", "moe_layernorm_workspace_size", "moe_layernorm_fwd", "moe_layernorm_bwd",
+                    "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd", "moe_glu_workspace_size",
+                    "moe_glu_fwd", "moe_glu_bwd")
+# activations of the dense operators (moe_act)
+ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4}
 # rows read by moe_mx_quantize_wgrad (moe_mxw_src)
 MXW_TOKEN, MXW_ROW, MXW_ACT_P = 0, 1, 2
 
@@ -67,6 +74,14 @@ class _CProblem(ctypes.Structure):
 class _CRouting(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("topk_idx", "topk_prob", "counts", "offsets",
                                                 "row_src", "row_tok", "row_prob", "slot_row", "sched")]
+
+
+class _CDense(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("z_dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldz", ctypes.c_int64),
+                ("ldr", ctypes.c_int64), ("debug_shuffle_seed", ctypes.c_uint64)]
 
 
 def library_path() -> str:
@@ -125,6 +140,21 @@ def load_library() -> ctypes.CDLL:
     lib.moe_route.argtypes = [P, vp, R, vp, sz, ctypes.c_int, vp]
     lib.moe_mx_quantize_wgrad.argtypes = [P, R, vp, ctypes.c_int, vp, vp, vp]
     lib.moe_mx_wgrad.argtypes = [P, R, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    i64, u64, N = ctypes.c_int64, ctypes.c_uint64, ctypes.POINTER(_CDense)
+    lib.moe_layernorm_fwd.argtypes = [vp, vp, vp, ctypes.c_int, i64, i64, i64, ctypes.c_float, vp, vp, vp, u64, vp]
+    lib.moe_layernorm_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    lib.moe_layernorm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_int, i64, i64, i64, i64, i64, vp, vp, vp, vp, sz,
+                                      u64, vp]
+    for f in ("moe_linear_workspace_size", "moe_glu_workspace_size"):
+        getattr(lib, f).argtypes = [N, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+        getattr(lib, f).restype = ctypes.c_int
+    lib.moe_linear_fwd.argtypes = [N] + [vp] * 7 + [sz, vp]
+    lib.moe_linear_bwd.argtypes = [N] + [vp] * 9 + [sz, vp]
+    lib.moe_glu_fwd.argtypes = [N] + [vp] * 7 + [sz, vp]
+    lib.moe_glu_bwd.argtypes = [N] + [vp] * 11 + [sz, vp]
+    for f in ("moe_layernorm_fwd", "moe_layernorm_workspace_size", "moe_layernorm_bwd", "moe_linear_fwd",
+              "moe_linear_bwd", "moe_glu_fwd", "moe_glu_bwd"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("moe_route", "moe_mx_wgrad_rows", "moe_mx_quantize_wgrad", "moe_mx_wgrad", "moe_rows_cap",
               "moe_sched_elems", "moe_workspace_size", "moe_fwd", "moe_bwd_dgrad_dprob",
               "moe_bwd_dgrad_dprob_noalloc", "moe_mx_quantize_t", "moe_mx_fwd_fc1", "moe_mx_fwd_fc2",
@@ -688,3 +718,349 @@ def moe_mfma_rate(blocks: int, iters: int, value: float = 0.125, sink: Optional[
         sink = torch.empty(256 * blocks, dtype=torch.float32, device="cuda")
     _check(lib.moe_mfma_rate(blocks, iters, value, _ptr(sink), _stream()), "moe_mfma_rate")
     return sink
+
+
+# ---------------------------------------------------------------- dense operators
+def _mat(t: torch.Tensor, cols: int, dtype, what: str, rows: Optional[int] = None):
+    """(rows, row distance) of a matrix [..., cols] of unit stride along its
+    rows: two-dimensional with any row distance, or contiguous."""
+    shape = t.shape
+    if t.dtype != dtype or len(shape) == 0 or shape[-1] != cols:
+        raise MoeError(f"{what}: need a {dtype} tensor [..., {cols}], got {t.dtype} {tuple(shape)}")
+    if len(shape) == 2:
+        n, ld = shape[0], t.stride(0)
+        if n and ((cols > 1 and t.stride(1) != 1) or (n > 1 and ld < cols)):
+            raise MoeError(f"{what}: rows of unit stride at least their length apart are needed, got strides {t.stride()}")
+        if n <= 1:
+            ld = cols
+    else:
+        if not t.is_contiguous():
+            raise MoeError(f"{what}: a tensor of {len(shape)} dimensions must be contiguous")
+        n, ld = t.numel() // cols if cols else 0, cols
+    if rows is not None and n != rows:
+        raise MoeError(f"{what}: need {rows} rows, got {n}")
+    return n, ld
+
+
+def _storage(t: torch.Tensor, what: str) -> int:
+    if t.dtype is torch.bfloat16:
+        return 1
+    if t.dtype is torch.float32:
+        return 0
+    raise MoeError(f"{what}: float32 or bfloat16 is needed, got {t.dtype}")
+
+
+def _grad_code(dtype, storage, what: str) -> int:
+    if dtype is not torch.float32 and dtype is not storage:
+        raise MoeError(f"{what}: grad_dtype must be torch.float32 or the storage type, got {dtype}")
+    return _TORCH_TO_CODE[dtype]
+
+
+def _z_mat(t, cols: int, storage, what: str, rows: int):
+    """(type code, row distance) of a saved pre-activation, float32 or of the
+    storage type."""
+    if t.dtype is not torch.float32 and t.dtype is not storage:
+        raise MoeError(f"{what}: need float32 or {storage}, got {t.dtype}")
+    return _TORCH_TO_CODE[t.dtype], _mat(t, cols, t.dtype, what, rows)[1]
+
+
+def _act_code(act: str, what: str) -> int:
+    try:
+        return ACTIVATIONS[act]
+    except (KeyError, TypeError):
+        raise MoeError(f"{what}: act must be one of {', '.join(ACTIVATIONS)}, got {act!r}") from None
+
+
+def _run(dev, tensors, what: str, call):
+    """call(stream) on the device of the call's tensors, which must all be
+    on that GPU, in its current stream."""
+    if dev.type != "cuda":
+        raise MoeError(f"{what}: tensors must be on a GPU, got {dev}")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise MoeError(f"{what}: tensors on {dev} and {t.device}")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            status = call(torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        status = call(torch.cuda.current_stream(dev).cuda_stream)
+    if status:
+        _check(status, what)
+
+
+def moe_layernorm_workspace_size(rows: int, cols: int) -> int:
+    """Workspace bytes of moe_layernorm_bwd."""
+    n = ctypes.c_size_t()
+    _check(load_library().moe_layernorm_workspace_size(rows, cols, ctypes.byref(n)), "moe_layernorm_workspace_size")
+    return n.value
+
+
+def moe_layernorm_fwd(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, y=None, mean=None, rstd=None,
+                      shuffle_seed: int = 0):
+    """Layer norm of the rows of x [..., D] (float32 or bf16):
+    y = (x - mean) rstd weight + bias.  Returns (y, mean, rstd), the last two
+    float32 per row, as the backward reads them."""
+    lib, what = load_library(), "moe_layernorm_fwd"
+    code = _storage(x, what)
+    if x.dim() == 0:
+        raise MoeError(f"{what}: x needs a dimension to normalise")
+    cols = x.shape[-1]
+    rows, ldx = _mat(x, cols, x.dtype, what + " x")
+    if not (0.0 <= eps < math.inf):
+        raise MoeError(f"{what}: eps must be finite and not negative, got {eps}")
+    dev = x.device
+    for t, n in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _need(t, cols, x.dtype, f"{what} {n}")
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _need(y, rows * cols, x.dtype, what + " y")
+    if mean is None:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    else:
+        _need(mean, rows, torch.float32, what + " mean")
+    if rstd is None:
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    else:
+        _need(rstd, rows, torch.float32, what + " rstd")
+    _run(dev, (weight, bias, y, mean, rstd), what, lambda st: lib.moe_layernorm_fwd(
+        _ptr(x), _ptr(weight), _ptr(bias), code, rows, cols, ldx, eps, _ptr(y), _ptr(mean), _ptr(rstd), shuffle_seed, st))
+    return y, mean, rstd
+
+
+def moe_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight, mean, rstd, dx_add=None, dx=None, dweight=None,
+                      dbias=None, ws=None, shuffle_seed: int = 0):
+    """Layer norm backward from the forward's x, weight, mean and rstd;
+    dx_add [..., D] (another branch's gradient) is added to dx.  Returns
+    (dx, dweight float32 [D], dbias float32 [D])."""
+    lib, what = load_library(), "moe_layernorm_bwd"
+    code = _storage(x, what)
+    if x.dim() == 0:
+        raise MoeError(f"{what}: x needs a dimension to normalise")
+    cols = x.shape[-1]
+    rows, ldx = _mat(x, cols, x.dtype, what + " x")
+    _, lddy = _mat(dy, cols, x.dtype, what + " dy", rows)
+    ldadd = _mat(dx_add, cols, x.dtype, what + " dx_add", rows)[1] if dx_add is not None else cols
+    dev = x.device
+    if weight is not None:
+        _need(weight, cols, x.dtype, what + " weight")
+    _need(mean, rows, torch.float32, what + " mean")
+    _need(rstd, rows, torch.float32, what + " rstd")
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _need(dx, rows * cols, x.dtype, what + " dx")
+    if dweight is None:
+        dweight = torch.empty(cols, dtype=torch.float32, device=dev)
+    else:
+        _need(dweight, cols, torch.float32, what + " dweight")
+    if dbias is None:
+        dbias = torch.empty(cols, dtype=torch.float32, device=dev)
+    else:
+        _need(dbias, cols, torch.float32, what + " dbias")
+    ws = _ws(moe_layernorm_workspace_size(rows, cols), ws, dev)
+    _run(dev, (dy, weight, mean, rstd, dx_add, dx, dweight, dbias, ws), what, lambda st: lib.moe_layernorm_bwd(
+        _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx_add), code, rows, cols, lddy, ldx, ldadd,
+        _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), _ws_bytes(ws), shuffle_seed, st))
+    return dx, dweight, dbias
+
+
+def _ws_bytes(ws: torch.Tensor) -> int:
+    if not ws.is_contiguous():
+        raise MoeError("the workspace must be contiguous")
+    return ws.numel() * ws.element_size()
+
+
+@functools.lru_cache(maxsize=4096)
+def _dense_plan(kind: str, rows: int, d_in: int, d_out: int, dtype: int, grad_dtype: int, z_dtype: int, act: int, ldx: int,
+                ldw: int, ldy: int, ldz: int, ldr: int, seed: int):
+    """The C description of a call (read-only) and its workspace sizes."""
+    what = f"moe_{kind}_workspace_size"
+    if max(rows, ldx, ldw, ldy, ldz, ldr) >= 1 << 31:
+        raise MoeError(f"{what}: sizes beyond 2^31")
+    c = _CDense(rows, d_in, d_out, dtype, grad_dtype, z_dtype, act, ldx, ldw, ldy, ldz, ldr, seed & 0xFFFFFFFFFFFFFFFF)
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(getattr(load_library(), what)(ctypes.byref(c), ctypes.byref(f), ctypes.byref(b)), what)
+    return c, f.value, b.value
+
+
+def _dense_sizes(kind, rows, d_in, d_out, dtype, act, grad_dtype):
+    code = {"f32": 0, "bf16": 1}[dtype]
+    g = code if grad_dtype is None else {"f32": 0, "bf16": 1}[grad_dtype]
+    return _dense_plan(kind, rows, d_in, d_out, code, g, 0, _act_code(act, kind), d_in, d_out, d_out, d_out, 0, 0)[1:]
+
+
+def moe_linear_workspace_size(rows: int, d_in: int, d_out: int, dtype: str = "bf16", act: str = "none",
+                              grad_dtype: Optional[str] = "f32"):
+    """Bytes of workspace for (moe_linear_fwd, moe_linear_bwd) on contiguous
+    tensors."""
+    return _dense_sizes("linear", rows, d_in, d_out, dtype, act, grad_dtype)
+
+
+def moe_glu_workspace_size(rows: int, d_in: int, d_out: int, dtype: str = "bf16", act: str = "silu",
+                           grad_dtype: Optional[str] = "f32"):
+    """Bytes of workspace for (moe_glu_fwd, moe_glu_bwd) on contiguous tensors."""
+    return _dense_sizes("glu", rows, d_in, d_out, dtype, act, grad_dtype)
+
+
+def _dense_ws(nbytes: int, ws, dev, what: str):
+    if ws is not None:
+        return ws, _ws_bytes(ws)
+    if nbytes == 0:
+        return None, 0
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
+
+
+def _dense_in(x, w, what: str):
+    """Sizes of x [..., D] and w [D, F]."""
+    code = _storage(x, what)
+    if w.dim() != 2:
+        raise MoeError(f"{what}: weights must be [d_in, d_out], got {tuple(w.shape)}")
+    d, f = w.shape
+    if d < 1 or f < 1:
+        raise MoeError(f"{what}: weights without elements: {tuple(w.shape)}")
+    rows, ldx = _mat(x, d, x.dtype, what + " x")
+    ldw = _mat(w, f, x.dtype, what + " weight")[1]
+    return code, rows, d, f, ldx, ldw
+
+
+def moe_linear_fwd(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act: str = "none", y=None, z=None,
+                   save_z: bool = False, ws=None, shuffle_seed: int = 0):
+    """y = act(x w + bias) + residual for x [..., D], w [D, F] (float32 or
+    bf16), bias [F], residual [..., F].  Returns (y, z): z the
+    pre-activation x w + bias for the backward, in the tensor given (float32 or
+    x's type), with save_z in a new float32 one, else None.  y may be the
+    residual itself."""
+    lib, what = load_library(), "moe_linear_fwd"
+    code, rows, d, f, ldx, ldw = _dense_in(x, w, what)
+    a = _act_code(act, what)
+    dev, dt = x.device, x.dtype
+    if bias is not None:
+        _need(bias, f, dt, what + " bias")
+    ldr = _mat(residual, f, dt, what + " residual", rows)[1] if residual is not None else 0
+    if y is None:
+        y, ldy = torch.empty(x.shape[:-1] + (f,), dtype=dt, device=dev), f
+    else:
+        ldy = _mat(y, f, dt, what + " y", rows)[1]
+    zc, ldz = 0, f
+    if z is not None:
+        zc, ldz = _z_mat(z, f, dt, what + " z", rows)
+    elif save_z:
+        z = torch.empty(x.shape[:-1] + (f,), dtype=torch.float32, device=dev)
+    c, need, _ = _dense_plan("linear", rows, d, f, code, code, zc, a, ldx, ldw, ldy, ldz, ldr, shuffle_seed)
+    ws, nb = _dense_ws(need, ws, dev, what)
+    _run(dev, (w, bias, residual, y, z, ws), what, lambda st: lib.moe_linear_fwd(
+        c, _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y), _ptr(z), _ptr(ws), nb, st))
+    return y, z
+
+
+def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z=None, act: str = "none", dx_add=None,
+                   need_db: bool = True, grad_dtype=torch.float32, dx=None, dw=None, db=None, ws=None,
+                   shuffle_seed: int = 0):
+    """Backward of moe_linear_fwd from dy [..., F], its inputs and the saved z
+    (unread with act "none"); dx_add [..., D] is added to dx.  The
+    residual's gradient is dy.  Returns (dx, dw, db): the weight gradients in
+    grad_dtype (float32 or the storage type), db None with need_db False."""
+    lib, what = load_library(), "moe_linear_bwd"
+    code, rows, d, f, ldx, ldw = _dense_in(x, w, what)
+    a = _act_code(act, what)
+    dev, dt = x.device, x.dtype
+    g = _grad_code(grad_dtype, dt, what)
+    ldy = _mat(dy, f, dt, what + " dy", rows)[1]
+    zc, ldz = 0, f
+    if a:
+        if z is None:
+            raise MoeError(f"{what}: act {act!r} needs the saved z")
+        zc, ldz = _z_mat(z, f, dt, what + " z", rows)
+    else:
+        z = None
+    ldr = _mat(dx_add, d, dt, what + " dx_add", rows)[1] if dx_add is not None else 0
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=dt, device=dev)
+    else:
+        _need(dx, rows * d, dt, what + " dx")
+    if dw is None:
+        dw = torch.empty((d, f), dtype=grad_dtype, device=dev)
+    else:
+        _need(dw, d * f, grad_dtype, what + " dw")
+    if db is not None:
+        _need(db, f, grad_dtype, what + " db")
+    elif need_db:
+        db = torch.empty(f, dtype=grad_dtype, device=dev)
+    c, _, need = _dense_plan("linear", rows, d, f, code, g, zc, a, ldx, ldw, ldy, ldz, ldr, shuffle_seed)
+    ws, nb = _dense_ws(need, ws, dev, what)
+    _run(dev, (dy, w, z, dx_add, dx, dw, db, ws), what, lambda st: lib.moe_linear_bwd(
+        c, _ptr(dy), _ptr(x), _ptr(w), _ptr(z), _ptr(dx_add), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), nb, st))
+    return dx, dw, db
+
+
+def moe_glu_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, act: str = "silu", save: bool = False, a=None,
+                g=None, u=None, ws=None, shuffle_seed: int = 0):
+    """Gated feed-forward product a = act(x wg) * (x wu) for x [..., D], wg
+    and wu [D, F] (two matrices, or the halves of one).  Returns (a, g, u): x wg
+    and x wu for the backward in the tensors given (float32 or x's type), with
+    save in new float32 ones, else None."""
+    lib, what = load_library(), "moe_glu_fwd"
+    code, rows, d, f, ldx, ldw = _dense_in(x, wg, what)
+    ac = _act_code(act, what)
+    dev, dt = x.device, x.dtype
+    if wu.dim() != 2 or _mat(wu, f, dt, what + " wu", d)[1] != ldw:
+        raise MoeError(f"{what}: wg and wu need the same shape and row distance")
+    if a is None:
+        a, ldy = torch.empty(x.shape[:-1] + (f,), dtype=dt, device=dev), f
+    else:
+        ldy = _mat(a, f, dt, what + " a", rows)[1]
+    if (g is None) != (u is None):
+        raise MoeError(f"{what}: g and u are given together")
+    zc, ldz = 0, f
+    if g is not None:
+        zc, ldz = _z_mat(g, f, dt, what + " g", rows)
+        if _z_mat(u, f, dt, what + " u", rows) != (zc, ldz):
+            raise MoeError(f"{what}: g and u need the same type and row distance")
+    elif save:
+        g = torch.empty(x.shape[:-1] + (f,), dtype=torch.float32, device=dev)
+        u = torch.empty(x.shape[:-1] + (f,), dtype=torch.float32, device=dev)
+    c, need, _ = _dense_plan("glu", rows, d, f, code, code, zc, ac, ldx, ldw, ldy, ldz, 0, shuffle_seed)
+    ws, nb = _dense_ws(need, ws, dev, what)
+    _run(dev, (wg, wu, a, g, u, ws), what, lambda st: lib.moe_glu_fwd(
+        c, _ptr(x), _ptr(wg), _ptr(wu), _ptr(a), _ptr(g), _ptr(u), _ptr(ws), nb, st))
+    return a, g, u
+
+
+def moe_glu_bwd(da: torch.Tensor, x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, g: torch.Tensor, u: torch.Tensor,
+                act: str = "silu", dx_add=None, grad_dtype=torch.float32, dx=None, dwg=None, dwu=None, ws=None,
+                shuffle_seed: int = 0):
+    """Backward of moe_glu_fwd from da [..., F], its inputs and the saved g
+    and u; dx_add [..., D] is added to dx.  Returns (dx, dwg, dwu), the weight
+    gradients in grad_dtype (float32 or the storage type)."""
+    lib, what = load_library(), "moe_glu_bwd"
+    code, rows, d, f, ldx, ldw = _dense_in(x, wg, what)
+    ac = _act_code(act, what)
+    dev, dt = x.device, x.dtype
+    gc = _grad_code(grad_dtype, dt, what)
+    if wu.dim() != 2 or _mat(wu, f, dt, what + " wu", d)[1] != ldw:
+        raise MoeError(f"{what}: wg and wu need the same shape and row distance")
+    ldy = _mat(da, f, dt, what + " da", rows)[1]
+    zc, ldz = _z_mat(g, f, dt, what + " g", rows)
+    if _z_mat(u, f, dt, what + " u", rows) != (zc, ldz):
+        raise MoeError(f"{what}: g and u need the same type and row distance")
+    ldr = _mat(dx_add, d, dt, what + " dx_add", rows)[1] if dx_add is not None else 0
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=dt, device=dev)
+    else:
+        _need(dx, rows * d, dt, what + " dx")
+    if dwg is None:
+        dwg = torch.empty((d, f), dtype=grad_dtype, device=dev)
+    else:
+        _need(dwg, d * f, grad_dtype, what + " dwg")
+    if dwu is None:
+        dwu = torch.empty((d, f), dtype=grad_dtype, device=dev)
+    else:
+        _need(dwu, d * f, grad_dtype, what + " dwu")
+    c, _, need = _dense_plan("glu", rows, d, f, code, gc, zc, ac, ldx, ldw, ldy, ldz, ldr, shuffle_seed)
+    ws, nb = _dense_ws(need, ws, dev, what)
+    _run(dev, (da, wg, wu, g, u, dx_add, dx, dwg, dwu, ws), what, lambda st: lib.moe_glu_bwd(
+        c, _ptr(da), _ptr(x), _ptr(wg), _ptr(wu), _ptr(g), _ptr(u), _ptr(dx_add), _ptr(dx), _ptr(dwg), _ptr(dwu),
+        _ptr(ws), nb, st))
+    return dx, dwg, dwu

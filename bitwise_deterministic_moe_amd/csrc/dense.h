@@ -1,0 +1,187 @@
+// Parameter blocks and host-side launchers of the dense operators (layer
+// norm, linear map, gated product).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.h"
+
+namespace moedet {
+
+// Activations (moe_act of the C ABI).
+enum { kActNone = 0, kActRelu = 1, kActRelu2 = 2, kActSilu = 3, kActGelu = 4 };
+
+// ------------------------------------------------------- vectors of any address
+// 16-byte vectors that may start at any element: gfx950 loads and stores
+// them in one instruction at any byte address.
+typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
+
+template <typename T>
+struct Vec;   // the 16-byte vector of a storage type
+template <>
+struct Vec<uint16_t> {
+  static constexpr int N = 8;
+  typedef u32x4_t raw;
+  // elements [0, n) of p, n >= 1; the others read as zero
+  DEV static raw load(const uint16_t* p, int n) {
+    if (n >= N) return *(const u32x4_any_t*)p;
+    raw r = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < N - 1; ++i)
+      if (i < n) r[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+    return r;
+  }
+  DEV static void get(const raw& r, float* v) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      v[2 * w] = __uint_as_float(r[w] << 16);
+      v[2 * w + 1] = __uint_as_float(r[w] & 0xffff0000u);
+    }
+  }
+  DEV static void store(uint16_t* p, const float* v, int n) {
+    const u32x4_t r = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    if (n >= N) {
+      *(u32x4_any_t*)p = r;
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N - 1; ++i)
+      if (i < n) p[i] = (uint16_t)(r[i >> 1] >> (16 * (i & 1)));
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  typedef f32x4_t raw;
+  DEV static raw load(const float* p, int n) {
+    if (n >= N) return *(const f32x4_any_t*)p;
+    raw r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < N - 1; ++i)
+      if (i < n) r[i] = p[i];
+    return r;
+  }
+  DEV static void get(const raw& r, float* v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = r[i];
+  }
+  DEV static void store(float* p, const float* v, int n) {
+    if (n >= N) {
+      *(f32x4_any_t*)p = f32x4_t{v[0], v[1], v[2], v[3]};
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N - 1; ++i)
+      if (i < n) p[i] = v[i];
+  }
+};
+
+// ---------------------------------------------------------------- layer norm
+constexpr int64_t kNormMaxCols = 16384;
+constexpr int kNormBlocks = 512;  // most row blocks of the weight gradient's partial sums
+
+struct NormParams {
+  const void* x;
+  const void* weight;   // or null: 1
+  const void* bias;     // or null: 0
+  const void* dy;
+  const void* add;      // or null
+  int64_t rows, ldx, lddy, ldadd;
+  int cols;
+  float eps;
+  void* y;              // forward y, backward dx
+  float* mean;
+  float* rstd;
+  float* part;          // backward: [blocks][2][cols] partial sums of dweight and dbias
+  int blocks;
+  uint64_t seed;
+};
+
+// Row blocks of the backward for a problem (from its sizes and type alone).
+int norm_bwd_blocks(int64_t rows, int64_t cols, bool bf16);
+hipError_t launch_norm_fwd(const NormParams& P, bool bf16, hipStream_t st);
+hipError_t launch_norm_bwd(const NormParams& P, bool bf16, hipStream_t st);
+// out[c] = sum over b ascending, in fixed phases, of part[b * stride + c], c < cols.
+hipError_t launch_block_sums(const float* part, int blocks, int64_t stride, int cols, void* out, bool out_bf16,
+                             hipStream_t st);
+
+// ------------------------------------------------------------ matrix operators
+// One matrix product of a dense operator,
+//   C[m, n] = sum_k A[m, k] B[n, k]
+// in one of four forms (kForm*), split into S chunks of the contraction when
+// S > 1: each chunk then stores its float32 partial and launch_dense_finish
+// adds them in chunk order and runs the epilogue.
+enum {
+  kFormLinear = 0,  // A = x [M][K], B = w [K][N]: z = C + bias, y = act(z) + residual
+  kFormGlu = 1,     // A = x, B = wg and wu [K][N]: g, u and act(g) u
+  kFormDx = 2,      // A = dz [M][nseg K], B = nseg matrices [N][K]: C + add
+  kFormDw = 3       // A = x [K][M], B = dz [K][nseg N]: nseg matrices C
+};
+
+struct DenseParams {
+  int64_t M;          // rows of C
+  int N;              // columns of C (of one matrix)
+  int64_t K;          // contraction (of one segment)
+  int nseg;           // kFormDx: K segments; kFormDw: matrices C
+  const void* a;
+  int64_t lda;
+  int64_t seg;        // kFormDx: elements between the K segments of a; kFormDw: between the column segments of b
+  const void* b[2];
+  int64_t ldb;
+  int S;              // chunks of the contraction
+  float* part;        // [S][M][part_ld] when S > 1
+  int64_t part_ld;
+  int part_seg;       // columns between the two matrices in a partial row
+  // epilogue
+  const void* bias;   // or null
+  const void* add;    // residual / dx_add, or null
+  int64_t ldadd;
+  void* c[2];         // y, a, dx or the weight gradients
+  int64_t ldc;
+  void* z[2];         // z or g and u; null: not stored
+  int64_t ldz;
+  bool z_f32;         // float32 z whatever the storage type
+  int act;
+  bool c_f32;         // kFormDw: float32 c whatever the storage type
+  uint64_t seed;
+};
+
+// Rows of the few-row kernels (weights streamed once).
+constexpr int kFewRowsBf16 = 64, kFewRowsF32 = 16;
+
+// bm: tile rows (bf16: 128 or 256; float32: 128)
+hipError_t launch_dense_gemm(const DenseParams& P, int form, bool bf16, int bm, hipStream_t st);
+hipError_t launch_dense_few(const DenseParams& P, int form, bool bf16, hipStream_t st);
+hipError_t launch_dense_finish(const DenseParams& P, int form, bool bf16, hipStream_t st);
+int dense_tile_n(int form, bool bf16);   // columns of one matrix a tile covers
+int dense_few_n(int form, bool bf16);    // the same for the few-row kernels
+
+// bf16 matrix [rows][cols] (row distance ld) into [rows][ldo], zeros past cols
+hipError_t launch_dense_pack(const void* in, int64_t rows, int cols, int64_t ld, void* out, int64_t ldo,
+                             hipStream_t st);
+// Gradients of the pre-activations, elementwise, with the column sums of dz
+// over row blocks.
+struct DenseEwParams {
+  int64_t rows;
+  int cols;
+  const void* dy;     // or da
+  int64_t lddy;
+  const void* z[2];   // z, or g and u
+  int64_t ldz;
+  bool z_f32;
+  int act;
+  void* out[2];       // dz, or dg and du; null: not stored
+  int64_t ldo;
+  int pad;            // columns up to which an output row is written (zeros past cols)
+  float* part;        // [blocks][cols] column sums of dz, or null
+  int blocks;
+  uint64_t seed;
+};
+int dense_ew_blocks(int64_t rows, int cols, bool bf16);
+hipError_t launch_dense_ew(const DenseEwParams& P, bool glu, bool bf16, hipStream_t st);
+hipError_t launch_dense_zero(void* p, int64_t n16, hipStream_t st);   // n16 16-bit words
+
+}  // namespace moedet

@@ -1,0 +1,832 @@
+// Matrix products of the dense operators (linear map, gated product), for
+// bf16 and float32 storage: tiles for many rows, a weight-streaming kernel for
+// few rows, the join of split contractions, and the elementwise passes.
+//
+//   linear  z = x w + bias, y = act(z) + residual
+//   glu     g = x wg, u = x wu, a = act(g) u
+//   dx      dz w^T (or dg wg^T + du wu^T as one contraction over both) + dx_add
+//   dw      x^T dz (x^T dg and x^T du as one launch)
+//
+// Every output element is accumulated in float32 by one workgroup in
+// ascending k, or, where the launch would leave compute units idle, by S
+// workgroups over chunks of k whose float32 partials a second launch adds in
+// chunk order.  S and every chunk bound depend on sizes only, and no atomics
+// are used, so the bits do not depend on scheduling.
+#include "dense_bf16.h"
+#include "dense_epilogue.h"
+#include "kernels.h"
+
+namespace moedet {
+
+// ------------------------------------------------------------------- units
+// Tile order: bands of kBand tile rows, down the band before across, so the
+// consecutive units that map_unit gives to an XCD share operand tiles in its
+// L2 both ways.
+constexpr int kBand = 4;
+struct DenseTile {
+  int64_t m0;
+  int n0, seg, chunk;
+  int s0, s1;       // slices of the contraction (over all K segments)
+};
+
+template <int FORM>
+DEV bool dense_tile(const DenseParams& P, int bm, int bn, int bk, DenseTile& t) {
+  const int64_t mT = (P.M + bm - 1) / bm;
+  const int nTs = (P.N + bn - 1) / bn;
+  const int nT = FORM == kFormDw ? nTs * P.nseg : nTs;
+  const int64_t tiles = mT * nT;
+  const int64_t L = map_unit(blockIdx.x, tiles * P.S, P.seed);
+  if (L < 0) return false;
+  t.chunk = (int)(L / tiles);
+  const int64_t tile = L - t.chunk * tiles;
+  const int64_t band = tile / ((int64_t)kBand * nT);
+  const int64_t in = tile - band * kBand * nT;
+  const int64_t left = mT - band * kBand;
+  const int h = left < kBand ? (int)left : kBand;
+  t.m0 = (band * kBand + in % h) * bm;
+  const int nt = (int)(in / h);
+  t.seg = FORM == kFormDw ? nt / nTs : 0;
+  t.n0 = (FORM == kFormDw ? nt % nTs : nt) * bn;
+  const int64_t steps = (P.K + bk - 1) / bk * (FORM == kFormDx ? P.nseg : 1);
+  t.s0 = (int)(t.chunk * steps / P.S);
+  t.s1 = (int)((t.chunk + 1) * steps / P.S);
+  return true;
+}
+
+// ---------------------------------------------------------------- bf16 tiles
+// The accumulator tile goes through LDS in passes of 64 rows (row stride
+// 260 floats), so that a wave reads and writes whole rows in global memory.
+constexpr int kDenseStageRow = 260;
+static_assert(64 * kDenseStageRow * 4 <= dn::kRingBytes<64>, "epilogue stage must fit in the ring");
+
+// Operands are read in chunks of 8 columns: their rows hold whole chunks
+// (sizes and row distances are multiples of 8, or the operand was copied into such rows).
+DEV int64_t up8(int64_t n) { return (n + 7) & ~(int64_t)7; }
+
+DEV void dense_lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+template <int FORM, int WTM>
+DEV void dense_store_tile(const DenseParams& P, const DenseTile& t, float* stage, f32x16_t (&acc)[4][4], int wm, int wn,
+                          int lane, int wave) {
+  const int r32 = lane & 31, half = lane >> 5;
+  const int rows = (int)(P.M - t.m0 < 2 * WTM ? P.M - t.m0 : 2 * WTM);
+#pragma unroll
+  for (int p = 0; p < 2 * WTM / 64; ++p) {
+    if (64 * p >= rows) break;
+#pragma unroll
+    for (int mb = 0; mb < WTM / 32; ++mb) {
+      const int r0 = wm * WTM + mb * 32 - 64 * p;
+      if (r0 >= 0 && r0 < 64) {
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // GLU: g in columns 0..127, u in 128..255
+            const int col = (FORM == kFormGlu ? (nb >> 1) * 128 + wn * 64 + (nb & 1) * 32 : wn * 128 + nb * 32) + 8 * i +
+                            4 * half;
+            const f32x16_t& a = acc[mb][nb];
+            *(f32x4_t*)(stage + (r0 + r32) * kDenseStageRow + col) =
+                f32x4_t{a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]};
+          }
+      }
+    }
+    dense_lds_barrier();
+    if constexpr (FORM == kFormGlu) {
+      const int c = (lane & 31) * 4, col = t.n0 + c;
+#pragma unroll 4
+      for (int st = 0; st < 8; ++st) {
+        const int m = 8 * st + 2 * wave + half;
+        const f32x4_t sg = *(const f32x4_t*)(stage + m * kDenseStageRow + c);
+        const f32x4_t su = *(const f32x4_t*)(stage + m * kDenseStageRow + 128 + c);
+        float g[4] = {sg[0], sg[1], sg[2], sg[3]}, u[4] = {su[0], su[1], su[2], su[3]};
+        if (64 * p + m < rows && col < P.N) {
+          const int64_t row = t.m0 + 64 * p + m;
+          if (P.S > 1) {
+            part4(P, t.chunk, 0, row, col, g);
+            part4(P, t.chunk, 1, row, col, u);
+          } else {
+            emit4_glu<uint16_t>(P, row, col, g, u);
+          }
+        }
+      }
+    } else {
+      const int c = lane * 4, col = t.n0 + c;
+#pragma unroll 4
+      for (int st = 0; st < 16; ++st) {
+        const int m = 4 * st + wave;
+        const f32x4_t sv = *(const f32x4_t*)(stage + m * kDenseStageRow + c);
+        float v[4] = {sv[0], sv[1], sv[2], sv[3]};
+        if (64 * p + m < rows && col < P.N) {
+          const int64_t row = t.m0 + 64 * p + m;
+          if (P.S > 1)
+            part4(P, t.chunk, t.seg, row, col, v);
+          else
+            emit4<uint16_t, FORM>(P, t.seg, row, col, v);
+        }
+      }
+    }
+    dense_lds_barrier();
+  }
+}
+
+template <int FORM, int WTM>
+__global__ __launch_bounds__(256) void dense_bf16_kernel(DenseParams P) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[dn::kRingBytes<WTM> / 2];
+  constexpr int BMv = 2 * WTM, BNv = FORM == kFormGlu ? 128 : 256;
+  DenseTile t;
+  if (!dense_tile<FORM>(P, BMv, BNv, dn::BK, t)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const uint32_t ring = bf::lds_base(lds);
+  constexpr int LA = dn::kALoads<WTM>;
+  constexpr uint32_t AB = dn::kAOper<WTM> * 2;   // bytes of an A slot
+  const int nsteps = t.s1 - t.s0;
+  const int mvalid = (int)(P.M - t.m0 < BMv ? P.M - t.m0 : BMv);
+  const int nvalid = P.N - t.n0;
+  f32x16_t acc[4][4];
+  if constexpr (FORM == kFormDw) {
+    // both operands row k = contraction; the chunk starts at row 32 s0
+    const int64_t k0 = (int64_t)t.s0 * dn::BK;
+    const int64_t kn = P.K - k0 < (int64_t)nsteps * dn::BK ? P.K - k0 : (int64_t)nsteps * dn::BK;
+    dn::MncOp<BMv, LA> oa;
+    dn::MncOp<256, 4> ob;
+    oa.init((const uint16_t*)P.a + k0 * P.lda + t.m0, ((kn - 1) * P.lda + up8(mvalid)) * 2, wave, lane, mvalid, P.lda);
+    ob.init((const uint16_t*)P.b[0] + k0 * P.ldb + t.seg * P.seg + t.n0, ((kn - 1) * P.ldb + up8(nvalid)) * 2, wave,
+            lane, nvalid, P.ldb);
+    const uint32_t sa = (uint32_t)(dn::BK * P.lda * 2), sb = (uint32_t)(dn::BK * P.ldb * 2);
+    dn::mainloop<dn::MNC, dn::MNC, WTM>(lds, ring, nsteps, [&](int s, uint32_t st, int i) {
+      if (i < LA)
+        oa.issue(st, wave, i, (uint32_t)s * sa);
+      else
+        ob.issue(st + AB, wave, i - LA, (uint32_t)s * sb);
+    }, acc, wm, wn, lane);
+  } else {
+    const int steps_seg = (int)((P.K + dn::BK - 1) / dn::BK);
+    dn::KcOp<LA> oa;
+    const int64_t a_cols = (FORM == kFormDx && P.nseg > 1 ? P.seg : 0) + up8(P.K);
+    oa.init((const uint16_t*)P.a + t.m0 * P.lda, ((mvalid - 1) * P.lda + a_cols) * 2, wave, lane, mvalid, P.lda);
+    const int kc = dn::KcOp<LA>::chunk(lane) * 8;   // first k of this lane's chunk in a slice
+    if constexpr (FORM == kFormDx) {
+      dn::KcOp<4> ob, ob1;
+      const int64_t eb = ((int64_t)(nvalid < 256 ? nvalid - 1 : 255) * P.ldb + up8(P.K)) * 2;
+      ob.init((const uint16_t*)P.b[0] + (int64_t)t.n0 * P.ldb, eb, wave, lane, nvalid, P.ldb);
+      ob1.rs = bf::make_rsrc((const uint16_t*)P.b[P.nseg - 1] + (int64_t)t.n0 * P.ldb, (uint32_t)eb);
+      dn::mainloop<dn::KC, dn::KC, WTM>(lds, ring, nsteps, [&](int s, uint32_t st, int i) {
+        const bool live = s < nsteps;
+        int ks = live ? t.s0 + s : 0;
+        const bool second = ks >= steps_seg;
+        if (second) ks -= steps_seg;
+        const bool ok = live && ks * dn::BK + kc < P.K;
+        if (i < LA) {
+          oa.issue(st, wave, i, ok, (uint32_t)ks * 64u + (second ? (uint32_t)P.seg * 2u : 0u));
+        } else {
+          const bf::i32x4_t rs = second ? ob1.rs : ob.rs;
+          bf::dma16(rs, st + AB + (uint32_t)(wave * 4 + i - LA) * 1024u, ok ? ob.voff[i - LA] : dn::kOOB, (uint32_t)ks * 64u);
+        }
+      }, acc, wm, wn, lane);
+    } else {
+      const int64_t k0 = (int64_t)t.s0 * dn::BK;
+      const uint32_t sb = (uint32_t)(dn::BK * P.ldb * 2);
+      auto issue_a = [&](int s, uint32_t st, int i) {
+        const bool live = s < nsteps;
+        const int ks = live ? t.s0 + s : 0;
+        oa.issue(st, wave, i, live && ks * dn::BK + kc < P.K, (uint32_t)ks * 64u);
+      };
+      // rows of w from the chunk's first to the matrix' last: rows past a
+      // chunk that is not the last one are read and never multiplied
+      const int64_t kn = P.K - k0;
+      if constexpr (FORM == kFormLinear) {
+        dn::MncOp<256, 4> ob;
+        ob.init((const uint16_t*)P.b[0] + k0 * P.ldb + t.n0, ((kn - 1) * P.ldb + up8(nvalid)) * 2, wave, lane, nvalid, P.ldb);
+        dn::mainloop<dn::KC, dn::MNC, WTM>(lds, ring, nsteps, [&](int s, uint32_t st, int i) {
+          if (i < LA)
+            issue_a(s, st, i);
+          else
+            ob.issue(st + AB, wave, i - LA, (uint32_t)s * sb);
+        }, acc, wm, wn, lane);
+      } else {
+        dn::MncOp<128, 2> og, ou;
+        const int64_t e = ((kn - 1) * P.ldb + up8(nvalid)) * 2;
+        og.init((const uint16_t*)P.b[0] + k0 * P.ldb + t.n0, e, wave, lane, nvalid, P.ldb);
+        ou.init((const uint16_t*)P.b[1] + k0 * P.ldb + t.n0, e, wave, lane, nvalid, P.ldb);
+        dn::mainloop<dn::KC, dn::GLU, WTM>(lds, ring, nsteps, [&](int s, uint32_t st, int i) {
+          if (i < LA)
+            issue_a(s, st, i);
+          else if (i < LA + 2)
+            og.issue(st + AB, wave, i - LA, (uint32_t)s * sb);
+          else
+            ou.issue(st + AB + 8192u, wave, i - LA - 2, (uint32_t)s * sb);
+        }, acc, wm, wn, lane);
+      }
+    }
+  }
+  dense_store_tile<FORM, WTM>(P, t, (float*)lds, acc, wm, wn, lane, wave);
+}
+
+// ------------------------------------------------------------- float32 tiles
+// Tile 128 x 128 x 16 (the gated product: 64 columns of both matrices), 4
+// waves of 64 x 64 in blocks of v_mfma_f32_32x32x2f32.  A thread holds the next
+// slice in registers while the current one is multiplied from LDS (two LDS
+// buffers, one barrier a slice).  LDS keeps each operand's own order:
+// K-contiguous rows [128][20], read four k at a time, or [16][132].  In both,
+// the MFMA e of group q takes k = 8 q + e from lanes 0..31 and k = 8 q + 4 + e
+// from lanes 32..63.  Loads are of any address; edges are read
+// element by element.
+namespace f32t {
+constexpr int BM = 128, BK = 16, KROW = 20, MROW = 132;
+constexpr int OPER = 128 * KROW;   // floats of an operand's LDS buffer (the larger layout)
+
+// v[i]: 4 floats; K-contiguous: row tid/4 + 64 i, k = 4 (tid % 4);
+// M/N-contiguous: k = tid/32 + 8 i, columns 4 (tid % 32)
+DEV void load_kc(f32x4_t (&v)[2], const float* base, int64_t ld, int rows, int64_t k, int64_t K, int tid) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = (tid >> 2) + 64 * i;
+    const int64_t kk = k + 4 * (tid & 3);
+    v[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (r < rows && kk < K) v[i] = Vec<float>::load(base + r * ld + kk, (int)(K - kk < 4 ? K - kk : 4));
+  }
+}
+DEV void load_mnc(f32x4_t (&v)[2], const float* base, int64_t ld, int cols, int64_t k, int64_t K, int tid) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t kk = k + (tid >> 5) + 8 * i;
+    const int c = 4 * (tid & 31);
+    v[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (c < cols && kk < K) v[i] = Vec<float>::load(base + kk * ld + c, cols - c);
+  }
+}
+DEV void store_kc(float* s, const f32x4_t (&v)[2], int tid) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) *(f32x4_t*)(s + ((tid >> 2) + 64 * i) * KROW + 4 * (tid & 3)) = v[i];
+}
+DEV void store_mnc(float* s, const f32x4_t (&v)[2], int tid) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) *(f32x4_t*)(s + ((tid >> 5) + 8 * i) * MROW + 4 * (tid & 31)) = v[i];
+}
+template <bool KCL>
+DEV f32x4_t frag(const float* s, int row, int q, int half) {
+  if constexpr (KCL) return *(const f32x4_t*)(s + row * KROW + 8 * q + 4 * half);
+  const float* p = s + (8 * q + 4 * half) * MROW + row;
+  return f32x4_t{p[0], p[MROW], p[2 * MROW], p[3 * MROW]};
+}
+}  // namespace f32t
+
+template <int FORM>
+__global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
+  using namespace f32t;
+  __shared__ __attribute__((aligned(16))) float sa[2][OPER], sb[2][OPER];
+  constexpr int BNv = FORM == kFormGlu ? 64 : 128;
+  constexpr bool AK = FORM != kFormDw, BKC = FORM == kFormDx;
+  DenseTile t;
+  if (!dense_tile<FORM>(P, BM, BNv, BK, t)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+  const int r32 = lane & 31, half = lane >> 5;
+  const int mvalid = (int)(P.M - t.m0 < BM ? P.M - t.m0 : BM), nvalid = P.N - t.n0;
+  const int64_t steps_seg = (P.K + BK - 1) / BK;
+  f32x4_t ra[2], rb[2];
+  auto load = [&](int s) {
+    int64_t ks = s;
+    const bool second = FORM == kFormDx && ks >= steps_seg;
+    if (second) ks -= steps_seg;
+    const int64_t k = ks * BK;
+    if constexpr (AK)
+      load_kc(ra, (const float*)P.a + t.m0 * P.lda + (second ? P.seg : 0), P.lda, mvalid, k, P.K, tid);
+    else
+      load_mnc(ra, (const float*)P.a + t.m0, P.lda, mvalid, k, P.K, tid);
+    if constexpr (FORM == kFormDx) {
+      load_kc(rb, (const float*)(second ? P.b[1] : P.b[0]) + t.n0 * P.ldb, P.ldb, nvalid, k, P.K, tid);
+    } else if constexpr (FORM == kFormGlu) {
+      // columns 0..63 of the tile from wg, 64..127 from wu
+      const bool up = (tid & 31) >= 16;
+      load_mnc(rb, (const float*)(up ? P.b[1] : P.b[0]) + t.n0 - (up ? 64 : 0), P.ldb, (up ? 64 : 0) + (nvalid < 64 ? nvalid : 64),
+               k, P.K, tid);
+    } else {
+      load_mnc(rb, (const float*)P.b[0] + (FORM == kFormDw ? t.seg * P.seg : 0) + t.n0, P.ldb, nvalid, k, P.K, tid);
+    }
+  };
+  auto store = [&](int b) {
+    if constexpr (AK) store_kc(sa[b], ra, tid); else store_mnc(sa[b], ra, tid);
+    if constexpr (BKC) store_kc(sb[b], rb, tid); else store_mnc(sb[b], rb, tid);
+  };
+  f32x16_t acc[2][2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
+  load(t.s0);
+  store(0);
+  __syncthreads();
+#pragma unroll 1
+  for (int s = t.s0; s < t.s1; ++s) {
+    const int cur = (s - t.s0) & 1;
+    if (s + 1 < t.s1) load(s + 1);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      f32x4_t fa[2], fb[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        fa[x] = frag<AK>(sa[cur], wm * 64 + x * 32 + r32, q, half);
+        fb[x] = frag<BKC>(sb[cur], (FORM == kFormGlu ? x * 64 + wn * 32 : wn * 64 + x * 32) + r32, q, half);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb)
+            acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[nb][e], fa[mb][e], acc[mb][nb], 0, 0, 0);
+    }
+    if (s + 1 < t.s1) store(cur ^ 1);
+    __syncthreads();
+  }
+  // lane l holds row l % 32 and columns 8 i + 4 (l / 32) + 0..3 of each block
+#pragma unroll
+  for (int mb = 0; mb < 2; ++mb) {
+    const int m = wm * 64 + mb * 32 + r32;
+    if (m >= mvalid) continue;
+    const int64_t row = t.m0 + m;
+    if constexpr (FORM == kFormGlu) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = t.n0 + wn * 32 + 8 * i + 4 * half;
+        if (col >= P.N) continue;
+        float g[4], u[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          g[q] = acc[mb][0][4 * i + q];
+          u[q] = acc[mb][1][4 * i + q];
+        }
+        if (P.S > 1) {
+          part4(P, t.chunk, 0, row, col, g);
+          part4(P, t.chunk, 1, row, col, u);
+        } else {
+          emit4_glu<float>(P, row, col, g, u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = t.n0 + wn * 64 + nb * 32 + 8 * i + 4 * half;
+          if (col >= P.N) continue;
+          float v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = acc[mb][nb][4 * i + q];
+          if (P.S > 1)
+            part4(P, t.chunk, t.seg, row, col, v);
+          else
+            emit4<float, FORM>(P, t.seg, row, col, v);
+        }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ few rows
+// Weights [K][N] streamed once past at most 16 MT rows of x.  A workgroup
+// owns a column tile and a chunk of K; its 4 waves take 32-row K steps in turn
+// and add their sums in wave order through LDS.  In a step, lane (i = l % 16,
+// g = l / 16) loads the weights' rows 8 g .. 8 g + 7 at its own consecutive columns,
+// and 8 consecutive k of each x row i: both go from the loads to the matrix
+// instruction's registers directly, with no LDS and no barrier, and the loads
+// of the next step are in flight while a step is multiplied.
+//  bf16     v_mfma_f32_16x16x32_bf16, one per column: a column's 8 k are
+//           picked out of the 8 loaded rows with one byte permute per pair.
+//  float32  v_mfma_f32_16x16x4f32, 8 per column.
+template <typename T, int FORM, int MT>
+struct FewCfg {
+  static constexpr int NM = FORM == kFormGlu ? 2 : 1;                           // matrices
+  static constexpr int CPL = sizeof(T) == 2 ? (FORM == kFormGlu ? 4 : 8) : 4;    // columns per lane and matrix
+  static constexpr int COLS = 16 * CPL;                                         // tile columns per matrix
+};
+
+template <typename T, int CPL>
+struct FewRow {   // CPL consecutive weights of a row
+  uint32_t w[CPL * (int)sizeof(T) / 4];
+  DEV void load(const T* p, int n) {
+    if constexpr (sizeof(T) == 2 && CPL == 4) {
+      if (n >= 4) {
+        const u32x2_t r = *(const u32x2_any_t*)p;
+        w[0] = r[0];
+        w[1] = r[1];
+      } else {
+        w[0] = w[1] = 0u;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (i < n) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+      }
+    } else {
+      const u32x4_t r = __builtin_bit_cast(u32x4_t, Vec<T>::load(p, n));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = r[i];
+    }
+  }
+  DEV void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)(CPL * sizeof(T) / 4); ++i) w[i] = 0u;
+  }
+};
+
+template <typename T, int FORM, int MT>
+__global__ __launch_bounds__(256) void dense_few_kernel(DenseParams P) {
+  using Cfg = FewCfg<T, FORM, MT>;
+  constexpr int NM = Cfg::NM, CPL = Cfg::CPL, COLS = Cfg::COLS, RS = NM * COLS + 4;
+  constexpr int XW = sizeof(T) == 2 ? 1 : 2;   // 16-byte loads of 8 consecutive k
+  __shared__ __attribute__((aligned(16))) float s_acc[4 * 16 * MT * RS];
+  const int nT = (P.N + COLS - 1) / COLS;
+  const int64_t L = map_unit(blockIdx.x, (int64_t)nT * P.S, P.seed);
+  if (L < 0) return;
+  const int chunk = (int)(L / nT), n0 = (int)(L % nT) * COLS;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i16 = lane & 15, g = lane >> 4;
+  const int steps = (int)((P.K + 31) / 32);
+  const int s0 = (int)((int64_t)chunk * steps / P.S), s1 = (int)((int64_t)(chunk + 1) * steps / P.S);
+  const int K = (int)P.K;
+  const int col = n0 + i16 * CPL, ncol = P.N - col;
+  f32x4_t acc[NM][CPL][MT];
+#pragma unroll
+  for (int m = 0; m < NM; ++m)
+#pragma unroll
+    for (int c = 0; c < CPL; ++c)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[m][c][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  struct Step {
+    FewRow<T, CPL> w[NM][8];
+    typename Vec<T>::raw x[MT][XW];
+  };
+  // rows of x past the last repeat it: their sums are not used
+  const T* xrow[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int row = 16 * t + i16;
+    xrow[t] = (const T*)P.a + (int64_t)(row < P.M ? row : (int)P.M - 1) * P.lda;
+  }
+  // steps below `whole` lie inside the matrix in both directions
+  const int whole = n0 + COLS <= P.N ? K / 32 : 0;
+  auto load_full = [&](Step& b, int s) __attribute__((always_inline)) {
+    const int k = 32 * s + 8 * g;
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+      for (int r = 0; r < 8; ++r) b.w[m][r].load((const T*)P.b[m] + (int64_t)(k + r) * P.ldb + col, CPL);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int h = 0; h < XW; ++h) b.x[t][h] = Vec<T>::load(xrow[t] + k + h * Vec<T>::N, Vec<T>::N);
+  };
+  auto load_edge = [&](Step& b, int s) __attribute__((always_inline)) {
+    const int k = 32 * s + 8 * g;
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        if (k + r < K && ncol > 0)
+          b.w[m][r].load((const T*)P.b[m] + (int64_t)(k + r) * P.ldb + col, ncol);
+        else
+          b.w[m][r].zero();
+      }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int h = 0; h < XW; ++h) {
+        const int kk = k + h * Vec<T>::N;
+        if (kk < K)
+          b.x[t][h] = Vec<T>::load(xrow[t] + kk, K - kk);
+        else
+          b.x[t][h] = typename Vec<T>::raw{};
+      }
+  };
+  auto mma = [&](const Step& b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        if constexpr (sizeof(T) == 2) {
+          u32x4_t f;
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            f[p] = __builtin_amdgcn_perm(b.w[m][2 * p + 1].w[c >> 1], b.w[m][2 * p].w[c >> 1],
+                                         (c & 1) ? 0x07060302u : 0x05040100u);
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+            acc[m][c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b.x[t][0]),
+                                                                   __builtin_bit_cast(bf16x8_t, f), acc[m][c][t], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+              acc[m][c][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                  __builtin_bit_cast(f32x4_t, b.x[t][r >> 2])[r & 3], __uint_as_float(b.w[m][r].w[c]), acc[m][c][t], 0, 0, 0);
+        }
+      }
+  };
+  int s = s0 + wave;
+  const int e = s1 < whole ? s1 : whole;
+  {
+    Step b0, b1;
+    if (s < e) load_full(b0, s);
+#pragma unroll 1
+    while (s < e) {
+      if (s + 4 < e) load_full(b1, s + 4);
+      mma(b0);
+      s += 4;
+      if (s >= e) break;
+      if (s + 4 < e) load_full(b0, s + 4);
+      mma(b1);
+      s += 4;
+    }
+  }
+#pragma unroll 1
+  for (; s < s1; s += 4) {
+    Step b;
+    load_edge(b, s);
+    mma(b);
+  }
+  // lane l holds rows 4 g + r and the columns CPL (l % 16) + c of its tiles
+#pragma unroll
+  for (int m = 0; m < NM; ++m)
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < CPL; c += 4)
+          *(f32x4_t*)(s_acc + ((wave * MT + t) * 16 + 4 * g + r) * RS + m * COLS + i16 * CPL + c) =
+              f32x4_t{acc[m][c][t][r], acc[m][c + 1][t][r], acc[m][c + 2][t][r], acc[m][c + 3][t][r]};
+  __syncthreads();
+  constexpr int QPR = COLS / 4;   // groups of four columns per row and matrix
+  for (int o = tid; o < 16 * MT * QPR; o += 256) {
+    const int row = o / QPR, c = (o % QPR) * 4;
+    if (row >= P.M || n0 + c >= P.N) continue;
+    float v[NM][4];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      const float* p = s_acc + row * RS + m * COLS + c;
+      f32x4_t a = *(const f32x4_t*)p;
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        const f32x4_t b = *(const f32x4_t*)(p + w * 16 * MT * RS);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) a[q] = a[q] + b[q];
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[m][q] = a[q];
+    }
+    if (P.S > 1) {
+#pragma unroll
+      for (int m = 0; m < NM; ++m) part4(P, chunk, m, row, n0 + c, v[m]);
+    } else if constexpr (FORM == kFormGlu) {
+      emit4_glu<T>(P, row, n0 + c, v[0], v[NM - 1]);
+    } else {
+      emit4<T, FORM>(P, 0, row, n0 + c, v[0]);
+    }
+  }
+}
+
+// -------------------------------------------------------------- join of chunks
+// One thread per four columns: the chunks' partials in chunk order, then the
+// epilogue.
+template <typename T, int FORM>
+__global__ __launch_bounds__(256) void dense_finish_kernel(DenseParams P) {
+  const int q = (P.N + 3) / 4;
+  const int nm = FORM == kFormDw ? P.nseg : 1;
+  const int64_t total = P.M * q * nm;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  const int64_t row = i / (q * nm);
+  const int rest = (int)(i - row * (q * nm));
+  const int seg = rest / q, col = (rest - seg * q) * 4;
+  auto sum = [&](int sg, float (&v)[4]) {
+    const float* p = P.part + row * P.part_ld + sg * P.part_seg + col;
+    f32x4_t a = *(const f32x4_t*)p;
+#pragma unroll 4
+    for (int s = 1; s < P.S; ++s) {
+      const f32x4_t o = *(const f32x4_t*)(p + (int64_t)s * P.M * P.part_ld);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) a[x] = a[x] + o[x];
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = a[x];
+  };
+  float v[4];
+  sum(seg, v);
+  if constexpr (FORM == kFormGlu) {
+    float u[4];
+    sum(1, u);
+    emit4_glu<T>(P, row, col, v, u);
+  } else {
+    emit4<T, FORM>(P, seg, row, col, v);
+  }
+}
+
+// ---------------------------------------------------------- elementwise passes
+__global__ __launch_bounds__(256) void dense_pack_kernel(const uint16_t* in, int64_t rows, int cols, int64_t ld,
+                                                         uint16_t* out, int64_t ldo) {
+  const int q = (int)(ldo / 8);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows * q) return;
+  const int64_t row = i / q;
+  const int c = (int)(i - row * q) * 8;
+  u32x4_t r = {0u, 0u, 0u, 0u};
+  if (c < cols) r = Vec<uint16_t>::load(in + row * ld + c, cols - c);
+  *(u32x4_t*)(out + row * ldo + c) = r;
+}
+
+// V elements of a saved pre-activation, zeros past n >= 1
+template <typename Z, int V>
+DEV void load_z(const Z* p, int n, float* v) {
+  constexpr int N = Vec<Z>::N;
+#pragma unroll
+  for (int i = 0; i < V / N; ++i) {
+    typename Vec<Z>::raw r{};
+    if (n > i * N) r = Vec<Z>::load(p + i * N, n - i * N);
+    Vec<Z>::get(r, v + i * N);
+  }
+}
+
+// dz = dy act'(z), or dg = da u act'(g) and du = da act(g).  A workgroup owns
+// 64 V columns and a block of rows; its 4 waves take the rows in turn, and
+// their column sums of the unrounded dz are added in wave order.
+template <typename T, typename Z, bool GLU>
+__global__ __launch_bounds__(256) void dense_ew_kernel(DenseEwParams P) {
+  constexpr int V = Vec<T>::N, CT = 64 * V;
+  __shared__ float s_sum[3][CT];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int cT = (P.pad + CT - 1) / CT;
+  const int64_t units = (int64_t)P.blocks * cT;
+  const int64_t L = map_unit(blockIdx.x, units, P.seed);
+  if (L < 0) return;
+  const int64_t blk = L / cT;
+  const int col = (int)(L % cT) * CT + lane * V;
+  const int64_t r0 = blk * P.rows / P.blocks, r1 = (blk + 1) * P.rows / P.blocks;
+  const int n = P.cols - col, no = P.pad - col;
+  const bool need_z = GLU || P.act != kActNone;
+  float sum[V];
+#pragma unroll
+  for (int q = 0; q < V; ++q) sum[q] = 0.f;
+  if (no > 0) {
+#pragma unroll 2
+    for (int64_t row = r0 + wave; row < r1; row += 4) {
+      float d[V], o0[V], o1[V];
+#pragma unroll
+      for (int q = 0; q < V; ++q) o0[q] = o1[q] = 0.f;
+      if (n > 0) {
+        Vec<T>::get(Vec<T>::load((const T*)P.dy + row * P.lddy + col, n), d);
+        if (need_z) {
+          float z[V], u[V];
+          load_z<Z, V>((const Z*)P.z[0] + row * P.ldz + col, n, z);
+          if (GLU) load_z<Z, V>((const Z*)P.z[1] + row * P.ldz + col, n, u);
+#pragma unroll
+          for (int q = 0; q < V; ++q) {
+            float v, dv;
+            act_df(P.act, z[q], v, dv);
+            o0[q] = GLU ? d[q] * u[q] * dv : d[q] * dv;
+            o1[q] = d[q] * v;
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < V; ++q) o0[q] = d[q];
+        }
+        // past the row every load gave 0; act(0) or act'(0) times 0 is 0
+      }
+#pragma unroll
+      for (int q = 0; q < V; ++q) sum[q] = sum[q] + o0[q];
+      if (P.out[0]) Vec<T>::store((T*)P.out[0] + row * P.ldo + col, o0, no);
+      if (GLU) Vec<T>::store((T*)P.out[1] + row * P.ldo + col, o1, no);
+    }
+  }
+  if (GLU || !P.part) return;
+  if (wave > 0)
+#pragma unroll
+    for (int q = 0; q < V; ++q) s_sum[wave - 1][q * 64 + lane] = sum[q];
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      float v = sum[q];
+#pragma unroll
+      for (int w = 0; w < 3; ++w) v = v + s_sum[w][q * 64 + lane];
+      if (col + q < P.cols) P.part[blk * P.cols + col + q] = v;
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void dense_zero_kernel(uint16_t* p, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = 0;
+}
+
+// -------------------------------------------------------------------- launches
+int dense_tile_n(int form, bool bf16) { return (bf16 ? 256 : 128) / (form == kFormGlu ? 2 : 1); }
+int dense_few_n(int form, bool bf16) { return bf16 && form != kFormGlu ? 128 : 64; }
+
+template <int FORM>
+static void dense_gemm_launch(const DenseParams& P, bool bf16, int bm, int64_t grid, hipStream_t st) {
+  if (!bf16)
+    dense_f32_kernel<FORM><<<grid, 256, 0, st>>>(P);
+  else if (bm == 256)
+    dense_bf16_kernel<FORM, 128><<<grid, 256, 0, st>>>(P);
+  else
+    dense_bf16_kernel<FORM, 64><<<grid, 256, 0, st>>>(P);
+}
+
+hipError_t launch_dense_gemm(const DenseParams& P, int form, bool bf16, int bm, hipStream_t st) {
+  const int bn = dense_tile_n(form, bf16);
+  const int64_t tiles = (P.M + bm - 1) / bm * ((P.N + bn - 1) / bn) * (form == kFormDw ? P.nseg : 1);
+  const int64_t grid = grid_for_units(tiles * P.S);
+  switch (form) {
+    case kFormLinear: dense_gemm_launch<kFormLinear>(P, bf16, bm, grid, st); break;
+    case kFormGlu: dense_gemm_launch<kFormGlu>(P, bf16, bm, grid, st); break;
+    case kFormDx: dense_gemm_launch<kFormDx>(P, bf16, bm, grid, st); break;
+    default: dense_gemm_launch<kFormDw>(P, bf16, bm, grid, st); break;
+  }
+  return hipGetLastError();
+}
+
+template <int FORM>
+static void dense_few_launch(const DenseParams& P, bool bf16, int64_t grid, hipStream_t st) {
+  if (!bf16)
+    dense_few_kernel<float, FORM, 1><<<grid, 256, 0, st>>>(P);
+  else if (P.M <= 16)
+    dense_few_kernel<uint16_t, FORM, 1><<<grid, 256, 0, st>>>(P);
+  else if (P.M <= 32)
+    dense_few_kernel<uint16_t, FORM, 2><<<grid, 256, 0, st>>>(P);
+  else
+    dense_few_kernel<uint16_t, FORM, 4><<<grid, 256, 0, st>>>(P);
+}
+
+hipError_t launch_dense_few(const DenseParams& P, int form, bool bf16, hipStream_t st) {
+  const int bn = dense_few_n(form, bf16);
+  const int64_t grid = grid_for_units((int64_t)((P.N + bn - 1) / bn) * P.S);
+  if (form == kFormGlu)
+    dense_few_launch<kFormGlu>(P, bf16, grid, st);
+  else
+    dense_few_launch<kFormLinear>(P, bf16, grid, st);
+  return hipGetLastError();
+}
+
+template <typename T>
+static void dense_finish_launch(const DenseParams& P, int form, int64_t grid, hipStream_t st) {
+  switch (form) {
+    case kFormLinear: dense_finish_kernel<T, kFormLinear><<<grid, 256, 0, st>>>(P); break;
+    case kFormGlu: dense_finish_kernel<T, kFormGlu><<<grid, 256, 0, st>>>(P); break;
+    case kFormDx: dense_finish_kernel<T, kFormDx><<<grid, 256, 0, st>>>(P); break;
+    default: dense_finish_kernel<T, kFormDw><<<grid, 256, 0, st>>>(P); break;
+  }
+}
+
+hipError_t launch_dense_finish(const DenseParams& P, int form, bool bf16, hipStream_t st) {
+  const int64_t total = P.M * ((P.N + 3) / 4) * (form == kFormDw ? P.nseg : 1);
+  const int64_t grid = (total + 255) / 256;
+  if (bf16)
+    dense_finish_launch<uint16_t>(P, form, grid, st);
+  else
+    dense_finish_launch<float>(P, form, grid, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_dense_pack(const void* in, int64_t rows, int cols, int64_t ld, void* out, int64_t ldo,
+                             hipStream_t st) {
+  dense_pack_kernel<<<(rows * (ldo / 8) + 255) / 256, 256, 0, st>>>((const uint16_t*)in, rows, cols, ld,
+                                                                  (uint16_t*)out, ldo);
+  return hipGetLastError();
+}
+
+// Row blocks of the elementwise pass: about 2048 workgroups, at least 4 rows each.
+int dense_ew_blocks(int64_t rows, int cols, bool bf16) {
+  const int ct = bf16 ? 512 : 256;
+  int64_t b = 2048 / ((cols + ct - 1) / ct);
+  const int64_t most = (rows + 3) / 4;
+  if (b > most) b = most;
+  return (int)(b < 1 ? 1 : b > 512 ? 512 : b);
+}
+
+template <typename T, typename Z>
+static void dense_ew_launch(const DenseEwParams& P, bool glu, int64_t grid, hipStream_t st) {
+  if (glu)
+    dense_ew_kernel<T, Z, true><<<grid, 256, 0, st>>>(P);
+  else
+    dense_ew_kernel<T, Z, false><<<grid, 256, 0, st>>>(P);
+}
+
+hipError_t launch_dense_ew(const DenseEwParams& P, bool glu, bool bf16, hipStream_t st) {
+  const int ct = bf16 ? 512 : 256;
+  const int64_t grid = grid_for_units((int64_t)P.blocks * ((P.pad + ct - 1) / ct));
+  if (!bf16)
+    dense_ew_launch<float, float>(P, glu, grid, st);
+  else if (P.z_f32)
+    dense_ew_launch<uint16_t, float>(P, glu, grid, st);
+  else
+    dense_ew_launch<uint16_t, uint16_t>(P, glu, grid, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_dense_zero(void* p, int64_t n16, hipStream_t st) {
+  dense_zero_kernel<<<(n16 + 255) / 256, 256, 0, st>>>((uint16_t*)p, n16);
+  return hipGetLastError();
+}
+
+}  // namespace moedet

@@ -1,0 +1,526 @@
+// Host side of the dense operators' C ABI (declared in include/moedet.h):
+// argument checks, workspace layout, and the choice of kernel and split from
+// sizes alone.
+#include "../../include/moedet.h"
+#include "dense.h"
+
+#define MOE_API extern "C" __attribute__((visibility("default")))
+
+namespace moedet {
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+
+// ------------------------------------------------------------------ description
+constexpr int64_t kMaxLd = (int64_t)1 << 20;
+
+struct Dense {
+  bool bf16;
+  int nm;             // weight matrices: 1 linear, 2 gated
+  int64_t T;
+  int D, F;
+  int64_t es;
+};
+
+moe_status check(const moe_dense* p, int nm, Dense* d) {
+  if (!p) return MOE_ERR_NULL;
+  if (p->dtype != MOE_F32 && p->dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (p->grad_dtype != MOE_F32 && p->grad_dtype != p->dtype) return MOE_ERR_DTYPE;
+  if (p->z_dtype != MOE_F32 && p->z_dtype != p->dtype) return MOE_ERR_DTYPE;
+  if (p->act < MOE_ACT_NONE || p->act > MOE_ACT_GELU) return MOE_ERR_MODE;
+  if (p->rows < 0 || p->rows >= (int64_t)1 << 31 || p->d_in < 1 || p->d_out < 1) return MOE_ERR_SHAPE;
+  if (p->d_in >= kMaxLd || p->d_out >= kMaxLd) return MOE_ERR_SHAPE;
+  if (p->ldx < p->d_in || p->ldw < p->d_out || p->ldy < p->d_out || p->ldz < p->d_out) return MOE_ERR_SHAPE;
+  if (p->ldx >= kMaxLd || p->ldw >= kMaxLd || p->ldy >= kMaxLd || p->ldz >= kMaxLd || p->ldr < 0 || p->ldr >= kMaxLd)
+    return MOE_ERR_SHAPE;
+  d->bf16 = p->dtype == MOE_BF16;
+  d->es = d->bf16 ? 2 : 4;
+  // a copied weight matrix has rows of d_out rounded up to 8, no longer than ldw + 7
+  if ((int64_t)p->d_in * up(p->ldw, 8) * d->es >= (int64_t)1 << 31) return MOE_ERR_SHAPE;
+  d->nm = nm;
+  d->T = p->rows;
+  d->D = p->d_in;
+  d->F = p->d_out;
+  return MOE_OK;
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// A bf16 matrix that the tile kernels read in place: whole 16-byte chunks.
+bool direct(const Dense& d, int64_t cols, int64_t ld) { return !d.bf16 || (cols % 8 == 0 && ld % 8 == 0); }
+
+// --------------------------------------------------------- tile and split choice
+struct Choice {
+  int bm, S;
+};
+constexpr int kCUs = 256;
+constexpr int64_t kMaxPartialBytes = (int64_t)1 << 30;
+
+// Time estimate in microseconds of a launch of `wgs` workgroups of `steps` slices
+// each, plus the float32 partials of a split and their join.
+double estimate(int64_t wgs, int64_t steps, double per_step, double fixed, int64_t S, double out_elems) {
+  const double rounds = (double)((wgs + kCUs - 1) / kCUs);
+  double t = rounds * (fixed + (double)steps * per_step);
+  if (S > 1) t += (double)S * out_elems * 8.0 / 4.5e6 + 4.0;
+  return t;
+}
+
+// Tile height and number of K chunks of one product.  The constants are
+// microseconds per slice of one tile with every CU busy, and the fixed cost of a
+// tile (lookup, first slice, epilogue).
+Choice choose(const Dense& d, int form, int64_t M, int64_t N, int nseg, int64_t K, int64_t ld_max) {
+  const int bn = dense_tile_n(form, d.bf16);
+  const int bk = d.bf16 ? 32 : 16;
+  const int64_t nT = (N + bn - 1) / bn * (form == kFormDw ? nseg : 1);
+  const int64_t steps = (K + bk - 1) / bk * (form == kFormDx ? nseg : 1);
+  const double outs = (double)M * N * (form == kFormDw ? nseg : form == kFormGlu ? 2 : 1);
+  // the weight gradient's operands are addressed by 32-bit offsets from the
+  // chunk's first row
+  int64_t smin = 1;
+  if (form == kFormDw && d.bf16) smin = (K + 64) * ld_max * 2 / ((int64_t)1 << 30) + 1;
+  Choice best{0, 0};
+  double tb = 0;
+  for (int bm : {256, 128}) {
+    if (!d.bf16 && bm == 256) continue;
+    const double per = !d.bf16 ? 0.9 : bm == 256 ? 0.92 : 0.55;
+    const double fixed = !d.bf16 ? 5.0 : bm == 256 ? 9.0 : 7.0;
+    const int64_t tiles = (M + bm - 1) / bm * nT;
+    for (int64_t S = smin; S <= (smin > 32 ? smin : 32) && (S == smin || (steps / S >= 4 && S * outs * 4 <= kMaxPartialBytes));
+         ++S) {
+      const double t = estimate(tiles * S, (steps + S - 1) / S, per, fixed, S, outs);
+      if (best.S == 0 || t < tb * 0.98) {
+        best = Choice{bm, (int)S};
+        tb = t;
+      }
+      if (tiles * S >= 4 * kCUs) break;
+    }
+  }
+  return best;
+}
+
+// Chunks of the few-row kernels: two workgroups a CU, each wave at least one
+// 32-row step, and partials of at most half of the weights' bytes.
+int few_chunks(const Dense& d, int form) {
+  const int bn = dense_few_n(form, d.bf16);
+  const int64_t tiles = (d.F + bn - 1) / bn, steps = (d.D + 31) / 32;
+  int64_t S = (2 * kCUs + tiles - 1) / tiles;
+  const int64_t by_bytes = (int64_t)d.D * d.es / (16 * d.T);
+  if (S > by_bytes) S = by_bytes;
+  if (S > steps / 4) S = steps / 4;
+  if (S < 1) S = 1;
+  const int64_t per = (steps + S - 1) / S;
+  return (int)((steps + per - 1) / per);
+}
+bool few(const Dense& d) { return d.T <= (d.bf16 ? kFewRowsBf16 : kFewRowsF32); }
+
+// ------------------------------------------------------------- workspace layout
+struct FwdPlan {
+  bool few, pack_x, pack_w;
+  Choice ch;
+  int64_t ldx, ldw;          // row distances that the kernel reads
+  int64_t part_seg, part_ld;
+  size_t x, w, part, total;  // byte offsets
+};
+
+FwdPlan fwd_plan(const moe_dense* p, const Dense& d) {
+  FwdPlan f{};
+  const int form = d.nm == 2 ? kFormGlu : kFormLinear;
+  f.few = few(d);
+  f.ldx = p->ldx;
+  f.ldw = p->ldw;
+  size_t o = 0;
+  if (d.T == 0) return f;
+  if (f.few) {
+    f.ch = Choice{0, few_chunks(d, form)};
+  } else {
+    f.pack_x = !direct(d, d.D, p->ldx);
+    f.pack_w = !direct(d, d.F, p->ldw);
+    f.ch = choose(d, form, d.T, d.F, 1, d.D, 0);
+    if (f.pack_x) {
+      f.ldx = up(d.D, 8);
+      f.x = o;
+      o += align_up((size_t)d.T * f.ldx * 2);
+    }
+    if (f.pack_w) {
+      f.ldw = up(d.F, 8);
+      f.w = o;
+      o += align_up((size_t)d.nm * d.D * f.ldw * 2);
+    }
+  }
+  f.part_seg = up(d.F, 4);
+  f.part_ld = d.nm * f.part_seg;
+  f.part = o;
+  if (f.ch.S > 1) o += align_up((size_t)f.ch.S * d.T * f.part_ld * 4);
+  f.total = o;
+  return f;
+}
+
+struct BwdPlan {
+  bool pack_x, pack_w, make_dz;
+  Choice dx, dw;
+  int64_t ldx, ldw, lddz, segdz;
+  int64_t dx_ld, dw_seg;
+  int ew_blocks;
+  size_t x, w, dz, colsum, part, total;
+};
+
+BwdPlan bwd_plan(const moe_dense* p, const Dense& d) {
+  BwdPlan b{};
+  b.ldx = p->ldx;
+  b.ldw = p->ldw;
+  b.lddz = p->ldy;
+  size_t o = 0;
+  if (d.T == 0) return b;
+  b.pack_x = !direct(d, d.D, p->ldx);
+  b.pack_w = !direct(d, d.F, p->ldw);
+  b.make_dz = d.nm == 2 || p->act != MOE_ACT_NONE || !direct(d, d.F, p->ldy);
+  if (b.pack_x) {
+    b.ldx = up(d.D, 8);
+    b.x = o;
+    o += align_up((size_t)d.T * b.ldx * 2);
+  }
+  if (b.pack_w) {
+    b.ldw = up(d.F, 8);
+    b.w = o;
+    o += align_up((size_t)d.nm * d.D * b.ldw * 2);
+  }
+  if (b.make_dz) {
+    b.segdz = up(d.F, 32);
+    b.lddz = d.nm * b.segdz;
+    b.dz = o;
+    o += align_up((size_t)d.T * b.lddz * d.es);
+  }
+  b.ew_blocks = dense_ew_blocks(d.T, d.F, d.bf16);
+  b.colsum = o;
+  if (d.nm == 1) o += align_up((size_t)b.ew_blocks * d.F * 4);
+  b.dx = choose(d, kFormDx, d.T, d.D, d.nm, d.F, 0);
+  b.dw = choose(d, kFormDw, d.D, d.F, d.nm, d.T, b.ldx > b.lddz ? b.ldx : b.lddz);
+  b.dx_ld = up(d.D, 4);
+  b.dw_seg = up(d.F, 4);
+  // the two products run one after the other and share the partials' space
+  size_t part = 0;
+  if (b.dx.S > 1) part = (size_t)b.dx.S * d.T * b.dx_ld * 4;
+  if (b.dw.S > 1) {
+    const size_t q = (size_t)b.dw.S * d.D * d.nm * b.dw_seg * 4;
+    if (q > part) part = q;
+  }
+  b.part = o;
+  o += align_up(part);
+  b.total = o;
+  return b;
+}
+
+moe_status workspace_size(const moe_dense* p, int nm, size_t* fwd, size_t* bwd) {
+  Dense d;
+  const moe_status s = check(p, nm, &d);
+  if (s != MOE_OK) return s;
+  if (fwd) *fwd = fwd_plan(p, d).total;
+  if (bwd) *bwd = bwd_plan(p, d).total;
+  return MOE_OK;
+}
+
+moe_status check_ws(const void* ws, size_t have, size_t need) {
+  if (need == 0) return MOE_OK;
+  if (!ws) return MOE_ERR_NULL;
+  if (have < need || ((uintptr_t)ws & (kAlign - 1))) return MOE_ERR_WORKSPACE;
+  return MOE_OK;
+}
+
+#define MOE_TRY(x)                               \
+  do {                                           \
+    if ((x) != hipSuccess) return MOE_ERR_HIP;   \
+  } while (0)
+
+// x (and the weights) copied into whole 16-byte rows where they are not
+moe_status pack_inputs(const Dense& d, const moe_dense* p, bool px, bool pw, int64_t ldx, int64_t ldw, char* wx, char* ww,
+                       const void*& x, const void* (&w)[2], hipStream_t st) {
+  if (px) {
+    MOE_TRY(launch_dense_pack(x, d.T, d.D, p->ldx, wx, ldx, st));
+    x = wx;
+  }
+  if (pw) {
+    for (int m = 0; m < d.nm; ++m) {
+      char* o = ww + (size_t)m * d.D * ldw * 2;
+      MOE_TRY(launch_dense_pack(w[m], d.D, d.F, p->ldw, o, ldw, st));
+      w[m] = o;
+    }
+  }
+  return MOE_OK;
+}
+
+moe_status run_product(DenseParams& P, int form, const Dense& d, int bm, hipStream_t st) {
+  MOE_TRY(launch_dense_gemm(P, form, d.bf16, bm, st));
+  if (P.S > 1) MOE_TRY(launch_dense_finish(P, form, d.bf16, st));
+  return MOE_OK;
+}
+
+moe_status forward(const moe_dense* p, int nm, const void* x, const void* w0, const void* w1, const void* bias,
+                   const void* residual, void* y, void* z0, void* z1, void* ws, size_t ws_bytes, hipStream_t st) {
+  Dense d;
+  moe_status s = check(p, nm, &d);
+  if (s != MOE_OK) return s;
+  if (residual && p->ldr < d.F) return MOE_ERR_SHAPE;
+  if (nm == 2 && (z0 == nullptr) != (z1 == nullptr)) return MOE_ERR_NULL;
+  if (d.T == 0) return MOE_OK;
+  if (!x || !w0 || !w1 || !y) return MOE_ERR_NULL;
+  for (const void* q : {x, w0, w1, bias, residual, (const void*)y, (const void*)z0, (const void*)z1})
+    if ((uintptr_t)q & (q == bias ? d.es - 1 : 15)) return MOE_ERR_SHAPE;
+  const FwdPlan f = fwd_plan(p, d);
+  if ((s = check_ws(ws, ws_bytes, f.total)) != MOE_OK) return s;
+  const void* w[2] = {w0, w1};
+  s = pack_inputs(d, p, f.pack_x, f.pack_w, f.ldx, f.ldw, (char*)ws + f.x, (char*)ws + f.w, x, w, st);
+  if (s != MOE_OK) return s;
+  const int form = nm == 2 ? kFormGlu : kFormLinear;
+  DenseParams P{};
+  P.M = d.T;
+  P.N = d.F;
+  P.K = d.D;
+  P.nseg = 1;
+  P.a = x;
+  P.lda = f.ldx;
+  P.b[0] = w[0];
+  P.b[1] = w[1];
+  P.ldb = f.ldw;
+  P.S = f.ch.S;
+  P.part = (float*)((char*)ws + f.part);
+  P.part_ld = f.part_ld;
+  P.part_seg = (int)f.part_seg;
+  P.bias = bias;
+  P.add = residual;
+  P.ldadd = p->ldr;
+  P.c[0] = y;
+  P.ldc = p->ldy;
+  P.z[0] = z0;
+  P.z[1] = z1;
+  P.ldz = p->ldz;
+  P.z_f32 = p->z_dtype == MOE_F32;
+  P.act = p->act;
+  P.seed = p->debug_shuffle_seed;
+  if (!f.few) return run_product(P, form, d, f.ch.bm, st);
+  MOE_TRY(launch_dense_few(P, form, d.bf16, st));
+  if (P.S > 1) MOE_TRY(launch_dense_finish(P, form, d.bf16, st));
+  return MOE_OK;
+}
+
+moe_status backward(const moe_dense* p, int nm, const void* dy, const void* x, const void* w0, const void* w1,
+                    const void* z0, const void* z1, const void* dx_add, void* dx, void* dw0, void* dw1, void* db,
+                    void* ws, size_t ws_bytes, hipStream_t st) {
+  Dense d;
+  moe_status s = check(p, nm, &d);
+  if (s != MOE_OK) return s;
+  if (dx_add && p->ldr < d.D) return MOE_ERR_SHAPE;
+  const bool g32 = p->grad_dtype == MOE_F32;
+  const int64_t gs = g32 ? 4 : 2;
+  if (!dw0 || !dw1) return MOE_ERR_NULL;
+  const bool need_z = nm == 2 || p->act != MOE_ACT_NONE;
+  if (d.T > 0 && (!dy || !x || !w0 || !w1 || !dx || (need_z && (!z0 || !z1)))) return MOE_ERR_NULL;
+  for (const void* q : {dy, x, w0, w1, need_z ? z0 : nullptr, need_z ? z1 : nullptr, dx_add, (const void*)dx,
+                        (const void*)dw0, (const void*)dw1})
+    if ((uintptr_t)q & 15) return MOE_ERR_SHAPE;
+  if ((uintptr_t)db & (gs - 1)) return MOE_ERR_SHAPE;
+  if (d.T == 0) {
+    const int64_t n16 = (int64_t)d.D * d.F * gs / 2;
+    MOE_TRY(launch_dense_zero(dw0, n16, st));
+    if (nm == 2) MOE_TRY(launch_dense_zero(dw1, n16, st));
+    if (db) MOE_TRY(launch_dense_zero(db, d.F * gs / 2, st));
+    return MOE_OK;
+  }
+  const BwdPlan b = bwd_plan(p, d);
+  if ((s = check_ws(ws, ws_bytes, b.total)) != MOE_OK) return s;
+  char* base = (char*)ws;
+  const void* w[2] = {w0, w1};
+  s = pack_inputs(d, p, b.pack_x, b.pack_w, b.ldx, b.ldw, base + b.x, base + b.w, x, w, st);
+  if (s != MOE_OK) return s;
+  const void* dz = dy;
+  if (b.make_dz || db) {
+    DenseEwParams E{};
+    E.rows = d.T;
+    E.cols = d.F;
+    E.dy = dy;
+    E.lddy = p->ldy;
+    E.z[0] = z0;
+    E.z[1] = z1;
+    E.ldz = p->ldz;
+    E.z_f32 = p->z_dtype == MOE_F32;
+    E.act = p->act;
+    if (b.make_dz) {
+      E.out[0] = base + b.dz;
+      E.out[1] = base + b.dz + b.segdz * d.es;
+      dz = E.out[0];
+    }
+    E.ldo = b.lddz;
+    E.pad = b.make_dz ? (int)b.segdz : d.F;
+    E.part = db ? (float*)(base + b.colsum) : nullptr;
+    E.blocks = b.ew_blocks;
+    E.seed = p->debug_shuffle_seed;
+    MOE_TRY(launch_dense_ew(E, nm == 2, d.bf16, st));
+    if (db) MOE_TRY(launch_block_sums(E.part, b.ew_blocks, d.F, d.F, db, !g32 && d.bf16, st));
+  }
+  DenseParams P{};
+  P.M = d.T;
+  P.N = d.D;
+  P.K = d.F;
+  P.nseg = nm;
+  P.a = dz;
+  P.lda = b.lddz;
+  P.seg = b.segdz;
+  P.b[0] = w[0];
+  P.b[1] = w[1];
+  P.ldb = b.ldw;
+  P.S = b.dx.S;
+  P.part = (float*)(base + b.part);
+  P.part_ld = b.dx_ld;
+  P.add = dx_add;
+  P.ldadd = p->ldr;
+  P.c[0] = dx;
+  P.ldc = d.D;
+  P.seed = p->debug_shuffle_seed;
+  if ((s = run_product(P, kFormDx, d, b.dx.bm, st)) != MOE_OK) return s;
+  DenseParams W{};
+  W.M = d.D;
+  W.N = d.F;
+  W.K = d.T;
+  W.nseg = nm;
+  W.a = x;
+  W.lda = b.ldx;
+  W.b[0] = dz;
+  W.ldb = b.lddz;
+  W.seg = b.segdz;
+  W.S = b.dw.S;
+  W.part = (float*)(base + b.part);
+  W.part_seg = (int)b.dw_seg;
+  W.part_ld = nm * b.dw_seg;
+  W.c[0] = dw0;
+  W.c[1] = dw1;
+  W.ldc = d.F;
+  W.c_f32 = g32;
+  W.seed = p->debug_shuffle_seed;
+  return run_product(W, kFormDw, d, b.dw.bm, st);
+}
+
+// --------------------------------------------------------------------- layer norm
+moe_status check_norm(moe_dtype dtype, int64_t rows, int64_t cols) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (rows < 0 || cols < 1 || cols > kNormMaxCols || rows >= (int64_t)1 << 40) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+bool ld_ok(int64_t rows, int64_t cols, int64_t ld) { return ld >= cols && ld < ((int64_t)1 << 40) / (rows < 1 ? 1 : rows); }
+
+}  // namespace
+}  // namespace moedet
+
+using namespace moedet;
+
+MOE_API moe_status moe_layernorm_fwd(const void* x, const void* weight, const void* bias, moe_dtype dtype,
+                                     int64_t rows, int64_t cols, int64_t ldx, float eps, void* y, float* mean,
+                                     float* rstd, uint64_t debug_shuffle_seed, void* stream) {
+  const moe_status s = check_norm(dtype, rows, cols);
+  if (s != MOE_OK) return s;
+  if (!ld_ok(rows, cols, ldx) || !(eps >= 0.f && eps < __builtin_inff())) return MOE_ERR_SHAPE;
+  if ((mean == nullptr) != (rstd == nullptr)) return MOE_ERR_NULL;
+  if (rows == 0) return MOE_OK;
+  if (!x || !y) return MOE_ERR_NULL;
+  const uintptr_t em = dtype == MOE_BF16 ? 1 : 3;
+  if (((uintptr_t)x | (uintptr_t)weight | (uintptr_t)bias | (uintptr_t)y) & em) return MOE_ERR_SHAPE;
+  if (((uintptr_t)mean | (uintptr_t)rstd) & 3) return MOE_ERR_SHAPE;
+  NormParams P{};
+  P.x = x;
+  P.weight = weight;
+  P.bias = bias;
+  P.rows = rows;
+  P.ldx = ldx;
+  P.cols = (int)cols;
+  P.eps = eps;
+  P.y = y;
+  P.mean = mean;
+  P.rstd = rstd;
+  P.seed = debug_shuffle_seed;
+  return hip_status(launch_norm_fwd(P, dtype == MOE_BF16, (hipStream_t)stream));
+}
+
+MOE_API moe_status moe_layernorm_workspace_size(int64_t rows, int64_t cols, size_t* bwd_bytes) {
+  const moe_status s = check_norm(MOE_F32, rows, cols);
+  if (s != MOE_OK) return s;
+  if (!bwd_bytes) return MOE_ERR_NULL;
+  // float32 rows may take more blocks than bf16 rows
+  *bwd_bytes = rows == 0 ? 0 : align_up((size_t)norm_bwd_blocks(rows, cols, false) * 2 * cols * 4);
+  return MOE_OK;
+}
+
+MOE_API moe_status moe_layernorm_bwd(const void* dy, const void* x, const void* weight, const float* mean,
+                                     const float* rstd, const void* dx_add, moe_dtype dtype, int64_t rows,
+                                     int64_t cols, int64_t lddy, int64_t ldx, int64_t ldadd, void* dx,
+                                     float* dweight, float* dbias, void* ws, size_t ws_bytes,
+                                     uint64_t debug_shuffle_seed, void* stream) {
+  moe_status s = check_norm(dtype, rows, cols);
+  if (s != MOE_OK) return s;
+  if (!ld_ok(rows, cols, lddy) || !ld_ok(rows, cols, ldx) || (dx_add && !ld_ok(rows, cols, ldadd))) return MOE_ERR_SHAPE;
+  if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return MOE_ERR_NULL;
+  const uintptr_t em = dtype == MOE_BF16 ? 1 : 3;
+  if (((uintptr_t)dy | (uintptr_t)x | (uintptr_t)weight | (uintptr_t)dx_add | (uintptr_t)dx) & em) return MOE_ERR_SHAPE;
+  if (((uintptr_t)mean | (uintptr_t)rstd | (uintptr_t)dweight | (uintptr_t)dbias) & 3) return MOE_ERR_SHAPE;
+  hipStream_t st = (hipStream_t)stream;
+  if (rows == 0) {
+    if (dweight) MOE_TRY(launch_dense_zero(dweight, 2 * cols, st));
+    if (dbias) MOE_TRY(launch_dense_zero(dbias, 2 * cols, st));
+    return MOE_OK;
+  }
+  const bool bf16 = dtype == MOE_BF16;
+  const int blocks = norm_bwd_blocks(rows, cols, bf16);
+  const bool sums = dweight || dbias;
+  if (sums && (s = check_ws(ws, ws_bytes, (size_t)blocks * 2 * cols * 4)) != MOE_OK) return s;
+  NormParams P{};
+  P.x = x;
+  P.weight = weight;
+  P.dy = dy;
+  P.add = dx_add;
+  P.rows = rows;
+  P.ldx = ldx;
+  P.lddy = lddy;
+  P.ldadd = ldadd;
+  P.cols = (int)cols;
+  P.y = dx;
+  P.mean = const_cast<float*>(mean);
+  P.rstd = const_cast<float*>(rstd);
+  P.part = sums ? (float*)ws : nullptr;
+  P.blocks = blocks;
+  P.seed = debug_shuffle_seed;
+  MOE_TRY(launch_norm_bwd(P, bf16, st));
+  if (dweight) MOE_TRY(launch_block_sums(P.part, blocks, 2 * cols, (int)cols, dweight, false, st));
+  if (dbias) MOE_TRY(launch_block_sums(P.part + cols, blocks, 2 * cols, (int)cols, dbias, false, st));
+  return MOE_OK;
+}
+
+// ------------------------------------------------------------ linear and gated
+MOE_API moe_status moe_linear_workspace_size(const moe_dense* p, size_t* fwd_bytes, size_t* bwd_bytes) {
+  return workspace_size(p, 1, fwd_bytes, bwd_bytes);
+}
+
+MOE_API moe_status moe_glu_workspace_size(const moe_dense* p, size_t* fwd_bytes, size_t* bwd_bytes) {
+  return workspace_size(p, 2, fwd_bytes, bwd_bytes);
+}
+
+MOE_API moe_status moe_linear_fwd(const moe_dense* p, const void* x, const void* w, const void* bias,
+                                  const void* residual, void* y, void* z, void* ws, size_t ws_bytes, void* stream) {
+  return forward(p, 1, x, w, w, bias, residual, y, z, nullptr, ws, ws_bytes, (hipStream_t)stream);
+}
+
+MOE_API moe_status moe_linear_bwd(const moe_dense* p, const void* dy, const void* x, const void* w, const void* z,
+                                  const void* dx_add, void* dx, void* dw, void* db, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  return backward(p, 1, dy, x, w, w, z, z, dx_add, dx, dw, dw, db, ws, ws_bytes, (hipStream_t)stream);
+}
+
+MOE_API moe_status moe_glu_fwd(const moe_dense* p, const void* x, const void* wg, const void* wu, void* a, void* g,
+                               void* u, void* ws, size_t ws_bytes, void* stream) {
+  return forward(p, 2, x, wg, wu, nullptr, nullptr, a, g, u, ws, ws_bytes, (hipStream_t)stream);
+}
+
+MOE_API moe_status moe_glu_bwd(const moe_dense* p, const void* da, const void* x, const void* wg, const void* wu,
+                               const void* g, const void* u, const void* dx_add, void* dx, void* dwg, void* dwu,
+                               void* ws, size_t ws_bytes, void* stream) {
+  return backward(p, 2, da, x, wg, wu, g, u, dx_add, dx, dwg, dwu, nullptr, ws, ws_bytes, (hipStream_t)stream);
+}

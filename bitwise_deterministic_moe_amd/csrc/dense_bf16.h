@@ -1,0 +1,188 @@
+// bf16 main loop of the dense matrix operators: the ring of gemm_bf16.h
+// (32-row K slices copied by DMA into four LDS slots, the loads of later
+// slices spread between the MFMAs) with a tile of 256 or 128 rows, a B tile
+// that may come from two matrices, K tails and K segments.
+//
+// Tile (2 WTM) x 256, K slice 32, 4 waves in a 2x2 grid, each wave WTM x 128 as blocks
+// of v_mfma_f32_32x32x16_bf16.
+//
+// LDS layouts besides KC and MNC of gemm_bf16.h:
+//  MNC tile of 128 columns: [32 k][128], rows of 256 bytes; chunk c (8
+//      elements) of row k sits at c ^ 4*(k&3): the four k rows that a transpose read
+//      takes then lie in four different 64-byte quarters of the row, and rows
+//      k+8 follow a cycle later.
+//  GLU the B tile of the gated product: a 128-column tile of wg, then one of
+//      wu.  The wave wn holds columns 64 wn .. 64 wn + 63 of both, so a
+//      lane ends with g and u of the same element.
+#pragma once
+
+#include "gemm_bf16.h"
+
+namespace moedet {
+namespace dn {
+
+using bf::kOOB;
+using bf::KC;
+using bf::MNC;
+constexpr int GLU = 2;
+constexpr int BK = bf::BK, BN = 256, NS = 4, BOPER = BN * BK;
+
+template <int WTM>
+constexpr int kAOper = 2 * WTM * BK;             // elements of an A slot
+template <int WTM>
+constexpr int kSlot = kAOper<WTM> + BOPER;       // elements of a ring slot
+template <int WTM>
+constexpr int kRingBytes = NS * kSlot<WTM> * 2;
+template <int WTM>
+constexpr int kALoads = WTM / 32;                // 16-byte loads per thread of an A slice
+
+DEV int mnc128_off(int k, int mn) { return k * 128 + (((mn >> 3) ^ ((k & 3) << 2)) << 3) + (mn & 7); }
+
+template <int W>
+DEV bf16x8_t frag_mnc_w(const uint16_t* s, int col_base, int kk, int lane) {
+  const int g = lane >> 4, i = lane & 15;
+  const int k = kk * 16 + 8 * (g >> 1) + (i >> 2);
+  const int mn = col_base + 16 * (g & 1) + 4 * (i & 3);
+  const int o0 = W == 256 ? bf::mnc_off(k, mn) : mnc128_off(k, mn);
+  const int o1 = W == 256 ? bf::mnc_off(k + 4, mn) : mnc128_off(k + 4, mn);
+  bf::v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS bf::v4i16*)(s + o0));
+  bf::v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS bf::v4i16*)(s + o1));
+  const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
+  return __builtin_bit_cast(bf16x8_t, u32x4_t{l2[0], l2[1], h2[0], h2[1]});
+}
+
+// A block mb of the wave row wm
+template <int AL, int WTM>
+DEV bf16x8_t frag_a(const uint16_t* s, int wm, int mb, int kk, int lane) {
+  const int r = wm * WTM + mb * 32;
+  if constexpr (AL == KC)
+    return bf::frag_kc(s, r + (lane & 31), kk, lane);
+  else
+    return frag_mnc_w<2 * WTM>(s, r, kk, lane);
+}
+// B block nb of the wave column wn
+template <int BL>
+DEV bf16x8_t frag_b(const uint16_t* s, int wn, int nb, int kk, int lane) {
+  if constexpr (BL == KC)
+    return bf::frag_kc(s, wn * 128 + nb * 32 + (lane & 31), kk, lane);
+  else if constexpr (BL == MNC)
+    return frag_mnc_w<256>(s, wn * 128 + nb * 32, kk, lane);
+  else
+    return frag_mnc_w<128>(s + (nb >> 1) * (128 * BK), wn * 64 + (nb & 1) * 32, kk, lane);
+}
+
+// ------------------------------------------------------------------ loaders
+// K-contiguous operand of ROWS tile rows (rows of `cols` readable elements):
+// wave-load j fills LDS rows 16 j .. 16 j + 15.
+template <int NL>
+struct KcOp {
+  bf::i32x4_t rs;
+  uint32_t voff[NL];
+  DEV void init(const void* base, int64_t extent, int wave, int lane, int valid, int64_t ld) {
+    rs = bf::make_rsrc(base, (uint32_t)extent);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int r = 16 * (wave * NL + i) + (lane >> 2);
+      const int c = (lane & 3) ^ bf::kc_swz(r);
+      voff[i] = r < valid ? (uint32_t)(r * ld * 2) + (uint32_t)c * 16u : kOOB;
+    }
+  }
+  // 16-byte chunk of a slice that this lane loads (the same in every load)
+  DEV static int chunk(int lane) { return (lane & 3) ^ ((lane >> 4) & 3); }
+  DEV void issue(uint32_t lds, int wave, int i, bool ok, uint32_t soff) const {
+    bf::dma16(rs, lds + (uint32_t)(wave * NL + i) * 1024u, ok ? voff[i] : kOOB, soff);
+  }
+};
+
+// M/N-contiguous operand of W columns: wave-load j fills 1 KiB of LDS rows.
+// Rows past the operand lie past its extent and read zeros.
+template <int W, int NL>
+struct MncOp {
+  bf::i32x4_t rs;
+  uint32_t voff[NL];   // row offset in slice 0 plus column offset, or kOOB for columns past `valid`
+  DEV void init(const void* base, int64_t extent, int wave, int lane, int valid, int64_t ld) {
+    rs = bf::make_rsrc(base, (uint32_t)extent);
+    constexpr int LPR = W / 8;          // lanes per k row
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int k = (64 / LPR) * (wave * NL + i) + lane / LPR;
+      const int c = (lane & (LPR - 1)) ^ (W == 256 ? bf::mnc_swz(k) : (k & 3) << 2);
+      voff[i] = 8 * c < valid ? (uint32_t)(k * ld * 2) + (uint32_t)c * 16u : kOOB;
+    }
+  }
+  DEV void issue(uint32_t lds, int wave, int i, uint32_t slice_off) const {
+    bf::dma16(rs, lds + (uint32_t)(wave * NL + i) * 1024u, voff[i] + slice_off, 0u);
+  }
+};
+
+// ----------------------------------------------------------------- main loop
+template <int N>
+DEV void wait_vm_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <int AL, int BL, int WTM>
+DEV void load_group(bf::Frags& f, const uint16_t* slot, int kk, int wm, int wn, int lane, int g) {
+  if (bf::kGrpA[g] >= 0) {
+    if (bf::kGrpA[g] < WTM / 32) f.a[bf::kGrpA[g]] = frag_a<AL, WTM>(slot, wm, bf::kGrpA[g], kk, lane);
+  } else {
+    f.b[bf::kGrpB[g]] = frag_b<BL>(slot + kAOper<WTM>, wn, bf::kGrpB[g], kk, lane);
+  }
+}
+
+// nsteps >= 1 slices.  issue(s, slot, i): load i of slice s into the slot at
+// that LDS address, i < kALoads of A, then 4 of B; slices at or past nsteps
+// must read zeros (their loads keep the count of outstanding loads the same
+// in every step).  The order of waits and reads is bf::mainloop's: in step s the
+// B loads of slice s + 2 go out while k-half 0 is multiplied; then slice s + 1
+// has landed, and the A loads of slice s + 3 go out while k-half 1 is.
+template <int AL, int BL, int WTM, class Issue>
+DEV void mainloop(const uint16_t* lds, uint32_t ring, int nsteps, Issue issue, f32x16_t (&acc)[4][4], int wm, int wn,
+                  int lane) {
+  constexpr int LA = kALoads<WTM>, L = LA + 4, NMB = WTM / 32, SLOT = kSlot<WTM>;
+  auto slot = [&](int s) { return lds + (s % NS) * SLOT; };
+  auto addr = [&](int s) { return ring + (uint32_t)(s % NS) * (SLOT * 2); };
+#pragma unroll
+  for (int s = 0; s < NS - 2; ++s)
+#pragma unroll
+    for (int i = 0; i < L; ++i) issue(s, addr(s), i);
+#pragma unroll
+  for (int i = 0; i < LA; ++i) issue(NS - 2, addr(NS - 2), i);
+  wait_vm_barrier<L*(NS - 3) + LA>();  // slice 0 landed
+  bf::Frags f0, f1;
+#pragma unroll
+  for (int g = 0; g < 8; ++g) load_group<AL, BL, WTM>(f0, lds, 0, wm, wn, lane, g);
+  auto phase1 = [&](int s, auto first) __attribute__((always_inline)) {
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      if (g & 1) issue(s + NS - 2, addr(s + NS - 2), LA + (g >> 1));
+      load_group<AL, BL, WTM>(f1, slot(s), 1, wm, wn, lane, g);
+      __builtin_amdgcn_sched_barrier(0);
+      bf::mma2<NMB, decltype(first)::value>(f0, acc, g);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto phase2 = [&](int s) __attribute__((always_inline)) {
+    wait_vm_barrier<L*(NS - 3)>();  // slice s+1 landed; slot of slice s-1 free
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      if ((g & 1) && (g >> 1) < LA) issue(s + NS - 1, addr(s + NS - 1), g >> 1);
+      load_group<AL, BL, WTM>(f0, slot(s + 1), 0, wm, wn, lane, g);
+      __builtin_amdgcn_sched_barrier(0);
+      bf::mma2<NMB>(f1, acc, g);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // past the last slice the next slot holds zeros, read and never multiplied
+  phase1(0, bf::BoolC<true>{});
+  phase2(0);
+#pragma unroll 1
+  for (int s = 1; s < nsteps; ++s) {
+    phase1(s, bf::BoolC<false>{});
+    phase2(s);
+  }
+  bf::block_barrier();
+}
+
+}  // namespace dn
+}  // namespace moedet

@@ -630,6 +630,170 @@ moe_status moe_mx_wgrad(const moe_problem* p, const moe_routing* routing, const 
  * (sink), MOE_ERR_HIP (launch failure).  Nothing is enqueued on error. */
 moe_status moe_mfma_rate(int64_t blocks, int64_t iters, float value, float* sink, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Dense operators around the expert layer: the layer norm in front of the
+ * router and the experts, the gated feed-forward product of a shared expert
+ * beside the routed ones, and the linear map (bias, activation, residual)
+ * that takes it into the residual stream.  The pages describe none of them;
+ * the definitions below are this library's, under the pages' general rule
+ * (every reduction in an order fixed by indices and shapes): there is one
+ * mode, without atomics, and the output bits are a function of the input
+ * bits, the call's arguments, the library build and the GPU model.
+ *
+ * Conventions beyond those at the top of this file:
+ *   - Matrices are row-major with unit stride inside a row; an `ld` is the
+ *     distance of two rows in elements, at least the row's length.  Gradients
+ *     (dx, dw, dwg, dwu) and packed outputs without an ld are contiguous.
+ *   - Any sizes >= 1 (rows >= 0).  bfloat16 matrices whose row length and
+ *     ld are multiples of 8 are read in place; others are copied into the
+ *     workspace first.  Matrix base addresses are multiples of 16 bytes,
+ *     except in the layer norm, which takes any element address.
+ *   - Sums are float32, every output is rounded once.  The backward of the
+ *     matrix operators rounds the pre-activation gradients (dz, dg, du) to
+ *     the storage type before their products, as the expert layer does with
+ *     dh.
+ *   - Outputs must not overlap inputs, except that y may be the residual and dx
+ *     may be dx_add, with the same row distance. */
+
+/* Activations.  ReLU2 is the expert layer's relu(z)^2; GELU is z Phi(z)
+ * with the normal distribution function Phi (the erf form).  At z = 0 the
+ * derivative of ReLU is 0. */
+typedef enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_RELU2 = 2,
+  MOE_ACT_SILU = 3,
+  MOE_ACT_GELU = 4
+} moe_act;
+
+/* Layer norm of each row of x [rows, cols]:
+ *   mean = sum(x) / cols,  rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps),
+ *   y = (x - mean) rstd weight + bias
+ *   x       DEVICE [rows, cols], row distance ldx, MOE_F32 or MOE_BF16
+ *   weight  DEVICE [cols] of dtype, or NULL for 1;  bias likewise, NULL for 0
+ *   eps     >= 0, finite
+ *   y       DEVICE [rows, cols] of dtype, contiguous, output
+ *   mean, rstd  DEVICE float[rows] outputs (the backward reads them), or both NULL
+ *   debug_shuffle_seed  0, or a test-only seed that shuffles the launch order
+ * cols is at most 16384 and rows * ldx below 2^40.  Errors: MOE_ERR_DTYPE,
+ * MOE_ERR_SHAPE, MOE_ERR_NULL before anything is enqueued; MOE_ERR_HIP for a
+ * launch failure. */
+moe_status moe_layernorm_fwd(const void* x, const void* weight, const void* bias, moe_dtype dtype, int64_t rows,
+                             int64_t cols, int64_t ldx, float eps, void* y, float* mean, float* rstd,
+                             uint64_t debug_shuffle_seed, void* stream);
+
+/* Workspace bytes of moe_layernorm_bwd.  Errors: MOE_ERR_SHAPE, MOE_ERR_NULL. */
+moe_status moe_layernorm_workspace_size(int64_t rows, int64_t cols, size_t* bwd_bytes);
+
+/* Layer norm backward.  With h = (x - mean) rstd and dh = dy weight:
+ *   dx      = rstd (dh - sum(dh) / cols - h sum(dh h) / cols) (+ dx_add)
+ *   dweight = sum over rows of dy h,   dbias = sum over rows of dy
+ * The sums over rows run in row blocks whose bounds depend on rows and cols only;
+ * the block sums are added in block order.
+ *   dy, x   DEVICE [rows, cols] of dtype, row distances lddy, ldx
+ *   weight  as given to the forward (NULL for 1)
+ *   mean, rstd  DEVICE float[rows], as written by the forward
+ *   dx_add  DEVICE [rows, cols] of dtype, row distance ldadd, or NULL: the
+ *           gradient of another branch, added before the rounding
+ *   dx      DEVICE [rows, cols] of dtype, contiguous, output
+ *   dweight, dbias  DEVICE float[cols] outputs (zeros when rows = 0); either
+ *           may be NULL
+ *   ws      moe_layernorm_workspace_size bytes, 256-byte aligned
+ * Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_WORKSPACE before
+ * anything is enqueued; MOE_ERR_HIP for a launch failure. */
+moe_status moe_layernorm_bwd(const void* dy, const void* x, const void* weight, const float* mean, const float* rstd,
+                             const void* dx_add, moe_dtype dtype, int64_t rows, int64_t cols, int64_t lddy,
+                             int64_t ldx, int64_t ldadd, void* dx, float* dweight, float* dbias, void* ws,
+                             size_t ws_bytes, uint64_t debug_shuffle_seed, void* stream);
+
+/* One call of a matrix operator.
+ *   rows     T >= 0 (below 2^31)
+ *   d_in     D, width of x;   d_out  F, width of the output
+ *   dtype    MOE_F32 or MOE_BF16: storage of the matrices and of the bias
+ *   grad_dtype  type of the weight and bias gradients: MOE_F32, or dtype
+ *   z_dtype  type of the saved pre-activations z (g and u): MOE_F32, or dtype.
+ *            In bf16 layers float32 keeps one rounding out of the gradients
+ *            for twice the bytes.
+ *   act      moe_act
+ *   ldx      row distance of x
+ *   ldw      row distance of the weights [D, F]
+ *   ldy      row distance of the output y (a); in the backward, of dy (da)
+ *   ldz      row distance of the saved pre-activations z (g and u)
+ *   ldr      row distance of the residual; in the backward, of dx_add
+ *            (unread without one)
+ *   debug_shuffle_seed  0, or a test-only seed that shuffles the launch order
+ * Each weight matrix (D * ldw elements) is below 2 GiB, and every ld below
+ * 2^20; the other matrices have no limit of their own. */
+typedef struct moe_dense {
+  int64_t rows;
+  int32_t d_in;
+  int32_t d_out;
+  int32_t dtype;
+  int32_t grad_dtype;
+  int32_t z_dtype;
+  int32_t act;
+  int64_t ldx;
+  int64_t ldw;
+  int64_t ldy;
+  int64_t ldz;
+  int64_t ldr;
+  uint64_t debug_shuffle_seed;
+} moe_dense;
+
+/* Workspace bytes of the linear calls (functions of the description alone).
+ * Either output pointer may be NULL.  Errors: those of the description. */
+moe_status moe_linear_workspace_size(const moe_dense* p, size_t* fwd_bytes, size_t* bwd_bytes);
+/* The same for the gated product. */
+moe_status moe_glu_workspace_size(const moe_dense* p, size_t* fwd_bytes, size_t* bwd_bytes);
+
+/* Linear map with its epilogue: z = x w + bias, y = act(z) + residual.
+ *   x [T, D], w [D, F]; bias [F] or NULL; residual [T, F] or NULL
+ *   y        DEVICE [T, F] output
+ *   z        DEVICE [T, F] of z_dtype, output (the backward reads it), or NULL
+ *   ws       moe_linear_workspace_size fwd_bytes, 256-byte aligned
+ * Few rows (at most 64 in bf16, 16 in float32) stream the weights once.
+ * Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_MODE (act), MOE_ERR_NULL,
+ * MOE_ERR_WORKSPACE before anything is enqueued; MOE_ERR_HIP for a launch
+ * failure. */
+moe_status moe_linear_fwd(const moe_dense* p, const void* x, const void* w, const void* bias, const void* residual,
+                          void* y, void* z, void* ws, size_t ws_bytes, void* stream);
+
+/* Linear backward: dz = dy act'(z), dx = dz w^T (+ dx_add), dw = x^T dz,
+ * db = sum over rows of dz (float32 dz, before its rounding).  The
+ * residual's gradient is dy itself.
+ *   dy [T, F]; x, w as in the forward; z as saved (unread with MOE_ACT_NONE)
+ *   dx_add   [T, D] of dtype, row distance ldr, or NULL
+ *   dx       DEVICE [T, D] of dtype, contiguous, output
+ *   dw       DEVICE [D, F] of grad_dtype, contiguous, output
+ *   db       DEVICE [F] of grad_dtype, output, or NULL
+ *   ws       moe_linear_workspace_size bwd_bytes, 256-byte aligned
+ * dw and db are zeros when rows = 0.  Errors: as moe_linear_fwd. */
+moe_status moe_linear_bwd(const moe_dense* p, const void* dy, const void* x, const void* w, const void* z,
+                          const void* dx_add, void* dx, void* dw, void* db, void* ws, size_t ws_bytes, void* stream);
+
+/* Gated feed-forward product, both projections, the activation and the
+ * product in one kernel: g = x wg, u = x wu, a = act(g) u (of the unrounded
+ * g and u).
+ *   x [T, D]; wg, wu [D, F], both with row distance ldw (the halves of one
+ *   [D, 2F] matrix, or two matrices)
+ *   a        DEVICE [T, F] output
+ *   g, u     DEVICE [T, F] of z_dtype, row distance ldz, outputs (the backward
+ *            reads them), or both NULL
+ * Workspace (moe_glu_workspace_size) and errors: as moe_linear_fwd. */
+moe_status moe_glu_fwd(const moe_dense* p, const void* x, const void* wg, const void* wu, void* a, void* g, void* u,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/* Gated product backward: dg = da u act'(g), du = da act(g),
+ * dx = dg wg^T + du wu^T (+ dx_add), dwg = x^T dg, dwu = x^T du.
+ *   da [T, F] (row distance ldy); x, wg, wu, g, u as in the forward
+ *   dx_add   [T, D] of dtype, row distance ldr, or NULL
+ *   dx       DEVICE [T, D] of dtype, contiguous, output
+ *   dwg, dwu DEVICE [D, F] of grad_dtype, contiguous, outputs (zeros when rows = 0)
+ * Workspace (moe_glu_workspace_size bwd_bytes) and errors: as moe_linear_bwd. */
+moe_status moe_glu_bwd(const moe_dense* p, const void* da, const void* x, const void* wg, const void* wu,
+                       const void* g, const void* u, const void* dx_add, void* dx, void* dwg, void* dwu, void* ws,
+                       size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,3 +19,6 @@ from .mx import (  # noqa: F401,E402
     MXW_PAD, mx_pad_offsets, mx_quantize_expert_rows, act_p_f32, mx_wgrad,
 )
 from .nvfp4 import e2m1_decode, e2m1_encode, nvfp4_quantize, nvfp4_dequantize  # noqa: F401,E402
+from .dense import (  # noqa: F401,E402
+    act, layernorm_forward, layernorm_backward, linear_forward, linear_backward, glu_forward, glu_backward,
+)
