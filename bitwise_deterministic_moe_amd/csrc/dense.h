@@ -15,6 +15,7 @@ enum { kActNone = 0, kActRelu = 1, kActRelu2 = 2, kActSilu = 3, kActGelu = 4 };
 // ------------------------------------------------------- vectors of any address
 // 16-byte vectors that may start at any element: gfx950 loads and stores
 // them in one instruction at any byte address.
+typedef uint32_t u32_any_t __attribute__((aligned(2)));
 typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
@@ -104,9 +105,10 @@ struct NormParams {
 int norm_bwd_blocks(int64_t rows, int64_t cols, bool bf16);
 hipError_t launch_norm_fwd(const NormParams& P, bool bf16, hipStream_t st);
 hipError_t launch_norm_bwd(const NormParams& P, bool bf16, hipStream_t st);
-// out[c] = sum over b ascending, in fixed phases, of part[b * stride + c], c < cols.
-hipError_t launch_block_sums(const float* part, int blocks, int64_t stride, int cols, void* out, bool out_bf16,
-                             hipStream_t st);
+// out[c] = sum over b ascending, in fixed phases, of part[b * stride + c], c <
+// cols; out2 the same of the next cols columns.  Either may be null.
+hipError_t launch_block_sums(const float* part, int blocks, int64_t stride, int cols, void* out, void* out2,
+                             bool out_bf16, hipStream_t st);
 
 // ------------------------------------------------------------ matrix operators
 // One matrix product of a dense operator,
@@ -157,7 +159,6 @@ hipError_t launch_dense_gemm(const DenseParams& P, int form, bool bf16, int bm, 
 hipError_t launch_dense_few(const DenseParams& P, int form, bool bf16, hipStream_t st);
 hipError_t launch_dense_finish(const DenseParams& P, int form, bool bf16, hipStream_t st);
 int dense_tile_n(int form, bool bf16);   // columns of one matrix a tile covers
-int dense_few_n(int form, bool bf16);    // the same for the few-row kernels
 
 // bf16 matrix [rows][cols] (row distance ld) into [rows][ldo], zeros past cols
 hipError_t launch_dense_pack(const void* in, int64_t rows, int cols, int64_t ld, void* out, int64_t ldo,

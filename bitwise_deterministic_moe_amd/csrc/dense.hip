@@ -91,37 +91,58 @@ DEV void dense_store_tile(const DenseParams& P, const DenseTile& t, float* stage
       }
     }
     dense_lds_barrier();
+    const int64_t end = t.m0 + rows;
     if constexpr (FORM == kFormGlu) {
+      // two rows per wave and step: lanes 0..31 one, lanes 32..63 the next
       const int c = (lane & 31) * 4, col = t.n0 + c;
-#pragma unroll 4
-      for (int st = 0; st < 8; ++st) {
+#pragma unroll
+      for (int st = 0; st < 8; st += 4) {
+        float g[16], u[16];
         const int m = 8 * st + 2 * wave + half;
-        const f32x4_t sg = *(const f32x4_t*)(stage + m * kDenseStageRow + c);
-        const f32x4_t su = *(const f32x4_t*)(stage + m * kDenseStageRow + 128 + c);
-        float g[4] = {sg[0], sg[1], sg[2], sg[3]}, u[4] = {su[0], su[1], su[2], su[3]};
-        if (64 * p + m < rows && col < P.N) {
-          const int64_t row = t.m0 + 64 * p + m;
-          if (P.S > 1) {
-            part4(P, t.chunk, 0, row, col, g);
-            part4(P, t.chunk, 1, row, col, u);
-          } else {
-            emit4_glu<uint16_t>(P, row, col, g, u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4_t sg = *(const f32x4_t*)(stage + (m + 8 * i) * kDenseStageRow + c);
+          const f32x4_t su = *(const f32x4_t*)(stage + (m + 8 * i) * kDenseStageRow + 128 + c);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            g[4 * i + q] = sg[q];
+            u[4 * i + q] = su[q];
           }
+        }
+        if (col >= P.N) continue;
+        const int64_t row = t.m0 + 64 * p + m;
+        if (P.S > 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (row + 8 * i < end) {
+              part4(P, t.chunk, 0, row + 8 * i, col, {g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]});
+              part4(P, t.chunk, 1, row + 8 * i, col, {u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]});
+            }
+        } else {
+          emit_rows_glu<uint16_t, 4>(P, row, 8, end, col, g, u);
         }
       }
     } else {
       const int c = lane * 4, col = t.n0 + c;
-#pragma unroll 4
-      for (int st = 0; st < 16; ++st) {
+#pragma unroll
+      for (int st = 0; st < 16; st += 4) {
+        float v[16];
         const int m = 4 * st + wave;
-        const f32x4_t sv = *(const f32x4_t*)(stage + m * kDenseStageRow + c);
-        float v[4] = {sv[0], sv[1], sv[2], sv[3]};
-        if (64 * p + m < rows && col < P.N) {
-          const int64_t row = t.m0 + 64 * p + m;
-          if (P.S > 1)
-            part4(P, t.chunk, t.seg, row, col, v);
-          else
-            emit4<uint16_t, FORM>(P, t.seg, row, col, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4_t sv = *(const f32x4_t*)(stage + (m + 4 * i) * kDenseStageRow + c);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[4 * i + q] = sv[q];
+        }
+        if (col >= P.N) continue;
+        const int64_t row = t.m0 + 64 * p + m;
+        if (P.S > 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (row + 4 * i < end)
+              part4(P, t.chunk, t.seg, row + 4 * i, col, {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]});
+        } else {
+          emit_rows<uint16_t, FORM, 4>(P, t.seg, row, 4, end, col, v);
         }
       }
     }
@@ -386,64 +407,51 @@ __global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
 }
 
 // ------------------------------------------------------------------ few rows
-// Weights [K][N] streamed once past at most 16 MT rows of x.  A workgroup
-// owns a column tile and a chunk of K; its 4 waves take 32-row K steps in turn
-// and add their sums in wave order through LDS.  In a step, lane (i = l % 16,
-// g = l / 16) loads the weights' rows 8 g .. 8 g + 7 at its own consecutive columns,
-// and 8 consecutive k of each x row i: both go from the loads to the matrix
-// instruction's registers directly, with no LDS and no barrier, and the loads
-// of the next step are in flight while a step is multiplied.
+// Weights [K][N] streamed once past at most 16 MT rows of x, mostly in one
+// launch and without a workspace (S = 1).  A workgroup owns 64 bytes of every weight row (32 bf16
+// or 16 float32 columns) of its chunk; its NW waves take 32-row K steps in turn and add their
+// sums in wave order through LDS.  In a step, lane (i = l % 16, g = l / 16) loads
+// its 4 bytes of the weights' rows 8 g .. 8 g + 7 and 8 consecutive k of
+// each x row i: both go from the loads to the matrix instruction's registers
+// directly, with no LDS and no barrier, and DEPTH steps are in flight.
 //  bf16     v_mfma_f32_16x16x32_bf16, one per column: a column's 8 k are
 //           picked out of the 8 loaded rows with one byte permute per pair.
 //  float32  v_mfma_f32_16x16x4f32, 8 per column.
+// Rows of x past the last repeat it (their sums are not used).
 template <typename T, int FORM, int MT>
 struct FewCfg {
-  static constexpr int NM = FORM == kFormGlu ? 2 : 1;                           // matrices
-  static constexpr int CPL = sizeof(T) == 2 ? (FORM == kFormGlu ? 4 : 8) : 4;    // columns per lane and matrix
-  static constexpr int COLS = 16 * CPL;                                         // tile columns per matrix
-};
-
-template <typename T, int CPL>
-struct FewRow {   // CPL consecutive weights of a row
-  uint32_t w[CPL * (int)sizeof(T) / 4];
-  DEV void load(const T* p, int n) {
-    if constexpr (sizeof(T) == 2 && CPL == 4) {
-      if (n >= 4) {
-        const u32x2_t r = *(const u32x2_any_t*)p;
-        w[0] = r[0];
-        w[1] = r[1];
-      } else {
-        w[0] = w[1] = 0u;
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-          if (i < n) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-      }
-    } else {
-      const u32x4_t r = __builtin_bit_cast(u32x4_t, Vec<T>::load(p, n));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = r[i];
-    }
-  }
-  DEV void zero() {
-#pragma unroll
-    for (int i = 0; i < (int)(CPL * sizeof(T) / 4); ++i) w[i] = 0u;
-  }
+  static constexpr int NM = FORM == kFormGlu ? 2 : 1;         // matrices
+  static constexpr int CPL = 4 / (int)sizeof(T);              // columns per lane and matrix
+  static constexpr int COLS = 16 * CPL;                       // tile columns per matrix
+  static constexpr int NW = MT == 1 ? 16 : 8;                 // waves
+  static constexpr int DEPTH = sizeof(T) == 2 ? 4 : 3;
 };
 
 template <typename T, int FORM, int MT>
-__global__ __launch_bounds__(256) void dense_few_kernel(DenseParams P) {
+__global__ __launch_bounds__((FewCfg<T, FORM, MT>::NW * 64)) void dense_few_kernel(DenseParams P) {
   using Cfg = FewCfg<T, FORM, MT>;
-  constexpr int NM = Cfg::NM, CPL = Cfg::CPL, COLS = Cfg::COLS, RS = NM * COLS + 4;
+  constexpr int NM = Cfg::NM, CPL = Cfg::CPL, COLS = Cfg::COLS, NW = Cfg::NW, DEPTH = Cfg::DEPTH, RS = NM * COLS + 4;
   constexpr int XW = sizeof(T) == 2 ? 1 : 2;   // 16-byte loads of 8 consecutive k
-  __shared__ __attribute__((aligned(16))) float s_acc[4 * 16 * MT * RS];
-  const int nT = (P.N + COLS - 1) / COLS;
-  const int64_t L = map_unit(blockIdx.x, (int64_t)nT * P.S, P.seed);
-  if (L < 0) return;
-  const int chunk = (int)(L / nT), n0 = (int)(L % nT) * COLS;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i16 = lane & 15, g = lane >> 4;
-  const int steps = (int)((P.K + 31) / 32);
-  const int s0 = (int)((int64_t)chunk * steps / P.S), s1 = (int)((int64_t)(chunk + 1) * steps / P.S);
+  __shared__ __attribute__((aligned(16))) float s_acc[NW * 16 * MT * RS];
+  // Chunk, then pairs of tiles dealt to the 8 XCDs in turn: the two 64-byte
+  // tiles of a 128-byte line share an XCD's L2, and an XCD's tiles lie 1 KiB apart
+  // (in one run they would use two of its L2's channels; measured against
+  // consecutive tiles: 37 rows of the 2048 x 8192 gated product 15.0 against
+  // 16.9 us, 5 rows of 8192 x 2048 unsplit 16.6 against 18.3 us).
+  const int tiles = (P.N + COLS - 1) / COLS, tgrid = (tiles + 15) / 16 * 16;
+  int b = blockIdx.x;
+  if (P.seed) {
+    shuffle_delay(P.seed, b);
+    b = (int)shuffle_unit(b, (int64_t)tgrid * P.S, P.seed);
+  }
+  const int chunk = b / tgrid, tb = b - chunk * tgrid;
+  const int tile = (tb / 16 * 8 + tb % 8) * 2 + tb / 8 % 2;
+  if (tile >= tiles) return;
+  const int n0 = tile * COLS;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i16 = lane & 15, g = lane >> 4;
   const int K = (int)P.K;
+  const int all = (K + 31) / 32;
+  const int s0 = (int)((int64_t)chunk * all / P.S), steps = (int)((int64_t)(chunk + 1) * all / P.S);
   const int col = n0 + i16 * CPL, ncol = P.N - col;
   f32x4_t acc[NM][CPL][MT];
 #pragma unroll
@@ -453,24 +461,21 @@ __global__ __launch_bounds__(256) void dense_few_kernel(DenseParams P) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[m][c][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   struct Step {
-    FewRow<T, CPL> w[NM][8];
+    uint32_t w[NM][8];
     typename Vec<T>::raw x[MT][XW];
   };
-  // rows of x past the last repeat it: their sums are not used
   const T* xrow[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const int row = 16 * t + i16;
     xrow[t] = (const T*)P.a + (int64_t)(row < P.M ? row : (int)P.M - 1) * P.lda;
   }
-  // steps below `whole` lie inside the matrix in both directions
-  const int whole = n0 + COLS <= P.N ? K / 32 : 0;
-  auto load_full = [&](Step& b, int s) __attribute__((always_inline)) {
+  auto load = [&](Step& b, int s) __attribute__((always_inline)) {
     const int k = 32 * s + 8 * g;
 #pragma unroll
     for (int m = 0; m < NM; ++m)
 #pragma unroll
-      for (int r = 0; r < 8; ++r) b.w[m][r].load((const T*)P.b[m] + (int64_t)(k + r) * P.ldb + col, CPL);
+      for (int r = 0; r < 8; ++r) b.w[m][r] = *(const u32_any_t*)((const T*)P.b[m] + (int64_t)(k + r) * P.ldb + col);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -482,20 +487,20 @@ __global__ __launch_bounds__(256) void dense_few_kernel(DenseParams P) {
     for (int m = 0; m < NM; ++m)
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        if (k + r < K && ncol > 0)
-          b.w[m][r].load((const T*)P.b[m] + (int64_t)(k + r) * P.ldb + col, ncol);
-        else
-          b.w[m][r].zero();
+        b.w[m][r] = 0u;
+        const T* p = (const T*)P.b[m] + (int64_t)(k + r) * P.ldb + col;
+        if (k + r < K && ncol >= CPL)
+          b.w[m][r] = *(const u32_any_t*)p;
+        else if (k + r < K && ncol > 0)
+          b.w[m][r] = *(const uint16_t*)p;   // the last of an odd number of bf16 columns
       }
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int h = 0; h < XW; ++h) {
         const int kk = k + h * Vec<T>::N;
-        if (kk < K)
-          b.x[t][h] = Vec<T>::load(xrow[t] + kk, K - kk);
-        else
-          b.x[t][h] = typename Vec<T>::raw{};
+        b.x[t][h] = typename Vec<T>::raw{};
+        if (kk < K) b.x[t][h] = Vec<T>::load(xrow[t] + kk, K - kk);
       }
   };
   auto mma = [&](const Step& b) __attribute__((always_inline)) {
@@ -507,8 +512,7 @@ __global__ __launch_bounds__(256) void dense_few_kernel(DenseParams P) {
           u32x4_t f;
 #pragma unroll
           for (int p = 0; p < 4; ++p)
-            f[p] = __builtin_amdgcn_perm(b.w[m][2 * p + 1].w[c >> 1], b.w[m][2 * p].w[c >> 1],
-                                         (c & 1) ? 0x07060302u : 0x05040100u);
+            f[p] = __builtin_amdgcn_perm(b.w[m][2 * p + 1], b.w[m][2 * p], c ? 0x07060302u : 0x05040100u);
 #pragma unroll
           for (int t = 0; t < MT; ++t)
             acc[m][c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b.x[t][0]),
@@ -519,28 +523,37 @@ __global__ __launch_bounds__(256) void dense_few_kernel(DenseParams P) {
 #pragma unroll
             for (int t = 0; t < MT; ++t)
               acc[m][c][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                  __builtin_bit_cast(f32x4_t, b.x[t][r >> 2])[r & 3], __uint_as_float(b.w[m][r].w[c]), acc[m][c][t], 0, 0, 0);
+                  __builtin_bit_cast(f32x4_t, b.x[t][r >> 2])[r & 3], __uint_as_float(b.w[m][r]), acc[m][c][t], 0, 0, 0);
         }
       }
   };
-  int s = s0 + wave;
-  const int e = s1 < whole ? s1 : whole;
-  {
-    Step b0, b1;
-    if (s < e) load_full(b0, s);
+  // steps below `whole` lie inside the matrix in both directions
+  const int whole = n0 + COLS <= P.N ? min(K / 32, steps) : 0, first = s0 + wave;
+  // this wave's whole steps in rounds of DEPTH.  Loads are unconditional, so
+  // that the waits can count them: past the last whole step they repeat it, and the last
+  // round loads nothing.
+  const int n = whole > first ? (whole - first + NW - 1) / NW : 0;
+  if (n > 0) {
+    Step st[DEPTH];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(st[d], first + (d < n ? d : n - 1) * NW);
+    int i = 0;
 #pragma unroll 1
-    while (s < e) {
-      if (s + 4 < e) load_full(b1, s + 4);
-      mma(b0);
-      s += 4;
-      if (s >= e) break;
-      if (s + 4 < e) load_full(b0, s + 4);
-      mma(b1);
-      s += 4;
+    for (; i + DEPTH < n; i += DEPTH) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        mma(st[d]);
+        const int j = i + DEPTH + d;
+        load(st[d], first + (j < n ? j : n - 1) * NW);
+      }
     }
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+      if (i + d < n) mma(st[d]);
   }
+  int s = first + n * NW;
 #pragma unroll 1
-  for (; s < s1; s += 4) {
+  for (; s < steps; s += NW) {
     Step b;
     load_edge(b, s);
     mma(b);
@@ -553,12 +566,11 @@ __global__ __launch_bounds__(256) void dense_few_kernel(DenseParams P) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int c = 0; c < CPL; c += 4)
-          *(f32x4_t*)(s_acc + ((wave * MT + t) * 16 + 4 * g + r) * RS + m * COLS + i16 * CPL + c) =
-              f32x4_t{acc[m][c][t][r], acc[m][c + 1][t][r], acc[m][c + 2][t][r], acc[m][c + 3][t][r]};
+        for (int c = 0; c < CPL; ++c)
+          s_acc[((wave * MT + t) * 16 + 4 * g + r) * RS + m * COLS + i16 * CPL + c] = acc[m][c][t][r];
   __syncthreads();
   constexpr int QPR = COLS / 4;   // groups of four columns per row and matrix
-  for (int o = tid; o < 16 * MT * QPR; o += 256) {
+  for (int o = tid; o < 16 * MT * QPR; o += NW * 64) {
     const int row = o / QPR, c = (o % QPR) * 4;
     if (row >= P.M || n0 + c >= P.N) continue;
     float v[NM][4];
@@ -567,7 +579,7 @@ __global__ __launch_bounds__(256) void dense_few_kernel(DenseParams P) {
       const float* p = s_acc + row * RS + m * COLS + c;
       f32x4_t a = *(const f32x4_t*)p;
 #pragma unroll
-      for (int w = 1; w < 4; ++w) {
+      for (int w = 1; w < NW; ++w) {
         const f32x4_t b = *(const f32x4_t*)(p + w * 16 * MT * RS);
 #pragma unroll
         for (int q = 0; q < 4; ++q) a[q] = a[q] + b[q];
@@ -721,7 +733,6 @@ __global__ __launch_bounds__(256) void dense_zero_kernel(uint16_t* p, int64_t n)
 
 // -------------------------------------------------------------------- launches
 int dense_tile_n(int form, bool bf16) { return (bf16 ? 256 : 128) / (form == kFormGlu ? 2 : 1); }
-int dense_few_n(int form, bool bf16) { return bf16 && form != kFormGlu ? 128 : 64; }
 
 template <int FORM>
 static void dense_gemm_launch(const DenseParams& P, bool bf16, int bm, int64_t grid, hipStream_t st) {
@@ -746,25 +757,32 @@ hipError_t launch_dense_gemm(const DenseParams& P, int form, bool bf16, int bm, 
   return hipGetLastError();
 }
 
+template <typename T, int FORM, int MT>
+static void dense_few_launch(const DenseParams& P, hipStream_t st) {
+  using Cfg = FewCfg<T, FORM, MT>;
+  const int tiles = (P.N + Cfg::COLS - 1) / Cfg::COLS;
+  dense_few_kernel<T, FORM, MT><<<(tiles + 15) / 16 * 16 * P.S, Cfg::NW * 64, 0, st>>>(P);
+}
+
 template <int FORM>
-static void dense_few_launch(const DenseParams& P, bool bf16, int64_t grid, hipStream_t st) {
+static void dense_few_form(const DenseParams& P, bool bf16, hipStream_t st) {
   if (!bf16)
-    dense_few_kernel<float, FORM, 1><<<grid, 256, 0, st>>>(P);
+    dense_few_launch<float, FORM, 1>(P, st);
   else if (P.M <= 16)
-    dense_few_kernel<uint16_t, FORM, 1><<<grid, 256, 0, st>>>(P);
+    dense_few_launch<uint16_t, FORM, 1>(P, st);
   else if (P.M <= 32)
-    dense_few_kernel<uint16_t, FORM, 2><<<grid, 256, 0, st>>>(P);
+    dense_few_launch<uint16_t, FORM, 2>(P, st);
+  else if (P.M <= 48)
+    dense_few_launch<uint16_t, FORM, 3>(P, st);
   else
-    dense_few_kernel<uint16_t, FORM, 4><<<grid, 256, 0, st>>>(P);
+    dense_few_launch<uint16_t, FORM, 4>(P, st);
 }
 
 hipError_t launch_dense_few(const DenseParams& P, int form, bool bf16, hipStream_t st) {
-  const int bn = dense_few_n(form, bf16);
-  const int64_t grid = grid_for_units((int64_t)((P.N + bn - 1) / bn) * P.S);
   if (form == kFormGlu)
-    dense_few_launch<kFormGlu>(P, bf16, grid, st);
+    dense_few_form<kFormGlu>(P, bf16, st);
   else
-    dense_few_launch<kFormLinear>(P, bf16, grid, st);
+    dense_few_form<kFormLinear>(P, bf16, st);
   return hipGetLastError();
 }
 

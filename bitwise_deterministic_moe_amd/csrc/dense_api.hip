@@ -101,18 +101,21 @@ Choice choose(const Dense& d, int form, int64_t M, int64_t N, int nseg, int64_t 
   return best;
 }
 
-// Chunks of the few-row kernels: two workgroups a CU, each wave at least one
-// 32-row step, and partials of at most half of the weights' bytes.
-int few_chunks(const Dense& d, int form) {
-  const int bn = dense_few_n(form, d.bf16);
-  const int64_t tiles = (d.F + bn - 1) / bn, steps = (d.D + 31) / 32;
-  int64_t S = (2 * kCUs + tiles - 1) / tiles;
-  const int64_t by_bytes = (int64_t)d.D * d.es / (16 * d.T);
-  if (S > by_bytes) S = by_bytes;
-  if (S > steps / 4) S = steps / 4;
-  if (S < 1) S = 1;
-  const int64_t per = (steps + S - 1) / S;
-  return (int)((steps + per - 1) / per);
+// Chunks of K of the few-row kernels.  A workgroup streams about 40 KB/us and
+// the device 4.6 TB/s; a launch of them takes 3 us beside the stream, and
+// partials with their join 4.5 us more (measured: 64 strips of 8192 x 2048
+// bf16 16.6 us unsplit; 256 in four chunks SPLIT_US us with the join).
+int few_chunks(const Dense& d) {
+  const double strip = (double)d.D * 64 * d.nm;
+  const int cols = 64 / (int)d.es;
+  const int64_t tiles = (d.F + cols - 1) / cols, steps = (d.D + 31) / 32;
+  const double all = (double)d.D * d.F * d.es * d.nm / 4.6e6;
+  int64_t S = kCUs / tiles;
+  if (S > steps / 16) S = steps / 16;
+  if (S < 2) return 1;
+  const double t1 = strip / 40e3 > all ? strip / 40e3 : all;
+  const double tS = 4.5 + (strip / S / 40e3 > all ? strip / S / 40e3 : all);
+  return tS < t1 ? (int)S : 1;
 }
 bool few(const Dense& d) { return d.T <= (d.bf16 ? kFewRowsBf16 : kFewRowsF32); }
 
@@ -134,7 +137,7 @@ FwdPlan fwd_plan(const moe_dense* p, const Dense& d) {
   size_t o = 0;
   if (d.T == 0) return f;
   if (f.few) {
-    f.ch = Choice{0, few_chunks(d, form)};
+    f.ch = Choice{0, few_chunks(d)};
   } else {
     f.pack_x = !direct(d, d.D, p->ldx);
     f.pack_w = !direct(d, d.F, p->ldw);
@@ -357,7 +360,7 @@ moe_status backward(const moe_dense* p, int nm, const void* dy, const void* x, c
     E.blocks = b.ew_blocks;
     E.seed = p->debug_shuffle_seed;
     MOE_TRY(launch_dense_ew(E, nm == 2, d.bf16, st));
-    if (db) MOE_TRY(launch_block_sums(E.part, b.ew_blocks, d.F, d.F, db, !g32 && d.bf16, st));
+    if (db) MOE_TRY(launch_block_sums(E.part, b.ew_blocks, d.F, d.F, db, nullptr, !g32 && d.bf16, st));
   }
   DenseParams P{};
   P.M = d.T;
@@ -489,8 +492,7 @@ MOE_API moe_status moe_layernorm_bwd(const void* dy, const void* x, const void* 
   P.blocks = blocks;
   P.seed = debug_shuffle_seed;
   MOE_TRY(launch_norm_bwd(P, bf16, st));
-  if (dweight) MOE_TRY(launch_block_sums(P.part, blocks, 2 * cols, (int)cols, dweight, false, st));
-  if (dbias) MOE_TRY(launch_block_sums(P.part + cols, blocks, 2 * cols, (int)cols, dbias, false, st));
+  if (sums) MOE_TRY(launch_block_sums(P.part, blocks, 2 * cols, (int)cols, dweight, dbias, false, st));
   return MOE_OK;
 }
 

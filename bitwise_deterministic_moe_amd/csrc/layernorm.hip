@@ -269,10 +269,17 @@ __global__ __launch_bounds__(norm_threads<TPR>) void norm_bwd_kernel(NormParams 
 // workgroup; phase p adds blocks [p B / 16, (p + 1) B / 16) ascending, then
 // the phases are added in order.
 __global__ __launch_bounds__(256) void block_sums_kernel(const float* part, int blocks, int64_t stride, int cols,
-                                                         void* out, int out_bf16) {
+                                                         void* out, void* out2, int out_bf16) {
   __shared__ float s[16][17];
   const int x = threadIdx.x & 15, p = threadIdx.x >> 4;
-  const int c = blockIdx.x * 16 + x;
+  // the second half of the grid sums the columns after the first `cols`
+  const int halves = out2 ? 2 : 1, per = gridDim.x / halves;
+  const int half = (int)blockIdx.x >= per;
+  const int c = ((int)blockIdx.x - half * per) * 16 + x;
+  if (half) {
+    part += cols;
+    out = out2;
+  }
   const int b0 = p * blocks / 16, b1 = (p + 1) * blocks / 16;
   float v = 0.f;
   if (c < cols) {
@@ -282,7 +289,7 @@ __global__ __launch_bounds__(256) void block_sums_kernel(const float* part, int 
   }
   s[p][x] = v;
   __syncthreads();
-  if (p == 0 && c < cols) {
+  if (p == 0 && c < cols && out) {
     v = s[0][x];
 #pragma unroll
     for (int i = 1; i < 16; ++i) v = v + s[i][x];
@@ -335,9 +342,9 @@ hipError_t launch_norm_bwd(const NormParams& P, bool bf16, hipStream_t st) {
   return bf16 ? norm_dispatch<uint16_t>(P, true, st) : norm_dispatch<float>(P, true, st);
 }
 
-hipError_t launch_block_sums(const float* part, int blocks, int64_t stride, int cols, void* out, bool out_bf16,
-                             hipStream_t st) {
-  block_sums_kernel<<<(cols + 15) / 16, 256, 0, st>>>(part, blocks, stride, cols, out, out_bf16);
+hipError_t launch_block_sums(const float* part, int blocks, int64_t stride, int cols, void* out, void* out2,
+                             bool out_bf16, hipStream_t st) {
+  block_sums_kernel<<<(cols + 15) / 16 * (out2 ? 2 : 1), 256, 0, st>>>(part, blocks, stride, cols, out, out2, out_bf16);
   return hipGetLastError();
 }
 
