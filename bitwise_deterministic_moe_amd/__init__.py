@@ -725,6 +725,8 @@ def _mat(t: torch.Tensor, cols: int, dtype, what: str, rows: Optional[int] = Non
     """(rows, row distance) of a matrix [..., cols] of unit stride along its
     rows: two-dimensional with any row distance, or contiguous."""
     shape = t.shape
+    if t.dtype is dtype and len(shape) == 2 and shape[1] == cols and t.is_contiguous() and rows in (None, shape[0]):
+        return shape[0], cols
     if t.dtype != dtype or len(shape) == 0 or shape[-1] != cols:
         raise MoeError(f"{what}: need a {dtype} tensor [..., {cols}], got {t.dtype} {tuple(shape)}")
     if len(shape) == 2:
@@ -780,15 +782,15 @@ def _raw_stream(device: int) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
-def _run(what: str, fn, args, *tensors):
+def _run(what: str, fn, args, first, *tensors):
     """fn(*args, stream) on the GPU of the call's tensors, in its current
     stream."""
-    dev = tensors[0].get_device()
+    dev = first.get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise MoeError(f"{what}: tensors on {tensors[0].device} and {t.device}")
+            raise MoeError(f"{what}: tensors on {first.device} and {t.device}")
     if dev < 0:
-        raise MoeError(f"{what}: tensors must be on a GPU, got {tensors[0].device}")
+        raise MoeError(f"{what}: tensors must be on a GPU, got {first.device}")
     if dev == torch.cuda.current_device():
         status = fn(*args, _raw_stream(dev))
     else:
@@ -796,6 +798,11 @@ def _run(what: str, fn, args, *tensors):
             status = fn(*args, _raw_stream(dev))
     if status:
         _check(status, what)
+
+
+def _like(x: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of x's shape and type."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
 def moe_layernorm_workspace_size(rows: int, cols: int) -> int:
@@ -823,11 +830,12 @@ def moe_layernorm_fwd(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5
     if bias is not None:
         _need(bias, cols, x.dtype, what + " bias")
     if y is None:
-        y = x.new_empty(x.shape)
+        y = _like(x)
     else:
         _need(y, rows * cols, x.dtype, what + " y")
     if mean is None and rstd is None:
-        mean, rstd = x.new_empty((2,) + x.shape[:-1], dtype=torch.float32).unbind(0)
+        mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+        rstd = torch.empty_like(mean)
     elif mean is None or rstd is None:
         raise MoeError(f"{what}: mean and rstd are given together")
     else:
@@ -857,7 +865,7 @@ def moe_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight, mean, rstd, dx_
     _need(mean, rows, torch.float32, what + " mean")
     _need(rstd, rows, torch.float32, what + " rstd")
     if dx is None:
-        dx = x.new_empty(x.shape)
+        dx = _like(x)
     else:
         _need(dx, rows * cols, x.dtype, what + " dx")
     if dweight is None:
@@ -991,7 +999,7 @@ def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z=None, a
         z = None
     ldr = _mat(dx_add, d, dt, what + " dx_add", rows)[1] if dx_add is not None else 0
     if dx is None:
-        dx = x.new_empty(x.shape)
+        dx = _like(x)
     else:
         _need(dx, rows * d, dt, what + " dx")
     if dw is None:
@@ -1062,7 +1070,7 @@ def moe_glu_bwd(da: torch.Tensor, x: torch.Tensor, wg: torch.Tensor, wu: torch.T
         raise MoeError(f"{what}: g and u need the same type and row distance")
     ldr = _mat(dx_add, d, dt, what + " dx_add", rows)[1] if dx_add is not None else 0
     if dx is None:
-        dx = x.new_empty(x.shape)
+        dx = _like(x)
     else:
         _need(dx, rows * d, dt, what + " dx")
     if dwg is None:

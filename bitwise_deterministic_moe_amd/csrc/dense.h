@@ -154,15 +154,22 @@ struct DenseParams {
 // Rows of the few-row kernels (weights streamed once).
 constexpr int kFewRowsBf16 = 64, kFewRowsF32 = 16;
 
-// bm: tile rows (bf16: 128 or 256; float32: 128)
+// bm: tile rows (bf16: 128 or 256; float32: 64 or 128)
 hipError_t launch_dense_gemm(const DenseParams& P, int form, bool bf16, int bm, hipStream_t st);
 hipError_t launch_dense_few(const DenseParams& P, int form, bool bf16, hipStream_t st);
 hipError_t launch_dense_finish(const DenseParams& P, int form, bool bf16, hipStream_t st);
-int dense_tile_n(int form, bool bf16);   // columns of one matrix a tile covers
+int dense_tile_n(int form, bool bf16, int bm);   // columns of one matrix a tile covers
 
-// bf16 matrix [rows][cols] (row distance ld) into [rows][ldo], zeros past cols
-hipError_t launch_dense_pack(const void* in, int64_t rows, int cols, int64_t ld, void* out, int64_t ldo,
-                             hipStream_t st);
+// bf16 matrices [rows][cols] (row distance ld) into [rows][ldo], zeros past cols
+struct DensePackParams {
+  const void* in[3];
+  void* out[3];
+  int64_t rows[3], ld[3], ldo[3], first[4];   // first workgroup of each
+  int cols[3];
+  int n;
+  void add(const void* src, int64_t r, int c, int64_t l, void* dst, int64_t lo);
+};
+hipError_t launch_dense_pack(const DensePackParams& P, hipStream_t st);
 // Gradients of the pre-activations, elementwise, with the column sums of dz
 // over row blocks.
 struct DenseEwParams {
@@ -181,7 +188,7 @@ struct DenseEwParams {
   int blocks;
   uint64_t seed;
 };
-int dense_ew_blocks(int64_t rows, int cols, bool bf16);
+int dense_ew_blocks(int64_t rows, int cols, bool bf16, bool sums);
 hipError_t launch_dense_ew(const DenseEwParams& P, bool glu, bool bf16, hipStream_t st);
 hipError_t launch_dense_zero(void* p, int64_t n16, hipStream_t st);   // n16 16-bit words
 

@@ -12,6 +12,8 @@
 // workgroups over chunks of k whose float32 partials a second launch adds in
 // chunk order.  S and every chunk bound depend on sizes only, and no atomics
 // are used, so the bits do not depend on scheduling.
+#include <type_traits>
+
 #include "dense_bf16.h"
 #include "dense_epilogue.h"
 #include "kernels.h"
@@ -22,7 +24,7 @@ namespace moedet {
 // Tile order: bands of kBand tile rows, down the band before across, so the
 // consecutive units that map_unit gives to an XCD share operand tiles in its
 // L2 both ways.
-constexpr int kBand = 4;
+constexpr uint32_t kBand = 4;
 struct DenseTile {
   int64_t m0;
   int n0, seg, chunk;
@@ -31,25 +33,26 @@ struct DenseTile {
 
 template <int FORM>
 DEV bool dense_tile(const DenseParams& P, int bm, int bn, int bk, DenseTile& t) {
-  const int64_t mT = (P.M + bm - 1) / bm;
-  const int nTs = (P.N + bn - 1) / bn;
-  const int nT = FORM == kFormDw ? nTs * P.nseg : nTs;
-  const int64_t tiles = mT * nT;
-  const int64_t L = map_unit(blockIdx.x, tiles * P.S, P.seed);
-  if (L < 0) return false;
+  // 32 bits: the launch has one workgroup per unit, fewer than 2^24
+  const uint32_t mT = (uint32_t)((P.M + bm - 1) / bm), nTs = (uint32_t)((P.N + bn - 1) / bn);
+  const uint32_t nT = FORM == kFormDw ? nTs * P.nseg : nTs;
+  const uint32_t tiles = mT * nT;
+  const int64_t unit = map_unit(blockIdx.x, (int64_t)tiles * P.S, P.seed);
+  if (unit < 0) return false;
+  const uint32_t L = (uint32_t)unit;
   t.chunk = (int)(L / tiles);
-  const int64_t tile = L - t.chunk * tiles;
-  const int64_t band = tile / ((int64_t)kBand * nT);
-  const int64_t in = tile - band * kBand * nT;
-  const int64_t left = mT - band * kBand;
-  const int h = left < kBand ? (int)left : kBand;
-  t.m0 = (band * kBand + in % h) * bm;
-  const int nt = (int)(in / h);
-  t.seg = FORM == kFormDw ? nt / nTs : 0;
-  t.n0 = (FORM == kFormDw ? nt % nTs : nt) * bn;
-  const int64_t steps = (P.K + bk - 1) / bk * (FORM == kFormDx ? P.nseg : 1);
-  t.s0 = (int)(t.chunk * steps / P.S);
-  t.s1 = (int)((t.chunk + 1) * steps / P.S);
+  const uint32_t tile = L - t.chunk * tiles;
+  const uint32_t band = tile / (kBand * nT), in = tile - band * kBand * nT;
+  const uint32_t left = mT - band * kBand, h = left < kBand ? left : kBand;
+  t.m0 = (int64_t)(band * kBand + in % h) * bm;
+  const uint32_t nt = in / h;
+  t.seg = FORM == kFormDw && nt >= nTs ? 1 : 0;
+  t.n0 = (int)(nt - t.seg * nTs) * bn;
+  // chunks of steps / S slices, the first steps % S of one more
+  const uint32_t steps = (uint32_t)((P.K + bk - 1) / bk * (FORM == kFormDx ? P.nseg : 1));
+  const uint32_t q = steps / P.S, r = steps - q * P.S;
+  t.s0 = (int)(t.chunk * q + min((uint32_t)t.chunk, r));
+  t.s1 = t.s0 + (int)(q + ((uint32_t)t.chunk < r ? 1 : 0));
   return true;
 }
 
@@ -245,128 +248,195 @@ __global__ __launch_bounds__(256) void dense_bf16_kernel(DenseParams P) {
 }
 
 // ------------------------------------------------------------- float32 tiles
-// Tile 128 x 128 x 16 (the gated product: 64 columns of both matrices), 4
-// waves of 64 x 64 in blocks of v_mfma_f32_32x32x2f32.  A thread holds the next
-// slice in registers while the current one is multiplied from LDS (two LDS
-// buffers, one barrier a slice).  LDS keeps each operand's own order:
-// K-contiguous rows [128][20], read four k at a time, or [16][132].  In both,
-// the MFMA e of group q takes k = 8 q + e from lanes 0..31 and k = 8 q + 4 + e
-// from lanes 32..63.  Loads are of any address; edges are read
-// element by element.
+// Tile (64 MB) x (64 NB) x 16 (the gated product: 32 NB columns of both
+// matrices, NB = 2), 4 waves of MB x NB blocks of v_mfma_f32_32x32x2f32.  A
+// thread holds the next kAhead slices in registers (a slice of a lone 64 x 64
+// tile is multiplied in about 0.3 us, a fraction of the load latency) and
+// copies one to LDS per step (three buffers, one barrier a slice).  LDS keeps each
+// operand's own order: K-contiguous rows [64 B][20], read four k at a time, or
+// [16][64 B + 4].  In both, the MFMA e of group q takes k = 8 q + e from lanes
+// 0..31 and k = 8 q + 4 + e from lanes 32..63.
+// Loads are buffer loads without branches (an offset past the buffer reads
+// zero), so that the compiler's waits can count them; V4 says that every group of
+// four columns is whole, otherwise elements are loaded one by one.
 namespace f32t {
-constexpr int BM = 128, BK = 16, KROW = 20, MROW = 132;
-constexpr int OPER = 128 * KROW;   // floats of an operand's LDS buffer (the larger layout)
+constexpr int BK = 16, KROW = 20, kAhead = 3;
+constexpr uint32_t kOut = 0x80000000u;
+template <int B>
+constexpr int MROW = 64 * B + 4;
+template <int B>
+constexpr int OPER = 64 * B * KROW;   // floats of an operand's LDS buffer (the larger layout)
 
-// v[i]: 4 floats; K-contiguous: row tid/4 + 64 i, k = 4 (tid % 4);
-// M/N-contiguous: k = tid/32 + 8 i, columns 4 (tid % 32)
-DEV void load_kc(f32x4_t (&v)[2], const float* base, int64_t ld, int rows, int64_t k, int64_t K, int tid) {
+DEV __amdgpu_buffer_rsrc_t rsrc(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, 0x7fffffff, 0x00020000);
+}
+// four elements at byte offset o, of which the first n exist (n <= 0: none)
+template <bool V4>
+DEV f32x4_t load4(__amdgpu_buffer_rsrc_t r, uint32_t o, int n) {
+  if constexpr (V4) return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, n > 0 ? o : kOut, 0, 0));
+  f32x4_t v;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = (tid >> 2) + 64 * i;
-    const int64_t kk = k + 4 * (tid & 3);
-    v[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    if (r < rows && kk < K) v[i] = Vec<float>::load(base + r * ld + kk, (int)(K - kk < 4 ? K - kk : 4));
+  for (int e = 0; e < 4; ++e)
+    v[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, n > e ? o + 4 * e : kOut, 0, 0));
+  return v;
+}
+
+// The thread's part of an operand's slice: K-contiguous, row tid / 4 + 64 i and
+// k = 4 (tid % 4); M/N-contiguous, k = tid / (16 B) + i (16 / B) and columns 4 (tid % (16 B)).
+template <bool KCL, int B, bool V4>
+struct Op {
+  int mn[B], k[B];
+  uint32_t off[B];
+  int n[B];     // M/N-contiguous: columns that exist from this thread's first; K-contiguous: 1 if the row exists
+  DEV void init(int tid, int64_t ld, int valid) {
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      mn[i] = KCL ? (tid >> 2) + 64 * i : 4 * (tid & (16 * B - 1));
+      k[i] = KCL ? 4 * (tid & 3) : tid / (16 * B) + i * (16 / B);
+      off[i] = (uint32_t)((KCL ? mn[i] * ld + k[i] : k[i] * ld + mn[i]) * 4);
+      n[i] = KCL ? (mn[i] < valid ? 1 : 0) : valid - mn[i];
+    }
   }
-}
-DEV void load_mnc(f32x4_t (&v)[2], const float* base, int64_t ld, int cols, int64_t k, int64_t K, int tid) {
+  // base: the slice's first k; left: k that remain from there
+  DEV void load(f32x4_t (&v)[B], __amdgpu_buffer_rsrc_t r, int left) const {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t kk = k + (tid >> 5) + 8 * i;
-    const int c = 4 * (tid & 31);
-    v[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    if (c < cols && kk < K) v[i] = Vec<float>::load(base + kk * ld + c, cols - c);
+    for (int i = 0; i < B; ++i) {
+      if constexpr (KCL)
+        v[i] = load4<V4>(r, off[i], n[i] ? left - k[i] : 0);
+      else
+        v[i] = load4<V4>(r, off[i], k[i] < left ? n[i] : 0);
+    }
   }
-}
-DEV void store_kc(float* s, const f32x4_t (&v)[2], int tid) {
+  DEV void store(float* s, const f32x4_t (&v)[B]) const {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) *(f32x4_t*)(s + ((tid >> 2) + 64 * i) * KROW + 4 * (tid & 3)) = v[i];
-}
-DEV void store_mnc(float* s, const f32x4_t (&v)[2], int tid) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) *(f32x4_t*)(s + ((tid >> 5) + 8 * i) * MROW + 4 * (tid & 31)) = v[i];
-}
-template <bool KCL>
+    for (int i = 0; i < B; ++i) *(f32x4_t*)(s + (KCL ? mn[i] * KROW + k[i] : k[i] * MROW<B> + mn[i])) = v[i];
+  }
+};
+template <bool KCL, int B>
 DEV f32x4_t frag(const float* s, int row, int q, int half) {
   if constexpr (KCL) return *(const f32x4_t*)(s + row * KROW + 8 * q + 4 * half);
-  const float* p = s + (8 * q + 4 * half) * MROW + row;
-  return f32x4_t{p[0], p[MROW], p[2 * MROW], p[3 * MROW]};
+  const float* p = s + (8 * q + 4 * half) * MROW<B> + row;
+  return f32x4_t{p[0], p[MROW<B>], p[2 * MROW<B>], p[3 * MROW<B>]};
 }
 }  // namespace f32t
 
-template <int FORM>
+template <int FORM, int MB, int NB, bool V4>
 __global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
   using namespace f32t;
-  __shared__ __attribute__((aligned(16))) float sa[2][OPER], sb[2][OPER];
-  constexpr int BNv = FORM == kFormGlu ? 64 : 128;
+  static_assert(FORM != kFormGlu || NB == 2, "a wave holds g and u of the same columns");
+  __shared__ __attribute__((aligned(16))) float sa[kAhead][OPER<MB>], sb[kAhead][OPER<NB>];
+  constexpr int BM = 64 * MB, BNv = FORM == kFormGlu ? 32 * NB : 64 * NB;
   constexpr bool AK = FORM != kFormDw, BKC = FORM == kFormDx;
   DenseTile t;
   if (!dense_tile<FORM>(P, BM, BNv, BK, t)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
   const int r32 = lane & 31, half = lane >> 5;
   const int mvalid = (int)(P.M - t.m0 < BM ? P.M - t.m0 : BM), nvalid = P.N - t.n0;
-  const int64_t steps_seg = (P.K + BK - 1) / BK;
-  f32x4_t ra[2], rb[2];
-  auto load = [&](int s) {
-    int64_t ks = s;
-    const bool second = FORM == kFormDx && ks >= steps_seg;
-    if (second) ks -= steps_seg;
-    const int64_t k = ks * BK;
-    if constexpr (AK)
-      load_kc(ra, (const float*)P.a + t.m0 * P.lda + (second ? P.seg : 0), P.lda, mvalid, k, P.K, tid);
-    else
-      load_mnc(ra, (const float*)P.a + t.m0, P.lda, mvalid, k, P.K, tid);
+  const int steps_seg = (int)((P.K + BK - 1) / BK);
+  // the gated product's B slice is one load a thread from each matrix,
+  // columns 0..63 of the LDS tile from wg, 64..127 from wu
+  constexpr int OB = FORM == kFormGlu ? 1 : NB;
+  Op<AK, MB, V4> oa;
+  Op<BKC, OB, V4> ob;
+  oa.init(tid, P.lda, mvalid);
+  ob.init(tid, P.ldb, nvalid);
+  f32x4_t ra[kAhead][MB], rb[kAhead][NB];
+  auto load = [&](f32x4_t (&va)[MB], f32x4_t (&vb)[NB], int s) __attribute__((always_inline)) {
+    const bool second = FORM == kFormDx && s >= steps_seg;
+    const int64_t k = (int64_t)(second ? s - steps_seg : s) * BK;
+    // past the last slice nothing is left to load
+    const int left = s < t.s1 ? (int)(P.K - k < BK ? P.K - k : BK) : 0;
+    const float* pa = (const float*)P.a + (AK ? t.m0 * P.lda + (second ? P.seg : 0) + k : k * P.lda + t.m0);
+    oa.load(va, rsrc(pa), left);
     if constexpr (FORM == kFormDx) {
-      load_kc(rb, (const float*)(second ? P.b[1] : P.b[0]) + t.n0 * P.ldb, P.ldb, nvalid, k, P.K, tid);
+      ob.load(vb, rsrc((const float*)(second ? P.b[1] : P.b[0]) + t.n0 * P.ldb + k), left);
     } else if constexpr (FORM == kFormGlu) {
-      // columns 0..63 of the tile from wg, 64..127 from wu
-      const bool up = (tid & 31) >= 16;
-      load_mnc(rb, (const float*)(up ? P.b[1] : P.b[0]) + t.n0 - (up ? 64 : 0), P.ldb, (up ? 64 : 0) + (nvalid < 64 ? nvalid : 64),
-               k, P.K, tid);
+      f32x4_t v[1];
+      ob.load(v, rsrc((const float*)P.b[0] + k * P.ldb + t.n0), left);
+      vb[0] = v[0];
+      ob.load(v, rsrc((const float*)P.b[1] + k * P.ldb + t.n0), left);
+      vb[1] = v[0];
     } else {
-      load_mnc(rb, (const float*)P.b[0] + (FORM == kFormDw ? t.seg * P.seg : 0) + t.n0, P.ldb, nvalid, k, P.K, tid);
+      ob.load(vb, rsrc((const float*)P.b[0] + (FORM == kFormDw ? t.seg * P.seg : 0) + k * P.ldb + t.n0), left);
     }
   };
-  auto store = [&](int b) {
-    if constexpr (AK) store_kc(sa[b], ra, tid); else store_mnc(sa[b], ra, tid);
-    if constexpr (BKC) store_kc(sb[b], rb, tid); else store_mnc(sb[b], rb, tid);
+  auto store_b = [&](float* s, const f32x4_t (&v)[NB]) __attribute__((always_inline)) {
+    if constexpr (FORM == kFormGlu) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) *(f32x4_t*)(s + ob.k[0] * MROW<NB> + 64 * i + ob.mn[0]) = v[i];
+    } else {
+      ob.store(s, v);
+    }
   };
-  f32x16_t acc[2][2];
+  f32x16_t acc[MB][NB];
 #pragma unroll
-  for (int a = 0; a < 2; ++a)
+  for (int a = 0; a < MB; ++a)
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
-  load(t.s0);
-  store(0);
-  __syncthreads();
-#pragma unroll 1
-  for (int s = t.s0; s < t.s1; ++s) {
-    const int cur = (s - t.s0) & 1;
-    if (s + 1 < t.s1) load(s + 1);
+  // Slice s sits in LDS buffer s % 3.  In step s, slice s + 2 goes from
+  // registers to the buffer that step s - 1 read, slice s + 5 is loaded, and each
+  // half slice is read from LDS while the one before it is multiplied; slice
+  // s + 1 was stored before the barrier that ended step s - 1.
+  struct Half {
+    f32x4_t a[MB], b[NB];
+  };
+  auto read = [&](Half& f, int buf, int q) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      f32x4_t fa[2], fb[2];
+    for (int x = 0; x < MB; ++x) f.a[x] = frag<AK, MB>(sa[buf], (wm * MB + x) * 32 + r32, q, half);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        fa[x] = frag<AK>(sa[cur], wm * 64 + x * 32 + r32, q, half);
-        fb[x] = frag<BKC>(sb[cur], (FORM == kFormGlu ? x * 64 + wn * 32 : wn * 64 + x * 32) + r32, q, half);
-      }
+    for (int x = 0; x < NB; ++x)
+      f.b[x] = frag<BKC, NB>(sb[buf], (FORM == kFormGlu ? x * 64 + wn * 32 : (wn * NB + x) * 32) + r32, q, half);
+  };
+  auto mul = [&](const Half& f) __attribute__((always_inline)) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb)
+      for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-            acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[nb][e], fa[mb][e], acc[mb][nb], 0, 0, 0);
-    }
-    if (s + 1 < t.s1) store(cur ^ 1);
+        for (int nb = 0; nb < NB; ++nb)
+          acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(f.b[nb][e], f.a[mb][e], acc[mb][nb], 0, 0, 0);
+  };
+  auto fill = [&](auto J, int s) __attribute__((always_inline)) {   // set J to its buffer, then slice s into set J
+    constexpr int j = decltype(J)::value;
+    oa.store(sa[j], ra[j]);
+    store_b(sb[j], rb[j]);
+    load(ra[j], rb[j], s);
+  };
+  typedef std::integral_constant<int, 0> J0;
+  typedef std::integral_constant<int, 1> J1;
+  typedef std::integral_constant<int, 2> J2;
+  static_assert(kAhead == 3, "three register sets and buffers");
+  Half f0, f1;
+  auto step = [&](int s, auto J, auto J2nd) __attribute__((always_inline)) {
+    constexpr int j = decltype(J)::value;
+    fill(J2nd, s + 5);
+    read(f1, j, 1);
+    mul(f0);
+    read(f0, (j + 1) % 3, 0);
+    mul(f1);
     __syncthreads();
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) load(ra[j], rb[j], t.s0 + j);
+  int s = t.s0;
+  fill(J0{}, s + 3);
+  fill(J1{}, s + 4);
+  __syncthreads();
+  read(f0, 0, 0);
+#pragma unroll 1
+  for (; s + 3 <= t.s1; s += 3) {
+    step(s, J0{}, J2{});
+    step(s + 1, J1{}, J0{});
+    step(s + 2, J2{}, J1{});
   }
+  if (s < t.s1) step(s, J0{}, J2{});
+  if (s + 1 < t.s1) step(s + 1, J1{}, J0{});
   // lane l holds row l % 32 and columns 8 i + 4 (l / 32) + 0..3 of each block
 #pragma unroll
-  for (int mb = 0; mb < 2; ++mb) {
-    const int m = wm * 64 + mb * 32 + r32;
+  for (int mb = 0; mb < MB; ++mb) {
+    const int m = (wm * MB + mb) * 32 + r32;
     if (m >= mvalid) continue;
     const int64_t row = t.m0 + m;
     if constexpr (FORM == kFormGlu) {
@@ -378,7 +448,7 @@ __global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           g[q] = acc[mb][0][4 * i + q];
-          u[q] = acc[mb][1][4 * i + q];
+          u[q] = acc[mb][NB - 1][4 * i + q];
         }
         if (P.S > 1) {
           part4(P, t.chunk, 0, row, col, g);
@@ -389,10 +459,10 @@ __global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
       }
     } else {
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int col = t.n0 + wn * 64 + nb * 32 + 8 * i + 4 * half;
+          const int col = t.n0 + (wn * NB + nb) * 32 + 8 * i + 4 * half;
           if (col >= P.N) continue;
           float v[4];
 #pragma unroll
@@ -635,16 +705,19 @@ __global__ __launch_bounds__(256) void dense_finish_kernel(DenseParams P) {
 }
 
 // ---------------------------------------------------------- elementwise passes
-__global__ __launch_bounds__(256) void dense_pack_kernel(const uint16_t* in, int64_t rows, int cols, int64_t ld,
-                                                         uint16_t* out, int64_t ldo) {
-  const int q = (int)(ldo / 8);
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * q) return;
+// Up to three matrices copied into rows of whole 16-byte chunks, zeros past
+// their columns: one launch, a matrix per range of workgroups.
+__global__ __launch_bounds__(256) void dense_pack_kernel(DensePackParams P) {
+  int m = 0;
+  while (m + 1 < P.n && (int64_t)blockIdx.x >= P.first[m + 1]) ++m;
+  const int q = (int)(P.ldo[m] / 8);
+  const int64_t i = ((int64_t)blockIdx.x - P.first[m]) * 256 + threadIdx.x;
+  if (i >= P.rows[m] * q) return;
   const int64_t row = i / q;
-  const int c = (int)(i - row * q) * 8;
+  const int c = (int)(i - row * q) * 8, left = P.cols[m] - c;
   u32x4_t r = {0u, 0u, 0u, 0u};
-  if (c < cols) r = Vec<uint16_t>::load(in + row * ld + c, cols - c);
-  *(u32x4_t*)(out + row * ldo + c) = r;
+  if (left > 0) r = Vec<uint16_t>::load((const uint16_t*)P.in[m] + row * P.ld[m] + c, left);
+  *(u32x4_t*)((uint16_t*)P.out[m] + row * P.ldo[m] + c) = r;
 }
 
 // V elements of a saved pre-activation, zeros past n >= 1
@@ -680,7 +753,7 @@ __global__ __launch_bounds__(256) void dense_ew_kernel(DenseEwParams P) {
 #pragma unroll
   for (int q = 0; q < V; ++q) sum[q] = 0.f;
   if (no > 0) {
-#pragma unroll 2
+#pragma unroll 4
     for (int64_t row = r0 + wave; row < r1; row += 4) {
       float d[V], o0[V], o1[V];
 #pragma unroll
@@ -732,20 +805,38 @@ __global__ __launch_bounds__(256) void dense_zero_kernel(uint16_t* p, int64_t n)
 }
 
 // -------------------------------------------------------------------- launches
-int dense_tile_n(int form, bool bf16) { return (bf16 ? 256 : 128) / (form == kFormGlu ? 2 : 1); }
+int dense_tile_n(int form, bool bf16, int bm) {
+  if (bf16) return form == kFormGlu ? 128 : 256;
+  return form == kFormGlu ? 64 : bm;
+}
+
+template <int FORM, bool V4>
+static void dense_f32_launch(const DenseParams& P, int bm, int64_t grid, hipStream_t st) {
+  if (bm == 128)
+    dense_f32_kernel<FORM, 2, 2, V4><<<grid, 256, 0, st>>>(P);
+  else
+    dense_f32_kernel<FORM, 1, FORM == kFormGlu ? 2 : 1, V4><<<grid, 256, 0, st>>>(P);
+}
 
 template <int FORM>
 static void dense_gemm_launch(const DenseParams& P, bool bf16, int bm, int64_t grid, hipStream_t st) {
-  if (!bf16)
-    dense_f32_kernel<FORM><<<grid, 256, 0, st>>>(P);
-  else if (bm == 256)
+  if (!bf16) {
+    // whole groups of four along each operand's contiguous direction
+    const bool ka = FORM != kFormDw, kb = FORM == kFormDx;
+    const bool v4 = (ka ? P.K : P.M) % 4 == 0 && (kb ? P.K : P.N) % 4 == 0;
+    if (v4)
+      dense_f32_launch<FORM, true>(P, bm, grid, st);
+    else
+      dense_f32_launch<FORM, false>(P, bm, grid, st);
+  } else if (bm == 256) {
     dense_bf16_kernel<FORM, 128><<<grid, 256, 0, st>>>(P);
-  else
+  } else {
     dense_bf16_kernel<FORM, 64><<<grid, 256, 0, st>>>(P);
+  }
 }
 
 hipError_t launch_dense_gemm(const DenseParams& P, int form, bool bf16, int bm, hipStream_t st) {
-  const int bn = dense_tile_n(form, bf16);
+  const int bn = dense_tile_n(form, bf16, bm);
   const int64_t tiles = (P.M + bm - 1) / bm * ((P.N + bn - 1) / bn) * (form == kFormDw ? P.nseg : 1);
   const int64_t grid = grid_for_units(tiles * P.S);
   switch (form) {
@@ -806,17 +897,31 @@ hipError_t launch_dense_finish(const DenseParams& P, int form, bool bf16, hipStr
   return hipGetLastError();
 }
 
-hipError_t launch_dense_pack(const void* in, int64_t rows, int cols, int64_t ld, void* out, int64_t ldo,
-                             hipStream_t st) {
-  dense_pack_kernel<<<(rows * (ldo / 8) + 255) / 256, 256, 0, st>>>((const uint16_t*)in, rows, cols, ld,
-                                                                  (uint16_t*)out, ldo);
+void DensePackParams::add(const void* src, int64_t r, int c, int64_t l, void* dst, int64_t lo) {
+  if (n == 0) first[0] = 0;
+  in[n] = src;
+  rows[n] = r;
+  cols[n] = c;
+  ld[n] = l;
+  out[n] = dst;
+  ldo[n] = lo;
+  first[n + 1] = first[n] + (r * (lo / 8) + 255) / 256;
+  ++n;
+}
+
+hipError_t launch_dense_pack(const DensePackParams& P, hipStream_t st) {
+  if (P.n == 0) return hipSuccess;
+  dense_pack_kernel<<<P.first[P.n], 256, 0, st>>>(P);
   return hipGetLastError();
 }
 
-// Row blocks of the elementwise pass: about 2048 workgroups, at least 4 rows each.
-int dense_ew_blocks(int64_t rows, int cols, bool bf16) {
+// Row blocks of the elementwise pass.  With column sums about 512 workgroups
+// (every block adds a row of partials to write and read again; 4096 x 2048
+// bf16: 4 MB of them with 2048 workgroups, 1 MB with 512), else about 2048; at
+// least 4 rows each.
+int dense_ew_blocks(int64_t rows, int cols, bool bf16, bool sums) {
   const int ct = bf16 ? 512 : 256;
-  int64_t b = 2048 / ((cols + ct - 1) / ct);
+  int64_t b = (sums ? 512 : 2048) / ((cols + ct - 1) / ct);
   const int64_t most = (rows + 3) / 4;
   if (b > most) b = most;
   return (int)(b < 1 ? 1 : b > 512 ? 512 : b);

@@ -59,43 +59,55 @@ struct Choice {
 constexpr int kCUs = 256;
 constexpr int64_t kMaxPartialBytes = (int64_t)1 << 30;
 
-// Time estimate in microseconds of a launch of `wgs` workgroups of `steps` slices
-// each, plus the float32 partials of a split and their join.
-double estimate(int64_t wgs, int64_t steps, double per_step, double fixed, int64_t S, double out_elems) {
-  const double rounds = (double)((wgs + kCUs - 1) / kCUs);
-  double t = rounds * (fixed + (double)steps * per_step);
+// A tile shape's cost in microseconds, measured on this card: `alone` per
+// slice of a workgroup that has a CU to itself, `busy` per slice and workgroup
+// of a CU that several share (a bf16 tile fills a CU: they follow each
+// other), `fixed` once (launch, first slice, epilogue).
+//   bf16     256 rows: 0.82 (8192^3) to 1.0; 128 rows: 0.52 (4096 x 8192 x 2048)
+//   float32  128 x 128: 1.06 busy (4096^3), 64 x 64: 0.27
+struct TileCost {
+  int bm;
+  double alone, busy, fixed;
+};
+constexpr TileCost kBf16Tiles[2] = {{256, 0.9, 0.9, 10.0}, {128, 0.52, 0.52, 8.0}};
+constexpr TileCost kF32Tiles[2] = {{128, 1.3, 1.06, 7.0}, {64, 0.38, 0.27, 6.0}};
+
+double estimate(const TileCost& c, int64_t wgs, int64_t steps, double width, int64_t S, double out_elems) {
+  const double per_cu = (double)((wgs + kCUs - 1) / kCUs);
+  const double shared = per_cu * c.busy, lone = c.alone;
+  double t = c.fixed + (double)steps * width * (shared > lone ? shared : lone);
+  // bf16 tiles of a later round pay their epilogue again
+  if (c.alone == c.busy) t += (per_cu - 1) * 0.6 * c.fixed;
+  // float32 partials written and read, and the launch that joins them
   if (S > 1) t += (double)S * out_elems * 8.0 / 4.5e6 + 4.0;
   return t;
 }
 
-// Tile height and number of K chunks of one product.  The constants are
-// microseconds per slice of one tile with every CU busy, and the fixed cost of a
-// tile (lookup, first slice, epilogue).
+// Tile and number of K chunks of one product: the cheapest estimate.
 Choice choose(const Dense& d, int form, int64_t M, int64_t N, int nseg, int64_t K, int64_t ld_max) {
-  const int bn = dense_tile_n(form, d.bf16);
   const int bk = d.bf16 ? 32 : 16;
-  const int64_t nT = (N + bn - 1) / bn * (form == kFormDw ? nseg : 1);
   const int64_t steps = (K + bk - 1) / bk * (form == kFormDx ? nseg : 1);
   const double outs = (double)M * N * (form == kFormDw ? nseg : form == kFormGlu ? 2 : 1);
-  // the weight gradient's operands are addressed by 32-bit offsets from the
-  // chunk's first row
+  // the weight gradient's bf16 operands are addressed by 32-bit offsets from
+  // the chunk's first row
   int64_t smin = 1;
   if (form == kFormDw && d.bf16) smin = (K + 64) * ld_max * 2 / ((int64_t)1 << 30) + 1;
   Choice best{0, 0};
   double tb = 0;
-  for (int bm : {256, 128}) {
-    if (!d.bf16 && bm == 256) continue;
-    const double per = !d.bf16 ? 0.9 : bm == 256 ? 0.92 : 0.55;
-    const double fixed = !d.bf16 ? 5.0 : bm == 256 ? 9.0 : 7.0;
-    const int64_t tiles = (M + bm - 1) / bm * nT;
-    for (int64_t S = smin; S <= (smin > 32 ? smin : 32) && (S == smin || (steps / S >= 4 && S * outs * 4 <= kMaxPartialBytes));
-         ++S) {
-      const double t = estimate(tiles * S, (steps + S - 1) / S, per, fixed, S, outs);
+  for (int i = 0; i < 2; ++i) {
+    const TileCost& c = d.bf16 ? kBf16Tiles[i] : kF32Tiles[i];
+    const int bn = dense_tile_n(form, d.bf16, c.bm);
+    // the small float32 tile of the gated product is twice as wide as high
+    const double width = !d.bf16 && form == kFormGlu && c.bm == 64 ? 2 : 1;
+    const int64_t tiles = (M + c.bm - 1) / c.bm * ((N + bn - 1) / bn * (form == kFormDw ? nseg : 1));
+    const int64_t smax = smin > 32 ? smin : 32;
+    for (int64_t S = smin; S <= smax; ++S) {
+      if (S > smin && (steps / S < 4 || S * outs * 4 > kMaxPartialBytes || tiles * (S - 1) >= 4 * kCUs)) break;
+      const double t = estimate(c, tiles * S, (steps + S - 1) / S, width, S, outs);
       if (best.S == 0 || t < tb * 0.98) {
-        best = Choice{bm, (int)S};
+        best = Choice{c.bm, (int)S};
         tb = t;
       }
-      if (tiles * S >= 4 * kCUs) break;
     }
   }
   return best;
@@ -104,7 +116,7 @@ Choice choose(const Dense& d, int form, int64_t M, int64_t N, int nseg, int64_t 
 // Chunks of K of the few-row kernels.  A workgroup streams about 40 KB/us and
 // the device 4.6 TB/s; a launch of them takes 3 us beside the stream, and
 // partials with their join 4.5 us more (measured: 64 strips of 8192 x 2048
-// bf16 16.6 us unsplit; 256 in four chunks SPLIT_US us with the join).
+// bf16 16.6 us unsplit; 256 in four chunks 10.5 us with the join).
 int few_chunks(const Dense& d) {
   const double strip = (double)d.D * 64 * d.nm;
   const int cols = 64 / (int)d.es;
@@ -196,7 +208,7 @@ BwdPlan bwd_plan(const moe_dense* p, const Dense& d) {
     b.dz = o;
     o += align_up((size_t)d.T * b.lddz * d.es);
   }
-  b.ew_blocks = dense_ew_blocks(d.T, d.F, d.bf16);
+  b.ew_blocks = dense_ew_blocks(d.T, d.F, d.bf16, d.nm == 1);
   b.colsum = o;
   if (d.nm == 1) o += align_up((size_t)b.ew_blocks * d.F * 4);
   b.dx = choose(d, kFormDx, d.T, d.D, d.nm, d.F, 0);
@@ -240,18 +252,19 @@ moe_status check_ws(const void* ws, size_t have, size_t need) {
 // x (and the weights) copied into whole 16-byte rows where they are not
 moe_status pack_inputs(const Dense& d, const moe_dense* p, bool px, bool pw, int64_t ldx, int64_t ldw, char* wx, char* ww,
                        const void*& x, const void* (&w)[2], hipStream_t st) {
+  DensePackParams K{};
   if (px) {
-    MOE_TRY(launch_dense_pack(x, d.T, d.D, p->ldx, wx, ldx, st));
+    K.add(x, d.T, d.D, p->ldx, wx, ldx);
     x = wx;
   }
   if (pw) {
     for (int m = 0; m < d.nm; ++m) {
       char* o = ww + (size_t)m * d.D * ldw * 2;
-      MOE_TRY(launch_dense_pack(w[m], d.D, d.F, p->ldw, o, ldw, st));
+      K.add(w[m], d.D, d.F, p->ldw, o, ldw);
       w[m] = o;
     }
   }
-  return MOE_OK;
+  return hip_status(launch_dense_pack(K, st));
 }
 
 moe_status run_product(DenseParams& P, int form, const Dense& d, int bm, hipStream_t st) {

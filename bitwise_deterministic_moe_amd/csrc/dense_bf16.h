@@ -130,6 +130,15 @@ DEV void load_group(bf::Frags& f, const uint16_t* slot, int kk, int wm, int wn, 
   }
 }
 
+// One of the two products of group g (bf::mma2).
+template <int NMB, bool FIRST = false>
+DEV void mma1(const bf::Frags& f, f32x16_t (&acc)[4][4], int g, int j) {
+  const int mb = bf::kGrpM[g], nb = bf::kGrpN[g] + j;
+  if (mb >= NMB) return;
+  const f32x16_t zero = {};
+  acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[nb], f.a[mb], FIRST ? zero : acc[mb][nb], 0, 0, 0);
+}
+
 // nsteps >= 1 slices.  issue(s, slot, i): load i of slice s into the slot at
 // that LDS address, i < kALoads of A, then 4 of B; slices at or past nsteps
 // must read zeros (their loads keep the count of outstanding loads the same
@@ -155,10 +164,13 @@ DEV void mainloop(const uint16_t* lds, uint32_t ring, int nsteps, Issue issue, f
   auto phase1 = [&](int s, auto first) __attribute__((always_inline)) {
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
-      if (g & 1) issue(s + NS - 2, addr(s + NS - 2), LA + (g >> 1));
       load_group<AL, BL, WTM>(f1, slot(s), 1, wm, wn, lane, g);
       __builtin_amdgcn_sched_barrier(0);
-      bf::mma2<NMB, decltype(first)::value>(f0, acc, g);
+      mma1<NMB, decltype(first)::value>(f0, acc, g, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (g & 1) issue(s + NS - 2, addr(s + NS - 2), LA + (g >> 1));
+      __builtin_amdgcn_sched_barrier(0);
+      mma1<NMB, decltype(first)::value>(f0, acc, g, 1);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -166,10 +178,13 @@ DEV void mainloop(const uint16_t* lds, uint32_t ring, int nsteps, Issue issue, f
     wait_vm_barrier<L*(NS - 3)>();  // slice s+1 landed; slot of slice s-1 free
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
-      if ((g & 1) && (g >> 1) < LA) issue(s + NS - 1, addr(s + NS - 1), g >> 1);
       load_group<AL, BL, WTM>(f0, slot(s + 1), 0, wm, wn, lane, g);
       __builtin_amdgcn_sched_barrier(0);
-      bf::mma2<NMB>(f1, acc, g);
+      mma1<NMB>(f1, acc, g, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if ((g & 1) && (g >> 1) < LA) issue(s + NS - 1, addr(s + NS - 1), g >> 1);
+      __builtin_amdgcn_sched_barrier(0);
+      mma1<NMB>(f1, acc, g, 1);
       __builtin_amdgcn_sched_barrier(0);
     }
   };

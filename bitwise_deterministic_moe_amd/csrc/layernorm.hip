@@ -50,20 +50,54 @@ DEV float row_sum(float v, float* s) {
 template <int TPR>
 constexpr int norm_threads = TPR > 256 ? TPR : 256;
 
-template <typename T, int TPR, int EPT>
+// Vector j of a row's `cols` elements, held by thread t of the row: loads give
+// zeros past the row (GUARD; without it the row fills every thread's
+// registers exactly, and no load or store is conditional).
+template <typename T, int TPR, bool GUARD>
+DEV typename Vec<T>::raw row_load(const T* p, int j, int t, int C) {
+  const int c = (j * TPR + t) * Vec<T>::N;
+  if constexpr (!GUARD) return Vec<T>::load(p + c, Vec<T>::N);
+  typename Vec<T>::raw r{};
+  if (c < C) r = Vec<T>::load(p + c, C - c);
+  return r;
+}
+template <typename T, int TPR, bool GUARD>
+DEV void row_store(T* p, int j, int t, int C, const float* v) {
+  const int c = (j * TPR + t) * Vec<T>::N;
+  if constexpr (!GUARD)
+    Vec<T>::store(p + c, v, Vec<T>::N);
+  else if (c < C)
+    Vec<T>::store(p + c, v, C - c);
+}
+// A weight that is not given is 1.
+template <typename T, int TPR, bool GUARD>
+DEV typename Vec<T>::raw weight_load(const void* w, int j, int t, int C) {
+  if (w) return row_load<T, TPR, GUARD>((const T*)w, j, t, C);
+  typename Vec<T>::raw r;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (sizeof(T) == 2)
+      r[q] = 0x3f803f80u;
+    else
+      r[q] = 1.f;
+  }
+  return r;
+}
+
+template <typename T, int TPR, int EPT, bool GUARD>
 __global__ __launch_bounds__(norm_threads<TPR>) void norm_fwd_kernel(NormParams P) {
   constexpr int NT = norm_threads<TPR>, V = Vec<T>::N, NV = EPT / V, RPB = NT / TPR;
   __shared__ float s_a[2][NT / kWave], s_b[2][NT / kWave];
   const int64_t units = (P.rows + RPB - 1) / RPB;
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-  const int C = P.cols;
+  const int C = GUARD ? P.cols : TPR * EPT;
   const float Cf = (float)C;
   typename Vec<T>::raw w[NV], b[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * TPR + t) * V;
-    if (P.weight && c < C) w[j] = Vec<T>::load((const T*)P.weight + c, C - c);
-    if (P.bias && c < C) b[j] = Vec<T>::load((const T*)P.bias + c, C - c);
+    w[j] = weight_load<T, TPR, GUARD>(P.weight, j, t, C);
+    b[j] = typename Vec<T>::raw{};
+    if (P.bias) b[j] = row_load<T, TPR, GUARD>((const T*)P.bias, j, t, C);
   }
   int odd = 0;
   for (int64_t i = blockIdx.x; i < units; i += gridDim.x, odd ^= 1) {
@@ -76,19 +110,10 @@ __global__ __launch_bounds__(norm_threads<TPR>) void norm_fwd_kernel(NormParams 
     float v[EPT];
     float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * V;
-      if (c < C) raw[j] = Vec<T>::load(xr + c, C - c);
-    }
+    for (int j = 0; j < NV; ++j) raw[j] = row_load<T, TPR, GUARD>(xr, j, t, C);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * V;
-      if (c < C) {
-        Vec<T>::get(raw[j], v + j * V);
-      } else {
-#pragma unroll
-        for (int q = 0; q < V; ++q) v[j * V + q] = 0.f;
-      }
+      Vec<T>::get(raw[j], v + j * V);
 #pragma unroll
       for (int q = 0; q < V; ++q) sum = sum + v[j * V + q];   // past the row: zeros
     }
@@ -96,18 +121,13 @@ __global__ __launch_bounds__(norm_threads<TPR>) void norm_fwd_kernel(NormParams 
     const float mean = row_sum<TPR>(sum, s_a[odd]) / Cf;
     float sq = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-{
+    for (int j = 0; j < NV; ++j) {
       const int c = (j * TPR + t) * V;
 #pragma unroll
-      for (int q = 0; q < V; ++q) v[j * V + q] = v[j * V + q] - mean;
-      if (c + V <= C) {
-#pragma unroll
-        for (int q = 0; q < V; ++q) sq = __builtin_fmaf(v[j * V + q], v[j * V + q], sq);
-      } else {
-#pragma unroll
-        for (int q = 0; q < V; ++q)
-          if (c + q < C) sq = __builtin_fmaf(v[j * V + q], v[j * V + q], sq);
+      for (int q = 0; q < V; ++q) {
+        v[j * V + q] = v[j * V + q] - mean;
+        const float d = GUARD && c + q >= C ? 0.f : v[j * V + q];
+        sq = __builtin_fmaf(d, d, sq);
       }
     }
     const float rstd = 1.f / sqrtf(row_sum<TPR>(sq, s_b[odd]) / Cf + P.eps);
@@ -115,22 +135,12 @@ __global__ __launch_bounds__(norm_threads<TPR>) void norm_fwd_kernel(NormParams 
     T* yr = (T*)P.y + row * C;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * V;
-      if (c >= C) continue;
-      float o[V], f[V];
+      float o[V], fw[V], fb[V];
+      Vec<T>::get(w[j], fw);
+      Vec<T>::get(b[j], fb);
 #pragma unroll
-      for (int q = 0; q < V; ++q) o[q] = v[j * V + q] * rstd;
-      if (P.weight) {
-        Vec<T>::get(w[j], f);
-#pragma unroll
-        for (int q = 0; q < V; ++q) o[q] = o[q] * f[q];
-      }
-      if (P.bias) {
-        Vec<T>::get(b[j], f);
-#pragma unroll
-        for (int q = 0; q < V; ++q) o[q] = o[q] + f[q];
-      }
-      Vec<T>::store(yr + c, o, C - c);
+      for (int q = 0; q < V; ++q) o[q] = __builtin_fmaf(v[j * V + q] * rstd, fw[q], fb[q]);
+      row_store<T, TPR, GUARD>(yr, j, t, C, o);
     }
     if (P.mean && t == 0) {
       P.mean[row] = mean;
@@ -141,7 +151,7 @@ __global__ __launch_bounds__(norm_threads<TPR>) void norm_fwd_kernel(NormParams 
 
 // Block u of P.blocks takes the rows [u rows / blocks, (u + 1) rows / blocks);
 // its row groups take them in turn.
-template <typename T, int TPR, int EPT>
+template <typename T, int TPR, int EPT, bool GUARD>
 __global__ __launch_bounds__(norm_threads<TPR>) void norm_bwd_kernel(NormParams P) {
   constexpr int NT = norm_threads<TPR>, V = Vec<T>::N, NV = EPT / V, RPB = NT / TPR;
   // the widest rows load the weight and the added gradient where they are
@@ -150,7 +160,7 @@ __global__ __launch_bounds__(norm_threads<TPR>) void norm_bwd_kernel(NormParams 
   __shared__ float s_a[2][NT / kWave], s_b[2][NT / kWave];
   __shared__ float s_col[RPB > 1 ? TPR * EPT : 1];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-  const int C = P.cols;
+  const int C = GUARD ? P.cols : TPR * EPT;
   const float Cf = (float)C;
   int64_t u = blockIdx.x;
   if (P.seed) {
@@ -159,10 +169,9 @@ __global__ __launch_bounds__(norm_threads<TPR>) void norm_bwd_kernel(NormParams 
   }
   const int64_t r0 = u * P.rows / P.blocks, r1 = (u + 1) * P.rows / P.blocks;
   typename Vec<T>::raw w[NV];
+  if constexpr (kHold) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * TPR + t) * V;
-    if (kHold && P.weight && c < C) w[j] = Vec<T>::load((const T*)P.weight + c, C - c);
+    for (int j = 0; j < NV; ++j) w[j] = weight_load<T, TPR, GUARD>(P.weight, j, t, C);
   }
   float dw[EPT], db[EPT];
 #pragma unroll
@@ -178,34 +187,35 @@ __global__ __launch_bounds__(norm_threads<TPR>) void norm_bwd_kernel(NormParams 
     const T* ar = P.add ? (const T*)P.add + rr * P.ldadd : nullptr;
     typename Vec<T>::raw rx[NV], rg[NV], ra[NV];
     const float mean = P.mean[rr], rstd = P.rstd[rr];
+    if constexpr (kHold) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * V;
-      if (c < C) {
-        rx[j] = Vec<T>::load(xr + c, C - c);
-        rg[j] = Vec<T>::load(gr + c, C - c);
-        if (kHold && ar) ra[j] = Vec<T>::load(ar + c, C - c);
+      for (int j = 0; j < NV; ++j) {
+        rx[j] = row_load<T, TPR, GUARD>(xr, j, t, C);
+        rg[j] = row_load<T, TPR, GUARD>(gr, j, t, C);
       }
     }
-    float s1 = 0.f, s2 = 0.f;
+    if (kHold && ar) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) ra[j] = row_load<T, TPR, GUARD>(ar, j, t, C);
+    }
+    // past the row dy = 0 and the weight are 0, which adds nothing
+    float h[EPT], dh[EPT], s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * V;
-      if (c >= C) continue;
       float x[V], g[V], f[V];
-      Vec<T>::get(rx[j], x);
-      Vec<T>::get(rg[j], g);
-      if (P.weight) Vec<T>::get(kHold ? w[j] : Vec<T>::load((const T*)P.weight + c, C - c), f);
+      Vec<T>::get(kHold ? rx[j] : row_load<T, TPR, GUARD>(xr, j, t, C), x);
+      Vec<T>::get(kHold ? rg[j] : row_load<T, TPR, GUARD>(gr, j, t, C), g);
+      Vec<T>::get(kHold ? w[j] : weight_load<T, TPR, GUARD>(P.weight, j, t, C), f);
 #pragma unroll
       for (int q = 0; q < V; ++q) {
-        // past the row g = 0, which adds nothing
-        const float h = (x[q] - mean) * rstd;
-        const float dh = P.weight ? g[q] * f[q] : g[q];
-        s1 = s1 + dh;
-        s2 = __builtin_fmaf(dh, h, s2);
-        if (live) {
-          dw[j * V + q] = __builtin_fmaf(g[q], h, dw[j * V + q]);
-          db[j * V + q] = db[j * V + q] + g[q];
+        const int e = j * V + q;
+        h[e] = (x[q] - mean) * rstd;
+        dh[e] = g[q] * f[q];
+        s1 = s1 + dh[e];
+        s2 = __builtin_fmaf(dh[e], h[e], s2);
+        if (RPB == 1 || live) {
+          dw[e] = __builtin_fmaf(g[q], h[e], dw[e]);
+          db[e] = db[e] + g[q];
         }
       }
     }
@@ -215,24 +225,19 @@ __global__ __launch_bounds__(norm_threads<TPR>) void norm_bwd_kernel(NormParams 
     T* dr = (T*)P.y + row * C;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * V;
-      if (c >= C) continue;
-      float x[V], g[V], f[V], o[V];
-      Vec<T>::get(rx[j], x);
-      Vec<T>::get(rg[j], g);
-      if (P.weight) Vec<T>::get(kHold ? w[j] : Vec<T>::load((const T*)P.weight + c, C - c), f);
+      float o[V];
 #pragma unroll
       for (int q = 0; q < V; ++q) {
-        const float h = (x[q] - mean) * rstd;
-        const float dh = P.weight ? g[q] * f[q] : g[q];
-        o[q] = (dh - m1 - h * m2) * rstd;
+        const int e = j * V + q;
+        o[q] = (dh[e] - m1 - h[e] * m2) * rstd;
       }
       if (ar) {
-        Vec<T>::get(kHold ? ra[j] : Vec<T>::load(ar + c, C - c), f);
+        float f[V];
+        Vec<T>::get(kHold ? ra[j] : row_load<T, TPR, GUARD>(ar, j, t, C), f);
 #pragma unroll
         for (int q = 0; q < V; ++q) o[q] = o[q] + f[q];
       }
-      Vec<T>::store(dr + c, o, C - c);
+      row_store<T, TPR, GUARD>(dr, j, t, C, o);
     }
   }
   if (!P.part) return;
@@ -306,18 +311,25 @@ int norm_bwd_blocks(int64_t rows, int64_t cols, bool bf16) {
   return (int)(b < 1 ? 1 : b > kNormBlocks ? kNormBlocks : b);
 }
 
+template <typename T, int TPR, int EPT, bool GUARD>
+static void norm_launch_as(const NormParams& P, bool bwd, unsigned blocks, hipStream_t st) {
+  if (bwd)
+    norm_bwd_kernel<T, TPR, EPT, GUARD><<<blocks, norm_threads<TPR>, 0, st>>>(P);
+  else
+    norm_fwd_kernel<T, TPR, EPT, GUARD><<<blocks, norm_threads<TPR>, 0, st>>>(P);
+}
+
 template <typename T, int TPR, int EPT>
 static hipError_t norm_launch(const NormParams& P, bool bwd, hipStream_t st) {
   constexpr int NT = norm_threads<TPR>, RPB = NT / TPR;
-  if (bwd) {
-    norm_bwd_kernel<T, TPR, EPT><<<P.blocks, NT, 0, st>>>(P);
-  } else {
-    // a block takes several rows only when every CU already holds 8 waves
-    // a SIMD: then the weight stays in registers
-    const int64_t units = (P.rows + RPB - 1) / RPB;
-    const int64_t most = 2048 * 256 / NT;
-    norm_fwd_kernel<T, TPR, EPT><<<(unsigned)(units < most ? units : most), NT, 0, st>>>(P);
-  }
+  // a forward block takes several rows only when every CU already holds 8
+  // waves a SIMD: then the weight stays in registers
+  const int64_t units = (P.rows + RPB - 1) / RPB, most = 2048 * 256 / NT;
+  const unsigned blocks = bwd ? P.blocks : (unsigned)(units < most ? units : most);
+  if (P.cols == TPR * EPT)
+    norm_launch_as<T, TPR, EPT, false>(P, bwd, blocks, st);
+  else
+    norm_launch_as<T, TPR, EPT, true>(P, bwd, blocks, st);
   return hipGetLastError();
 }
 
