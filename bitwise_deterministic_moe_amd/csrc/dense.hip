@@ -68,18 +68,28 @@ DEV int64_t up8(int64_t n) { return (n + 7) & ~(int64_t)7; }
 
 DEV void dense_lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// Only the copy into LDS is written out per pass (its registers are fixed);
+// the rest is one loop body: unrolled, the kernels took 50 to 67 KB of code, about the
+// whole instruction cache, run through once.
 template <int FORM, int WTM>
 DEV void dense_store_tile(const DenseParams& P, const DenseTile& t, float* stage, f32x16_t (&acc)[4][4], int wm, int wn,
                           int lane, int wave) {
   const int r32 = lane & 31, half = lane >> 5;
   const int rows = (int)(P.M - t.m0 < 2 * WTM ? P.M - t.m0 : 2 * WTM);
+  const int64_t end = t.m0 + rows;
+  // a thread's four columns, and so its bias, are the same in every row
+  float bias[4] = {0.f, 0.f, 0.f, 0.f};
+  if (FORM == kFormLinear && P.bias && P.S == 1 && t.n0 + lane * 4 < P.N)
+    get4((const uint16_t*)P.bias + t.n0 + lane * 4, P.N - t.n0 - lane * 4, bias);
+#pragma unroll 1
+  for (int p = 0; 64 * p < rows; ++p) {
 #pragma unroll
-  for (int p = 0; p < 2 * WTM / 64; ++p) {
-    if (64 * p >= rows) break;
+    for (int q = 0; q < 2 * WTM / 64; ++q) {
+      if (p != q) continue;
 #pragma unroll
-    for (int mb = 0; mb < WTM / 32; ++mb) {
-      const int r0 = wm * WTM + mb * 32 - 64 * p;
-      if (r0 >= 0 && r0 < 64) {
+      for (int mb = 0; mb < WTM / 32; ++mb) {
+        const int r0 = wm * WTM + mb * 32 - 64 * q;
+        if (r0 < 0 || r0 >= 64) continue;
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
@@ -94,7 +104,6 @@ DEV void dense_store_tile(const DenseParams& P, const DenseTile& t, float* stage
       }
     }
     dense_lds_barrier();
-    const int64_t end = t.m0 + rows;
     if constexpr (FORM == kFormGlu) {
       // two rows per wave and step: lanes 0..31 one, lanes 32..63 the next
       const int c = (lane & 31) * 4, col = t.n0 + c;
@@ -113,16 +122,12 @@ DEV void dense_store_tile(const DenseParams& P, const DenseTile& t, float* stage
           }
         }
         if (col >= P.N) continue;
-        const int64_t row = t.m0 + 64 * p + m;
+        const AtRows at{t.m0 + 64 * p + m, end, 8, col};
         if (P.S > 1) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (row + 8 * i < end) {
-              part4(P, t.chunk, 0, row + 8 * i, col, {g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]});
-              part4(P, t.chunk, 1, row + 8 * i, col, {u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]});
-            }
+          part<4>(P, t.chunk, 0, at, g);
+          part<4>(P, t.chunk, 1, at, u);
         } else {
-          emit_rows_glu<uint16_t, 4>(P, row, 8, end, col, g, u);
+          emit_glu<uint16_t, 4, true>(P, at, g, u);
         }
       }
     } else {
@@ -135,18 +140,14 @@ DEV void dense_store_tile(const DenseParams& P, const DenseTile& t, float* stage
         for (int i = 0; i < 4; ++i) {
           const f32x4_t sv = *(const f32x4_t*)(stage + (m + 4 * i) * kDenseStageRow + c);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[4 * i + q] = sv[q];
+          for (int q = 0; q < 4; ++q) v[4 * i + q] = FORM == kFormLinear ? sv[q] + bias[q] : sv[q];
         }
         if (col >= P.N) continue;
-        const int64_t row = t.m0 + 64 * p + m;
-        if (P.S > 1) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (row + 4 * i < end)
-              part4(P, t.chunk, t.seg, row + 4 * i, col, {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]});
-        } else {
-          emit_rows<uint16_t, FORM, 4>(P, t.seg, row, 4, end, col, v);
-        }
+        const AtRows at{t.m0 + 64 * p + m, end, 4, col};
+        if (P.S > 1)
+          part<4>(P, t.chunk, t.seg, at, v);
+        else
+          emit<uint16_t, FORM, 4, true, true>(P, t.seg, at, v);
       }
     }
     dense_lds_barrier();
@@ -178,7 +179,7 @@ __global__ __launch_bounds__(256) void dense_bf16_kernel(DenseParams P) {
     ob.init((const uint16_t*)P.b[0] + k0 * P.ldb + t.seg * P.seg + t.n0, ((kn - 1) * P.ldb + up8(nvalid)) * 2, wave,
             lane, nvalid, P.ldb);
     const uint32_t sa = (uint32_t)(dn::BK * P.lda * 2), sb = (uint32_t)(dn::BK * P.ldb * 2);
-    dn::mainloop<dn::MNC, dn::MNC, WTM>(lds, ring, nsteps, [&](int s, uint32_t st, int i) {
+    dn::mainloop<dn::MNC, dn::MNC, WTM>(ring, nsteps, [&](int s, uint32_t st, int i) {
       if (i < LA)
         oa.issue(st, wave, i, (uint32_t)s * sa);
       else
@@ -195,7 +196,7 @@ __global__ __launch_bounds__(256) void dense_bf16_kernel(DenseParams P) {
       const int64_t eb = ((int64_t)(nvalid < 256 ? nvalid - 1 : 255) * P.ldb + up8(P.K)) * 2;
       ob.init((const uint16_t*)P.b[0] + (int64_t)t.n0 * P.ldb, eb, wave, lane, nvalid, P.ldb);
       ob1.rs = bf::make_rsrc((const uint16_t*)P.b[P.nseg - 1] + (int64_t)t.n0 * P.ldb, (uint32_t)eb);
-      dn::mainloop<dn::KC, dn::KC, WTM>(lds, ring, nsteps, [&](int s, uint32_t st, int i) {
+      dn::mainloop<dn::KC, dn::KC, WTM>(ring, nsteps, [&](int s, uint32_t st, int i) {
         const bool live = s < nsteps;
         int ks = live ? t.s0 + s : 0;
         const bool second = ks >= steps_seg;
@@ -222,7 +223,7 @@ __global__ __launch_bounds__(256) void dense_bf16_kernel(DenseParams P) {
       if constexpr (FORM == kFormLinear) {
         dn::MncOp<256, 4> ob;
         ob.init((const uint16_t*)P.b[0] + k0 * P.ldb + t.n0, ((kn - 1) * P.ldb + up8(nvalid)) * 2, wave, lane, nvalid, P.ldb);
-        dn::mainloop<dn::KC, dn::MNC, WTM>(lds, ring, nsteps, [&](int s, uint32_t st, int i) {
+        dn::mainloop<dn::KC, dn::MNC, WTM>(ring, nsteps, [&](int s, uint32_t st, int i) {
           if (i < LA)
             issue_a(s, st, i);
           else
@@ -233,7 +234,7 @@ __global__ __launch_bounds__(256) void dense_bf16_kernel(DenseParams P) {
         const int64_t e = ((kn - 1) * P.ldb + up8(nvalid)) * 2;
         og.init((const uint16_t*)P.b[0] + k0 * P.ldb + t.n0, e, wave, lane, nvalid, P.ldb);
         ou.init((const uint16_t*)P.b[1] + k0 * P.ldb + t.n0, e, wave, lane, nvalid, P.ldb);
-        dn::mainloop<dn::KC, dn::GLU, WTM>(lds, ring, nsteps, [&](int s, uint32_t st, int i) {
+        dn::mainloop<dn::KC, dn::GLU, WTM>(ring, nsteps, [&](int s, uint32_t st, int i) {
           if (i < LA)
             issue_a(s, st, i);
           else if (i < LA + 2)
@@ -433,45 +434,39 @@ __global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
   }
   if (s < t.s1) step(s, J0{}, J2{});
   if (s + 1 < t.s1) step(s + 1, J1{}, J0{});
-  // lane l holds row l % 32 and columns 8 i + 4 (l / 32) + 0..3 of each block
+  // lane l holds row l % 32 and columns 8 i + 4 (l / 32) + 0..3 of each
+  // block; one loop body for all blocks, whose registers are picked by
+  // uniform branches
+#pragma unroll 1
+  for (int b = 0; b < (FORM == kFormGlu ? MB : MB * NB); ++b) {
+    float v[16], u[16];
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
+    for (int c = 0; c < MB * NB; ++c) {
+      if (FORM == kFormGlu ? c / NB != b : c != b) continue;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        if (FORM == kFormGlu && c % NB == 1)
+          u[r] = acc[c / NB][c % NB][r];
+        else
+          v[r] = acc[c / NB][c % NB][r];
+      }
+    }
+    const int mb = FORM == kFormGlu ? b : b / NB, nb = FORM == kFormGlu ? 0 : b % NB;
     const int m = (wm * MB + mb) * 32 + r32;
     if (m >= mvalid) continue;
-    const int64_t row = t.m0 + m;
+    const AtCols at{t.m0 + m, 8, t.n0 + (FORM == kFormGlu ? wn * 32 : (wn * NB + nb) * 32) + 4 * half};
     if constexpr (FORM == kFormGlu) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int col = t.n0 + wn * 32 + 8 * i + 4 * half;
-        if (col >= P.N) continue;
-        float g[4], u[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          g[q] = acc[mb][0][4 * i + q];
-          u[q] = acc[mb][NB - 1][4 * i + q];
-        }
-        if (P.S > 1) {
-          part4(P, t.chunk, 0, row, col, g);
-          part4(P, t.chunk, 1, row, col, u);
-        } else {
-          emit4_glu<float>(P, row, col, g, u);
-        }
+      if (P.S > 1) {
+        part<4>(P, t.chunk, 0, at, v);
+        part<4>(P, t.chunk, 1, at, u);
+      } else {
+        emit_glu<float, 4, true>(P, at, v, u);
       }
     } else {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = t.n0 + (wn * NB + nb) * 32 + 8 * i + 4 * half;
-          if (col >= P.N) continue;
-          float v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = acc[mb][nb][4 * i + q];
-          if (P.S > 1)
-            part4(P, t.chunk, t.seg, row, col, v);
-          else
-            emit4<float, FORM>(P, t.seg, row, col, v);
-        }
+      if (P.S > 1)
+        part<4>(P, t.chunk, t.seg, at, v);
+      else
+        emit<float, FORM, 4, true, false>(P, t.seg, at, v);
     }
   }
 }
@@ -752,35 +747,56 @@ __global__ __launch_bounds__(256) void dense_ew_kernel(DenseEwParams P) {
   float sum[V];
 #pragma unroll
   for (int q = 0; q < V; ++q) sum[q] = 0.f;
-  if (no > 0) {
-#pragma unroll 4
-    for (int64_t row = r0 + wave; row < r1; row += 4) {
-      float d[V], o0[V], o1[V];
+  // R rows at a time, loaded before any is used; a wave's columns are whole
+  // except in the last column tile
+  constexpr int R = 2;
+  auto rows = [&](int64_t row, int count, auto WHOLE) __attribute__((always_inline)) {
+    constexpr bool whole = decltype(WHOLE)::value;
+    float d[R][V], z[R][V], u[R][V];
 #pragma unroll
-      for (int q = 0; q < V; ++q) o0[q] = o1[q] = 0.f;
-      if (n > 0) {
-        Vec<T>::get(Vec<T>::load((const T*)P.dy + row * P.lddy + col, n), d);
-        if (need_z) {
-          float z[V], u[V];
-          load_z<Z, V>((const Z*)P.z[0] + row * P.ldz + col, n, z);
-          if (GLU) load_z<Z, V>((const Z*)P.z[1] + row * P.ldz + col, n, u);
+    for (int i = 0; i < R; ++i) {
 #pragma unroll
-          for (int q = 0; q < V; ++q) {
-            float v, dv;
-            act_df(P.act, z[q], v, dv);
-            o0[q] = GLU ? d[q] * u[q] * dv : d[q] * dv;
-            o1[q] = d[q] * v;
-          }
-        } else {
+      for (int q = 0; q < V; ++q) d[i][q] = z[i][q] = u[i][q] = 0.f;
+      if (i >= count || (!whole && n <= 0)) continue;
+      const int64_t r = row + 4 * i;
+      const int m = whole ? V : n;
+      Vec<T>::get(Vec<T>::load((const T*)P.dy + r * P.lddy + col, m), d[i]);
+      if (need_z) load_z<Z, V>((const Z*)P.z[0] + r * P.ldz + col, m, z[i]);
+      if (GLU) load_z<Z, V>((const Z*)P.z[1] + r * P.ldz + col, m, u[i]);
+    }
 #pragma unroll
-          for (int q = 0; q < V; ++q) o0[q] = d[q];
+    for (int i = 0; i < R; ++i) {
+      if (i >= count) continue;
+      // past the row every load gave 0, and act(0) or act'(0) times 0 is 0
+      float o0[V], o1[V];
+      if (need_z) {
+        float v[V], dv[V];
+        act_df_n<V>(P.act, z[i], v, dv);
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          o0[q] = GLU ? d[i][q] * u[i][q] * dv[q] : d[i][q] * dv[q];
+          o1[q] = d[i][q] * v[q];
         }
-        // past the row every load gave 0; act(0) or act'(0) times 0 is 0
+      } else {
+#pragma unroll
+        for (int q = 0; q < V; ++q) o0[q] = o1[q] = d[i][q];
       }
+      const int64_t at = (row + 4 * i) * P.ldo + col;
+      const int m = whole ? V : no;
 #pragma unroll
       for (int q = 0; q < V; ++q) sum[q] = sum[q] + o0[q];
-      if (P.out[0]) Vec<T>::store((T*)P.out[0] + row * P.ldo + col, o0, no);
-      if (GLU) Vec<T>::store((T*)P.out[1] + row * P.ldo + col, o1, no);
+      if (P.out[0]) Vec<T>::store((T*)P.out[0] + at, o0, m);
+      if (GLU) Vec<T>::store((T*)P.out[1] + at, o1, m);
+    }
+  };
+  if (no > 0) {
+    const bool whole = (col - lane * V) + CT <= P.cols;   // uniform
+    int64_t row = r0 + wave;
+    if (whole) {
+      for (; row + 4 * (R - 1) < r1; row += 4 * R) rows(row, R, std::true_type{});
+      for (; row < r1; row += 4) rows(row, 1, std::true_type{});
+    } else {
+      for (; row < r1; row += 4) rows(row, 1, std::false_type{});
     }
   }
   if (GLU || !P.part) return;

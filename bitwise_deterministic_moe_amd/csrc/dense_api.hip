@@ -63,13 +63,13 @@ constexpr int64_t kMaxPartialBytes = (int64_t)1 << 30;
 // slice of a workgroup that has a CU to itself, `busy` per slice and workgroup
 // of a CU that several share (a bf16 tile fills a CU: they follow each
 // other), `fixed` once (launch, first slice, epilogue).
-//   bf16     256 rows: 0.82 (8192^3) to 1.0; 128 rows: 0.52 (4096 x 8192 x 2048)
+//   bf16     256 rows: 0.77 (8192^3) to 0.85; 128 rows: 0.48 (4096 x 8192 x 2048)
 //   float32  128 x 128: 1.06 busy (4096^3), 64 x 64: 0.27
 struct TileCost {
   int bm;
   double alone, busy, fixed;
 };
-constexpr TileCost kBf16Tiles[2] = {{256, 0.9, 0.9, 10.0}, {128, 0.52, 0.52, 8.0}};
+constexpr TileCost kBf16Tiles[2] = {{256, 0.8, 0.8, 9.0}, {128, 0.48, 0.48, 8.0}};
 constexpr TileCost kF32Tiles[2] = {{128, 1.3, 1.06, 7.0}, {64, 0.38, 0.27, 6.0}};
 
 double estimate(const TileCost& c, int64_t wgs, int64_t steps, double width, int64_t S, double out_elems) {

@@ -38,38 +38,58 @@ constexpr int kALoads = WTM / 32;                // 16-byte loads per thread of 
 
 DEV int mnc128_off(int k, int mn) { return k * 128 + (((mn >> 3) ^ ((k & 3) << 2)) << 3) + (mn & 7); }
 
-template <int W>
-DEV bf16x8_t frag_mnc_w(const uint16_t* s, int col_base, int kk, int lane) {
-  const int g = lane >> 4, i = lane & 15;
-  const int k = kk * 16 + 8 * (g >> 1) + (i >> 2);
-  const int mn = col_base + 16 * (g & 1) + 4 * (i & 3);
-  const int o0 = W == 256 ? bf::mnc_off(k, mn) : mnc128_off(k, mn);
-  const int o1 = W == 256 ? bf::mnc_off(k + 4, mn) : mnc128_off(k + 4, mn);
-  bf::v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS bf::v4i16*)(s + o0));
-  bf::v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS bf::v4i16*)(s + o1));
-  const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
-  return __builtin_bit_cast(bf16x8_t, u32x4_t{l2[0], l2[1], h2[0], h2[1]});
-}
-
-// A block mb of the wave row wm
-template <int AL, int WTM>
-DEV bf16x8_t frag_a(const uint16_t* s, int wm, int mb, int kk, int lane) {
-  const int r = wm * WTM + mb * 32;
-  if constexpr (AL == KC)
-    return bf::frag_kc(s, r + (lane & 31), kk, lane);
-  else
-    return frag_mnc_w<2 * WTM>(s, r, kk, lane);
-}
-// B block nb of the wave column wn
-template <int BL>
-DEV bf16x8_t frag_b(const uint16_t* s, int wn, int nb, int kk, int lane) {
-  if constexpr (BL == KC)
-    return bf::frag_kc(s, wn * 128 + nb * 32 + (lane & 31), kk, lane);
-  else if constexpr (BL == MNC)
-    return frag_mnc_w<256>(s, wn * 128 + nb * 32, kk, lane);
-  else
-    return frag_mnc_w<128>(s + (nb >> 1) * (128 * BK), wn * 64 + (nb & 1) * 32, kk, lane);
-}
+// Fragment read addresses of one operand.  Per lane, the LDS byte addresses
+// of the reads that differ by more than a constant, in ring slot 0 (s0)
+// and in slot 2 (s1); every read is one of them plus a constant that fits the
+// instruction's 16-bit offset (slot parity, k half, block), so the loop,
+// unrolled over the 4 slots, spends no instruction on addresses.  The second
+// set goes through an asm add so that it stays in registers.
+//  KC   the two k halves (the swizzle is the same for rows 32 apart)
+//  MNC  rows k and k + 4 of each 32-column block
+//  GLU  rows k and k + 4 of the two blocks of a matrix; wu 8 KiB past wg
+template <int L, int NBLK>
+struct FragAddr {
+  static constexpr int N = L == KC ? 2 : L == MNC ? 2 * NBLK : 4;
+  uint32_t s0[N], s1[N];
+  template <int W>
+  DEV static uint32_t mnc_at(int col, int lane, int hi) {
+    const int g = lane >> 4, i = lane & 15;
+    const int k = 8 * (g >> 1) + (i >> 2) + 4 * hi, mn = col + 16 * (g & 1) + 4 * (i & 3);
+    return 2u * (uint32_t)(W == 256 ? bf::mnc_off(k, mn) : mnc128_off(k, mn));
+  }
+  // base: byte address of the operand in slot 0; first: first row or column of
+  // the wave's blocks; W: columns of an MNC tile
+  template <int W>
+  DEV void init(uint32_t base, int first, int lane, uint32_t two_slots) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if constexpr (L == KC)
+        s0[j] = base + 2u * (uint32_t)bf::kc_off(first + (lane & 31), 2 * j + (lane >> 5));
+      else
+        s0[j] = base + mnc_at<W>(first + 32 * (j >> 1), lane, j & 1);
+      asm("v_add_u32 %0, %2, %1" : "=v"(s1[j]) : "v"(s0[j]), "s"(two_slots));
+    }
+  }
+  // block b, k half kk, in slot sl (constants); slot: bytes of a slot
+  template <int W, int SLOT_BYTES>
+  DEV bf16x8_t read(int b, int kk, int sl) const {
+    const uint32_t* set = sl >= 2 ? s1 : s0;
+    const uint32_t so = (uint32_t)(sl & 1) * SLOT_BYTES;
+    if constexpr (L == KC) {
+      const LDS_AS char* p = (const LDS_AS char*)(uintptr_t)set[kk];
+      return __builtin_bit_cast(bf16x8_t, *(const LDS_AS u32x4_t*)(p + so + (uint32_t)b * 2048u));
+    } else {
+      const int j = L == GLU ? 2 * (b & 1) : 2 * b;
+      const uint32_t off = so + (uint32_t)kk * (16u * W * 2u) + (L == GLU ? (uint32_t)(b >> 1) * 8192u : 0u);
+      const LDS_AS char* plo = (const LDS_AS char*)(uintptr_t)set[j];
+      const LDS_AS char* phi = (const LDS_AS char*)(uintptr_t)set[j + 1];
+      bf::v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS bf::v4i16*)(plo + off));
+      bf::v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS bf::v4i16*)(phi + off));
+      const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
+      return __builtin_bit_cast(bf16x8_t, u32x4_t{l2[0], l2[1], h2[0], h2[1]});
+    }
+  }
+};
 
 // ------------------------------------------------------------------ loaders
 // K-contiguous operand of ROWS tile rows (rows of `cols` readable elements):
@@ -122,13 +142,23 @@ DEV void wait_vm_barrier() {
 }
 
 template <int AL, int BL, int WTM>
-DEV void load_group(bf::Frags& f, const uint16_t* slot, int kk, int wm, int wn, int lane, int g) {
-  if (bf::kGrpA[g] >= 0) {
-    if (bf::kGrpA[g] < WTM / 32) f.a[bf::kGrpA[g]] = frag_a<AL, WTM>(slot, wm, bf::kGrpA[g], kk, lane);
-  } else {
-    f.b[bf::kGrpB[g]] = frag_b<BL>(slot + kAOper<WTM>, wn, bf::kGrpB[g], kk, lane);
+struct TileAddr {
+  static constexpr int WB = BL == GLU ? 128 : 256, SB = kSlot<WTM> * 2;
+  FragAddr<AL, WTM / 32> a;
+  FragAddr<BL, 4> b;
+  DEV void init(uint32_t ring, int wm, int wn, int lane) {
+    a.template init<2 * WTM>(ring, wm * WTM, lane, 2u * SB);
+    b.template init<WB>(ring + kAOper<WTM> * 2, wn * (BL == GLU ? 64 : 128), lane, 2u * SB);
   }
-}
+  // the fragment that group g of the phase reads (bf::kGrpA, kGrpB)
+  DEV void load(bf::Frags& f, int kk, int sl, int g) const {
+    if (bf::kGrpA[g] >= 0) {
+      if (bf::kGrpA[g] < WTM / 32) f.a[bf::kGrpA[g]] = a.template read<2 * WTM, SB>(bf::kGrpA[g], kk, sl);
+    } else {
+      f.b[bf::kGrpB[g]] = b.template read<WB, SB>(bf::kGrpB[g], kk, sl);
+    }
+  }
+};
 
 // One of the two products of group g (bf::mma2).
 template <int NMB, bool FIRST = false>
@@ -146,55 +176,68 @@ DEV void mma1(const bf::Frags& f, f32x16_t (&acc)[4][4], int g, int j) {
 // B loads of slice s + 2 go out while k-half 0 is multiplied; then slice s + 1
 // has landed, and the A loads of slice s + 3 go out while k-half 1 is.
 template <int AL, int BL, int WTM, class Issue>
-DEV void mainloop(const uint16_t* lds, uint32_t ring, int nsteps, Issue issue, f32x16_t (&acc)[4][4], int wm, int wn,
-                  int lane) {
-  constexpr int LA = kALoads<WTM>, L = LA + 4, NMB = WTM / 32, SLOT = kSlot<WTM>;
-  auto slot = [&](int s) { return lds + (s % NS) * SLOT; };
-  auto addr = [&](int s) { return ring + (uint32_t)(s % NS) * (SLOT * 2); };
+DEV void mainloop(uint32_t ring, int nsteps, Issue issue, f32x16_t (&acc)[4][4], int wm, int wn, int lane) {
+  constexpr int LA = kALoads<WTM>, L = LA + 4, NMB = WTM / 32, SB = kSlot<WTM> * 2;
+  static_assert(NS == 4, "the unrolling over the slots");
+  auto addr = [&](int sl) { return ring + (uint32_t)sl * SB; };
 #pragma unroll
   for (int s = 0; s < NS - 2; ++s)
 #pragma unroll
     for (int i = 0; i < L; ++i) issue(s, addr(s), i);
 #pragma unroll
   for (int i = 0; i < LA; ++i) issue(NS - 2, addr(NS - 2), i);
+  TileAddr<AL, BL, WTM> ta;
+  ta.init(ring, wm, wn, lane);
   wait_vm_barrier<L*(NS - 3) + LA>();  // slice 0 landed
   bf::Frags f0, f1;
 #pragma unroll
-  for (int g = 0; g < 8; ++g) load_group<AL, BL, WTM>(f0, lds, 0, wm, wn, lane, g);
-  auto phase1 = [&](int s, auto first) __attribute__((always_inline)) {
+  for (int g = 0; g < 8; ++g) ta.load(f0, 0, 0, g);
+  // step s in slot sl = s % 4
+  auto phase1 = [&](int s, auto first, int sl) __attribute__((always_inline)) {
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
-      load_group<AL, BL, WTM>(f1, slot(s), 1, wm, wn, lane, g);
+      ta.load(f1, 1, sl, g);
       __builtin_amdgcn_sched_barrier(0);
       mma1<NMB, decltype(first)::value>(f0, acc, g, 0);
       __builtin_amdgcn_sched_barrier(0);
-      if (g & 1) issue(s + NS - 2, addr(s + NS - 2), LA + (g >> 1));
+      if (g & 1) issue(s + NS - 2, addr((sl + 2) % NS), LA + (g >> 1));
       __builtin_amdgcn_sched_barrier(0);
       mma1<NMB, decltype(first)::value>(f0, acc, g, 1);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto phase2 = [&](int s) __attribute__((always_inline)) {
+  auto phase2 = [&](int s, int sl) __attribute__((always_inline)) {
     wait_vm_barrier<L*(NS - 3)>();  // slice s+1 landed; slot of slice s-1 free
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
-      load_group<AL, BL, WTM>(f0, slot(s + 1), 0, wm, wn, lane, g);
+      ta.load(f0, 0, (sl + 1) % NS, g);
       __builtin_amdgcn_sched_barrier(0);
       mma1<NMB>(f1, acc, g, 0);
       __builtin_amdgcn_sched_barrier(0);
-      if ((g & 1) && (g >> 1) < LA) issue(s + NS - 1, addr(s + NS - 1), g >> 1);
+      if ((g & 1) && (g >> 1) < LA) issue(s + NS - 1, addr((sl + 3) % NS), g >> 1);
       __builtin_amdgcn_sched_barrier(0);
       mma1<NMB>(f1, acc, g, 1);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   // past the last slice the next slot holds zeros, read and never multiplied
-  phase1(0, bf::BoolC<true>{});
-  phase2(0);
+  phase1(0, bf::BoolC<true>{}, 0);
+  phase2(0, 0);
+  int s = 1;
 #pragma unroll 1
-  for (int s = 1; s < nsteps; ++s) {
-    phase1(s, bf::BoolC<false>{});
-    phase2(s);
+  for (; s + NS <= nsteps; s += NS) {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      phase1(s + j, bf::BoolC<false>{}, (1 + j) % NS);
+      phase2(s + j, (1 + j) % NS);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NS - 1; ++j) {
+    if (s + j < nsteps) {
+      phase1(s + j, bf::BoolC<false>{}, (1 + j) % NS);
+      phase2(s + j, (1 + j) % NS);
+    }
   }
   bf::block_barrier();
 }

@@ -25,6 +25,16 @@ One train step on the layer (all device work through the library's C ABI):
     dlogits, dwr, dx_router = moe_router_bwd(dprob)
     SGD on the float32 masters of W1, W2, wr; bf16 (or f32) runtime copies
     rebuilt by the same kernel (moe_sgd_step).
+With block=True the step covers the dense operators around the layer too: a
+layer norm in front of the experts, a gated shared expert beside them, and
+its down projection into the routed output:
+    xn = moe_layernorm_fwd(x)                   (the router reads x)
+    ym = moe_fwd(logits, xn, W1, W2)
+    a = moe_glu_fwd(xn, Wg, Wu);  y = moe_linear_fwd(a, Wd, bd, residual=ym)
+    da, dWd, dbd = moe_linear_bwd(dy, a, Wd)
+    dxm = moe_bwd_dgrad_dprob(dy);  dxn = moe_glu_bwd(da, xn, dx_add=dxm)
+    dx = moe_layernorm_bwd(dxn, x, dx_add=dx_router)
+and SGD on their masters.
 With mx=True (bf16 layers) every expert GEMM runs on MXFP8 operands: the
 routing stage alone (moe_route), then moe_mx_fwd_fc1 / moe_mx_fwd_fc2 on x,
 act and the transposed weights (moe_mx_quantize, moe_mx_quantize_t), the
@@ -46,10 +56,12 @@ import numpy as np
 import torch
 
 from . import (MXW_ACT_P, MXW_ROW, MXW_TOKEN, MoeError, Problem, TORCH_DTYPE, moe_bwd_dgrad_dprob,
-               moe_bwd_wgrad, moe_fingerprint, moe_fwd, moe_mx_dgrad_fc1, moe_mx_dgrad_fc2, moe_mx_fwd_fc1,
+               moe_bwd_wgrad, moe_fingerprint, moe_fwd, moe_glu_bwd, moe_glu_fwd, moe_layernorm_bwd, moe_layernorm_fwd,
+               moe_linear_bwd, moe_linear_fwd, moe_mx_dgrad_fc1, moe_mx_dgrad_fc2, moe_mx_fwd_fc1,
                moe_mx_fwd_fc2, moe_mx_quantize, moe_mx_quantize_t, moe_mx_quantize_wgrad, moe_mx_wgrad,
                moe_nvfp4_quantize, moe_route, moe_router_bwd, moe_router_fwd, moe_sgd_step)
 
+BLOCK_WEIGHTS = ("nw", "nb", "wg", "wu", "wd", "bd")   # the dense operators' masters (block=True)
 LEVELS = {"metrics": 0, "phases": 1, "ops": 2}
 
 
@@ -150,20 +162,23 @@ class TrainState:
     @staticmethod
     def load(path: str, prob: Problem) -> "TrainState":
         with np.load(path, allow_pickle=False) as z:
-            master = {n: torch.from_numpy(z[n].copy()).cuda() for n in ("w1", "w2", "wr")}
+            names = [n for n in ("w1", "w2", "wr") + BLOCK_WEIGHTS if n in z.files]
+            master = {n: torch.from_numpy(z[n].copy()).cuda() for n in names}
             st = TrainState(prob, float(z["lr"]), int(z["step"]), master)
         st.rebuild_runtime()
         return st
 
 
-def initial_state(cfg, lr: float = 0.05) -> TrainState:
+def initial_state(cfg, lr: float = 0.05, block: bool = False) -> TrainState:
     """Masters from the seeded weights (exact widening of the storage values)."""
-    from synth import make_inputs, make_router_inputs
+    from synth import make_block_inputs, make_inputs, make_router_inputs
     from synth.inputs import bf16_bits_to_f32
     host = make_inputs(cfg, parts=("w1", "w2"))
     host["wr"] = make_router_inputs(cfg)["wr"]
+    if block:
+        host.update(make_block_inputs(cfg))
     widen = (lambda a: bf16_bits_to_f32(a)) if cfg.dtype == "bf16" else (lambda a: np.asarray(a, np.float32))
-    master = {n: torch.from_numpy(np.ascontiguousarray(widen(host[n]))).cuda() for n in ("w1", "w2", "wr")}
+    master = {n: torch.from_numpy(np.ascontiguousarray(widen(host[n]))).cuda() for n in host}
     st = TrainState(Problem.from_config(cfg), lr, 0, master)
     st.rebuild_runtime()
     return st
@@ -189,20 +204,30 @@ def _mx(t, rows: int, cols: int):
     return moe_mx_quantize(t.reshape(rows, cols))
 
 
-def train_step(cfg, st: TrainState, tracer: Tracer, hook: Optional[Callable] = None, mx: bool = False):
+def train_step(cfg, st: TrainState, tracer: Tracer, hook: Optional[Callable] = None, mx: bool = False,
+               block: bool = False):
     """One step at st.step; advances st.step.  ``hook(step, where, st)`` may
     change the state at "before_forward" (a fault injector for tests).  With
-    ``mx`` every expert GEMM runs on MXFP8 operands."""
+    ``mx`` every expert GEMM runs on MXFP8 operands; with ``block`` the dense
+    operators around the layer take part."""
     if cfg.combine != 1 or cfg.num_local != cfg.num_experts:
         raise MoeError("the train step covers the full layer (token layout, all experts local)")
     if mx and (cfg.dtype != "bf16" or cfg.d_model > 2048 or cfg.d_ffn > 2048):
         raise MoeError("the MXFP8 train step needs a bf16 layer with d_model and d_ffn at most 2048")
+    if block and mx:
+        raise MoeError("the block's train step runs the expert GEMMs on bf16 or float32 operands, not MXFP8: it adds "
+                       "their dx per token")
+    if block and any(n not in st.master for n in BLOCK_WEIGHTS):
+        raise MoeError("the state holds no weights of the block's dense operators")
     s, prob = st.step, st.prob
-    x, dy = _device_batch(cfg, s)
+    batch, dy = _device_batch(cfg, s)
     if hook:
         hook(s, "before_forward", st)
     R = st.runtime
-    logits = moe_router_fwd(prob, x, R["wr"])
+    logits = moe_router_fwd(prob, batch, R["wr"])
+    x = batch
+    if block:
+        x, mean, rstd = moe_layernorm_fwd(batch, R["nw"], R["nb"])
     enc, fwd_enc, wg_enc = {}, {}, {}
     if mx:
         el, D, F = cfg.num_local, cfg.d_model, cfg.d_ffn
@@ -213,6 +238,10 @@ def train_step(cfg, st: TrainState, tracer: Tracer, hook: Optional[Callable] = N
         y = moe_mx_fwd_fc2(prob, routing, fwd_enc["act"], fwd_enc["w2t"])
     else:
         routing, h, y = moe_fwd(prob, logits, x, R["w1"], R["w2"])
+    if block:
+        ym = y
+        a, g, u = moe_glu_fwd(x, R["wg"], R["wu"], save=True)
+        y, _ = moe_linear_fwd(a, R["wd"], R["bd"], residual=ym)
     if mx:
         el, D, F = cfg.num_local, cfg.d_model, cfg.d_ffn
         enc["dy"], enc["w2"] = _mx(dy, cfg.tokens, D), _mx(R["w2"], el * F, D)
@@ -227,7 +256,11 @@ def train_step(cfg, st: TrainState, tracer: Tracer, hook: Optional[Callable] = N
     else:
         dx, dprob, dh = moe_bwd_dgrad_dprob(prob, routing, dy, R["w1"], R["w2"], h)
         dw1, dw2 = moe_bwd_wgrad(prob, routing, x, dy, h, dh)
-    dlogits, dwr, dxr = moe_router_bwd(prob, routing, dprob, x, R["wr"])
+    dlogits, dwr, dxr = moe_router_bwd(prob, routing, dprob, batch, R["wr"])
+    if block:
+        da, dwd, dbd = moe_linear_bwd(dy, a, R["wd"])
+        dxn, dwg, dwu = moe_glu_bwd(da, x, R["wg"], R["wu"], g, u, dx_add=dx)
+        dxb, dnw, dnb = moe_layernorm_bwd(dxn, batch, R["nw"], mean, rstd, dx_add=dxr)
     torch.cuda.synchronize()
 
     T = tracer
@@ -245,8 +278,15 @@ def train_step(cfg, st: TrainState, tracer: Tracer, hook: Optional[Callable] = N
             T.tensor(s, "forward", op, f"{n}_scales", fwd_enc[n][1], 2)
         T.tensor(s, "forward", "moe_mx_fwd_fc2", "y", y, 1)
     else:
+        if block:
+            for n, t in (("xn", x), ("mean", mean), ("rstd", rstd)):
+                T.tensor(s, "forward", "moe_layernorm_fwd", n, t, 2)
         T.tensor(s, "forward", "moe_fwd", "h", h, 2)
-        T.tensor(s, "forward", "moe_fwd", "y", y, 1)
+        T.tensor(s, "forward", "moe_fwd", "y", ym if block else y, 1)
+        if block:
+            for n, t in (("g", g), ("u", u), ("a", a)):
+                T.tensor(s, "forward", "moe_glu_fwd", n, t, 2)
+            T.tensor(s, "forward", "moe_linear_fwd", "y_block", y, 1)
     # backward
     if mx:
         for n in ("dy", "w2"):
@@ -279,27 +319,40 @@ def train_step(cfg, st: TrainState, tracer: Tracer, hook: Optional[Callable] = N
     T.tensor(s, "router", "moe_router_bwd", "dlogits", dlogits, 2)
     T.tensor(s, "router", "moe_router_bwd", "dwr", dwr, 1)
     T.tensor(s, "router", "moe_router_bwd", "dx_router", dxr, 1)
+    if block:
+        T.tensor(s, "backward", "moe_linear_bwd", "da", da, 2)
+        T.tensor(s, "backward", "moe_linear_bwd", "dwd", dwd, 1)
+        T.tensor(s, "backward", "moe_linear_bwd", "dbd", dbd, 1)
+        T.tensor(s, "backward", "moe_glu_bwd", "dxn", dxn, 2)
+        T.tensor(s, "backward", "moe_glu_bwd", "dwg", dwg, 1)
+        T.tensor(s, "backward", "moe_glu_bwd", "dwu", dwu, 1)
+        T.tensor(s, "backward", "moe_layernorm_bwd", "dx_block", dxb, 1)
+        T.tensor(s, "backward", "moe_layernorm_bwd", "dnw", dnw, 1)
+        T.tensor(s, "backward", "moe_layernorm_bwd", "dnb", dnb, 1)
     # end-to-end metrics of the step (host float64 in a fixed order)
     yd = (y.double() * dy.double()).cpu().numpy().ravel()
     T.metric(s, "loss", float(math.fsum(yd.tolist())) if yd.size < 1 << 21 else float(np.sum(yd)))
-    T.metric(s, "grad_norm", math.sqrt(_host_sum_sq(dw1) + _host_sum_sq(dw2) + _host_sum_sq(dwr)))
+    grads = {"w1": dw1, "w2": dw2, "wr": dwr}
+    if block:
+        grads.update(nw=dnw, nb=dnb, wg=dwg, wu=dwu, wd=dwd, bd=dbd)
+    T.metric(s, "grad_norm", math.sqrt(sum(_host_sum_sq(t) for t in grads.values())))
     # optimizer: SGD on the masters, runtime copies rebuilt by the same kernel
-    for n, g in (("w1", dw1), ("w2", dw2), ("wr", dwr)):
-        moe_sgd_step(st.master[n], g.reshape(st.master[n].shape), st.lr, R[n])
+    for n, t in grads.items():
+        moe_sgd_step(st.master[n], t.reshape(st.master[n].shape), st.lr, R[n])
     torch.cuda.synchronize()
-    for n in ("w1", "w2", "wr"):
+    for n in grads:
         T.tensor(s, "optimizer", "moe_sgd_step", f"master_{n}", st.master[n], 1)
         T.tensor(s, "optimizer", "moe_sgd_step", f"runtime_{n}", R[n], 2)
     st.step += 1
 
 
 def run(cfg, steps: int, level: str = "phases", window: Optional[range] = None, st: Optional[TrainState] = None,
-        hook: Optional[Callable] = None, lr: float = 0.05, mx: bool = False):
+        hook: Optional[Callable] = None, lr: float = 0.05, mx: bool = False, block: bool = False):
     """Train from st (or the initial state) until st.step == steps."""
-    st = st or initial_state(cfg, lr)
+    st = st or initial_state(cfg, lr, block)
     tr = Tracer(level, window)
     while st.step < steps:
-        train_step(cfg, st, tr, hook, mx)
+        train_step(cfg, st, tr, hook, mx, block)
     return st, tr
 
 
@@ -348,6 +401,8 @@ def main(argv=None):
     ap.add_argument("--out", help="write the trace (JSON lines)")
     ap.add_argument("--compare", nargs=2, metavar=("A", "B"), help="report the first divergence of two traces")
     ap.add_argument("--mx", action="store_true", help="every expert GEMM on MXFP8 operands (bf16 layers)")
+    ap.add_argument("--block", action="store_true", help="with the dense operators around the layer: norm, gated shared "
+                    "expert, down projection")
     a = ap.parse_args(argv)
     if a.compare:
         d = first_divergence(Tracer.load(a.compare[0]), Tracer.load(a.compare[1]))
@@ -355,7 +410,7 @@ def main(argv=None):
                                                  "b": d[2] and d[2].__dict__}))
         return
     from synth import CONFIGS
-    _, tr = run(CONFIGS[a.config], a.steps, a.level, mx=a.mx)
+    _, tr = run(CONFIGS[a.config], a.steps, a.level, mx=a.mx, block=a.block)
     if a.out:
         tr.save(a.out)
     print(json.dumps({"records": len(tr.records), "steps": a.steps, "level": a.level}))

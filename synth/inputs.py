@@ -22,7 +22,8 @@ import numpy as np
 
 from .configs import Config
 
-_TENSOR_CODE = {"logits": 0, "x": 1, "w1": 2, "w2": 3, "dy": 4, "zipf_rank": 5, "wr": 6, "dprob": 7}
+_TENSOR_CODE = {"logits": 0, "x": 1, "w1": 2, "w2": 3, "dy": 4, "zipf_rank": 5, "wr": 6, "dprob": 7,
+                "nw": 8, "nb": 9, "wg": 10, "wu": 11, "wd": 12, "bd": 13}
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
 
@@ -151,6 +152,19 @@ def make_router_inputs(cfg: Config) -> dict:
         "wr": _draw(_rng(cfg.seed, "wr"), (cfg.num_experts, cfg.d_model), cfg.w_std, cfg.dtype),
         "dprob": _draw(_rng(cfg.seed, "dprob"), (cfg.tokens, cfg.top_k), 1.0, "f32"),
     }
+
+
+def make_block_inputs(cfg: Config) -> dict:
+    """Weights of the dense operators around the layer: the norm's weight and
+    bias nw, nb [D], the gated shared expert's wg, wu [D, F], and the down
+    projection's wd [F, D] and bd [D] (storage dtype; matrices N(0, w_std), the
+    norm's weight around 1).  Streams of their own."""
+    D, F = cfg.d_model, cfg.d_ffn
+    one = 1.0 + 0.1 * _rng(cfg.seed, "nw").standard_normal(D, dtype=np.float32)
+    out = {"nw": f32_to_bf16_bits(one) if cfg.dtype == "bf16" else one}
+    for name, shape in (("nb", (D,)), ("wg", (D, F)), ("wu", (D, F)), ("wd", (F, D)), ("bd", (D,))):
+        out[name] = _draw(_rng(cfg.seed, name), shape, cfg.w_std, cfg.dtype)
+    return out
 
 
 def make_batch(cfg: Config, step: int) -> dict:
