@@ -108,7 +108,34 @@ hipError_t launch_norm_bwd(const NormParams& P, bool bf16, hipStream_t st);
 // out[c] = sum over b ascending, in fixed phases, of part[b * stride + c], c <
 // cols; out2 the same of the next cols columns.  Either may be null.
 hipError_t launch_block_sums(const float* part, int blocks, int64_t stride, int cols, void* out, void* out2,
-                             bool out_bf16, hipStream_t st);
+                             hipStream_t st);
+
+// The column sums of one workgroup of 256 threads: columns 16 block .. 16
+// block + 15 in 16 phases; phase p adds blocks [p B / 16, (p + 1) B / 16)
+// ascending, then the phases are added in order.  Nothing is written where out is null.
+DEV void block_sum16(const float* part, int blocks, int64_t stride, int cols, uint32_t block, void* out, bool out_bf16) {
+  __shared__ float s[16][17];
+  const int x = threadIdx.x & 15, p = threadIdx.x >> 4;
+  const int c = (int)block * 16 + x;
+  const int b0 = p * blocks / 16, b1 = (p + 1) * blocks / 16;
+  float v = 0.f;
+  if (c < cols) {
+    const float* q = part + (int64_t)b0 * stride + c;
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b, q += stride) v = v + *q;
+  }
+  s[p][x] = v;
+  __syncthreads();
+  if (p == 0 && c < cols && out) {
+    v = s[0][x];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v = v + s[i][x];
+    if (out_bf16)
+      ((uint16_t*)out)[c] = (uint16_t)f32_to_bf16(v);
+    else
+      ((float*)out)[c] = v;
+  }
+}
 
 // ------------------------------------------------------------ matrix operators
 // One matrix product of a dense operator,
@@ -189,7 +216,20 @@ struct DenseEwParams {
   uint64_t seed;
 };
 int dense_ew_blocks(int64_t rows, int cols, bool bf16, bool sums);
-hipError_t launch_dense_ew(const DenseEwParams& P, bool glu, bool bf16, hipStream_t st);
+// K: operands to copy in the same launch (K.n may be 0)
+hipError_t launch_dense_ew(const DenseEwParams& P, const DensePackParams& K, bool glu, bool bf16, hipStream_t st);
+// What a backward call joins at its end: chunks of dx and dw (where S > 1) and
+// the bias gradient's column sums (where db is set).
+struct DenseJoin {
+  DenseParams dx, dw;
+  uint32_t nx, nw;     // workgroups of each
+  const float* sums;   // [blocks][cols]
+  int blocks, cols;
+  void* db;
+  bool db_bf16;
+};
+hipError_t launch_dense_join(const DenseParams& dx, const DenseParams& dw, const float* sums, int blocks, int cols,
+                             void* db, bool db_bf16, bool bf16, hipStream_t st);
 hipError_t launch_dense_zero(void* p, int64_t n16, hipStream_t st);   // n16 16-bit words
 
 }  // namespace moedet

@@ -667,15 +667,13 @@ __global__ __launch_bounds__((FewCfg<T, FORM, MT>::NW * 64)) void dense_few_kern
 // One thread per four columns: the chunks' partials in chunk order, then the
 // epilogue.
 template <typename T, int FORM>
-__global__ __launch_bounds__(256) void dense_finish_kernel(DenseParams P) {
-  const int q = (P.N + 3) / 4;
-  const int nm = FORM == kFormDw ? P.nseg : 1;
-  const int64_t total = P.M * q * nm;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= total) return;
-  const int64_t row = i / (q * nm);
-  const int rest = (int)(i - row * (q * nm));
-  const int seg = rest / q, col = (rest - seg * q) * 4;
+DEV void finish_at(const DenseParams& P, uint32_t block) {
+  const uint32_t q = ((uint32_t)P.N + 3) / 4, per = FORM == kFormDw ? q * P.nseg : q;
+  const uint32_t i = block * 256u + threadIdx.x;   // a split product has fewer than 2^30 elements
+  if (i >= (uint64_t)P.M * per) return;
+  const int64_t row = i / per;
+  const uint32_t rest = i % per;
+  const int seg = rest >= q ? 1 : 0, col = (int)(rest - seg * q) * 4;
   auto sum = [&](int sg, float (&v)[4]) {
     const float* p = P.part + row * P.part_ld + sg * P.part_seg + col;
     f32x4_t a = *(const f32x4_t*)p;
@@ -699,21 +697,42 @@ __global__ __launch_bounds__(256) void dense_finish_kernel(DenseParams P) {
   }
 }
 
+template <typename T, int FORM>
+__global__ __launch_bounds__(256) void dense_finish_kernel(DenseParams P) {
+  finish_at<T, FORM>(P, blockIdx.x);
+}
+
+// Everything that a backward call joins at its end, in one launch: the chunks
+// of dx and of the weight gradients, and the row blocks' column sums.
+// Workgroups [0, nx) join dx, [nx, nx + nw) dw, the others add column sums.
+template <typename T>
+__global__ __launch_bounds__(256) void dense_join_kernel(DenseJoin J) {
+  const uint32_t b = blockIdx.x;
+  if (b < J.nx)
+    finish_at<T, kFormDx>(J.dx, b);
+  else if (b < J.nx + J.nw)
+    finish_at<T, kFormDw>(J.dw, b - J.nx);
+  else
+    block_sum16(J.sums, J.blocks, J.cols, J.cols, b - J.nx - J.nw, J.db, J.db_bf16);
+}
+
 // ---------------------------------------------------------- elementwise passes
 // Up to three matrices copied into rows of whole 16-byte chunks, zeros past
-// their columns: one launch, a matrix per range of workgroups.
-__global__ __launch_bounds__(256) void dense_pack_kernel(DensePackParams P) {
+// their columns: a matrix per range of workgroups.
+DEV void pack_at(const DensePackParams& P, uint32_t block) {
   int m = 0;
-  while (m + 1 < P.n && (int64_t)blockIdx.x >= P.first[m + 1]) ++m;
-  const int q = (int)(P.ldo[m] / 8);
-  const int64_t i = ((int64_t)blockIdx.x - P.first[m]) * 256 + threadIdx.x;
-  if (i >= P.rows[m] * q) return;
+  while (m + 1 < P.n && (int64_t)block >= P.first[m + 1]) ++m;
+  // 32 bits: a launch has fewer than 2^32 threads
+  const uint32_t q = (uint32_t)P.ldo[m] / 8;
+  const uint32_t i = (block - (uint32_t)P.first[m]) * 256u + threadIdx.x;
+  if (i >= (uint64_t)P.rows[m] * q) return;
   const int64_t row = i / q;
-  const int c = (int)(i - row * q) * 8, left = P.cols[m] - c;
+  const int c = (int)(i % q) * 8, left = P.cols[m] - c;
   u32x4_t r = {0u, 0u, 0u, 0u};
   if (left > 0) r = Vec<uint16_t>::load((const uint16_t*)P.in[m] + row * P.ld[m] + c, left);
   *(u32x4_t*)((uint16_t*)P.out[m] + row * P.ldo[m] + c) = r;
 }
+__global__ __launch_bounds__(256) void dense_pack_kernel(DensePackParams P) { pack_at(P, blockIdx.x); }
 
 // V elements of a saved pre-activation, zeros past n >= 1
 template <typename Z, int V>
@@ -729,9 +748,14 @@ DEV void load_z(const Z* p, int n, float* v) {
 
 // dz = dy act'(z), or dg = da u act'(g) and du = da act(g).  A workgroup owns
 // 64 V columns and a block of rows; its 4 waves take the rows in turn, and
-// their column sums of the unrounded dz are added in wave order.
+// their column sums of the unrounded dz are added in wave order.  Workgroups
+// past `grid` copy unaligned operands in the same launch.
 template <typename T, typename Z, bool GLU>
-__global__ __launch_bounds__(256) void dense_ew_kernel(DenseEwParams P) {
+__global__ __launch_bounds__(256) void dense_ew_kernel(DenseEwParams P, DensePackParams K, uint32_t grid) {
+  if (blockIdx.x >= grid) {
+    pack_at(K, blockIdx.x - grid);
+    return;
+  }
   constexpr int V = Vec<T>::N, CT = 64 * V;
   __shared__ float s_sum[3][CT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -893,19 +917,20 @@ hipError_t launch_dense_few(const DenseParams& P, int form, bool bf16, hipStream
   return hipGetLastError();
 }
 
+static uint32_t finish_blocks(const DenseParams& P, int form) {
+  return (uint32_t)((P.M * ((P.N + 3) / 4) * (form == kFormDw ? P.nseg : 1) + 255) / 256);
+}
+
 template <typename T>
 static void dense_finish_launch(const DenseParams& P, int form, int64_t grid, hipStream_t st) {
   switch (form) {
     case kFormLinear: dense_finish_kernel<T, kFormLinear><<<grid, 256, 0, st>>>(P); break;
-    case kFormGlu: dense_finish_kernel<T, kFormGlu><<<grid, 256, 0, st>>>(P); break;
-    case kFormDx: dense_finish_kernel<T, kFormDx><<<grid, 256, 0, st>>>(P); break;
-    default: dense_finish_kernel<T, kFormDw><<<grid, 256, 0, st>>>(P); break;
+    default: dense_finish_kernel<T, kFormGlu><<<grid, 256, 0, st>>>(P); break;
   }
 }
 
 hipError_t launch_dense_finish(const DenseParams& P, int form, bool bf16, hipStream_t st) {
-  const int64_t total = P.M * ((P.N + 3) / 4) * (form == kFormDw ? P.nseg : 1);
-  const int64_t grid = (total + 255) / 256;
+  const int64_t grid = finish_blocks(P, form);
   if (bf16)
     dense_finish_launch<uint16_t>(P, form, grid, st);
   else
@@ -944,22 +969,37 @@ int dense_ew_blocks(int64_t rows, int cols, bool bf16, bool sums) {
 }
 
 template <typename T, typename Z>
-static void dense_ew_launch(const DenseEwParams& P, bool glu, int64_t grid, hipStream_t st) {
+static void dense_ew_launch(const DenseEwParams& P, const DensePackParams& K, bool glu, uint32_t grid, hipStream_t st) {
+  const uint32_t all = grid + (K.n ? (uint32_t)K.first[K.n] : 0);
   if (glu)
-    dense_ew_kernel<T, Z, true><<<grid, 256, 0, st>>>(P);
+    dense_ew_kernel<T, Z, true><<<all, 256, 0, st>>>(P, K, grid);
   else
-    dense_ew_kernel<T, Z, false><<<grid, 256, 0, st>>>(P);
+    dense_ew_kernel<T, Z, false><<<all, 256, 0, st>>>(P, K, grid);
 }
 
-hipError_t launch_dense_ew(const DenseEwParams& P, bool glu, bool bf16, hipStream_t st) {
+hipError_t launch_dense_ew(const DenseEwParams& P, const DensePackParams& K, bool glu, bool bf16, hipStream_t st) {
   const int ct = bf16 ? 512 : 256;
-  const int64_t grid = grid_for_units((int64_t)P.blocks * ((P.pad + ct - 1) / ct));
+  const uint32_t grid = (uint32_t)grid_for_units((int64_t)P.blocks * ((P.pad + ct - 1) / ct));
   if (!bf16)
-    dense_ew_launch<float, float>(P, glu, grid, st);
+    dense_ew_launch<float, float>(P, K, glu, grid, st);
   else if (P.z_f32)
-    dense_ew_launch<uint16_t, float>(P, glu, grid, st);
+    dense_ew_launch<uint16_t, float>(P, K, glu, grid, st);
   else
-    dense_ew_launch<uint16_t, uint16_t>(P, glu, grid, st);
+    dense_ew_launch<uint16_t, uint16_t>(P, K, glu, grid, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_dense_join(const DenseParams& dx, const DenseParams& dw, const float* sums, int blocks, int cols,
+                             void* db, bool db_bf16, bool bf16, hipStream_t st) {
+  DenseJoin J{dx, dw, 0, 0, sums, blocks, cols, db, db_bf16};
+  if (dx.S > 1) J.nx = finish_blocks(dx, kFormDx);
+  if (dw.S > 1) J.nw = finish_blocks(dw, kFormDw);
+  const uint32_t grid = J.nx + J.nw + (db ? (uint32_t)(cols + 15) / 16 : 0);
+  if (grid == 0) return hipSuccess;
+  if (bf16)
+    dense_join_kernel<uint16_t><<<grid, 256, 0, st>>>(J);
+  else
+    dense_join_kernel<float><<<grid, 256, 0, st>>>(J);
   return hipGetLastError();
 }
 

@@ -179,7 +179,7 @@ struct BwdPlan {
   int64_t ldx, ldw, lddz, segdz;
   int64_t dx_ld, dw_seg;
   int ew_blocks;
-  size_t x, w, dz, colsum, part, total;
+  size_t x, w, dz, colsum, part_dx, part_dw, total;
 };
 
 BwdPlan bwd_plan(const moe_dense* p, const Dense& d) {
@@ -215,15 +215,11 @@ BwdPlan bwd_plan(const moe_dense* p, const Dense& d) {
   b.dw = choose(d, kFormDw, d.D, d.F, d.nm, d.T, b.ldx > b.lddz ? b.ldx : b.lddz);
   b.dx_ld = up(d.D, 4);
   b.dw_seg = up(d.F, 4);
-  // the two products run one after the other and share the partials' space
-  size_t part = 0;
-  if (b.dx.S > 1) part = (size_t)b.dx.S * d.T * b.dx_ld * 4;
-  if (b.dw.S > 1) {
-    const size_t q = (size_t)b.dw.S * d.D * d.nm * b.dw_seg * 4;
-    if (q > part) part = q;
-  }
-  b.part = o;
-  o += align_up(part);
+  // both products' partials live until the joining launch at the end
+  b.part_dx = o;
+  if (b.dx.S > 1) o += align_up((size_t)b.dx.S * d.T * b.dx_ld * 4);
+  b.part_dw = o;
+  if (b.dw.S > 1) o += align_up((size_t)b.dw.S * d.D * d.nm * b.dw_seg * 4);
   b.total = o;
   return b;
 }
@@ -249,9 +245,10 @@ moe_status check_ws(const void* ws, size_t have, size_t need) {
     if ((x) != hipSuccess) return MOE_ERR_HIP;   \
   } while (0)
 
-// x (and the weights) copied into whole 16-byte rows where they are not
-moe_status pack_inputs(const Dense& d, const moe_dense* p, bool px, bool pw, int64_t ldx, int64_t ldw, char* wx, char* ww,
-                       const void*& x, const void* (&w)[2], hipStream_t st) {
+// The copies of x and the weights into whole 16-byte rows, where they need
+// one; x and w then point to them.
+DensePackParams plan_copies(const Dense& d, const moe_dense* p, bool px, bool pw, int64_t ldx, int64_t ldw, char* wx,
+                            char* ww, const void*& x, const void* (&w)[2]) {
   DensePackParams K{};
   if (px) {
     K.add(x, d.T, d.D, p->ldx, wx, ldx);
@@ -264,13 +261,7 @@ moe_status pack_inputs(const Dense& d, const moe_dense* p, bool px, bool pw, int
       w[m] = o;
     }
   }
-  return hip_status(launch_dense_pack(K, st));
-}
-
-moe_status run_product(DenseParams& P, int form, const Dense& d, int bm, hipStream_t st) {
-  MOE_TRY(launch_dense_gemm(P, form, d.bf16, bm, st));
-  if (P.S > 1) MOE_TRY(launch_dense_finish(P, form, d.bf16, st));
-  return MOE_OK;
+  return K;
 }
 
 moe_status forward(const moe_dense* p, int nm, const void* x, const void* w0, const void* w1, const void* bias,
@@ -287,8 +278,8 @@ moe_status forward(const moe_dense* p, int nm, const void* x, const void* w0, co
   const FwdPlan f = fwd_plan(p, d);
   if ((s = check_ws(ws, ws_bytes, f.total)) != MOE_OK) return s;
   const void* w[2] = {w0, w1};
-  s = pack_inputs(d, p, f.pack_x, f.pack_w, f.ldx, f.ldw, (char*)ws + f.x, (char*)ws + f.w, x, w, st);
-  if (s != MOE_OK) return s;
+  MOE_TRY(launch_dense_pack(
+      plan_copies(d, p, f.pack_x, f.pack_w, f.ldx, f.ldw, (char*)ws + f.x, (char*)ws + f.w, x, w), st));
   const int form = nm == 2 ? kFormGlu : kFormLinear;
   DenseParams P{};
   P.M = d.T;
@@ -315,8 +306,10 @@ moe_status forward(const moe_dense* p, int nm, const void* x, const void* w0, co
   P.z_f32 = p->z_dtype == MOE_F32;
   P.act = p->act;
   P.seed = p->debug_shuffle_seed;
-  if (!f.few) return run_product(P, form, d, f.ch.bm, st);
-  MOE_TRY(launch_dense_few(P, form, d.bf16, st));
+  if (f.few)
+    MOE_TRY(launch_dense_few(P, form, d.bf16, st));
+  else
+    MOE_TRY(launch_dense_gemm(P, form, d.bf16, f.ch.bm, st));
   if (P.S > 1) MOE_TRY(launch_dense_finish(P, form, d.bf16, st));
   return MOE_OK;
 }
@@ -348,8 +341,7 @@ moe_status backward(const moe_dense* p, int nm, const void* dy, const void* x, c
   if ((s = check_ws(ws, ws_bytes, b.total)) != MOE_OK) return s;
   char* base = (char*)ws;
   const void* w[2] = {w0, w1};
-  s = pack_inputs(d, p, b.pack_x, b.pack_w, b.ldx, b.ldw, base + b.x, base + b.w, x, w, st);
-  if (s != MOE_OK) return s;
+  const DensePackParams K = plan_copies(d, p, b.pack_x, b.pack_w, b.ldx, b.ldw, base + b.x, base + b.w, x, w);
   const void* dz = dy;
   if (b.make_dz || db) {
     DenseEwParams E{};
@@ -372,8 +364,9 @@ moe_status backward(const moe_dense* p, int nm, const void* dy, const void* x, c
     E.part = db ? (float*)(base + b.colsum) : nullptr;
     E.blocks = b.ew_blocks;
     E.seed = p->debug_shuffle_seed;
-    MOE_TRY(launch_dense_ew(E, nm == 2, d.bf16, st));
-    if (db) MOE_TRY(launch_block_sums(E.part, b.ew_blocks, d.F, d.F, db, nullptr, !g32 && d.bf16, st));
+    MOE_TRY(launch_dense_ew(E, K, nm == 2, d.bf16, st));
+  } else {
+    MOE_TRY(launch_dense_pack(K, st));
   }
   DenseParams P{};
   P.M = d.T;
@@ -387,14 +380,14 @@ moe_status backward(const moe_dense* p, int nm, const void* dy, const void* x, c
   P.b[1] = w[1];
   P.ldb = b.ldw;
   P.S = b.dx.S;
-  P.part = (float*)(base + b.part);
+  P.part = (float*)(base + b.part_dx);
   P.part_ld = b.dx_ld;
   P.add = dx_add;
   P.ldadd = p->ldr;
   P.c[0] = dx;
   P.ldc = d.D;
   P.seed = p->debug_shuffle_seed;
-  if ((s = run_product(P, kFormDx, d, b.dx.bm, st)) != MOE_OK) return s;
+  MOE_TRY(launch_dense_gemm(P, kFormDx, d.bf16, b.dx.bm, st));
   DenseParams W{};
   W.M = d.D;
   W.N = d.F;
@@ -406,7 +399,7 @@ moe_status backward(const moe_dense* p, int nm, const void* dy, const void* x, c
   W.ldb = b.lddz;
   W.seg = b.segdz;
   W.S = b.dw.S;
-  W.part = (float*)(base + b.part);
+  W.part = (float*)(base + b.part_dw);
   W.part_seg = (int)b.dw_seg;
   W.part_ld = nm * b.dw_seg;
   W.c[0] = dw0;
@@ -414,7 +407,8 @@ moe_status backward(const moe_dense* p, int nm, const void* dy, const void* x, c
   W.ldc = d.F;
   W.c_f32 = g32;
   W.seed = p->debug_shuffle_seed;
-  return run_product(W, kFormDw, d, b.dw.bm, st);
+  MOE_TRY(launch_dense_gemm(W, kFormDw, d.bf16, b.dw.bm, st));
+  return hip_status(launch_dense_join(P, W, (const float*)(base + b.colsum), b.ew_blocks, d.F, db, !g32 && d.bf16, d.bf16, st));
 }
 
 // --------------------------------------------------------------------- layer norm
@@ -505,7 +499,7 @@ MOE_API moe_status moe_layernorm_bwd(const void* dy, const void* x, const void* 
   P.blocks = blocks;
   P.seed = debug_shuffle_seed;
   MOE_TRY(launch_norm_bwd(P, bf16, st));
-  if (sums) MOE_TRY(launch_block_sums(P.part, blocks, 2 * cols, (int)cols, dweight, dbias, false, st));
+  if (sums) MOE_TRY(launch_block_sums(P.part, blocks, 2 * cols, (int)cols, dweight, dbias, st));
   return MOE_OK;
 }
 

@@ -1,5 +1,5 @@
 // bf16 main loop of the dense matrix operators: the ring of gemm_bf16.h
-// (32-row K slices copied by DMA into four LDS slots, the loads of later
+// (32-row K slices copied by DMA into LDS slots, the loads of later
 // slices spread between the MFMAs) with a tile of 256 or 128 rows, a B tile
 // that may come from two matrices, K tails and K segments.
 //
@@ -25,32 +25,36 @@ using bf::kOOB;
 using bf::KC;
 using bf::MNC;
 constexpr int GLU = 2;
-constexpr int BK = bf::BK, BN = 256, NS = 4, BOPER = BN * BK;
+constexpr int BK = bf::BK, BN = 256, BOPER = BN * BK;
 
 template <int WTM>
 constexpr int kAOper = 2 * WTM * BK;             // elements of an A slot
 template <int WTM>
 constexpr int kSlot = kAOper<WTM> + BOPER;       // elements of a ring slot
+// Ring slots: 4 of 32 KiB, or 6 of 24 KiB for the 128-row tile, whose slices are
+// multiplied in half the time while the loads take as long.
 template <int WTM>
-constexpr int kRingBytes = NS * kSlot<WTM> * 2;
+constexpr int kSlots = WTM == 128 ? 4 : 6;
+template <int WTM>
+constexpr int kRingBytes = kSlots<WTM> * kSlot<WTM> * 2;
 template <int WTM>
 constexpr int kALoads = WTM / 32;                // 16-byte loads per thread of an A slice
 
 DEV int mnc128_off(int k, int mn) { return k * 128 + (((mn >> 3) ^ ((k & 3) << 2)) << 3) + (mn & 7); }
 
 // Fragment read addresses of one operand.  Per lane, the LDS byte addresses
-// of the reads that differ by more than a constant, in ring slot 0 (s0)
-// and in slot 2 (s1); every read is one of them plus a constant that fits the
-// instruction's 16-bit offset (slot parity, k half, block), so the loop,
-// unrolled over the 4 slots, spends no instruction on addresses.  The second
-// set goes through an asm add so that it stays in registers.
+// of the reads that differ by more than a constant, in the even ring slots;
+// every read is one of them plus a constant that fits the instruction's
+// 16-bit offset (slot parity, k half, block), so the loop, unrolled over the slots,
+// spends no instruction on addresses.  The sets past the first go through
+// an asm add so that they stay in registers.
 //  KC   the two k halves (the swizzle is the same for rows 32 apart)
 //  MNC  rows k and k + 4 of each 32-column block
 //  GLU  rows k and k + 4 of the two blocks of a matrix; wu 8 KiB past wg
-template <int L, int NBLK>
+template <int L, int NBLK, int NS>
 struct FragAddr {
   static constexpr int N = L == KC ? 2 : L == MNC ? 2 * NBLK : 4;
-  uint32_t s0[N], s1[N];
+  uint32_t at[NS / 2][N];
   template <int W>
   DEV static uint32_t mnc_at(int col, int lane, int hi) {
     const int g = lane >> 4, i = lane & 15;
@@ -64,16 +68,17 @@ struct FragAddr {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       if constexpr (L == KC)
-        s0[j] = base + 2u * (uint32_t)bf::kc_off(first + (lane & 31), 2 * j + (lane >> 5));
+        at[0][j] = base + 2u * (uint32_t)bf::kc_off(first + (lane & 31), 2 * j + (lane >> 5));
       else
-        s0[j] = base + mnc_at<W>(first + 32 * (j >> 1), lane, j & 1);
-      asm("v_add_u32 %0, %2, %1" : "=v"(s1[j]) : "v"(s0[j]), "s"(two_slots));
+        at[0][j] = base + mnc_at<W>(first + 32 * (j >> 1), lane, j & 1);
+#pragma unroll
+      for (int p = 1; p < NS / 2; ++p) asm("v_add_u32 %0, %2, %1" : "=v"(at[p][j]) : "v"(at[p - 1][j]), "s"(two_slots));
     }
   }
   // block b, k half kk, in slot sl (constants); slot: bytes of a slot
   template <int W, int SLOT_BYTES>
   DEV bf16x8_t read(int b, int kk, int sl) const {
-    const uint32_t* set = sl >= 2 ? s1 : s0;
+    const uint32_t* set = at[sl >> 1];
     const uint32_t so = (uint32_t)(sl & 1) * SLOT_BYTES;
     if constexpr (L == KC) {
       const LDS_AS char* p = (const LDS_AS char*)(uintptr_t)set[kk];
@@ -144,8 +149,8 @@ DEV void wait_vm_barrier() {
 template <int AL, int BL, int WTM>
 struct TileAddr {
   static constexpr int WB = BL == GLU ? 128 : 256, SB = kSlot<WTM> * 2;
-  FragAddr<AL, WTM / 32> a;
-  FragAddr<BL, 4> b;
+  FragAddr<AL, WTM / 32, kSlots<WTM>> a;
+  FragAddr<BL, 4, kSlots<WTM>> b;
   DEV void init(uint32_t ring, int wm, int wn, int lane) {
     a.template init<2 * WTM>(ring, wm * WTM, lane, 2u * SB);
     b.template init<WB>(ring + kAOper<WTM> * 2, wn * (BL == GLU ? 64 : 128), lane, 2u * SB);
@@ -173,12 +178,11 @@ DEV void mma1(const bf::Frags& f, f32x16_t (&acc)[4][4], int g, int j) {
 // that LDS address, i < kALoads of A, then 4 of B; slices at or past nsteps
 // must read zeros (their loads keep the count of outstanding loads the same
 // in every step).  The order of waits and reads is bf::mainloop's: in step s the
-// B loads of slice s + 2 go out while k-half 0 is multiplied; then slice s + 1
-// has landed, and the A loads of slice s + 3 go out while k-half 1 is.
+// B loads of slice s + NS - 2 go out while k-half 0 is multiplied; then slice
+// s + 1 has landed, and the A loads of slice s + NS - 1 go out while k-half 1 is.
 template <int AL, int BL, int WTM, class Issue>
 DEV void mainloop(uint32_t ring, int nsteps, Issue issue, f32x16_t (&acc)[4][4], int wm, int wn, int lane) {
-  constexpr int LA = kALoads<WTM>, L = LA + 4, NMB = WTM / 32, SB = kSlot<WTM> * 2;
-  static_assert(NS == 4, "the unrolling over the slots");
+  constexpr int LA = kALoads<WTM>, L = LA + 4, NMB = WTM / 32, SB = kSlot<WTM> * 2, NS = kSlots<WTM>;
   auto addr = [&](int sl) { return ring + (uint32_t)sl * SB; };
 #pragma unroll
   for (int s = 0; s < NS - 2; ++s)
@@ -192,7 +196,7 @@ DEV void mainloop(uint32_t ring, int nsteps, Issue issue, f32x16_t (&acc)[4][4],
   bf::Frags f0, f1;
 #pragma unroll
   for (int g = 0; g < 8; ++g) ta.load(f0, 0, 0, g);
-  // step s in slot sl = s % 4
+  // step s in slot sl = s % NS
   auto phase1 = [&](int s, auto first, int sl) __attribute__((always_inline)) {
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
@@ -200,7 +204,7 @@ DEV void mainloop(uint32_t ring, int nsteps, Issue issue, f32x16_t (&acc)[4][4],
       __builtin_amdgcn_sched_barrier(0);
       mma1<NMB, decltype(first)::value>(f0, acc, g, 0);
       __builtin_amdgcn_sched_barrier(0);
-      if (g & 1) issue(s + NS - 2, addr((sl + 2) % NS), LA + (g >> 1));
+      if (g & 1) issue(s + NS - 2, addr((sl + NS - 2) % NS), LA + (g >> 1));
       __builtin_amdgcn_sched_barrier(0);
       mma1<NMB, decltype(first)::value>(f0, acc, g, 1);
       __builtin_amdgcn_sched_barrier(0);
@@ -214,7 +218,7 @@ DEV void mainloop(uint32_t ring, int nsteps, Issue issue, f32x16_t (&acc)[4][4],
       __builtin_amdgcn_sched_barrier(0);
       mma1<NMB>(f1, acc, g, 0);
       __builtin_amdgcn_sched_barrier(0);
-      if ((g & 1) && (g >> 1) < LA) issue(s + NS - 1, addr((sl + 3) % NS), g >> 1);
+      if ((g & 1) && (g >> 1) < LA) issue(s + NS - 1, addr((sl + NS - 1) % NS), g >> 1);
       __builtin_amdgcn_sched_barrier(0);
       mma1<NMB>(f1, acc, g, 1);
       __builtin_amdgcn_sched_barrier(0);

@@ -270,39 +270,14 @@ __global__ __launch_bounds__(norm_threads<TPR>) void norm_bwd_kernel(NormParams 
   }
 }
 
-// Column sums over the blocks' partial rows: 16 columns x 16 phases a
-// workgroup; phase p adds blocks [p B / 16, (p + 1) B / 16) ascending, then
-// the phases are added in order.
+// One launch for dweight and dbias: the second half of the grid sums the
+// columns after the first `cols`.
 __global__ __launch_bounds__(256) void block_sums_kernel(const float* part, int blocks, int64_t stride, int cols,
-                                                         void* out, void* out2, int out_bf16) {
-  __shared__ float s[16][17];
-  const int x = threadIdx.x & 15, p = threadIdx.x >> 4;
-  // the second half of the grid sums the columns after the first `cols`
-  const int halves = out2 ? 2 : 1, per = gridDim.x / halves;
-  const int half = (int)blockIdx.x >= per;
-  const int c = ((int)blockIdx.x - half * per) * 16 + x;
-  if (half) {
-    part += cols;
-    out = out2;
-  }
-  const int b0 = p * blocks / 16, b1 = (p + 1) * blocks / 16;
-  float v = 0.f;
-  if (c < cols) {
-    const float* q = part + (int64_t)b0 * stride + c;
-#pragma unroll 8
-    for (int b = b0; b < b1; ++b, q += stride) v = v + *q;
-  }
-  s[p][x] = v;
-  __syncthreads();
-  if (p == 0 && c < cols && out) {
-    v = s[0][x];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) v = v + s[i][x];
-    if (out_bf16)
-      ((uint16_t*)out)[c] = (uint16_t)f32_to_bf16(v);
-    else
-      ((float*)out)[c] = v;
-  }
+                                                         void* out, void* out2) {
+  const uint32_t per = (uint32_t)(cols + 15) / 16;
+  const bool second = blockIdx.x >= per;
+  block_sum16(second ? part + cols : part, blocks, stride, cols, second ? blockIdx.x - per : blockIdx.x,
+              second ? out2 : out, false);
 }
 
 int norm_bwd_blocks(int64_t rows, int64_t cols, bool bf16) {
@@ -355,8 +330,8 @@ hipError_t launch_norm_bwd(const NormParams& P, bool bf16, hipStream_t st) {
 }
 
 hipError_t launch_block_sums(const float* part, int blocks, int64_t stride, int cols, void* out, void* out2,
-                             bool out_bf16, hipStream_t st) {
-  block_sums_kernel<<<(cols + 15) / 16 * (out2 ? 2 : 1), 256, 0, st>>>(part, blocks, stride, cols, out, out2, out_bf16);
+                             hipStream_t st) {
+  block_sums_kernel<<<(cols + 15) / 16 * (out2 ? 2 : 1), 256, 0, st>>>(part, blocks, stride, cols, out, out2);
   return hipGetLastError();
 }
 
