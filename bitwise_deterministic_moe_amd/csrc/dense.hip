@@ -321,19 +321,19 @@ DEV f32x4_t frag(const float* s, int row, int q, int half) {
 }
 }  // namespace f32t
 
-template <int FORM, int MB, int NB, bool V4>
-__global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
+// The product of a tile over its slices, for the tile of SUB slices of 16.
+template <int FORM, int MB, int NB, bool V4, int SUB>
+DEV void f32_loop(const DenseParams& P, const DenseTile& t, float (*sa)[f32t::OPER<MB>], float (*sb)[f32t::OPER<NB>],
+                  f32x16_t (&acc)[MB][NB]) {
   using namespace f32t;
   static_assert(FORM != kFormGlu || NB == 2, "a wave holds g and u of the same columns");
-  __shared__ __attribute__((aligned(16))) float sa[kAhead][OPER<MB>], sb[kAhead][OPER<NB>];
-  constexpr int BM = 64 * MB, BNv = FORM == kFormGlu ? 32 * NB : 64 * NB;
+  constexpr int BM = 64 * MB;
   constexpr bool AK = FORM != kFormDw, BKC = FORM == kFormDx;
-  DenseTile t;
-  if (!dense_tile<FORM>(P, BM, BNv, BK, t)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
   const int r32 = lane & 31, half = lane >> 5;
   const int mvalid = (int)(P.M - t.m0 < BM ? P.M - t.m0 : BM), nvalid = P.N - t.n0;
-  const int steps_seg = (int)((P.K + BK - 1) / BK);
+  const int steps_seg = (int)((P.K + BK * SUB - 1) / (BK * SUB));
+  const int s0 = t.s0 * SUB, s1 = t.s1 * SUB;
   // the gated product's B slice is one load a thread from each matrix,
   // columns 0..63 of the LDS tile from wg, 64..127 from wu
   constexpr int OB = FORM == kFormGlu ? 1 : NB;
@@ -343,10 +343,11 @@ __global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
   ob.init(tid, P.ldb, nvalid);
   f32x4_t ra[kAhead][MB], rb[kAhead][NB];
   auto load = [&](f32x4_t (&va)[MB], f32x4_t (&vb)[NB], int s) __attribute__((always_inline)) {
-    const bool second = FORM == kFormDx && s >= steps_seg;
-    const int64_t k = (int64_t)(second ? s - steps_seg : s) * BK;
+    const int whole = s / SUB;
+    const bool second = FORM == kFormDx && whole >= steps_seg;
+    const int64_t k = (int64_t)(second ? whole - steps_seg : whole) * (BK * SUB) + s % SUB * BK;
     // past the last slice nothing is left to load
-    const int left = s < t.s1 ? (int)(P.K - k < BK ? P.K - k : BK) : 0;
+    const int left = s < s1 ? (int)(P.K - k < BK ? P.K - k : BK) : 0;
     const float* pa = (const float*)P.a + (AK ? t.m0 * P.lda + (second ? P.seg : 0) + k : k * P.lda + t.m0);
     oa.load(va, rsrc(pa), left);
     if constexpr (FORM == kFormDx) {
@@ -369,7 +370,6 @@ __global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
       ob.store(s, v);
     }
   };
-  f32x16_t acc[MB][NB];
 #pragma unroll
   for (int a = 0; a < MB; ++a)
 #pragma unroll
@@ -420,20 +420,29 @@ __global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
     __syncthreads();
   };
 #pragma unroll
-  for (int j = 0; j < kAhead; ++j) load(ra[j], rb[j], t.s0 + j);
-  int s = t.s0;
+  for (int j = 0; j < kAhead; ++j) load(ra[j], rb[j], s0 + j);
+  int s = s0;
   fill(J0{}, s + 3);
   fill(J1{}, s + 4);
   __syncthreads();
   read(f0, 0, 0);
 #pragma unroll 1
-  for (; s + 3 <= t.s1; s += 3) {
+  for (; s + 3 <= s1; s += 3) {
     step(s, J0{}, J2{});
     step(s + 1, J1{}, J0{});
     step(s + 2, J2{}, J1{});
   }
-  if (s < t.s1) step(s, J0{}, J2{});
-  if (s + 1 < t.s1) step(s + 1, J1{}, J0{});
+  if (s < s1) step(s, J0{}, J2{});
+  if (s + 1 < s1) step(s + 1, J1{}, J0{});
+}
+
+// The epilogue of a tile whose wave holds MB x NB blocks.
+template <int FORM, int MB, int NB>
+DEV void f32_store(const DenseParams& P, const DenseTile& t, f32x16_t (&acc)[MB][NB]) {
+  constexpr int BM = 64 * MB;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+  const int r32 = lane & 31, half = lane >> 5;
+  const int mvalid = (int)(P.M - t.m0 < BM ? P.M - t.m0 : BM);
   // lane l holds row l % 32 and columns 8 i + 4 (l / 32) + 0..3 of each
   // block; one loop body for all blocks, whose registers are picked by
   // uniform branches
@@ -469,6 +478,314 @@ __global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
         emit<float, FORM, 4, true, false>(P, t.seg, at, v);
     }
   }
+}
+
+template <int FORM, int MB, int NB, bool V4>
+__global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
+  using namespace f32t;
+  __shared__ __attribute__((aligned(16))) float sa[kAhead][OPER<MB>], sb[kAhead][OPER<NB>];
+  DenseTile t;
+  if (!dense_tile<FORM>(P, 64 * MB, FORM == kFormGlu ? 32 * NB : 64 * NB, BK, t)) return;
+  f32x16_t acc[MB][NB];
+  f32_loop<FORM, MB, NB, V4, 1>(P, t, sa, sb, acc);
+  f32_store<FORM, MB, NB>(P, t, acc);
+}
+
+// ------------------------------------------------- float32 tiles in three parts
+// The same 128 x 128 tile (64 columns of both matrices for the gated product)
+// at the rate of the bf16 matrix instructions.  A float32 number is the exact
+// sum of three bf16 numbers, its significand cut into three runs of 8 bits:
+//   x = h + m + l,   h = cut(x),  m = cut(x - h),  l = x - h - m,
+// |m| < 2^-7 |x| and |l| < 2^-15 |x|, all of x's sign, so
+//   a b = l_a h_b + h_a l_b + m_a m_b + m_a h_b + h_a m_b + h_a h_b + e,
+// where e, the three products left out, lies between 0 and 2^-21 a b, 2^-25 a b on
+// average: a common factor of the result below the rounding of one float32
+// product, beside a part that differs from product to product.  (Against float64,
+// 4096^3 normal numbers: 1.02e-6 of the norm, the library's float32 product
+// 1.15e-6; 2048^3: 7.1e-7 against 8.1e-7.)  Each product of two bf16
+// numbers is exact, the sums are float32.  Six v_mfma_f32_32x32x16_bf16 do the work
+// of eight v_mfma_f32_32x32x2f32 in three eighths of their time.
+//
+// An infinite or NaN number has no such parts: its m is NaN, which reaches every
+// sum it takes part in.  And what lies below 2^-133, the smallest bf16 number, is
+// lost of each operand: with |b| K < 2^29 less than 2^-24 of a sum of 2^-80.
+// So a sum that is not finite, or smaller than 2^-80 and not zero, is computed
+// again with the float32 instructions (with its whole tile, whose other sums stay
+// as they are) and is what a float32 product gives.  (Operands that are all
+// below 2^-133 count as zeros.)
+//
+// A slice is 32 k.  A thread loads 4 groups of four numbers of each operand two
+// slices ahead, splits the groups of the next-but-one slice between the
+// matrix instructions of the current one, and stores the parts into one of three LDS
+// buffers; each part is a [128][32] or [32][128] tile in the layouts of the bf16
+// kernels (no bank conflicts).
+namespace f32s {
+constexpr int BK = 32, PART = 128 * BK * 2, OPER = 3 * PART, BUF = 2 * OPER, NBUF = 3;   // bytes
+
+// The groups of four that a thread loads: K-contiguous, rows tid / 8 + 32 i and
+// k = 4 (tid % 8); M/N-contiguous, k = tid / 32 + 8 i and columns 4 (tid % 32);
+// the gated product's B, k = tid / 16 + 16 (i % 2) and columns 4 (tid % 16)
+// of matrix i / 2.
+template <bool KCL, bool GLU, bool V4>
+struct Op {
+  int k0, n[4];
+  uint32_t off[4];
+  uint32_t dst[GLU ? 2 : 1];   // LDS byte offset of group 0 in a part (GLU: also of group 2)
+  DEV void init(int tid, int64_t ld, int valid) {
+    if constexpr (KCL) {
+      const int r = tid >> 3;
+      k0 = 4 * (tid & 7);
+      dst[0] = 2u * (uint32_t)(bf::kc_off(r, k0 >> 3) + (k0 & 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        off[i] = (uint32_t)(((r + 32 * i) * ld + k0) * 4);
+        n[i] = r + 32 * i < valid ? 1 : 0;
+      }
+    } else {
+      const int c = GLU ? 4 * (tid & 15) : 4 * (tid & 31);
+      k0 = GLU ? tid >> 4 : tid >> 5;
+      dst[0] = 2u * (uint32_t)dn::mnc128_off(k0, c);
+      if constexpr (GLU) dst[1] = 2u * (uint32_t)dn::mnc128_off(k0, 64 + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        off[i] = (uint32_t)(((k0 + kOf(i)) * ld + c) * 4);
+        n[i] = valid - c;
+      }
+    }
+  }
+  DEV static int kOf(int i) { return GLU ? 16 * (i & 1) : 8 * i; }
+  // group i of a slice with `left` k, from r
+  DEV f32x4_t load(__amdgpu_buffer_rsrc_t r, int i, int left) const {
+    if constexpr (KCL) return f32t::load4<V4>(r, off[i], n[i] ? left - k0 : 0);
+    return f32t::load4<V4>(r, off[i], k0 + kOf(i) < left ? n[i] : 0);
+  }
+  // group i's place: rows 32 i (K-contiguous) or k rows further, where the
+  // swizzles repeat
+  DEV uint32_t place(int i) const {
+    if constexpr (GLU) return dst[i >> 1] + 4096u * (i & 1);
+    return dst[0] + 2048u * i;
+  }
+};
+
+// The three parts of four numbers.
+DEV float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+DEV uint32_t upper_halves(float lo, float hi) {
+  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+DEV void split4(const f32x4_t& x, u32x2_t& h, u32x2_t& m, u32x2_t& l) {
+  float r[4], q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[i] = x[i] - cut(x[i]);
+    q[i] = r[i] - cut(r[i]);
+  }
+  h = u32x2_t{upper_halves(x[0], x[1]), upper_halves(x[2], x[3])};
+  m = u32x2_t{upper_halves(r[0], r[1]), upper_halves(r[2], r[3])};
+  l = u32x2_t{upper_halves(q[0], q[1]), upper_halves(q[2], q[3])};
+}
+
+// Fragment addresses of an operand's two 32-row blocks, relative to a buffer.
+template <bool KCL, bool GLU>
+struct Addr {
+  uint32_t a[4];
+  DEV void init(uint32_t base, int first, int lane) {
+    if constexpr (KCL) {
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) a[kk] = base + 2u * (uint32_t)bf::kc_off(first + (lane & 31), 2 * kk + (lane >> 5));
+    } else {
+      const int g = lane >> 4, i = lane & 15;
+      const int k = 8 * (g >> 1) + (i >> 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {   // block j / 2, rows k + 4 (j % 2)
+        const int mn = first + (GLU ? 64 : 32) * (j >> 1) + 16 * (g & 1) + 4 * (i & 3);
+        a[j] = base + 2u * (uint32_t)dn::mnc128_off(k + 4 * (j & 1), mn);
+      }
+    }
+  }
+  DEV bf16x8_t read(uint32_t buf, int block, int part, int kk) const {
+    if constexpr (KCL) {
+      const LDS_AS char* p = (const LDS_AS char*)(uintptr_t)(buf + a[kk]);
+      return __builtin_bit_cast(bf16x8_t, *(const LDS_AS u32x4_t*)(p + PART * part + 2048 * block));
+    } else {
+      const LDS_AS char* lo = (const LDS_AS char*)(uintptr_t)(buf + a[2 * block]);
+      const LDS_AS char* hi = (const LDS_AS char*)(uintptr_t)(buf + a[2 * block + 1]);
+      bf::v4i16 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS bf::v4i16*)(lo + PART * part + 4096 * kk));
+      bf::v4i16 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS bf::v4i16*)(hi + PART * part + 4096 * kk));
+      const u32x2_t l2 = __builtin_bit_cast(u32x2_t, x), h2 = __builtin_bit_cast(u32x2_t, y);
+      return __builtin_bit_cast(bf16x8_t, u32x4_t{l2[0], l2[1], h2[0], h2[1]});
+    }
+  }
+};
+// parts of A and B of the six products, smallest first: (l,h) (h,l) (m,m) (m,h) (h,m) (h,h)
+constexpr int kPa[6] = {2, 0, 1, 1, 0, 0}, kPb[6] = {0, 2, 1, 0, 1, 0};
+}  // namespace f32s
+
+template <int FORM, bool V4>
+__global__ __launch_bounds__(256) void dense_f32s_kernel(DenseParams P) {
+  using namespace f32s;
+  __shared__ __attribute__((aligned(16))) char lds[NBUF * BUF];
+  constexpr bool AK = FORM != kFormDw, BKC = FORM == kFormDx, GLU = FORM == kFormGlu;
+  DenseTile t;
+  if (!dense_tile<FORM>(P, 128, GLU ? 64 : 128, BK, t)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
+  const int mvalid = (int)(P.M - t.m0 < 128 ? P.M - t.m0 : 128), nvalid = P.N - t.n0;
+  const int steps_seg = (int)((P.K + BK - 1) / BK);
+  const uint32_t base = bf::lds_base(lds);
+  Op<AK, false, V4> oa;
+  Op<BKC, GLU, V4> ob;
+  oa.init(tid, P.lda, mvalid);
+  ob.init(tid, P.ldb, nvalid);
+  Addr<AK, false> fa;
+  Addr<BKC, GLU> fb;
+  fa.init(base, wm * 64, lane);
+  fb.init(base + OPER, GLU ? wn * 32 : wn * 64, lane);
+  f32x4_t ra[2][4], rb[2][4];
+  struct Src {   // where slice s comes from
+    __amdgpu_buffer_rsrc_t a, b, u;
+    int left;
+  };
+  auto src = [&](int s) __attribute__((always_inline)) {
+    const bool second = FORM == kFormDx && s >= steps_seg;
+    const int64_t k = (int64_t)(second ? s - steps_seg : s) * BK;
+    Src q;
+    q.left = s < t.s1 ? (int)(P.K - k < BK ? P.K - k : BK) : 0;   // past the last slice: nothing
+    q.a = f32t::rsrc((const float*)P.a + (AK ? t.m0 * P.lda + (second ? P.seg : 0) + k : k * P.lda + t.m0));
+    q.b = f32t::rsrc((const float*)(second ? P.b[1] : P.b[0]) +
+                     (BKC ? t.n0 * P.ldb + k : (FORM == kFormDw ? t.seg * P.seg : 0) + k * P.ldb + t.n0));
+    if constexpr (GLU) q.u = f32t::rsrc((const float*)P.b[1] + k * P.ldb + t.n0);
+    return q;
+  };
+  // group u (0..3 of A, 4..7 of B) of a slice
+  auto load1 = [&](f32x4_t (&va)[4], f32x4_t (&vb)[4], const Src& q, int u) __attribute__((always_inline)) {
+    if (u < 4)
+      va[u & 3] = oa.load(q.a, u & 3, q.left);
+    else
+      vb[u & 3] = ob.load(GLU && u >= 6 ? q.u : q.b, u & 3, q.left);
+  };
+  auto load = [&](f32x4_t (&va)[4], f32x4_t (&vb)[4], int s) __attribute__((always_inline)) {
+    const Src q = src(s);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) load1(va, vb, q, u);
+  };
+  // group u of a register set, split, into the buffer at buf
+  auto put = [&](const f32x4_t (&va)[4], const f32x4_t (&vb)[4], uint32_t buf, int u) __attribute__((always_inline)) {
+    u32x2_t h, m, l;
+    split4(u < 4 ? va[u & 3] : vb[u & 3], h, m, l);
+    LDS_AS char* p = (LDS_AS char*)(uintptr_t)(base + buf + (u < 4 ? oa.place(u & 3) : OPER + ob.place(u & 3)));
+    *(LDS_AS u32x2_t*)p = h;
+    *(LDS_AS u32x2_t*)(p + PART) = m;
+    *(LDS_AS u32x2_t*)(p + 2 * PART) = l;
+  };
+  struct Frag {
+    bf16x8_t a[2][3], b[2][3];
+  };
+  // third g of a half slice's fragments, in the order the products need them
+  auto read3 = [&](Frag& f, uint32_t buf, int kk, int g) __attribute__((always_inline)) {
+    const int pa = g == 0 ? 2 : g == 1 ? 0 : 1, pb = g == 0 ? 0 : g == 1 ? 2 : 1;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      f.a[x][pa] = fa.read(buf, x, pa, kk);
+      f.b[x][pb] = fb.read(buf, x, pb, kk);
+    }
+  };
+  f32x16_t acc[2][2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
+  // product j (0..23) of a k half: part pair j / 4, block j % 4
+  auto mul6 = [&](const Frag& f, int j0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = j0; j < j0 + 6; ++j) {
+      const int q = j >> 2, mb = (j >> 1) & 1, nb = j & 1;
+      acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[nb][kPb[q]], f.a[mb][kPa[q]], acc[mb][nb], 0, 0, 0);
+    }
+  };
+  // six products with the splitting of one group, its next load and a third of
+  // a fragment set between them.  (4096^3: 203 us a round of tiles; 206 us with the
+  // reads and loads in one run per half.)
+  auto mix = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one matrix instruction
+      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // four vector ones
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  Frag f0, f1;
+  // Slice s lies in buffer s % 3 (byte offsets c, n, w of slices s, s + 1, s +
+  // 2).  In step s the parts of slice s + 2 are stored from the set that holds it,
+  // which then loads slice s + 4; slice s + 1 was stored before the barrier that
+  // ended step s - 1, so its first half can be read before this step's barrier.
+  auto step = [&](f32x4_t (&va)[4], f32x4_t (&vb)[4], int s, uint32_t c, uint32_t n, uint32_t w) __attribute__((always_inline)) {
+    const Src q = src(s + 4);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      mul6(u < 4 ? f0 : f1, 6 * (u & 3));
+      put(va, vb, w, u);
+      load1(va, vb, q, u);
+      if (u < 3) read3(f1, c, 1, u);
+      if (u >= 4 && u < 7) read3(f0, n, 0, u - 4);
+      mix();
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // loads stay in flight
+  };
+  load(ra[0], rb[0], t.s0);
+  load(ra[1], rb[1], t.s0 + 1);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) put(ra[0], rb[0], 0, u);
+  load(ra[0], rb[0], t.s0 + 2);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) put(ra[1], rb[1], BUF, u);
+  load(ra[1], rb[1], t.s0 + 3);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+  for (int g = 0; g < 3; ++g) read3(f0, 0, 0, g);
+  uint32_t c = 0, n = BUF, w = 2 * BUF;
+  int s = t.s0;
+#pragma unroll 1
+  for (; s + 2 <= t.s1; s += 2) {
+    step(ra[0], rb[0], s, c, n, w);
+    step(ra[1], rb[1], s + 1, n, w, c);
+    const uint32_t x = c;   // two slices on
+    c = w;
+    w = n;
+    n = x;
+  }
+  if (s < t.s1) step(ra[0], rb[0], s, c, n, w);
+  // One bit a sum: not finite, or between 0 and 2^-80 (sums of rows and columns that
+  // do not exist are zeros, which are kept).  Whole words, opaque to the compiler,
+  // rather than 64 lane masks that live through the second loop.
+  uint32_t bad[2] = {0, 0};
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const uint32_t v = __float_as_uint(acc[a][b][r]) & 0x7fffffffu;
+        bad[a] |= (uint32_t)((v >= 0x7f800000u) | (v - 1 < 0x17800000u - 1)) << (16 * b + r);
+      }
+  asm volatile("" : "+v"(bad[0]), "+v"(bad[1]));
+  if (__syncthreads_or((bad[0] | bad[1]) != 0)) {
+    constexpr int A = f32t::kAhead * f32t::OPER<2>;
+    static_assert(2 * A * 4 <= NBUF * BUF, "the float32 buffers fit");
+    float* f = (float*)lds;
+    f32x16_t again[2][2];
+    f32_loop<FORM, 2, 2, V4, 2>(P, t, (float (*)[f32t::OPER<2>])f, (float (*)[f32t::OPER<2>])(f + A), again);
+    // the other sums keep their bits, whatever another row or column holds
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          acc[a][b][r] = bad[a] >> (16 * b + r) & 1 ? again[a][b][r] : acc[a][b][r];
+  }
+  f32_store<FORM, 2, 2>(P, t, acc);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -853,7 +1170,7 @@ int dense_tile_n(int form, bool bf16, int bm) {
 template <int FORM, bool V4>
 static void dense_f32_launch(const DenseParams& P, int bm, int64_t grid, hipStream_t st) {
   if (bm == 128)
-    dense_f32_kernel<FORM, 2, 2, V4><<<grid, 256, 0, st>>>(P);
+    dense_f32s_kernel<FORM, V4><<<grid, 256, 0, st>>>(P);
   else
     dense_f32_kernel<FORM, 1, FORM == kFormGlu ? 2 : 1, V4><<<grid, 256, 0, st>>>(P);
 }

@@ -61,22 +61,24 @@ constexpr int64_t kMaxPartialBytes = (int64_t)1 << 30;
 
 // A tile shape's cost in microseconds, measured on this card: `alone` per
 // slice of a workgroup that has a CU to itself, `busy` per slice and workgroup
-// of a CU that several share (a bf16 tile fills a CU: they follow each
-// other), `fixed` once (launch, first slice, epilogue).
+// of a CU that several share (all but the 64-row float32 tile fill a CU: they
+// follow each other), `fixed` once (launch, first slice, epilogue).
 //   bf16     256 rows: 0.77 (8192^3) to 0.85; 128 rows: 0.48 (4096 x 8192 x 2048)
-//   float32  128 x 128: 1.06 busy (4096^3), 64 x 64: 0.27
+//   float32  128 x 128 in three parts (slices of 32): 1.54 (4096^3); 64 x 64 (of
+//            16): 0.27 busy.  The two meet near 1024^3: 50 us and 27 us forward,
+//            at 2048^3 107 us and 147 us
 struct TileCost {
-  int bm;
+  int bm, bk;
   double alone, busy, fixed;
 };
-constexpr TileCost kBf16Tiles[2] = {{256, 0.8, 0.8, 9.0}, {128, 0.48, 0.48, 8.0}};
-constexpr TileCost kF32Tiles[2] = {{128, 1.3, 1.06, 7.0}, {64, 0.38, 0.27, 6.0}};
+constexpr TileCost kBf16Tiles[2] = {{256, 32, 0.8, 0.8, 9.0}, {128, 32, 0.48, 0.48, 8.0}};
+constexpr TileCost kF32Tiles[2] = {{128, 32, 1.5, 1.5, 9.0}, {64, 16, 0.38, 0.27, 6.0}};
 
 double estimate(const TileCost& c, int64_t wgs, int64_t steps, double width, int64_t S, double out_elems) {
   const double per_cu = (double)((wgs + kCUs - 1) / kCUs);
   const double shared = per_cu * c.busy, lone = c.alone;
   double t = c.fixed + (double)steps * width * (shared > lone ? shared : lone);
-  // bf16 tiles of a later round pay their epilogue again
+  // tiles that fill a CU: those of a later round pay their epilogue again
   if (c.alone == c.busy) t += (per_cu - 1) * 0.6 * c.fixed;
   // float32 partials written and read, and the launch that joins them
   if (S > 1) t += (double)S * out_elems * 8.0 / 4.5e6 + 4.0;
@@ -85,8 +87,6 @@ double estimate(const TileCost& c, int64_t wgs, int64_t steps, double width, int
 
 // Tile and number of K chunks of one product: the cheapest estimate.
 Choice choose(const Dense& d, int form, int64_t M, int64_t N, int nseg, int64_t K, int64_t ld_max) {
-  const int bk = d.bf16 ? 32 : 16;
-  const int64_t steps = (K + bk - 1) / bk * (form == kFormDx ? nseg : 1);
   const double outs = (double)M * N * (form == kFormDw ? nseg : form == kFormGlu ? 2 : 1);
   // the weight gradient's bf16 operands are addressed by 32-bit offsets from
   // the chunk's first row
@@ -97,6 +97,7 @@ Choice choose(const Dense& d, int form, int64_t M, int64_t N, int nseg, int64_t 
   for (int i = 0; i < 2; ++i) {
     const TileCost& c = d.bf16 ? kBf16Tiles[i] : kF32Tiles[i];
     const int bn = dense_tile_n(form, d.bf16, c.bm);
+    const int64_t steps = (K + c.bk - 1) / c.bk * (form == kFormDx ? nseg : 1);
     // the small float32 tile of the gated product is twice as wide as high
     const double width = !d.bf16 && form == kFormGlu && c.bm == 64 ? 2 : 1;
     const int64_t tiles = (M + c.bm - 1) / c.bm * ((N + bn - 1) / bn * (form == kFormDw ? nseg : 1));

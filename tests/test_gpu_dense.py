@@ -140,6 +140,14 @@ def test_linear(dtype, rows, d, f):
                  zdtype=dtype if d % 2 else "f32", gdtype="f32" if rows % 2 else dtype)
 
 
+# few rows and few columns: the rows of the weights are split between workgroups
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,d,f", [(1, 16384, 72), (5, 8200, 264), (12, 4100, 130), (48, 6001, 40)])
+def test_few_rows_in_chunks(dtype, rows, d, f):
+    _linear_case(dtype, rows, d, f, "silu", True, True, 8 if f % 8 == 0 else 3, "f32", "f32")
+    test_glu(dtype, rows, d, f)
+
+
 @pytest.mark.parametrize("act", list(moe.ACTIVATIONS))
 @pytest.mark.parametrize("rows", [5, 130])
 def test_linear_activations(act, rows):
@@ -254,6 +262,68 @@ def test_nan_and_inf_stay_in_their_rows(rows, dtype):
     w2[69, 199] = float("inf")
     got, _ = moe.moe_linear_fwd(x, w2)
     assert torch.equal(got[:, :199], want[:, :199]) and not torch.isfinite(got[:, 199]).any()
+
+
+# ------------------------------------------------ float32 products in three parts
+@pytest.mark.parametrize("rows,d,f", [(2050, 1031, 2047), (1900, 1540, 2052), (4100, 2049, 260)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_large_float32_products(rows, d, f, gated):
+    if gated:
+        test_glu("f32", rows, d, f)
+    else:
+        _linear_case("f32", rows, d, f, "gelu", True, True, 3 if d % 2 else 0, "f32", "f32")
+
+
+@pytest.mark.parametrize("n,d,f", [(2048, 512, 2048), (2051, 515, 2047)])
+def test_large_float32_products_at_the_ends_of_the_range(n, d, f):
+    """Infinite, NaN, near-largest and very small numbers give what float32
+    products of them give: each in its row, the finite ones within the bound."""
+    rng = np.random.default_rng(n)
+    x, w = (rng.standard_normal(s).astype(np.float32) for s in ((n, d), (d, f)))
+    top = np.finfo(np.float32).max
+    x[5] *= 2.0 ** -130                      # denormal
+    x[700] *= 2.0 ** -112
+    x[900] = 0
+    x[1000, 3] = top                         # above the largest bf16; its row stays finite:
+    w[3] *= 2.0 ** -10                       # |w| < 0.01
+    x[1, d - 1] = np.nan
+    x[300, 0] = np.inf
+    xd, wd = torch.from_numpy(x).to(DEV), torch.from_numpy(w).to(DEV)
+    y, _ = moe.moe_linear_fwd(xd, wd)
+    assert torch.isnan(y[1]).all() and not torch.isfinite(y[300]).any()
+    assert torch.equal(y[300].sign(), wd[0].sign())
+    assert not y[900].any()
+    rows = np.array([i for i in range(n) if i not in (1, 300)])
+    x64, w64 = x[rows].astype(np.float64), w.astype(np.float64)
+    # a number below 2^-126 is kept to 2^-150, and so is each sum
+    def tol(a, b):
+        return B.rounded(B.prod_err(a.shape[1], np.abs(a), np.abs(b)) + a.shape[1] * 2.0 ** -147, a @ b, B.U["f32"])
+    B.check(y[torch.from_numpy(rows).to(DEV)], x64 @ w64, tol(x64, w64), "y")
+    # a gradient that is small throughout
+    dy = (rng.standard_normal((n, f)) * 2.0 ** -120).astype(np.float32)
+    x[[1, 300, 1000]] = 1
+    xd = torch.from_numpy(x).to(DEV)
+    dx, dw, _ = moe.moe_linear_bwd(torch.from_numpy(dy).to(DEV), xd, wd, need_db=False)
+    a, x64 = dy.astype(np.float64), x.astype(np.float64)
+    B.check(dx, a @ w64.T, tol(a, w64.T), "dx")
+    B.check(dw, x64.T @ a, tol(x64.T, a), "dw")
+    da = torch.from_numpy(x[:, :1] * np.ones((1, f), np.float32)).to(DEV)
+    da[7, 9] = float("nan")
+    wu = torch.from_numpy(rng.standard_normal((d, f)).astype(np.float32)).to(DEV)
+    a, g, u = moe.moe_glu_fwd(xd, wd, wu, "relu", save=True)
+    xn = xd.clone()
+    xn[2, 2] = float("-inf")
+    an = moe.moe_glu_fwd(xn, wd, wu, "none")[0]
+    assert not torch.isfinite(an[2]).any()
+    keep = torch.arange(n, device=DEV) != 2
+    assert torch.equal(an[keep], moe.moe_glu_fwd(xd, wd, wu, "none")[0][keep])
+    want = moe.moe_glu_bwd(da.nan_to_num(0.5), xd, wd, wu, g, u, "relu")
+    got = moe.moe_glu_bwd(da, xd, wd, wu, g, u, "relu")
+    keep = torch.arange(n, device=DEV) != 7
+    assert torch.isnan(got[0][7]).all() and torch.equal(got[0][keep], want[0][keep])
+    cols = torch.arange(f, device=DEV) != 9
+    for i in (1, 2):
+        assert torch.isnan(got[i][:, 9]).all() and torch.equal(got[i][:, cols], want[i][:, cols])
 
 
 # --------------------------------------------------------- order and workspaces
