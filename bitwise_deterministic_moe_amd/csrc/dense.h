@@ -182,10 +182,15 @@ struct DenseParams {
 constexpr int kFewRowsBf16 = 64, kFewRowsF32 = 16;
 
 // bm: tile rows (bf16: 128 or 256; float32: 64 or 128)
-hipError_t launch_dense_gemm(const DenseParams& P, int form, bool bf16, int bm, hipStream_t st);
+hipError_t launch_dense_gemm(const DenseParams& P, int form, bool bf16, int tile, hipStream_t st);
 hipError_t launch_dense_few(const DenseParams& P, int form, bool bf16, hipStream_t st);
 hipError_t launch_dense_finish(const DenseParams& P, int form, bool bf16, hipStream_t st);
-int dense_tile_n(int form, bool bf16, int bm);   // columns of one matrix a tile covers
+// Rows, columns (of one matrix) and K slice of a tile
+struct DenseShape {
+  int bm, bn, bk;
+};
+constexpr int kDenseBf16Tiles = 4, kDenseF32Tiles = 2;
+DenseShape dense_shape(int form, bool bf16, int tile);
 
 // bf16 matrices [rows][cols] (row distance ld) into [rows][ldo], zeros past cols
 struct DensePackParams {

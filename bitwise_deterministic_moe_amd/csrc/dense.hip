@@ -248,6 +248,130 @@ __global__ __launch_bounds__(256) void dense_bf16_kernel(DenseParams P) {
   dense_store_tile<FORM, WTM>(P, t, (float*)lds, acc, wm, wn, lane, wave);
 }
 
+// The small tiles: operands as above, two K slices of 32 a step.
+template <int FORM, int MB, int NB>
+__global__ __launch_bounds__(256) void dense_bf16_small_kernel(DenseParams P) {
+  using S = dn::Small<MB, NB>;
+  constexpr int BM = 64 * MB, BN = FORM == kFormGlu ? 64 : 64 * NB;
+  constexpr int ROW = 64 * NB + 4;   // floats of a staged row
+  static_assert(BM * ROW * 4 <= S::RING, "epilogue stage must fit in the ring");
+  __shared__ __attribute__((aligned(16))) uint16_t lds[S::RING / 2];
+  DenseTile t;
+  if (!dense_tile<FORM>(P, BM, BN, dn::SBK, t)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const uint32_t ring = bf::lds_base(lds);
+  const uint32_t own = (uint32_t)wave * 1024u;   // this wave's share of a 64 x 32 part
+  const int nsteps = t.s1 - t.s0;
+  const int mvalid = (int)(P.M - t.m0 < BM ? P.M - t.m0 : BM), nvalid = P.N - t.n0;
+  f32x16_t acc[MB][NB];
+  if constexpr (FORM == kFormDw) {
+    const int64_t k0 = (int64_t)t.s0 * dn::SBK;
+    const int64_t kn = P.K - k0 < (int64_t)nsteps * dn::SBK ? P.K - k0 : (int64_t)nsteps * dn::SBK;
+    dn::MncOp<64, 1> oa[MB], ob[NB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+      oa[m].init((const uint16_t*)P.a + k0 * P.lda + t.m0, ((kn - 1) * P.lda + up8(mvalid)) * 2, wave, lane, 64 * m, mvalid,
+                 P.lda);
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+      ob[n].init((const uint16_t*)P.b[0] + k0 * P.ldb + t.seg * P.seg + t.n0, ((kn - 1) * P.ldb + up8(nvalid)) * 2, wave,
+                 lane, 64 * n, nvalid, P.ldb);
+    const uint32_t sa = (uint32_t)(dn::BK * P.lda * 2), sb = (uint32_t)(dn::BK * P.ldb * 2);
+    dn::small_mainloop<dn::MNC, dn::MNC, MB, NB>(ring, nsteps, [&](int h, uint32_t at, int i) {
+      if (i < MB)
+        oa[i < MB ? i : 0].issue(at, wave, 0, (uint32_t)h * sa);
+      else
+        ob[i < MB ? 0 : i - MB].issue(at, wave, 0, (uint32_t)h * sb);
+    }, acc, wm, wn, lane);
+  } else {
+    const int64_t a_cols = (FORM == kFormDx && P.nseg > 1 ? P.seg : 0) + up8(P.K);
+    dn::KcPart<MB> oa;
+    oa.init((const uint16_t*)P.a + t.m0 * P.lda, ((mvalid - 1) * P.lda + a_cols) * 2, wave, lane, mvalid, P.lda);
+    const int kc = dn::KcOp<1>::chunk(lane) * 8;
+    // half slices of a K segment
+    const int halves_seg = 2 * (int)((P.K + dn::SBK - 1) / dn::SBK);
+    if constexpr (FORM == kFormDx) {
+      const int rows = nvalid < BN ? nvalid : BN;
+      const int64_t eb = ((int64_t)(rows - 1) * P.ldb + up8(P.K)) * 2;
+      dn::KcPart<NB> ob;
+      ob.init((const uint16_t*)P.b[0] + (int64_t)t.n0 * P.ldb, eb, wave, lane, rows, P.ldb);
+      const bf::i32x4_t rs1 = bf::make_rsrc((const uint16_t*)P.b[P.nseg - 1] + (int64_t)t.n0 * P.ldb, (uint32_t)eb);
+      dn::small_mainloop<dn::KC, dn::KC, MB, NB>(ring, nsteps, [&](int h, uint32_t at, int i) {
+        const bool live = h < 2 * nsteps;
+        int ks = live ? 2 * t.s0 + h : 0;
+        const bool second = ks >= halves_seg;
+        if (second) ks -= halves_seg;
+        const bool ok = live && ks * dn::BK + kc < P.K;
+        if (i < MB)
+          bf::dma16(oa.rs, at + own, ok ? oa.voff[i < MB ? i : 0] : dn::kOOB,
+                    (uint32_t)ks * 64u + (second ? (uint32_t)P.seg * 2u : 0u));
+        else
+          bf::dma16(second ? rs1 : ob.rs, at + own, ok ? ob.voff[i < MB ? 0 : i - MB] : dn::kOOB, (uint32_t)ks * 64u);
+      }, acc, wm, wn, lane);
+    } else {
+      const int64_t k0 = (int64_t)t.s0 * dn::SBK, kn = P.K - k0;
+      const uint32_t sb = (uint32_t)(dn::BK * P.ldb * 2);
+      dn::MncOp<64, 1> ob[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+        ob[n].init((const uint16_t*)P.b[FORM == kFormGlu ? n : 0] + k0 * P.ldb + t.n0,
+                   ((kn - 1) * P.ldb + up8(nvalid)) * 2, wave, lane, FORM == kFormGlu ? 0 : 64 * n, nvalid, P.ldb);
+      dn::small_mainloop<dn::KC, dn::MNC, MB, NB>(ring, nsteps, [&](int h, uint32_t at, int i) {
+        const bool live = h < 2 * nsteps;
+        const int ks = live ? 2 * t.s0 + h : 0;
+        if (i < MB)
+          bf::dma16(oa.rs, at + own, live && ks * dn::BK + kc < P.K ? oa.voff[i < MB ? i : 0] : dn::kOOB, (uint32_t)ks * 64u);
+        else
+          ob[i < MB ? 0 : i - MB].issue(at, wave, 0, (uint32_t)h * sb);
+      }, acc, wm, wn, lane);
+    }
+  }
+  // through LDS, so that 16 lanes write 64 columns of a row
+  float* stage = (float*)lds;
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(f32x4_t*)(stage + (mb * 64 + wm * 32 + (lane & 31)) * ROW + 64 * n + wn * 32 + 8 * i + 4 * (lane >> 5)) =
+            f32x4_t{acc[mb][n][4 * i], acc[mb][n][4 * i + 1], acc[mb][n][4 * i + 2], acc[mb][n][4 * i + 3]};
+  dense_lds_barrier();
+  const int c = (lane & 15) * 4, m = 4 * wave + (lane >> 4);
+  auto get = [&](int mb, int n, float (&v)[16]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4_t sv = *(const f32x4_t*)(stage + (mb * 64 + m + 16 * i) * ROW + 64 * n + c);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[4 * i + q] = sv[q];
+    }
+  };
+#pragma unroll 1
+  for (int p = 0; p < (FORM == kFormGlu ? MB : MB * NB); ++p) {
+    const int mb = FORM == kFormGlu ? p : p / NB, n = FORM == kFormGlu ? 0 : p % NB;
+    const int col = t.n0 + 64 * n + c;
+    if (col >= P.N) continue;
+    const AtRows at{t.m0 + mb * 64 + m, t.m0 + mvalid, 16, col};
+    float v[16];
+    get(mb, n, v);
+    if constexpr (FORM == kFormGlu) {
+      float u[16];
+      get(mb, 1, u);
+      if (P.S > 1) {
+        part<4>(P, t.chunk, 0, at, v);
+        part<4>(P, t.chunk, 1, at, u);
+      } else {
+        emit_glu<uint16_t, 4, false>(P, at, v, u);
+      }
+    } else if (P.S > 1) {
+      part<4>(P, t.chunk, t.seg, at, v);
+    } else {
+      emit<uint16_t, FORM, 4, false, false>(P, t.seg, at, v);
+    }
+  }
+}
+
 // ------------------------------------------------------------- float32 tiles
 // Tile (64 MB) x (64 NB) x 16 (the gated product: 32 NB columns of both
 // matrices, NB = 2), 4 waves of MB x NB blocks of v_mfma_f32_32x32x2f32.  A
@@ -1162,45 +1286,52 @@ __global__ __launch_bounds__(256) void dense_zero_kernel(uint16_t* p, int64_t n)
 }
 
 // -------------------------------------------------------------------- launches
-int dense_tile_n(int form, bool bf16, int bm) {
-  if (bf16) return form == kFormGlu ? 128 : 256;
-  return form == kFormGlu ? 64 : bm;
+DenseShape dense_shape(int form, bool bf16, int tile) {
+  static constexpr DenseShape kBf16[kDenseBf16Tiles] = {{256, 256, 32}, {128, 256, 32}, {128, 128, 64}, {64, 64, 64}};
+  static constexpr DenseShape kF32[kDenseF32Tiles] = {{128, 128, 32}, {64, 64, 16}};
+  DenseShape s = bf16 ? kBf16[tile] : kF32[tile];
+  // half the columns of both matrices; the 64-row tiles are twice as wide
+  if (form == kFormGlu && s.bm > 64) s.bn /= 2;
+  return s;
 }
 
 template <int FORM, bool V4>
-static void dense_f32_launch(const DenseParams& P, int bm, int64_t grid, hipStream_t st) {
-  if (bm == 128)
+static void dense_f32_launch(const DenseParams& P, int tile, int64_t grid, hipStream_t st) {
+  if (tile == 0)
     dense_f32s_kernel<FORM, V4><<<grid, 256, 0, st>>>(P);
   else
     dense_f32_kernel<FORM, 1, FORM == kFormGlu ? 2 : 1, V4><<<grid, 256, 0, st>>>(P);
 }
 
 template <int FORM>
-static void dense_gemm_launch(const DenseParams& P, bool bf16, int bm, int64_t grid, hipStream_t st) {
+static void dense_gemm_launch(const DenseParams& P, bool bf16, int tile, int64_t grid, hipStream_t st) {
   if (!bf16) {
     // whole groups of four along each operand's contiguous direction
     const bool ka = FORM != kFormDw, kb = FORM == kFormDx;
     const bool v4 = (ka ? P.K : P.M) % 4 == 0 && (kb ? P.K : P.N) % 4 == 0;
     if (v4)
-      dense_f32_launch<FORM, true>(P, bm, grid, st);
+      dense_f32_launch<FORM, true>(P, tile, grid, st);
     else
-      dense_f32_launch<FORM, false>(P, bm, grid, st);
-  } else if (bm == 256) {
-    dense_bf16_kernel<FORM, 128><<<grid, 256, 0, st>>>(P);
-  } else {
-    dense_bf16_kernel<FORM, 64><<<grid, 256, 0, st>>>(P);
+      dense_f32_launch<FORM, false>(P, tile, grid, st);
+    return;
+  }
+  switch (tile) {
+    case 0: dense_bf16_kernel<FORM, 128><<<grid, 256, 0, st>>>(P); break;
+    case 1: dense_bf16_kernel<FORM, 64><<<grid, 256, 0, st>>>(P); break;
+    case 2: dense_bf16_small_kernel<FORM, 2, 2><<<grid, 256, 0, st>>>(P); break;
+    default: dense_bf16_small_kernel<FORM, 1, FORM == kFormGlu ? 2 : 1><<<grid, 256, 0, st>>>(P); break;
   }
 }
 
-hipError_t launch_dense_gemm(const DenseParams& P, int form, bool bf16, int bm, hipStream_t st) {
-  const int bn = dense_tile_n(form, bf16, bm);
-  const int64_t tiles = (P.M + bm - 1) / bm * ((P.N + bn - 1) / bn) * (form == kFormDw ? P.nseg : 1);
+hipError_t launch_dense_gemm(const DenseParams& P, int form, bool bf16, int tile, hipStream_t st) {
+  const DenseShape sh = dense_shape(form, bf16, tile);
+  const int64_t tiles = (P.M + sh.bm - 1) / sh.bm * ((P.N + sh.bn - 1) / sh.bn) * (form == kFormDw ? P.nseg : 1);
   const int64_t grid = grid_for_units(tiles * P.S);
   switch (form) {
-    case kFormLinear: dense_gemm_launch<kFormLinear>(P, bf16, bm, grid, st); break;
-    case kFormGlu: dense_gemm_launch<kFormGlu>(P, bf16, bm, grid, st); break;
-    case kFormDx: dense_gemm_launch<kFormDx>(P, bf16, bm, grid, st); break;
-    default: dense_gemm_launch<kFormDw>(P, bf16, bm, grid, st); break;
+    case kFormLinear: dense_gemm_launch<kFormLinear>(P, bf16, tile, grid, st); break;
+    case kFormGlu: dense_gemm_launch<kFormGlu>(P, bf16, tile, grid, st); break;
+    case kFormDx: dense_gemm_launch<kFormDx>(P, bf16, tile, grid, st); break;
+    default: dense_gemm_launch<kFormDw>(P, bf16, tile, grid, st); break;
   }
   return hipGetLastError();
 }

@@ -54,38 +54,58 @@ bool direct(const Dense& d, int64_t cols, int64_t ld) { return !d.bf16 || (cols 
 
 // --------------------------------------------------------- tile and split choice
 struct Choice {
-  int bm, S;
+  int tile, S;
 };
 constexpr int kCUs = 256;
 constexpr int64_t kMaxPartialBytes = (int64_t)1 << 30;
+constexpr int64_t kMaxUnits = ((int64_t)1 << 24) - 8;   // workgroups of 256 in a launch
 
-// A tile shape's cost in microseconds, measured on this card: `alone` per
-// slice of a workgroup that has a CU to itself, `busy` per slice and workgroup
-// of a CU that several share (all but the 64-row float32 tile fill a CU: they
-// follow each other), `fixed` once (launch, first slice, epilogue).
-//   bf16     256 rows: 0.77 (8192^3) to 0.85; 128 rows: 0.48 (4096 x 8192 x 2048)
-//   float32  128 x 128 in three parts (slices of 32): 1.54 (4096^3); 64 x 64 (of
-//            16): 0.27 busy.  The two meet near 1024^3: 50 us and 27 us forward,
-//            at 2048^3 107 us and 147 us
+// A tile's cost in microseconds, measured on this card, by dense_shape's
+// numbers.  `fixed`: launch, first slice, epilogue.  Per K slice and workgroup:
+// `alone` while at most half of the CUs have one, `busy` when all do (they share the
+// caches' bandwidth); where several workgroups fit on a CU (`shares`), `alone`
+// for one and `busy` for each of several.
+//   bf16     256 x 256: 0.77 (8192^3) to 0.85; 128 x 256: 0.48 (4096 x 8192 x 2048),
+//            0.36 on half the CUs; 128 x 128 (slices of 64): 0.54 (2048^3), 0.38;
+//            64 x 64 (of 64): 0.2 alone, 0.23 each of two, 1.6 of it for both
+//            matrices of the gated product.
+//            512^3 takes 5.9 us with the 64 x 64 tile, 9 with 128 x 128 and 13.6
+//            with 128 x 256; 2048^3 35, 24 and 31; 4096 x 2048 x 8192 240,
+//            167 and 125 (with 256 x 256)
+//   float32  128 x 128 in three parts: 1.54 (4096^3); 64 x 64 (slices of 16): 0.27 of
+//            several.  They meet near 1024^3: 50 us and 27 us forward, at 2048^3
+//            107 us and 147 us
 struct TileCost {
-  int bm, bk;
   double alone, busy, fixed;
+  bool shares;
 };
-constexpr TileCost kBf16Tiles[2] = {{256, 32, 0.8, 0.8, 9.0}, {128, 32, 0.48, 0.48, 8.0}};
-constexpr TileCost kF32Tiles[2] = {{128, 32, 1.5, 1.5, 9.0}, {64, 16, 0.38, 0.27, 6.0}};
+constexpr TileCost kBf16Tiles[] = {{0.7, 0.8, 9.0, false}, {0.36, 0.48, 8.0, false}, {0.38, 0.52, 5.8, false}, {0.2, 0.23, 4.5, true}};
+constexpr TileCost kF32Tiles[] = {{1.5, 1.5, 9.0, false}, {0.38, 0.27, 6.0, true}};
 
 double estimate(const TileCost& c, int64_t wgs, int64_t steps, double width, int64_t S, double out_elems) {
   const double per_cu = (double)((wgs + kCUs - 1) / kCUs);
-  const double shared = per_cu * c.busy, lone = c.alone;
-  double t = c.fixed + (double)steps * width * (shared > lone ? shared : lone);
-  // tiles that fill a CU: those of a later round pay their epilogue again
-  if (c.alone == c.busy) t += (per_cu - 1) * 0.6 * c.fixed;
-  // float32 partials written and read, and the launch that joins them
-  if (S > 1) t += (double)S * out_elems * 8.0 / 4.5e6 + 4.0;
+  double slice, t = c.fixed;
+  if (c.shares) {
+    slice = per_cu * c.busy > c.alone ? per_cu * c.busy : c.alone;
+  } else {
+    const double over = 2.0 * (double)wgs / kCUs - 1;
+    slice = per_cu * (over <= 0 ? c.alone : over >= 1 ? c.busy : c.alone + over * (c.busy - c.alone));
+    // later rounds pay their epilogue again
+    t += (per_cu - 1) * 0.6 * c.fixed;
+  }
+  t += (double)steps * width * slice;
+  // float32 partials written and read, mostly in the caches, and the launch that
+  // joins them
+  if (S > 1) t += (double)S * out_elems * 8.0 / 1e7 + 3.0;
   return t;
 }
 
-// Tile and number of K chunks of one product: the cheapest estimate.
+// Whether one launch copies x into rows of ld elements, beside the weights and the
+// elementwise pass (together at most 2^22 workgroups).
+bool copies_fit(const Dense& d, int64_t ld) { return d.T * (ld / 8) / 256 < kMaxUnits - (1 << 22); }
+
+// Tile and number of K chunks of one product: the cheapest estimate.  S = 0 if
+// no tile covers it in one launch.
 Choice choose(const Dense& d, int form, int64_t M, int64_t N, int nseg, int64_t K, int64_t ld_max) {
   const double outs = (double)M * N * (form == kFormDw ? nseg : form == kFormGlu ? 2 : 1);
   // the weight gradient's bf16 operands are addressed by 32-bit offsets from
@@ -94,19 +114,20 @@ Choice choose(const Dense& d, int form, int64_t M, int64_t N, int nseg, int64_t 
   if (form == kFormDw && d.bf16) smin = (K + 64) * ld_max * 2 / ((int64_t)1 << 30) + 1;
   Choice best{0, 0};
   double tb = 0;
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < (d.bf16 ? kDenseBf16Tiles : kDenseF32Tiles); ++i) {
     const TileCost& c = d.bf16 ? kBf16Tiles[i] : kF32Tiles[i];
-    const int bn = dense_tile_n(form, d.bf16, c.bm);
-    const int64_t steps = (K + c.bk - 1) / c.bk * (form == kFormDx ? nseg : 1);
-    // the small float32 tile of the gated product is twice as wide as high
-    const double width = !d.bf16 && form == kFormGlu && c.bm == 64 ? 2 : 1;
-    const int64_t tiles = (M + c.bm - 1) / c.bm * ((N + bn - 1) / bn * (form == kFormDw ? nseg : 1));
+    const DenseShape sh = dense_shape(form, d.bf16, i);
+    const int64_t steps = (K + sh.bk - 1) / sh.bk * (form == kFormDx ? nseg : 1);
+    // the 64-row tile of the gated product is twice as wide as high
+    const double width = form == kFormGlu && sh.bm == 64 ? (d.bf16 ? 1.6 : 2) : 1;
+    const int64_t tiles = (M + sh.bm - 1) / sh.bm * ((N + sh.bn - 1) / sh.bn * (form == kFormDw ? nseg : 1));
     const int64_t smax = smin > 32 ? smin : 32;
     for (int64_t S = smin; S <= smax; ++S) {
       if (S > smin && (steps / S < 4 || S * outs * 4 > kMaxPartialBytes || tiles * (S - 1) >= 4 * kCUs)) break;
+      if (tiles * S > kMaxUnits) break;
       const double t = estimate(c, tiles * S, (steps + S - 1) / S, width, S, outs);
       if (best.S == 0 || t < tb * 0.98) {
-        best = Choice{c.bm, (int)S};
+        best = Choice{i, (int)S};
         tb = t;
       }
     }
@@ -157,6 +178,7 @@ FwdPlan fwd_plan(const moe_dense* p, const Dense& d) {
     f.ch = choose(d, form, d.T, d.F, 1, d.D, 0);
     if (f.pack_x) {
       f.ldx = up(d.D, 8);
+      if (!copies_fit(d, f.ldx)) f.ch.S = 0;
       f.x = o;
       o += align_up((size_t)d.T * f.ldx * 2);
     }
@@ -214,6 +236,7 @@ BwdPlan bwd_plan(const moe_dense* p, const Dense& d) {
   if (d.nm == 1) o += align_up((size_t)b.ew_blocks * d.F * 4);
   b.dx = choose(d, kFormDx, d.T, d.D, d.nm, d.F, 0);
   b.dw = choose(d, kFormDw, d.D, d.F, d.nm, d.T, b.ldx > b.lddz ? b.ldx : b.lddz);
+  if (b.pack_x && !copies_fit(d, b.ldx)) b.dx.S = 0;
   b.dx_ld = up(d.D, 4);
   b.dw_seg = up(d.F, 4);
   // both products' partials live until the joining launch at the end
@@ -277,6 +300,7 @@ moe_status forward(const moe_dense* p, int nm, const void* x, const void* w0, co
   for (const void* q : {x, w0, w1, bias, residual, (const void*)y, (const void*)z0, (const void*)z1})
     if ((uintptr_t)q & (q == bias ? d.es - 1 : 15)) return MOE_ERR_SHAPE;
   const FwdPlan f = fwd_plan(p, d);
+  if (!f.ch.S) return MOE_ERR_SHAPE;
   if ((s = check_ws(ws, ws_bytes, f.total)) != MOE_OK) return s;
   const void* w[2] = {w0, w1};
   MOE_TRY(launch_dense_pack(
@@ -310,7 +334,7 @@ moe_status forward(const moe_dense* p, int nm, const void* x, const void* w0, co
   if (f.few)
     MOE_TRY(launch_dense_few(P, form, d.bf16, st));
   else
-    MOE_TRY(launch_dense_gemm(P, form, d.bf16, f.ch.bm, st));
+    MOE_TRY(launch_dense_gemm(P, form, d.bf16, f.ch.tile, st));
   if (P.S > 1) MOE_TRY(launch_dense_finish(P, form, d.bf16, st));
   return MOE_OK;
 }
@@ -339,6 +363,7 @@ moe_status backward(const moe_dense* p, int nm, const void* dy, const void* x, c
     return MOE_OK;
   }
   const BwdPlan b = bwd_plan(p, d);
+  if (!b.dx.S || !b.dw.S) return MOE_ERR_SHAPE;
   if ((s = check_ws(ws, ws_bytes, b.total)) != MOE_OK) return s;
   char* base = (char*)ws;
   const void* w[2] = {w0, w1};
@@ -388,7 +413,7 @@ moe_status backward(const moe_dense* p, int nm, const void* dy, const void* x, c
   P.c[0] = dx;
   P.ldc = d.D;
   P.seed = p->debug_shuffle_seed;
-  MOE_TRY(launch_dense_gemm(P, kFormDx, d.bf16, b.dx.bm, st));
+  MOE_TRY(launch_dense_gemm(P, kFormDx, d.bf16, b.dx.tile, st));
   DenseParams W{};
   W.M = d.D;
   W.N = d.F;
@@ -408,7 +433,7 @@ moe_status backward(const moe_dense* p, int nm, const void* dy, const void* x, c
   W.ldc = d.F;
   W.c_f32 = g32;
   W.seed = p->debug_shuffle_seed;
-  MOE_TRY(launch_dense_gemm(W, kFormDw, d.bf16, b.dw.bm, st));
+  MOE_TRY(launch_dense_gemm(W, kFormDw, d.bf16, b.dw.tile, st));
   return hip_status(launch_dense_join(P, W, (const float*)(base + b.colsum), b.ew_blocks, d.F, db, !g32 && d.bf16, d.bf16, st));
 }
 

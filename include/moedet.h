@@ -726,7 +726,9 @@ moe_status moe_layernorm_bwd(const void* dy, const void* x, const void* weight, 
  *            (unread without one)
  *   debug_shuffle_seed  0, or a test-only seed that shuffles the launch order
  * Each weight matrix (D * ldw elements) is below 2 GiB, and every ld below
- * 2^20; the other matrices have no limit of their own. */
+ * 2^20; the other matrices have no limit of their own.  A call whose tiles, or
+ * whose copy of an unaligned x, would take more than 2^24 workgroups is
+ * refused (MOE_ERR_SHAPE). */
 typedef struct moe_dense {
   int64_t rows;
   int32_t d_in;

@@ -160,6 +160,21 @@ def test_description_status(bad, status):
     assert lib.moe_glu_bwd(c, p, p, p, p, p, p, p, p, p, p, p, 1 << 40, None) == status
 
 
+# more tiles, or more of x to copy, than one launch covers
+@pytest.mark.parametrize("big", [dict(dtype=0, rows=(1 << 31) - 1, d_in=1, d_out=1), dict(rows=(1 << 31) - 1, d_in=4096, d_out=4096),
+                                 dict(rows=1 << 22, d_in=8199, d_out=8)])
+def test_rows_past_one_launch(big):
+    lib, p = moe.load_library(), PTR
+    v = dict(rows=100, d_in=64, d_out=96)
+    v.update(big)
+    v.update(ldx=v["d_in"], ldw=v["d_out"], ldy=v["d_out"], ldz=v["d_out"])
+    c = _desc(**v)
+    assert lib.moe_linear_fwd(c, p, p, p, None, p, p, p, 1 << 62, None) == SHAPE
+    assert lib.moe_linear_bwd(c, p, p, p, p, None, p, p, p, p, 1 << 62, None) == SHAPE
+    assert lib.moe_glu_fwd(c, p, p, p, p, p, p, p, 1 << 62, None) == SHAPE
+    assert lib.moe_glu_bwd(c, p, p, p, p, p, p, None, p, p, p, p, 1 << 62, None) == SHAPE
+
+
 def test_pointer_and_workspace_status():
     lib, p = moe.load_library(), PTR
     big = 1 << 40

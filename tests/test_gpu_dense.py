@@ -264,6 +264,14 @@ def test_nan_and_inf_stay_in_their_rows(rows, dtype):
     assert torch.equal(got[:, :199], want[:, :199]) and not torch.isfinite(got[:, 199]).any()
 
 
+# products for each of the bf16 tiles, whole and ragged, split and unsplit
+@pytest.mark.parametrize("rows,d,f", [(1030, 1032, 1040), (2000, 2056, 2049), (2049, 512, 2320), (1100, 2048, 4360),
+                                      (130, 4104, 264)])
+def test_bf16_tiles(rows, d, f):
+    _linear_case("bf16", rows, d, f, "gelu", True, True, 8 if f % 8 == 0 else 0, "f32", "bf16")
+    test_glu("bf16", rows, d, f)
+
+
 # ------------------------------------------------ float32 products in three parts
 @pytest.mark.parametrize("rows,d,f", [(2050, 1031, 2047), (1900, 1540, 2052), (4100, 2049, 260)])
 @pytest.mark.parametrize("gated", [False, True])
