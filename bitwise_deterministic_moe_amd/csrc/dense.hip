@@ -249,9 +249,9 @@ __global__ __launch_bounds__(256) void dense_bf16_kernel(DenseParams P) {
 }
 
 // The small tiles: operands as above, two K slices of 32 a step.
-template <int FORM, int MB, int NB>
+template <int FORM, int MB, int NB, bool SHORT>
 __global__ __launch_bounds__(256) void dense_bf16_small_kernel(DenseParams P) {
-  using S = dn::Small<MB, NB>;
+  using S = dn::Small<MB, NB, SHORT>;
   constexpr int BM = 64 * MB, BN = FORM == kFormGlu ? 64 : 64 * NB;
   constexpr int ROW = 64 * NB + 4;   // floats of a staged row
   static_assert(BM * ROW * 4 <= S::RING, "epilogue stage must fit in the ring");
@@ -278,7 +278,7 @@ __global__ __launch_bounds__(256) void dense_bf16_small_kernel(DenseParams P) {
       ob[n].init((const uint16_t*)P.b[0] + k0 * P.ldb + t.seg * P.seg + t.n0, ((kn - 1) * P.ldb + up8(nvalid)) * 2, wave,
                  lane, 64 * n, nvalid, P.ldb);
     const uint32_t sa = (uint32_t)(dn::BK * P.lda * 2), sb = (uint32_t)(dn::BK * P.ldb * 2);
-    dn::small_mainloop<dn::MNC, dn::MNC, MB, NB>(ring, nsteps, [&](int h, uint32_t at, int i) {
+    dn::small_mainloop<dn::MNC, dn::MNC, MB, NB, SHORT>(ring, nsteps, [&](int h, uint32_t at, int i) {
       if (i < MB)
         oa[i < MB ? i : 0].issue(at, wave, 0, (uint32_t)h * sa);
       else
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(256) void dense_bf16_small_kernel(DenseParams P) {
       dn::KcPart<NB> ob;
       ob.init((const uint16_t*)P.b[0] + (int64_t)t.n0 * P.ldb, eb, wave, lane, rows, P.ldb);
       const bf::i32x4_t rs1 = bf::make_rsrc((const uint16_t*)P.b[P.nseg - 1] + (int64_t)t.n0 * P.ldb, (uint32_t)eb);
-      dn::small_mainloop<dn::KC, dn::KC, MB, NB>(ring, nsteps, [&](int h, uint32_t at, int i) {
+      dn::small_mainloop<dn::KC, dn::KC, MB, NB, SHORT>(ring, nsteps, [&](int h, uint32_t at, int i) {
         const bool live = h < 2 * nsteps;
         int ks = live ? 2 * t.s0 + h : 0;
         const bool second = ks >= halves_seg;
@@ -317,7 +317,7 @@ __global__ __launch_bounds__(256) void dense_bf16_small_kernel(DenseParams P) {
       for (int n = 0; n < NB; ++n)
         ob[n].init((const uint16_t*)P.b[FORM == kFormGlu ? n : 0] + k0 * P.ldb + t.n0,
                    ((kn - 1) * P.ldb + up8(nvalid)) * 2, wave, lane, FORM == kFormGlu ? 0 : 64 * n, nvalid, P.ldb);
-      dn::small_mainloop<dn::KC, dn::MNC, MB, NB>(ring, nsteps, [&](int h, uint32_t at, int i) {
+      dn::small_mainloop<dn::KC, dn::MNC, MB, NB, SHORT>(ring, nsteps, [&](int h, uint32_t at, int i) {
         const bool live = h < 2 * nsteps;
         const int ks = live ? 2 * t.s0 + h : 0;
         if (i < MB)
@@ -362,12 +362,12 @@ __global__ __launch_bounds__(256) void dense_bf16_small_kernel(DenseParams P) {
         part<4>(P, t.chunk, 0, at, v);
         part<4>(P, t.chunk, 1, at, u);
       } else {
-        emit_glu<uint16_t, 4, false>(P, at, v, u);
+        emit_glu<uint16_t, 4, SHORT>(P, at, v, u);
       }
     } else if (P.S > 1) {
       part<4>(P, t.chunk, t.seg, at, v);
     } else {
-      emit<uint16_t, FORM, 4, false, false>(P, t.seg, at, v);
+      emit<uint16_t, FORM, 4, SHORT, false>(P, t.seg, at, v);
     }
   }
 }
@@ -1318,8 +1318,15 @@ static void dense_gemm_launch(const DenseParams& P, bool bf16, int tile, int64_t
   switch (tile) {
     case 0: dense_bf16_kernel<FORM, 128><<<grid, 256, 0, st>>>(P); break;
     case 1: dense_bf16_kernel<FORM, 64><<<grid, 256, 0, st>>>(P); break;
-    case 2: dense_bf16_small_kernel<FORM, 2, 2><<<grid, 256, 0, st>>>(P); break;
-    default: dense_bf16_small_kernel<FORM, 1, FORM == kFormGlu ? 2 : 1><<<grid, 256, 0, st>>>(P); break;
+    case 2: dense_bf16_small_kernel<FORM, 2, 2, false><<<grid, 256, 0, st>>>(P); break;
+    default: {
+      constexpr int NB = FORM == kFormGlu ? 2 : 1;
+      const int64_t steps = (P.K + dn::SBK - 1) / dn::SBK * (FORM == kFormDx ? P.nseg : 1);
+      if (steps <= 2 * (int64_t)P.S)
+        dense_bf16_small_kernel<FORM, 1, NB, true><<<grid, 256, 0, st>>>(P);
+      else
+        dense_bf16_small_kernel<FORM, 1, NB, false><<<grid, 256, 0, st>>>(P);
+    }
   }
 }
 
@@ -1349,12 +1356,10 @@ static void dense_few_form(const DenseParams& P, bool bf16, hipStream_t st) {
     dense_few_launch<float, FORM, 1>(P, st);
   else if (P.M <= 16)
     dense_few_launch<uint16_t, FORM, 1>(P, st);
-  else if (P.M <= 32)
+  else if (FORM == kFormLinear || P.M <= 32)
     dense_few_launch<uint16_t, FORM, 2>(P, st);
-  else if (P.M <= 48)
-    dense_few_launch<uint16_t, FORM, 3>(P, st);
   else
-    dense_few_launch<uint16_t, FORM, 4>(P, st);
+    dense_few_launch<uint16_t, FORM, FORM == kFormGlu ? 3 : 2>(P, st);
 }
 
 hipError_t launch_dense_few(const DenseParams& P, int form, bool bf16, hipStream_t st) {

@@ -151,7 +151,7 @@ int few_chunks(const Dense& d) {
   const double tS = 4.5 + (strip / S / 40e3 > all ? strip / S / 40e3 : all);
   return tS < t1 ? (int)S : 1;
 }
-bool few(const Dense& d) { return d.T <= (d.bf16 ? kFewRowsBf16 : kFewRowsF32); }
+bool few(const Dense& d) { return d.T <= few_rows(d.bf16, d.nm); }
 
 // ------------------------------------------------------------- workspace layout
 struct FwdPlan {

@@ -270,16 +270,20 @@ DEV void mainloop(uint32_t ring, int nsteps, Issue issue, f32x16_t (&acc)[4][4],
 // 6), products between the reads one at a time are (128 x 128, 2048^3:
 // 24.7 -> 23.0 us).
 constexpr int SBK = 64;
-template <int MB, int NB>
+template <int MB, int NB, bool SHORT>
 struct Small {
   static constexpr int PARTS = MB + NB;
-  static constexpr int NS = MB == 1 && NB == 2 ? 3 : 4;      // ring slots
+  // Ring slots.  SHORT: contractions of at most two slices a workgroup, where
+  // five workgroups a CU (three of the gated product) hide each other's first loads
+  // and stores (backward of 2048 x 8192 with 33 rows, of it the weight gradient two
+  // thirds: 36.6 -> 27.8 us, 25.8 with non-temporal stores)
+  static constexpr int NS = SHORT ? 2 : MB == 1 && NB == 2 ? 3 : 4;
   // Fragments are read one slice ahead of their products (512 x 2048 x 2048 with
   // 64 x 64: 12.1 -> 11.1 us), but not where that needs a fourth slot and
   // leaves room for one workgroup a CU (gated, 1024 x 2048 x 8192: 85 and 106 us)
   static constexpr bool AHEAD = NS == 4;
   static constexpr uint32_t HALF = 4096 * PARTS, SLOT = 2 * HALF;
-  static constexpr int RING = NS * SLOT;                     // 64, 72 or 128 KiB
+  static constexpr int RING = NS * SLOT;                     // 64, 72 or 128 KiB; SHORT 32 or 48
 };
 
 // One operand's fragment addresses in the first slot's first half.
@@ -325,9 +329,9 @@ struct KcPart {
 
 // issue(h, addr, i): load i (the parts of A, then those of B) of half slice h to
 // addr; half slices past 2 nsteps may hold anything.
-template <int AL, int BL, int MB, int NB, class Issue>
+template <int AL, int BL, int MB, int NB, bool SHORT, class Issue>
 DEV void small_mainloop(uint32_t ring, int nsteps, Issue issue, f32x16_t (&acc)[MB][NB], int wm, int wn, int lane) {
-  using S = Small<MB, NB>;
+  using S = Small<MB, NB, SHORT>;
   constexpr uint32_t HALF = S::HALF, SB = S::SLOT, END = S::NS * SB;
   constexpr int L = 2 * S::PARTS, NS = S::NS;
   auto fill = [&](int s, uint32_t off) __attribute__((always_inline)) {

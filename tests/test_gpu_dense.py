@@ -264,9 +264,11 @@ def test_nan_and_inf_stay_in_their_rows(rows, dtype):
     assert torch.equal(got[:, :199], want[:, :199]) and not torch.isfinite(got[:, 199]).any()
 
 
-# products for each of the bf16 tiles, whole and ragged, split and unsplit
+# products for each of the bf16 tiles, whole and ragged, split and unsplit, of one
+# or two slices
 @pytest.mark.parametrize("rows,d,f", [(1030, 1032, 1040), (2000, 2056, 2049), (2049, 512, 2320), (1100, 2048, 4360),
-                                      (130, 4104, 264)])
+                                      (130, 4104, 264), (50, 1032, 2056), (128, 1001, 600),
+                                      (3000, 128, 264), (2000, 72, 1000)])
 def test_bf16_tiles(rows, d, f):
     _linear_case("bf16", rows, d, f, "gelu", True, True, 8 if f % 8 == 0 else 0, "f32", "bf16")
     test_glu("bf16", rows, d, f)
