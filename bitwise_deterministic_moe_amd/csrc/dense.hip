@@ -1356,10 +1356,12 @@ static void dense_few_form(const DenseParams& P, bool bf16, hipStream_t st) {
     dense_few_launch<float, FORM, 1>(P, st);
   else if (P.M <= 16)
     dense_few_launch<uint16_t, FORM, 1>(P, st);
-  else if (FORM == kFormLinear || P.M <= 32)
+  else if (P.M <= 32)
     dense_few_launch<uint16_t, FORM, 2>(P, st);
+  else if (P.M <= 48)
+    dense_few_launch<uint16_t, FORM, 3>(P, st);
   else
-    dense_few_launch<uint16_t, FORM, FORM == kFormGlu ? 3 : 2>(P, st);
+    dense_few_launch<uint16_t, FORM, 4>(P, st);
 }
 
 hipError_t launch_dense_few(const DenseParams& P, int form, bool bf16, hipStream_t st) {

@@ -151,7 +151,9 @@ int few_chunks(const Dense& d) {
   const double tS = 4.5 + (strip / S / 40e3 > all ? strip / S / 40e3 : all);
   return tS < t1 ? (int)S : 1;
 }
-bool few(const Dense& d) { return d.T <= few_rows(d.bf16, d.nm); }
+bool few(const Dense& d, const moe_dense* p) {
+  return d.T <= few_rows(d.bf16, d.nm, !direct(d, d.D, p->ldx) || !direct(d, d.F, p->ldw));
+}
 
 // ------------------------------------------------------------- workspace layout
 struct FwdPlan {
@@ -165,7 +167,7 @@ struct FwdPlan {
 FwdPlan fwd_plan(const moe_dense* p, const Dense& d) {
   FwdPlan f{};
   const int form = d.nm == 2 ? kFormGlu : kFormLinear;
-  f.few = few(d);
+  f.few = few(d, p);
   f.ldx = p->ldx;
   f.ldw = p->ldw;
   size_t o = 0;
