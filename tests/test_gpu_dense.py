@@ -423,6 +423,40 @@ def test_side_stream_and_two_graphs(n, d, f):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_two_streams_at_once(dtype):
+    ts = [_inputs(n, 520, 264, dtype, s) for n, s in ((200, 1), (1100, 2))]
+    ref = [[o.clone() for o in _all_calls(t, 0, 0.0)] for t in ts]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ts]
+    for _ in range(3):
+        got = []
+        for st, t in zip(streams, ts):
+            with torch.cuda.stream(st):
+                got.append(_all_calls(t, 0, float("nan")))
+        torch.cuda.synchronize()
+        for g, r in zip(got, ref):
+            for j, (a, b) in enumerate(zip(g, r)):
+                assert torch.equal(a, b), j
+        del got
+
+
+@pytest.mark.parametrize("n", [7, 300])
+def test_one_tensor_as_several_inputs(n):
+    torch.manual_seed(n)
+    x, w = torch.randn(n, 264, device=DEV).bfloat16(), torch.randn(264, 264, device=DEV).bfloat16()
+    assert torch.equal(moe.moe_linear_fwd(x, w, residual=x)[0], moe.moe_linear_fwd(x, w, residual=x.clone())[0])
+    a, g, u = moe.moe_glu_fwd(x, w, w, save=True)
+    b, g2, u2 = moe.moe_glu_fwd(x, w, w.clone(), save=True)
+    assert torch.equal(a, b) and torch.equal(g, u) and torch.equal(u, u2)
+    one = moe.moe_linear_bwd(x, x, w, dx_add=x)
+    two = moe.moe_linear_bwd(x.clone(), x.clone(), w, dx_add=x.clone())
+    assert all(torch.equal(p, q) for p, q in zip(one, two))
+    one = moe.moe_glu_bwd(x, x, w, w, g, g, dx_add=x)
+    two = moe.moe_glu_bwd(x.clone(), x, w, w.clone(), g, g2, dx_add=x.clone())
+    assert all(torch.equal(p, q) for p, q in zip(one, two))
+
+
 def test_rows_past_two_gib():
     """Activations beyond 2 GiB (and 2^31 elements): the first, a middle and
     the last rows, and the weight gradients, whose contraction is cut into chunks
