@@ -183,8 +183,8 @@ struct DenseParams {
 // 64 rows 13.8 and 13.0; 2048^2, 33 rows 8.5 and 8.3, 64 rows 11.5 and 9.8;
 // gated 2048 x 8192, 48 rows 16.4 and 19.0, 64 rows 18.2 and 19.3; 4096^2, 64 rows
 // 29.8 and 20.4.  Operands that the tiles would have to copy first are streamed up to
-// 64 rows.
-constexpr int few_rows(bool bf16, int nm, bool copies) { return !bf16 ? 16 : copies ? 64 : nm == 2 ? 48 : 32; }
+// 64 rows.  float32, one matrix 2048^2, 32 rows 12.5 and 13.9, 48 rows 17.7 and 15.6.
+constexpr int few_rows(bool bf16, int nm, bool copies) { return !bf16 ? 32 : copies ? 64 : nm == 2 ? 48 : 32; }
 
 // tile: as in dense_shape
 hipError_t launch_dense_gemm(const DenseParams& P, int form, bool bf16, int tile, hipStream_t st);

@@ -1352,8 +1352,10 @@ static void dense_few_launch(const DenseParams& P, hipStream_t st) {
 
 template <int FORM>
 static void dense_few_form(const DenseParams& P, bool bf16, hipStream_t st) {
-  if (!bf16)
+  if (!bf16 && P.M <= 16)
     dense_few_launch<float, FORM, 1>(P, st);
+  else if (!bf16)
+    dense_few_launch<float, FORM, 2>(P, st);
   else if (P.M <= 16)
     dense_few_launch<uint16_t, FORM, 1>(P, st);
   else if (P.M <= 32)

@@ -138,7 +138,9 @@ Choice choose(const Dense& d, int form, int64_t M, int64_t N, int nseg, int64_t 
 // Chunks of K of the few-row kernels.  A workgroup streams about 40 KB/us and
 // the device 4.6 TB/s; a launch of them takes 3 us beside the stream, and
 // partials with their join 4.5 us more (measured: 64 strips of 8192 x 2048
-// bf16 16.6 us unsplit; 256 in four chunks 10.5 us with the join).
+// bf16 16.6 us unsplit; 256 in four chunks 10.5 us with the join).  Two row blocks of
+// float32 products halve a workgroup's rate (4096 x 1024, 32 rows: 20.9 us unsplit,
+// 12.2 us in chunks).
 int few_chunks(const Dense& d) {
   const double strip = (double)d.D * 64 * d.nm;
   const int cols = 64 / (int)d.es;
@@ -147,8 +149,9 @@ int few_chunks(const Dense& d) {
   int64_t S = kCUs / tiles;
   if (S > steps / 16) S = steps / 16;
   if (S < 2) return 1;
-  const double t1 = strip / 40e3 > all ? strip / 40e3 : all;
-  const double tS = 4.5 + (strip / S / 40e3 > all ? strip / S / 40e3 : all);
+  const double rate = !d.bf16 && d.T > 16 ? 20e3 : 40e3;
+  const double t1 = strip / rate > all ? strip / rate : all;
+  const double tS = 4.5 + (strip / S / rate > all ? strip / S / rate : all);
   return tS < t1 ? (int)S : 1;
 }
 bool few(const Dense& d, const moe_dense* p) {

@@ -142,7 +142,8 @@ def test_linear(dtype, rows, d, f):
 
 # few rows and few columns: the rows of the weights are split between workgroups
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,d,f", [(1, 16384, 72), (5, 8200, 264), (12, 4100, 130), (48, 6001, 40), (64, 4099, 72)])
+@pytest.mark.parametrize("rows,d,f", [(1, 16384, 72), (5, 8200, 264), (12, 4100, 130), (48, 6001, 40), (64, 4099, 72),
+                                      (29, 4100, 136)])
 def test_few_rows_in_chunks(dtype, rows, d, f):
     _linear_case(dtype, rows, d, f, "silu", True, True, 8 if f % 8 == 0 else 3, "f32", "f32")
     test_glu(dtype, rows, d, f)
