@@ -302,8 +302,9 @@ moe_status forward(const moe_dense* p, int nm, const void* x, const void* w0, co
   if (nm == 2 && (z0 == nullptr) != (z1 == nullptr)) return MOE_ERR_NULL;
   if (d.T == 0) return MOE_OK;
   if (!x || !w0 || !w1 || !y) return MOE_ERR_NULL;
-  for (const void* q : {x, w0, w1, bias, residual, (const void*)y, (const void*)z0, (const void*)z1})
-    if ((uintptr_t)q & (q == bias ? d.es - 1 : 15)) return MOE_ERR_SHAPE;
+  for (const void* q : {x, w0, w1, residual, (const void*)y, (const void*)z0, (const void*)z1})
+    if ((uintptr_t)q & 15) return MOE_ERR_SHAPE;
+  if ((uintptr_t)bias & (d.es - 1)) return MOE_ERR_SHAPE;
   const FwdPlan f = fwd_plan(p, d);
   if (!f.ch.S) return MOE_ERR_SHAPE;
   if ((s = check_ws(ws, ws_bytes, f.total)) != MOE_OK) return s;

@@ -239,3 +239,15 @@ def test_workspace_of_unaligned_rows_holds_copies():
     fwd, _ = moe.moe_linear_workspace_size(1000, 513, 769)
     assert fwd >= 1000 * 520 * 2 + 513 * 776 * 2
     assert moe.moe_linear_workspace_size(40, 513, 769)[0] < 513 * 776 * 2   # few rows are read in place
+
+
+def test_alignment_is_checked_by_argument():
+    """A bias may start at any element, and lets no matrix that starts at the
+    same address (a row of x, a column of w) past the matrices' own check."""
+    lib, p, big = moe.load_library(), PTR, 1 << 40
+    c = _desc(act=4, ldr=96)
+    for odd in (p + 2, p + 8):
+        for i in (0, 1, 3, 4, 5):   # x, w, residual, y, z
+            a = [p, p, odd, p, p, p]
+            a[i] = odd
+            assert lib.moe_linear_fwd(c, *a, p, big, None) == SHAPE, (odd, i)
