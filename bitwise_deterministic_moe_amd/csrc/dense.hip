@@ -445,10 +445,24 @@ DEV f32x4_t frag(const float* s, int row, int q, int half) {
 }
 }  // namespace f32t
 
+namespace f32s {
+// The upper 16 bits of a float32 number, which are a bf16 number.
+DEV float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+// Not zero where x is not the sum of its three bf16 parts (the third one's lower half).
+DEV uint32_t cut_off(float x) {
+  const float r = x - cut(x);
+  return __float_as_uint(r - cut(r)) & 0xffffu;
+}
+}  // namespace f32s
+
 // The product of a tile over its slices, for the tile of SUB slices of 16.
-template <int FORM, int MB, int NB, bool V4, int SUB>
+// MARK: `marks`, zeros before the call, then tells of each row of the tile (words 0..64
+// MB - 1) and each column (the next 64 NB; the gated product's in the order of its LDS
+// tile) whether it holds a number that is not the sum of its three bf16 parts; the caller
+// waits for the other waves before it reads them.
+template <int FORM, int MB, int NB, bool V4, int SUB, bool MARK>
 DEV void f32_loop(const DenseParams& P, const DenseTile& t, float (*sa)[f32t::OPER<MB>], float (*sb)[f32t::OPER<NB>],
-                  f32x16_t (&acc)[MB][NB]) {
+                  f32x16_t (&acc)[MB][NB], uint32_t* marks) {
   using namespace f32t;
   static_assert(FORM != kFormGlu || NB == 2, "a wave holds g and u of the same columns");
   constexpr int BM = 64 * MB;
@@ -523,8 +537,19 @@ DEV void f32_loop(const DenseParams& P, const DenseTile& t, float (*sa)[f32t::OP
         for (int nb = 0; nb < NB; ++nb)
           acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(f.b[nb][e], f.a[mb][e], acc[mb][nb], 0, 0, 0);
   };
+  uint32_t la[4] = {0, 0, 0, 0}, lb[2][4] = {};
   auto fill = [&](auto J, int s) __attribute__((always_inline)) {   // set J to its buffer, then slice s into set J
     constexpr int j = decltype(J)::value;
+    if constexpr (MARK) {
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) la[AK ? i : e] |= f32s::cut_off(ra[j][i][e]);
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lb[FORM == kFormGlu ? i : 0][BKC ? i : e] |= f32s::cut_off(rb[j][i][e]);
+    }
     oa.store(sa[j], ra[j]);
     store_b(sb[j], rb[j]);
     load(ra[j], rb[j], s);
@@ -558,6 +583,17 @@ DEV void f32_loop(const DenseParams& P, const DenseTile& t, float (*sa)[f32t::OP
   }
   if (s < s1) step(s, J0{}, J2{});
   if (s + 1 < s1) step(s + 1, J1{}, J0{});
+  if constexpr (MARK) {   // several threads may write the same word, all of them 1
+    uint32_t* mb = marks + 64 * MB;
+#pragma unroll
+    for (int i = 0; i < (AK ? MB : 4); ++i)
+      if (la[i]) marks[AK ? oa.mn[AK ? i : 0] : oa.mn[0] + i] = 1;
+#pragma unroll
+    for (int m = 0; m < (FORM == kFormGlu ? 2 : 1); ++m)
+#pragma unroll
+      for (int i = 0; i < (BKC ? NB : 4); ++i)
+        if (lb[m][i]) mb[BKC ? ob.mn[BKC ? i : 0] : 64 * m + ob.mn[0] + i] = 1;
+  }
 }
 
 // The epilogue of a tile whose wave holds MB x NB blocks.
@@ -611,7 +647,7 @@ __global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
   DenseTile t;
   if (!dense_tile<FORM>(P, 64 * MB, FORM == kFormGlu ? 32 * NB : 64 * NB, BK, t)) return;
   f32x16_t acc[MB][NB];
-  f32_loop<FORM, MB, NB, V4, 1>(P, t, sa, sb, acc);
+  f32_loop<FORM, MB, NB, V4, 1, false>(P, t, sa, sb, acc, nullptr);
   f32_store<FORM, MB, NB>(P, t, acc);
 }
 
@@ -631,12 +667,15 @@ __global__ __launch_bounds__(256) void dense_f32_kernel(DenseParams P) {
 // of eight v_mfma_f32_32x32x2f32 in three eighths of their time.
 //
 // An infinite or NaN number has no such parts: its m is NaN, which reaches every
-// sum it takes part in.  And what lies below 2^-133, the smallest bf16 number, is
-// lost of each operand: with |b| K < 2^29 less than 2^-24 of a sum of 2^-80.
-// So a sum that is not finite, or smaller than 2^-80 and not zero, is computed
+// sum it takes part in.  A number below 2^-110 may have a bit below 2^-133, the smallest
+// bf16 number: then the lower half of x - h - m is not zero, which every split is
+// checked for.  And the small parts' products leave the float32 range before the
+// numbers' own do.  So every sum of a row or column with a number that is not its three
+// parts, and every sum that is not finite, or smaller than 2^-80 and not zero, is computed
 // again with the float32 instructions (with its whole tile, whose other sums stay
-// as they are) and is what a float32 product gives.  (Operands that are all
-// below 2^-133 count as zeros.)
+// as they are: a row's bits do not depend on another row's numbers) and is what a
+// float32 product gives.  The check is two of the split's 24 vector instructions per four
+// numbers.
 //
 // A slice is 32 k.  A thread loads 4 groups of four numbers of each operand two
 // slices ahead, splits the groups of the next-but-one slice between the
@@ -691,12 +730,11 @@ struct Op {
   }
 };
 
-// The three parts of four numbers.
-DEV float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+// The three parts of four numbers; what the last one cuts off goes into `off`.
 DEV uint32_t upper_halves(float lo, float hi) {
   return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
 }
-DEV void split4(const f32x4_t& x, u32x2_t& h, u32x2_t& m, u32x2_t& l) {
+DEV void split4(const f32x4_t& x, u32x2_t& h, u32x2_t& m, u32x2_t& l, uint32_t& off) {
   float r[4], q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -706,6 +744,9 @@ DEV void split4(const f32x4_t& x, u32x2_t& h, u32x2_t& m, u32x2_t& l) {
   h = u32x2_t{upper_halves(x[0], x[1]), upper_halves(x[2], x[3])};
   m = u32x2_t{upper_halves(r[0], r[1]), upper_halves(r[2], r[3])};
   l = u32x2_t{upper_halves(q[0], q[1]), upper_halves(q[2], q[3])};
+  // Written out as one unit of the schedule: as C the two went in front of the matrix
+  // instructions (4096^3: 780 us without the check, 826 in C, 790 so).
+  asm("v_or3_b32 %0, %1, %2, %0\n\tv_or3_b32 %0, %3, %4, %0" : "+v"(off) : "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3]));
 }
 
 // Fragment addresses of an operand's two 32-row blocks, relative to a buffer.
@@ -791,10 +832,11 @@ __global__ __launch_bounds__(256) void dense_f32s_kernel(DenseParams P) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) load1(va, vb, q, u);
   };
+  uint32_t off = 0;
   // group u of a register set, split, into the buffer at buf
   auto put = [&](const f32x4_t (&va)[4], const f32x4_t (&vb)[4], uint32_t buf, int u) __attribute__((always_inline)) {
     u32x2_t h, m, l;
-    split4(u < 4 ? va[u & 3] : vb[u & 3], h, m, l);
+    split4(u < 4 ? va[u & 3] : vb[u & 3], h, m, l, off);
     LDS_AS char* p = (LDS_AS char*)(uintptr_t)(base + buf + (u < 4 ? oa.place(u & 3) : OPER + ob.place(u & 3)));
     *(LDS_AS u32x2_t*)p = h;
     *(LDS_AS u32x2_t*)(p + PART) = m;
@@ -894,12 +936,27 @@ __global__ __launch_bounds__(256) void dense_f32s_kernel(DenseParams P) {
         bad[a] |= (uint32_t)((v >= 0x7f800000u) | (v - 1 < 0x17800000u - 1)) << (16 * b + r);
       }
   asm volatile("" : "+v"(bad[0]), "+v"(bad[1]));
-  if (__syncthreads_or((bad[0] | bad[1]) != 0)) {
+  if (__syncthreads_or((bad[0] | bad[1] | (off & 0xffffu)) != 0)) {
     constexpr int A = f32t::kAhead * f32t::OPER<2>;
-    static_assert(2 * A * 4 <= NBUF * BUF, "the float32 buffers fit");
+    static_assert((2 * A + 256) * 4 <= NBUF * BUF, "the float32 buffers and marks fit");
     float* f = (float*)lds;
+    uint32_t* marks = (uint32_t*)(f + 2 * A);
+    marks[tid] = 0;
     f32x16_t again[2][2];
-    f32_loop<FORM, 2, 2, V4, 2>(P, t, (float (*)[f32t::OPER<2>])f, (float (*)[f32t::OPER<2>])(f + A), again);
+    f32_loop<FORM, 2, 2, V4, 2, true>(P, t, (float (*)[f32t::OPER<2>])f, (float (*)[f32t::OPER<2>])(f + A), again, marks);
+    __syncthreads();
+    // lane l holds rows l % 32 and columns 8 i + 4 (l / 32) + 0..3 of each block (f32_store)
+    uint32_t cols = 0;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int col = (GLU ? 64 * b + 32 * wn : 64 * wn + 32 * b) + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        cols |= marks[128 + col] << (16 * b + r);
+      }
+#pragma unroll
+    for (int a = 0; a < 2; ++a) bad[a] |= marks[64 * wm + 32 * a + (lane & 31)] ? ~0u : cols;
+    asm volatile("" : "+v"(bad[0]), "+v"(bad[1]));
     // the other sums keep their bits, whatever another row or column holds
 #pragma unroll
     for (int a = 0; a < 2; ++a)

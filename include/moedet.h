@@ -649,9 +649,9 @@ moe_status moe_mfma_rate(int64_t blocks, int64_t iters, float value, float* sink
  *     workspace first.  Matrix base addresses are multiples of 16 bytes,
  *     except in the layer norm, which takes any element address.
  *   - Sums are float32, every output is rounded once.  Large float32 products
- *     read each number as the exact sum of three bfloat16 numbers; what is
- *     below 2^-133 of a number does not count beside larger terms there.  Infinite
- *     and NaN numbers act as in float32.  The backward of the
+ *     read each number as the exact sum of three bfloat16 numbers; a row or
+ *     column with a number that is not such a sum (some below 2^-110, infinite
+ *     and NaN numbers) is multiplied in float32.  The backward of the
  *     matrix operators rounds the pre-activation gradients (dz, dg, du) to
  *     the storage type before their products, as the expert layer does with
  *     dh.
