@@ -1293,7 +1293,7 @@ __global__ __launch_bounds__(256) void dense_ew_kernel(DenseEwParams P, DensePac
       float o0[V], o1[V];
       if (need_z) {
         float v[V], dv[V];
-        act_df_n<V>(P.act, z[i], v, dv);
+        act_df_n<sizeof(T) == 4, V>(P.act, z[i], v, dv);
 #pragma unroll
         for (int q = 0; q < V; ++q) {
           o0[q] = GLU ? d[i][q] * u[i][q] * dv[q] : d[i][q] * dv[q];

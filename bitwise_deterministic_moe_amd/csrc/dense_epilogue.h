@@ -7,28 +7,79 @@
 
 namespace moedet {
 
-// Activation and derivative in float32.  SiLU takes the hardware reciprocal
-// and exponential (about 2^-22 relative); for z below about -88 the exponential
-// overflows to infinity and the product is -0, the limit.  GELU's
-// distribution function is Abramowitz and Stegun 7.1.26 for erfc, within
-// 0.75e-7 of Phi and without the cancellation of 1 + erf for negative z:
-//   Phi(-|z|) = 0.5 t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) exp(-z^2 / 2),
-//   t = 1 / (1 + 0.3275911 |z| / sqrt 2).
+// Activations and derivatives in float32, accurate for a result in float32 (FINE) or
+// rounded to bf16.  Errors are relative, in the tails too, down to results of about
+// 2^-120, where the exponential's underflow ends them.  E = 2^-24.
+//
+// SiLU is z s(z), s(z) = 1 / (1 + exp(-z)), s' = s (1 - s).  The hardware's
+// exponential (of base 2) and reciprocal are within 2 E.
+//   FINE  from e = exp(-|z|), which cannot overflow: s(|z|) = 1 / (1 + e) and s(-|z|) =
+//         e / (1 + e), so neither s nor 1 - s cancels, and the error stays below 12 E.
+//   else  s directly: the rounding of the exponential's argument grows with |z|, and
+//         the error with it to about (2 |z| + 8) E.
+//
+// GELU is z Phi(z) with Phi(-|z|) = erfc(|z| / sqrt 2) / 2 = t P(t) exp(-z^2 / 2),
+// t = 1 / (1 + p |z|), and Phi(|z|) = 1 - Phi(-|z|), which does not cancel either.
+// P is a polynomial fitted to erfcx(|z| / sqrt 2) / (2 t) for the least relative error
+// over 0 <= |z| <= 13.3, beyond which the exponential is 0.
+//   FINE  9 coefficients, within 1.9e-8, and z^2 / 2 in two parts: below 24 E altogether.
+//   else  7 coefficients, within 1.2e-6, below (3 z^2 + 64) E altogether.
 // (The library's erff, with its branch, took 40 us of the epilogues of a 4096 x
-// 2048 x 8192 product, this form about 11.)
-DEV float sigmoid_f(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
+// 2048 x 8192 product, this form and the bias about 15.)
+//
+// exp(-(h + l)) for h >= 0 and a small l, the product with log2 e in two parts
+DEV float exp_neg(float h, float l) {
+  const float c = 1.44269502f, c2 = 1.92596299e-8f, ln2 = 0.693147182f;
+  const float y = h * c;
+  const float r = __builtin_fmaf(l, c, __builtin_fmaf(h, c2, __builtin_fmaf(h, c, -y)));
+  const float e = __builtin_amdgcn_exp2f(-y);
+  return __builtin_fmaf(e, -ln2 * r, e);
+}
+// s(z) and s(-z)
+template <bool FINE>
+DEV void sigmoid_f(float z, float& s, float& c) {
+  if constexpr (FINE) {
+    const float e = exp_neg(__builtin_fminf(__builtin_fabsf(z), 128.f), 0.f), r = __builtin_amdgcn_rcpf(1.f + e);
+    s = z >= 0.f ? r : e * r;
+    c = z >= 0.f ? e * r : r;
+  } else {
+    s = __builtin_amdgcn_rcpf(1.f + __expf(-z));
+    c = 1.f - s;
+  }
+}
 // Phi(z), and exp(-z^2 / 2) in e
+template <bool FINE>
 DEV float normal_cdf(float z, float& e) {
-  const float x = __builtin_fabsf(z) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.f));
-  float p = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
-  p = __builtin_fmaf(t, p, 1.421413741f);
-  p = __builtin_fmaf(t, p, -0.284496736f);
-  p = __builtin_fmaf(t, p, 0.254829592f);
-  e = __expf(-x * x);
-  const float q = 0.5f * t * p * e;
+  float q;
+  if constexpr (FINE) {
+    const float x = __builtin_fminf(__builtin_fabsf(z), 16.f), h = x * x;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.344f, x, 1.f));
+    q = __builtin_fmaf(t, -2.826836167e-2f, 1.457166378e-1f);
+    q = __builtin_fmaf(t, q, -2.746732555e-1f);
+    q = __builtin_fmaf(t, q, 1.934512497e-1f);
+    q = __builtin_fmaf(t, q, -4.106735419e-2f);
+    q = __builtin_fmaf(t, q, 1.133146049e-1f);
+    q = __builtin_fmaf(t, q, 1.166451889e-1f);
+    q = __builtin_fmaf(t, q, 1.376630181e-1f);
+    q = __builtin_fmaf(t, q, 1.372182633e-1f);
+    e = exp_neg(0.5f * h, 0.5f * __builtin_fmaf(x, x, -h));
+    q = q * t * e;
+  } else {
+    const float x = __builtin_fabsf(z);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.199f, x, 1.f));
+    q = __builtin_fmaf(t, 3.008919769e-1f, -4.435143378e-1f);
+    q = __builtin_fmaf(t, q, 5.122382957e-1f);
+    q = __builtin_fmaf(t, q, -1.644029879e-1f);
+    q = __builtin_fmaf(t, q, 1.466305782e-1f);
+    q = __builtin_fmaf(t, q, 6.799873163e-2f);
+    q = __builtin_fmaf(t, q, 8.015767340e-2f);
+    // exp(-z^2 / 2) as a power of 2: one product less than through the base e
+    e = __builtin_amdgcn_exp2f(-0.721347520f * x * x);
+    q = q * t * e;
+  }
   return z > 0.f ? 1.f - q : q;
 }
+template <bool FINE>
 DEV float act_f(int act, float z) {
   switch (act) {
     case kActRelu: return z < 0.f ? 0.f : z;
@@ -36,15 +87,20 @@ DEV float act_f(int act, float z) {
       const float r = z < 0.f ? 0.f : z;
       return r * r;
     }
-    case kActSilu: return z * sigmoid_f(z);
+    case kActSilu: {
+      float s, c;
+      sigmoid_f<FINE>(z, s, c);
+      return z * s;
+    }
     case kActGelu: {
       float e;
-      return z * normal_cdf(z, e);
+      return z * normal_cdf<FINE>(z, e);
     }
     default: return z;
   }
 }
 // value and derivative
+template <bool FINE>
 DEV void act_df(int act, float z, float& v, float& d) {
   switch (act) {
     case kActRelu:
@@ -58,14 +114,15 @@ DEV void act_df(int act, float z, float& v, float& d) {
       break;
     }
     case kActSilu: {
-      const float p = sigmoid_f(z);
-      v = z * p;
-      d = __builtin_fmaf(v, 1.f - p, p);
+      float s, c;
+      sigmoid_f<FINE>(z, s, c);
+      v = z * s;
+      d = __builtin_fmaf(v, c, s);
       break;
     }
     case kActGelu: {
       float e;
-      const float c = normal_cdf(z, e);
+      const float c = normal_cdf<FINE>(z, e);
       v = z * c;
       d = __builtin_fmaf(z * 0.39894228040143268f, e, c);
       break;
@@ -77,28 +134,28 @@ DEV void act_df(int act, float z, float& v, float& d) {
 }
 
 // N values and derivatives, with the switch outside as in act_n.
-template <int N>
+template <bool FINE, int N>
 DEV void act_df_n(int act, const float (&z)[N], float (&v)[N], float (&d)[N]) {
   switch (act) {
     case kActNone:
 #pragma unroll
-      for (int i = 0; i < N; ++i) act_df(kActNone, z[i], v[i], d[i]);
+      for (int i = 0; i < N; ++i) act_df<FINE>(kActNone, z[i], v[i], d[i]);
       return;
     case kActRelu:
 #pragma unroll
-      for (int i = 0; i < N; ++i) act_df(kActRelu, z[i], v[i], d[i]);
+      for (int i = 0; i < N; ++i) act_df<FINE>(kActRelu, z[i], v[i], d[i]);
       return;
     case kActRelu2:
 #pragma unroll
-      for (int i = 0; i < N; ++i) act_df(kActRelu2, z[i], v[i], d[i]);
+      for (int i = 0; i < N; ++i) act_df<FINE>(kActRelu2, z[i], v[i], d[i]);
       return;
     case kActSilu:
 #pragma unroll
-      for (int i = 0; i < N; ++i) act_df(kActSilu, z[i], v[i], d[i]);
+      for (int i = 0; i < N; ++i) act_df<FINE>(kActSilu, z[i], v[i], d[i]);
       return;
     default:
 #pragma unroll
-      for (int i = 0; i < N; ++i) act_df(kActGelu, z[i], v[i], d[i]);
+      for (int i = 0; i < N; ++i) act_df<FINE>(kActGelu, z[i], v[i], d[i]);
   }
 }
 
@@ -156,25 +213,25 @@ DEV void put_z(const DenseParams& P, int m, int64_t row, int col, int n, const f
 
 // Activation of N values: the switch is outside, so that the values' chains of
 // dependent operations overlap (a wave is alone on its SIMD in the tile kernels).
-template <int N>
+template <bool FINE, int N>
 DEV void act_n(int act, float (&v)[N]) {
   switch (act) {
     case kActNone: return;
     case kActRelu:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = act_f(kActRelu, v[i]);
+      for (int i = 0; i < N; ++i) v[i] = act_f<FINE>(kActRelu, v[i]);
       return;
     case kActRelu2:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = act_f(kActRelu2, v[i]);
+      for (int i = 0; i < N; ++i) v[i] = act_f<FINE>(kActRelu2, v[i]);
       return;
     case kActSilu:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = act_f(kActSilu, v[i]);
+      for (int i = 0; i < N; ++i) v[i] = act_f<FINE>(kActSilu, v[i]);
       return;
     default:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = act_f(kActGelu, v[i]);
+      for (int i = 0; i < N; ++i) v[i] = act_f<FINE>(kActGelu, v[i]);
   }
 }
 
@@ -224,7 +281,7 @@ DEV void emit(const DenseParams& P, int seg, const At& at, float (&v)[4 * R]) {
         if (at.ok(i, P.N))
           put_z<T, STREAM>(P, 0, at.row(i), at.col(i), P.N - at.col(i), {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]});
     }
-    act_n<4 * R>(P.act, v);
+    act_n<sizeof(T) == 4, 4 * R>(P.act, v);
   }
   if (FORM != kFormDw && P.add) {
 #pragma unroll
@@ -255,7 +312,7 @@ DEV void emit_glu(const DenseParams& P, const At& at, float (&g)[4 * R], const f
         put_z<T, STREAM>(P, 1, at.row(i), at.col(i), n, {u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]});
       }
   }
-  act_n<4 * R>(P.act, g);
+  act_n<sizeof(T) == 4, 4 * R>(P.act, g);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     if (!at.ok(i, P.N)) continue;

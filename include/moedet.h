@@ -659,8 +659,11 @@ moe_status moe_mfma_rate(int64_t blocks, int64_t iters, float value, float* sink
  *     may be dx_add, with the same row distance. */
 
 /* Activations.  ReLU2 is the expert layer's relu(z)^2; GELU is z Phi(z)
- * with the normal distribution function Phi (the erf form).  At z = 0 the
- * derivative of ReLU is 0. */
+ * with the normal distribution function Phi (the erf form).  Their float32
+ * values have relative errors below 12 * 2^-24 (SiLU) and 24 * 2^-24 (GELU)
+ * for MOE_F32 storage, the tails included, and (2 |z| + 8) * 2^-24 and
+ * (3 z^2 + 64) * 2^-24 for MOE_BF16; results below 2^-120 may be 0.  At z = 0
+ * the derivative of ReLU is 0. */
 typedef enum moe_act {
   MOE_ACT_NONE = 0,
   MOE_ACT_RELU = 1,

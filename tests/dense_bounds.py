@@ -10,9 +10,10 @@ Bounds are first-order, element by element, from the arithmetic:
     of a product, 8 of the 10 above, and the six run in chains of 16 k an
     instruction, 6 n / 16 sums at 2^-23 = 0.75 n 2^-24 beside at most
     2 * 16 2^-24 inside one: below 2 n for n >= 32;
-  * the activations' exponential has an argument error of 2^-23 |z| and two
-    units of its own, the reciprocal and erf two units each, which gives
-    the bounds of ACT below;
+  * the activations' errors are relative, at most 12 (SiLU) and 24 (GELU) times
+    2^-24 for float32 storage, 2 |z| + 8 and 3 z^2 + 64 times for bf16
+    (test_gpu_dense_values.py holds them to that); act_err below is no smaller
+    around 0, where these tests' z lie;
   * |act''| <= 0.5 (SiLU), 0.8 (GELU), 2 (ReLU^2): an error of z becomes at most
     that much of act'(z).  ReLU's derivative jumps at 0, so it is
     tested on inputs whose z is exact.

@@ -1,9 +1,10 @@
 """The dense operators' values where the numbers themselves are hard: small
-numbers times large ones in float32 products, element by element against
-float64 within the bounds of dense_bounds.py."""
+numbers times large ones in float32 products, and the activations over their
+whole range, tails included; element by element against float64."""
 import numpy as np
 import pytest
 import torch
+from scipy.special import erfc, expit
 
 import bitwise_deterministic_moe_amd as moe
 import dense_bounds as B
@@ -73,3 +74,77 @@ def test_small_times_large_float32_numbers(n, d, f):
     y1 = moe.moe_linear_fwd(up(x), up(w1))[0]
     keep = torch.tensor([i not in cols for i in range(f)], device=DEV)
     assert torch.equal(y1[:, keep], y[:, keep])
+
+
+# ----------------------------------------------------------------- activations
+def _truth(name, z):
+    """Value and derivative in float64, and the magnitudes of the derivative's two
+    terms, without cancellation in the tails."""
+    if name == "silu":
+        s, c = expit(z), expit(-z)
+        return z * s, s + z * s * c, s * (1 + np.abs(z) * c), s
+    p, e = 0.5 * erfc(-z / np.sqrt(2.0)), np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
+    return z * p, p + z * e, p + np.abs(z) * e, p
+
+
+def _errors(name, dtype, z, truth):
+    """Bounds of the float32 value and derivative, from the arithmetic, with E =
+    2^-24 a float32 rounding, exponential and reciprocal within 2 E, 2^-120 for what
+    lies below the exponential's range.
+    Accurate form: SiLU 4 E (the exponential in two parts), 3 E (1 + e), 2 E, E, E; GELU
+    the fit 0.4 E, t 3 E times its condition 2.4, a sum of 9 terms with twice its value
+    in magnitudes 9 E, the products and the exponential 6 E.
+    For bf16: SiLU's exponential has an argument error of 1.5 E |z|, and 1 - s another
+    E; GELU 20 E for the fit, 12 E for t, 12 E for the sum, (1.3 z^2 + 5) E for the
+    exponential and products."""
+    v, _, mag, s = truth
+    a, E = np.abs(z), B.E
+    if dtype == "f32":
+        k = 12 if name == "silu" else 24
+        return k * E * np.abs(v) + 2.0 ** -120, (k + 4) * E * mag + 2.0 ** -120
+    if name == "silu":
+        return (2 * a + 8) * E * np.abs(v) + 2.0 ** -120, (2 * a + 16) * E * (1 + a) * s + 2.0 ** -120
+    return (3 * a * a + 64) * E * np.abs(v) + 2.0 ** -120, (3 * a * a + 68) * E * mag + 2.0 ** -120
+
+
+def _sweep(dtype):
+    z = np.concatenate([np.linspace(-14, 14, 1793), np.linspace(-86, 86, 173), [0.0, 1e-30, -1e-30, 1e-6, -1e-6, 300.0, -300.0]])
+    t = torch.from_numpy(z.astype(np.float32)).to(B.TORCH[dtype]).to(DEV)
+    return t.reshape(1, -1), B.host(t)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+@pytest.mark.parametrize("rows", [1, 70, 1100])
+def test_activations_over_their_range(name, dtype, rows):
+    """act(1 z) and its derivative for one input of 1, so that z is exact: the
+    weight-streaming kernel, and tiles of both sizes."""
+    w, z = _sweep(dtype)
+    n = z.size
+    x = torch.ones(rows, 1, dtype=w.dtype, device=DEV)
+    truth = _truth(name, z)
+    ev, ed = _errors(name, dtype, z, truth)
+    y, zs = moe.moe_linear_fwd(x, w, act=name, save_z=True)
+    assert torch.equal(zs, w.float().expand(rows, n))
+    B.check(y[0], truth[0], B.rounded(ev, truth[0], B.U[dtype]), "y")
+    assert torch.equal(y, y[:1].expand(rows, n))
+    a = moe.moe_glu_fwd(x, w, torch.ones_like(w), name)[0]
+    assert torch.equal(a, y)
+    # the bias gradient is the sum over rows of the unrounded dz, here one row of dy
+    dy = torch.zeros(rows, n, dtype=w.dtype, device=DEV)
+    dy[rows // 2] = 1
+    dx, dw, db = moe.moe_linear_bwd(dy, x, w, zs, name)
+    B.check(db, truth[1], B.rounded(ed, truth[1], B.E), "db")
+    B.check(dw[0], truth[1], B.rounded(B.rounded(ed, truth[1], B.U[dtype]), truth[1], B.E), "dw")
+    # dg = da u act'(g) and du = da act(g)
+    dx, dwg, dwu = moe.moe_glu_bwd(dy, x, w, torch.ones_like(w), zs, torch.ones_like(zs), name)
+    B.check(dwg[0], truth[1], B.rounded(B.rounded(ed, truth[1], B.U[dtype]), truth[1], B.E), "dwg")
+    B.check(dwu[0], truth[0], B.rounded(B.rounded(ev, truth[0], B.U[dtype]), truth[0], B.E), "dwu")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+def test_activations_of_infinite_and_nan_numbers(name, dtype):
+    z = torch.tensor([[float("inf"), float("nan"), 1.0]], dtype=B.TORCH[dtype], device=DEV)
+    y = moe.moe_linear_fwd(torch.ones(1, 1, dtype=z.dtype, device=DEV), z, act=name)[0][0]
+    assert y[0] == float("inf") and torch.isnan(y[1]) and torch.isfinite(y[2])
