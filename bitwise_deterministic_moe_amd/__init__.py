@@ -43,6 +43,8 @@ EXPORTED_SYMBOLS = ("moe_abi_version", "moe_status_string", "moe_rows_cap", "moe
                     "moe_glu_fwd", "moe_glu_bwd")
 # activations of the dense operators (moe_act)
 ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4}
+# matrices of a dense call that may start at any element (moe_any)
+_ANY = {"x": 0x100, "w": 0x200, "y": 0x400, "rest": 0x800}
 # rows read by moe_mx_quantize_wgrad (moe_mxw_src)
 MXW_TOKEN, MXW_ROW, MXW_ACT_P = 0, 1, 2
 
@@ -773,6 +775,14 @@ def _act_code(act: str, what: str) -> int:
         raise MoeError(f"{what}: act must be one of {', '.join(ACTIVATIONS)}, got {act!r}") from None
 
 
+def _any_code(x: int, w: int, y: int, rest: int) -> int:
+    """The moe_any bits of a call: which addresses (of several matrices, their
+    or) are no multiples of 16 bytes."""
+    if not (x | w | y | rest) & 15:
+        return 0
+    return (x & 15 and _ANY["x"]) | (w & 15 and _ANY["w"]) | (y & 15 and _ANY["y"]) | (rest & 15 and _ANY["rest"])
+
+
 def _raw_stream(device: int) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
@@ -984,10 +994,11 @@ def moe_linear_fwd(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, a
         zc, ldz = _z_mat(z, f, dt, what + " z", rows)
     elif save_z:
         z = _new(x, f, torch.float32)
+    px, pw, py, pr, pz = x.data_ptr(), w.data_ptr(), y.data_ptr(), _ptr(residual), _ptr(z)
+    a |= _any_code(px, pw, py, (pr or 0) | (pz or 0))
     c, need, _ = _dense_plan("linear", rows, d, f, code, code, zc, a, ldx, ldw, ldy, ldz, ldr, shuffle_seed)
     ws, nb = _dense_ws(need, ws, x)
-    _run(what, lib.moe_linear_fwd, (c, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(z),
-                                    _ptr(ws), nb), x, w, bias, residual, y, z, ws)
+    _run(what, lib.moe_linear_fwd, (c, px, pw, _ptr(bias), pr, py, pz, _ptr(ws), nb), x, w, bias, residual, y, z, ws)
     return y, z
 
 
@@ -1024,11 +1035,13 @@ def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z=None, a
         _need(db, f, grad_dtype, what + " db")
     elif need_db:
         db = _flat(x, (f,), (1,), grad_dtype)
+    py, px, pw, pz, pa, pdx, pdw = (dy.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(z), _ptr(dx_add), dx.data_ptr(),
+                                    dw.data_ptr())
+    a |= _any_code(px, pw, py, (pz or 0) | (pa or 0) | pdx | pdw)
     c, _, need = _dense_plan("linear", rows, d, f, code, g, zc, a, ldx, ldw, ldy, ldz, ldr, shuffle_seed)
     ws, nb = _dense_ws(need, ws, x)
-    _run(what, lib.moe_linear_bwd,
-         (c, dy.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(z), _ptr(dx_add), dx.data_ptr(), dw.data_ptr(), _ptr(db),
-          _ptr(ws), nb), x, dy, w, z, dx_add, dx, dw, db, ws)
+    _run(what, lib.moe_linear_bwd, (c, py, px, pw, pz, pa, pdx, pdw, _ptr(db), _ptr(ws), nb), x, dy, w, z, dx_add, dx, dw,
+         db, ws)
     return dx, dw, db
 
 
@@ -1058,10 +1071,11 @@ def moe_glu_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, act: str = 
     elif save:
         g = _new(x, f, torch.float32)
         u = _new(x, f, torch.float32)
+    px, pg, pu, pa, zg, zu = x.data_ptr(), wg.data_ptr(), wu.data_ptr(), a.data_ptr(), _ptr(g), _ptr(u)
+    ac |= _any_code(px, pg | pu, pa, (zg or 0) | (zu or 0))
     c, need, _ = _dense_plan("glu", rows, d, f, code, code, zc, ac, ldx, ldw, ldy, ldz, 0, shuffle_seed)
     ws, nb = _dense_ws(need, ws, x)
-    _run(what, lib.moe_glu_fwd, (c, x.data_ptr(), wg.data_ptr(), wu.data_ptr(), a.data_ptr(), _ptr(g), _ptr(u), _ptr(ws),
-                                 nb), x, wg, wu, a, g, u, ws)
+    _run(what, lib.moe_glu_fwd, (c, px, pg, pu, pa, zg, zu, _ptr(ws), nb), x, wg, wu, a, g, u, ws)
     return a, g, u
 
 
@@ -1095,9 +1109,12 @@ def moe_glu_bwd(da: torch.Tensor, x: torch.Tensor, wg: torch.Tensor, wu: torch.T
         dwu = _flat(x, (d, f), (f, 1), grad_dtype)
     else:
         _need(dwu, d * f, grad_dtype, what + " dwu")
+    py, px, pg, pu, zg, zu, pa = (da.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), g.data_ptr(), u.data_ptr(),
+                                  _ptr(dx_add))
+    pdx, dg, du = dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr()
+    ac |= _any_code(px, pg | pu, py, zg | zu | (pa or 0) | pdx | dg | du)
     c, _, need = _dense_plan("glu", rows, d, f, code, gc, zc, ac, ldx, ldw, ldy, ldz, ldr, shuffle_seed)
     ws, nb = _dense_ws(need, ws, x)
-    _run(what, lib.moe_glu_bwd,
-         (c, da.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), g.data_ptr(), u.data_ptr(), _ptr(dx_add),
-          dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), _ptr(ws), nb), x, da, wg, wu, g, u, dx_add, dx, dwg, dwu, ws)
+    _run(what, lib.moe_glu_bwd, (c, py, px, pg, pu, zg, zu, pa, pdx, dg, du, _ptr(ws), nb), x, da, wg, wu, g, u, dx_add, dx,
+         dwg, dwu, ws)
     return dx, dwg, dwu

@@ -23,14 +23,19 @@ struct Dense {
   int64_t T;
   int D, F;
   int64_t es;
+  int act;
+  int any;            // moe_any bits
 };
+constexpr int kAnyBits = MOE_ANY_X | MOE_ANY_W | MOE_ANY_Y | MOE_ANY_REST;
 
 moe_status check(const moe_dense* p, int nm, Dense* d) {
   if (!p) return MOE_ERR_NULL;
   if (p->dtype != MOE_F32 && p->dtype != MOE_BF16) return MOE_ERR_DTYPE;
   if (p->grad_dtype != MOE_F32 && p->grad_dtype != p->dtype) return MOE_ERR_DTYPE;
   if (p->z_dtype != MOE_F32 && p->z_dtype != p->dtype) return MOE_ERR_DTYPE;
-  if (p->act < MOE_ACT_NONE || p->act > MOE_ACT_GELU) return MOE_ERR_MODE;
+  d->any = p->act & kAnyBits;
+  d->act = p->act - d->any;
+  if (d->act < MOE_ACT_NONE || d->act > MOE_ACT_GELU) return MOE_ERR_MODE;
   if (p->rows < 0 || p->rows >= (int64_t)1 << 31 || p->d_in < 1 || p->d_out < 1) return MOE_ERR_SHAPE;
   if (p->d_in >= kMaxLd || p->d_out >= kMaxLd) return MOE_ERR_SHAPE;
   if (p->ldx < p->d_in || p->ldw < p->d_out || p->ldy < p->d_out || p->ldz < p->d_out) return MOE_ERR_SHAPE;
@@ -47,10 +52,17 @@ moe_status check(const moe_dense* p, int nm, Dense* d) {
   return MOE_OK;
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+// Whether a base address is a multiple of 16 bytes, or of `es` where the call allows it.
+bool based(const Dense& d, const void* p, int any, int64_t es) {
+  return ((uintptr_t)p & (uintptr_t)(d.any & any ? es - 1 : 15)) == 0;
+}
 
 // A bf16 matrix that the tile kernels read in place: whole 16-byte chunks.
-bool direct(const Dense& d, int64_t cols, int64_t ld) { return !d.bf16 || (cols % 8 == 0 && ld % 8 == 0); }
+bool direct(const Dense& d, int64_t cols, int64_t ld, int any) {
+  return !d.bf16 || (cols % 8 == 0 && ld % 8 == 0 && !(d.any & any));
+}
+bool direct_x(const Dense& d, const moe_dense* p) { return direct(d, d.D, p->ldx, MOE_ANY_X); }
+bool direct_w(const Dense& d, const moe_dense* p) { return direct(d, d.F, p->ldw, MOE_ANY_W); }
 
 // --------------------------------------------------------- tile and split choice
 struct Choice {
@@ -155,7 +167,7 @@ int few_chunks(const Dense& d) {
   return tS < t1 ? (int)S : 1;
 }
 bool few(const Dense& d, const moe_dense* p) {
-  return d.T <= few_rows(d.bf16, d.nm, !direct(d, d.D, p->ldx) || !direct(d, d.F, p->ldw));
+  return d.T <= few_rows(d.bf16, d.nm, !direct_x(d, p) || !direct_w(d, p));
 }
 
 // ------------------------------------------------------------- workspace layout
@@ -178,8 +190,8 @@ FwdPlan fwd_plan(const moe_dense* p, const Dense& d) {
   if (f.few) {
     f.ch = Choice{0, few_chunks(d)};
   } else {
-    f.pack_x = !direct(d, d.D, p->ldx);
-    f.pack_w = !direct(d, d.F, p->ldw);
+    f.pack_x = !direct_x(d, p);
+    f.pack_w = !direct_w(d, p);
     f.ch = choose(d, form, d.T, d.F, 1, d.D, 0);
     if (f.pack_x) {
       f.ldx = up(d.D, 8);
@@ -217,9 +229,9 @@ BwdPlan bwd_plan(const moe_dense* p, const Dense& d) {
   b.lddz = p->ldy;
   size_t o = 0;
   if (d.T == 0) return b;
-  b.pack_x = !direct(d, d.D, p->ldx);
-  b.pack_w = !direct(d, d.F, p->ldw);
-  b.make_dz = d.nm == 2 || p->act != MOE_ACT_NONE || !direct(d, d.F, p->ldy);
+  b.pack_x = !direct_x(d, p);
+  b.pack_w = !direct_w(d, p);
+  b.make_dz = d.nm == 2 || d.act != MOE_ACT_NONE || !direct(d, d.F, p->ldy, MOE_ANY_Y);
   if (b.pack_x) {
     b.ldx = up(d.D, 8);
     b.x = o;
@@ -302,9 +314,11 @@ moe_status forward(const moe_dense* p, int nm, const void* x, const void* w0, co
   if (nm == 2 && (z0 == nullptr) != (z1 == nullptr)) return MOE_ERR_NULL;
   if (d.T == 0) return MOE_OK;
   if (!x || !w0 || !w1 || !y) return MOE_ERR_NULL;
-  for (const void* q : {x, w0, w1, residual, (const void*)y, (const void*)z0, (const void*)z1})
-    if ((uintptr_t)q & 15) return MOE_ERR_SHAPE;
-  if ((uintptr_t)bias & (d.es - 1)) return MOE_ERR_SHAPE;
+  const int64_t zs = p->z_dtype == MOE_F32 ? 4 : 2;
+  if (!based(d, x, MOE_ANY_X, d.es) || !based(d, w0, MOE_ANY_W, d.es) || !based(d, w1, MOE_ANY_W, d.es) ||
+      !based(d, y, MOE_ANY_Y, d.es) || !based(d, residual, MOE_ANY_REST, d.es) || !based(d, z0, MOE_ANY_REST, zs) ||
+      !based(d, z1, MOE_ANY_REST, zs) || ((uintptr_t)bias & (d.es - 1)))
+    return MOE_ERR_SHAPE;
   const FwdPlan f = fwd_plan(p, d);
   if (!f.ch.S) return MOE_ERR_SHAPE;
   if ((s = check_ws(ws, ws_bytes, f.total)) != MOE_OK) return s;
@@ -335,7 +349,7 @@ moe_status forward(const moe_dense* p, int nm, const void* x, const void* w0, co
   P.z[1] = z1;
   P.ldz = p->ldz;
   P.z_f32 = p->z_dtype == MOE_F32;
-  P.act = p->act;
+  P.act = d.act;
   P.seed = p->debug_shuffle_seed;
   if (f.few)
     MOE_TRY(launch_dense_few(P, form, d.bf16, st));
@@ -355,12 +369,14 @@ moe_status backward(const moe_dense* p, int nm, const void* dy, const void* x, c
   const bool g32 = p->grad_dtype == MOE_F32;
   const int64_t gs = g32 ? 4 : 2;
   if (!dw0 || !dw1) return MOE_ERR_NULL;
-  const bool need_z = nm == 2 || p->act != MOE_ACT_NONE;
+  const bool need_z = nm == 2 || d.act != MOE_ACT_NONE;
   if (d.T > 0 && (!dy || !x || !w0 || !w1 || !dx || (need_z && (!z0 || !z1)))) return MOE_ERR_NULL;
-  for (const void* q : {dy, x, w0, w1, need_z ? z0 : nullptr, need_z ? z1 : nullptr, dx_add, (const void*)dx,
-                        (const void*)dw0, (const void*)dw1})
-    if ((uintptr_t)q & 15) return MOE_ERR_SHAPE;
-  if ((uintptr_t)db & (gs - 1)) return MOE_ERR_SHAPE;
+  const int64_t zs = p->z_dtype == MOE_F32 ? 4 : 2;
+  if (!based(d, dy, MOE_ANY_Y, d.es) || !based(d, x, MOE_ANY_X, d.es) || !based(d, w0, MOE_ANY_W, d.es) ||
+      !based(d, w1, MOE_ANY_W, d.es) || !based(d, dx_add, MOE_ANY_REST, d.es) || !based(d, dx, MOE_ANY_REST, d.es) ||
+      !based(d, dw0, MOE_ANY_REST, gs) || !based(d, dw1, MOE_ANY_REST, gs) || ((uintptr_t)db & (gs - 1)))
+    return MOE_ERR_SHAPE;
+  if (need_z && (!based(d, z0, MOE_ANY_REST, zs) || !based(d, z1, MOE_ANY_REST, zs))) return MOE_ERR_SHAPE;
   if (d.T == 0) {
     const int64_t n16 = (int64_t)d.D * d.F * gs / 2;
     MOE_TRY(launch_dense_zero(dw0, n16, st));
@@ -385,7 +401,7 @@ moe_status backward(const moe_dense* p, int nm, const void* dy, const void* x, c
     E.z[1] = z1;
     E.ldz = p->ldz;
     E.z_f32 = p->z_dtype == MOE_F32;
-    E.act = p->act;
+    E.act = d.act;
     if (b.make_dz) {
       E.out[0] = base + b.dz;
       E.out[1] = base + b.dz + b.segdz * d.es;

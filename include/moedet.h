@@ -644,10 +644,12 @@ moe_status moe_mfma_rate(int64_t blocks, int64_t iters, float value, float* sink
  *   - Matrices are row-major with unit stride inside a row; an `ld` is the
  *     distance of two rows in elements, at least the row's length.  Gradients
  *     (dx, dw, dwg, dwu) and packed outputs without an ld are contiguous.
- *   - Any sizes >= 1 (rows >= 0).  bfloat16 matrices whose row length and
- *     ld are multiples of 8 are read in place; others are copied into the
- *     workspace first.  Matrix base addresses are multiples of 16 bytes,
- *     except in the layer norm, which takes any element address.
+ *   - Any sizes >= 1 (rows >= 0).  Matrix base addresses are multiples of 16
+ *     bytes, or of the element size in the layer norm and where a call's
+ *     description says so (moe_any).  bfloat16 matrices at a 16-byte base whose
+ *     row length and ld are multiples of 8 are read in place; other x,
+ *     weights and dy (da) are copied into the workspace first where tiles read
+ *     them.
  *   - Sums are float32, every output is rounded once.  Large float32 products
  *     read each number as the exact sum of three bfloat16 numbers; a row or
  *     column with a number that is not such a sum (some below 2^-110, infinite
@@ -671,6 +673,16 @@ typedef enum moe_act {
   MOE_ACT_SILU = 3,
   MOE_ACT_GELU = 4
 } moe_act;
+
+/* Added to a description's act: these matrices' base addresses may be any
+ * multiple of the element size.  (A description tells the workspace's size,
+ * and bfloat16 operands at such addresses may need room for a copy.) */
+typedef enum moe_any {
+  MOE_ANY_X = 0x100,
+  MOE_ANY_W = 0x200,     /* w; wg and wu */
+  MOE_ANY_Y = 0x400,     /* y or a; in the backward, dy or da */
+  MOE_ANY_REST = 0x800   /* z, g, u, residual, dx_add, dx and the weight gradients */
+} moe_any;
 
 /* Layer norm of each row of x [rows, cols]:
  *   mean = sum(x) / cols,  rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps),
@@ -720,7 +732,7 @@ moe_status moe_layernorm_bwd(const void* dy, const void* x, const void* weight, 
  *   z_dtype  type of the saved pre-activations z (g and u): MOE_F32, or dtype.
  *            In bf16 layers float32 keeps one rounding out of the gradients
  *            for twice the bytes.
- *   act      moe_act
+ *   act      moe_act, plus any of moe_any
  *   ldx      row distance of x
  *   ldw      row distance of the weights [D, F]
  *   ldy      row distance of the output y (a); in the backward, of dy (da)

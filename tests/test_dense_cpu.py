@@ -251,3 +251,47 @@ def test_alignment_is_checked_by_argument():
             a = [p, p, odd, p, p, p]
             a[i] = odd
             assert lib.moe_linear_fwd(c, *a, p, big, None) == SHAPE, (odd, i)
+
+
+ANY_X, ANY_W, ANY_Y, ANY_REST = 0x100, 0x200, 0x400, 0x800
+
+
+def test_addresses_that_a_description_allows():
+    """moe_any: element addresses for the matrices named, 16 bytes for the others;
+    the float32 matrices of a bf16 call keep to 4 bytes.  (A call that passes
+    every check would be launched: here the missing workspace ends it.)"""
+    lib, p = moe.load_library(), PTR
+    need = lambda c, bwd: _sizes(lib, c)[bwd]  # noqa: E731
+    c = _desc(act=4 | ANY_X | ANY_W)
+    assert need(c, 0) > 0
+    fwd = lambda c, *a: lib.moe_linear_fwd(c, *a, None, 0, None)  # noqa: E731
+    assert fwd(c, p + 2, p + 6, p, None, p, p) == NULL
+    assert fwd(c, p + 1, p, p, None, p, p) == SHAPE
+    assert fwd(c, p + 2, p, p, None, p + 2, p) == SHAPE
+    assert fwd(c, p + 2, p, p, None, p, p + 4) == SHAPE
+    c = _desc(act=4 | ANY_X | ANY_Y | ANY_REST, ldr=96)
+    assert fwd(c, p, p, p, p + 2, p + 2, p + 4) == NULL
+    assert fwd(c, p, p, p, p + 2, p + 2, p + 2) == SHAPE      # z is float32
+    assert fwd(c, p, p + 2, p, p + 2, p + 2, p + 4) == SHAPE
+    bwd = lambda c, *a: lib.moe_linear_bwd(c, *a, None, 0, None)  # noqa: E731
+    assert bwd(c, p + 2, p + 2, p, p + 4, None, p + 2, p + 4, p) == NULL
+    assert bwd(c, p + 2, p + 2, p, p + 4, None, p + 2, p + 2, p) == SHAPE   # dw is float32
+    c = _desc(act=0x1000)
+    assert lib.moe_linear_workspace_size(c, None, None) == MODE
+
+
+def _sizes(lib, c):
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    assert lib.moe_linear_workspace_size(c, ctypes.byref(f), ctypes.byref(b)) == 0
+    return f.value, b.value
+
+
+def test_workspace_of_unaligned_bases_holds_copies():
+    lib = moe.load_library()
+    v = dict(rows=1000, d_in=512, d_out=768, ldx=512, ldw=768, ldy=768, ldz=768)
+    none, allx = _sizes(lib, _desc(**v)), _sizes(lib, _desc(**v, act=ANY_X | ANY_W | ANY_Y))
+    assert allx[0] >= none[0] + 1000 * 512 * 2 + 512 * 768 * 2
+    assert allx[1] >= none[1] + 1000 * 512 * 2 + 512 * 768 * 2 + 1000 * 768 * 2   # and dy
+    assert _sizes(lib, _desc(**v, act=ANY_REST)) == none
+    f32 = dict(v, dtype=0)
+    assert _sizes(lib, _desc(**f32)) == _sizes(lib, _desc(**f32, act=ANY_X | ANY_W | ANY_Y | ANY_REST))
