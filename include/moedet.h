@@ -771,7 +771,8 @@ moe_status moe_glu_workspace_size(const moe_dense* p, size_t* fwd_bytes, size_t*
  *   y        DEVICE [T, F] output
  *   z        DEVICE [T, F] of z_dtype, output (the backward reads it), or NULL
  *   ws       moe_linear_workspace_size fwd_bytes, 256-byte aligned
- * Few rows (at most 64 in bf16, 16 in float32) stream the weights once.
+ * Few rows stream the weights once: at most 32, in bfloat16 48 for the gated
+ * product and 64 where tiles would have to copy an operand.
  * Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_MODE (act), MOE_ERR_NULL,
  * MOE_ERR_WORKSPACE before anything is enqueued; MOE_ERR_HIP for a launch
  * failure. */
