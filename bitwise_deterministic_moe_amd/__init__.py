@@ -930,23 +930,39 @@ def _dense_plan(kind: str, rows: int, d_in: int, d_out: int, dtype: int, grad_dt
     return c, f.value, b.value
 
 
-def _dense_sizes(kind, rows, d_in, d_out, dtype, act, grad_dtype):
-    code = {"f32": 0, "bf16": 1}[dtype]
-    g = code if grad_dtype is None else {"f32": 0, "bf16": 1}[grad_dtype]
-    return _dense_plan(kind, rows, d_in, d_out, code, g, 0, _act_code(act, kind), d_in, d_out, d_out, d_out, 0, 0)[1:]
+def _dense_sizes(kind, rows, d_in, d_out, dtype, act, grad_dtype, ldx, ldw, ldy, unaligned):
+    what = f"moe_{kind}_workspace_size"
+    if grad_dtype is None:
+        grad_dtype = dtype
+    for t in (dtype, grad_dtype):
+        if t not in ("f32", "bf16"):
+            raise MoeError(f"{what}: dtypes are f32 and bf16, got {t!r}")
+    a = _act_code(act, what)
+    for n in unaligned:
+        if n not in ("x", "w", "y"):
+            raise MoeError(f"{what}: unaligned names x, w or y, got {n!r}")
+        a |= _ANY[n]
+    code, g = DTYPE_CODE[dtype], DTYPE_CODE[grad_dtype]
+    ld = [d if v is None else v for v, d in ((ldx, d_in), (ldw, d_out), (ldy, d_out))]
+    return _dense_plan(kind, rows, d_in, d_out, code, g, 0, a, *ld, d_out, 0, 0)[1:]
 
 
 def moe_linear_workspace_size(rows: int, d_in: int, d_out: int, dtype: str = "bf16", act: str = "none",
-                              grad_dtype: Optional[str] = "f32"):
-    """Bytes of workspace for (moe_linear_fwd, moe_linear_bwd) on contiguous
-    tensors."""
-    return _dense_sizes("linear", rows, d_in, d_out, dtype, act, grad_dtype)
+                              grad_dtype: Optional[str] = "f32", ldx: Optional[int] = None, ldw: Optional[int] = None,
+                              ldy: Optional[int] = None, unaligned=()):
+    """Bytes of workspace for (moe_linear_fwd, moe_linear_bwd): ldx, ldw and ldy
+    the row distances of x, w and y (in the backward dy), where they are not
+    contiguous; unaligned names those of "x", "w" and "y" whose address is not a
+    multiple of 16 bytes."""
+    return _dense_sizes("linear", rows, d_in, d_out, dtype, act, grad_dtype, ldx, ldw, ldy, unaligned)
 
 
 def moe_glu_workspace_size(rows: int, d_in: int, d_out: int, dtype: str = "bf16", act: str = "silu",
-                           grad_dtype: Optional[str] = "f32"):
-    """Bytes of workspace for (moe_glu_fwd, moe_glu_bwd) on contiguous tensors."""
-    return _dense_sizes("glu", rows, d_in, d_out, dtype, act, grad_dtype)
+                           grad_dtype: Optional[str] = "f32", ldx: Optional[int] = None, ldw: Optional[int] = None,
+                           ldy: Optional[int] = None, unaligned=()):
+    """Bytes of workspace for (moe_glu_fwd, moe_glu_bwd); ldx, ldw (of wg and wu),
+    ldy (of a, in the backward da) and unaligned as in moe_linear_workspace_size."""
+    return _dense_sizes("glu", rows, d_in, d_out, dtype, act, grad_dtype, ldx, ldw, ldy, unaligned)
 
 
 def _dense_ws(nbytes: int, ws, like):

@@ -295,3 +295,22 @@ def test_workspace_of_unaligned_bases_holds_copies():
     assert _sizes(lib, _desc(**v, act=ANY_REST)) == none
     f32 = dict(v, dtype=0)
     assert _sizes(lib, _desc(**f32)) == _sizes(lib, _desc(**f32, act=ANY_X | ANY_W | ANY_Y | ANY_REST))
+
+
+@pytest.mark.parametrize("size", [moe.moe_linear_workspace_size, moe.moe_glu_workspace_size])
+def test_workspace_size_of_strided_and_unaligned_tensors(size):
+    """The sizes that the calls themselves ask for."""
+    kind = "linear" if size is moe.moe_linear_workspace_size else "glu"
+    plan = lambda a, *ld: moe._dense_plan(kind, 1000, 512, 768, 1, 0, 0, a, *ld, 768, 0, 0)[1:]  # noqa: E731
+    kw = dict(act="gelu")
+    base = size(1000, 512, 768, **kw)
+    assert base == plan(4, 512, 768, 768) == size(1000, 512, 768, ldx=512, ldw=768, ldy=768, **kw)
+    assert size(1000, 512, 768, ldx=515, **kw) == plan(4, 515, 768, 768) > base
+    assert size(1000, 512, 768, ldw=769, **kw) == plan(4, 512, 769, 768) > base
+    assert size(1000, 512, 768, ldx=520, ldw=776, **kw)[0] == base[0]
+    assert size(1000, 512, 768, unaligned=("x", "w"), **kw) == plan(4 | ANY_X | ANY_W, 512, 768, 768) > base
+    assert moe.moe_linear_workspace_size(1000, 512, 768, ldy=769)[1] > moe.moe_linear_workspace_size(1000, 512, 768)[1]
+    for bad, match in ((dict(dtype="fp8"), "dtypes"), (dict(dtype=None, grad_dtype=None), "dtypes"), (dict(grad_dtype="i32"), "dtypes"), (dict(unaligned=("z",)), "unaligned"),
+                       (dict(ldx=511), "status 2"), (dict(act="tanh"), "act")):
+        with pytest.raises(moe.MoeError, match=match):
+            size(1000, 512, 768, **bad)

@@ -124,3 +124,26 @@ def test_no_rows_at_an_odd_address(rows):
     moe.moe_linear_bwd(torch.zeros(rows, 10, device=DEV), x, w, dw=dw.t)
     assert not dw.t.any()
     dw.check()
+
+
+@pytest.mark.parametrize("off,pad", [(0, 3), (0, 8), (3, 0), (5, 8)])
+def test_workspaces_of_the_stated_sizes(off, pad):
+    """Strided and unaligned tensors with workspaces allocated beforehand."""
+    n, d, f = 200, 72, 136
+    torch.manual_seed(off + pad)
+    r = lambda *s: _at(torch.randn(*s).bfloat16(), off, pad)  # noqa: E731
+    x, w, w2, dy = r(n, d), r(d, f), r(d, f), r(n, f)
+    kw = dict(ldx=d + pad, ldw=f + pad, ldy=f + pad, unaligned=("x", "w", "y") if off else ())
+    W = lambda k: torch.empty(k, dtype=torch.uint8, device=DEV) if k else None  # noqa: E731
+    lf, lb = moe.moe_linear_workspace_size(n, d, f, act="gelu", **kw)
+    gf, gb = moe.moe_glu_workspace_size(n, d, f, **kw)
+    y = _Out(n, f, torch.bfloat16, off, pad)
+    _, z = moe.moe_linear_fwd(x, w, act="gelu", y=y.t, save_z=True, ws=W(lf))
+    assert torch.equal(y.t, moe.moe_linear_fwd(x, w, act="gelu")[0])
+    for a, b in zip(moe.moe_linear_bwd(dy, x, w, z, "gelu", ws=W(lb)), moe.moe_linear_bwd(dy, x, w, z, "gelu")):
+        assert torch.equal(a, b)
+    a = _Out(n, f, torch.bfloat16, off, pad)
+    _, g, u = moe.moe_glu_fwd(x, w, w2, a=a.t, save=True, ws=W(gf))
+    assert torch.equal(a.t, moe.moe_glu_fwd(x, w, w2)[0])
+    for p, q in zip(moe.moe_glu_bwd(dy, x, w, w2, g, u, ws=W(gb)), moe.moe_glu_bwd(dy, x, w, w2, g, u)):
+        assert torch.equal(p, q)
