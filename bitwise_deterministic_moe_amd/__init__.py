@@ -24,6 +24,7 @@ __all__ = [
     "moe_mx_wgrad_rows", "moe_mx_quantize_wgrad", "moe_mx_wgrad", "MXW_TOKEN", "MXW_ROW", "MXW_ACT_P",
     "moe_route", "moe_layernorm_fwd", "moe_layernorm_bwd", "moe_linear_fwd", "moe_linear_bwd", "moe_glu_fwd",
     "moe_glu_bwd", "moe_layernorm_workspace_size", "moe_linear_workspace_size", "moe_glu_workspace_size", "ACTIVATIONS",
+    "moe_linear_stage_names", "moe_glu_stage_names",
 ]
 
 DETERMINISTIC = 0
@@ -40,7 +41,7 @@ EXPORTED_SYMBOLS = ("moe_abi_version", "moe_status_string", "moe_rows_cap", "moe
                     "moe_mx_fwd_fc2", "moe_mx_wgrad_rows", "moe_mx_quantize_wgrad", "moe_mx_wgrad", "moe_route",
                     "moe_source_hash", "moe_layernorm_workspace_size", "moe_layernorm_fwd", "moe_layernorm_bwd",
                     "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd", "moe_glu_workspace_size",
-                    "moe_glu_fwd", "moe_glu_bwd")
+                    "moe_glu_fwd", "moe_glu_bwd", "moe_linear_stage_names", "moe_glu_stage_names")
 # activations of the dense operators (moe_act)
 ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4}
 # matrices of a dense call that may start at any element (moe_any)
@@ -149,6 +150,9 @@ def load_library() -> ctypes.CDLL:
                                       u64, vp]
     for f in ("moe_linear_workspace_size", "moe_glu_workspace_size"):
         getattr(lib, f).argtypes = [N, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+        getattr(lib, f).restype = ctypes.c_int
+    for f in ("moe_linear_stage_names", "moe_glu_stage_names"):
+        getattr(lib, f).argtypes = [N, ctypes.c_int, ctypes.c_char_p, sz]
         getattr(lib, f).restype = ctypes.c_int
     lib.moe_linear_fwd.argtypes = [N] + [vp] * 7 + [sz, vp]
     lib.moe_linear_bwd.argtypes = [N] + [vp] * 9 + [sz, vp]
@@ -930,8 +934,8 @@ def _dense_plan(kind: str, rows: int, d_in: int, d_out: int, dtype: int, grad_dt
     return c, f.value, b.value
 
 
-def _dense_sizes(kind, rows, d_in, d_out, dtype, act, grad_dtype, ldx, ldw, ldy, unaligned):
-    what = f"moe_{kind}_workspace_size"
+def _dense_key(what, rows, d_in, d_out, dtype, act, grad_dtype, ldx, ldw, ldy, unaligned):
+    """_dense_plan's arguments after its first."""
     if grad_dtype is None:
         grad_dtype = dtype
     for t in (dtype, grad_dtype):
@@ -942,9 +946,8 @@ def _dense_sizes(kind, rows, d_in, d_out, dtype, act, grad_dtype, ldx, ldw, ldy,
         if n not in ("x", "w", "y"):
             raise MoeError(f"{what}: unaligned names x, w or y, got {n!r}")
         a |= _ANY[n]
-    code, g = DTYPE_CODE[dtype], DTYPE_CODE[grad_dtype]
     ld = [d if v is None else v for v, d in ((ldx, d_in), (ldw, d_out), (ldy, d_out))]
-    return _dense_plan(kind, rows, d_in, d_out, code, g, 0, a, *ld, d_out, 0, 0)[1:]
+    return (rows, d_in, d_out, DTYPE_CODE[dtype], DTYPE_CODE[grad_dtype], 0, a, *ld, d_out, 0, 0)
 
 
 def moe_linear_workspace_size(rows: int, d_in: int, d_out: int, dtype: str = "bf16", act: str = "none",
@@ -954,7 +957,8 @@ def moe_linear_workspace_size(rows: int, d_in: int, d_out: int, dtype: str = "bf
     the row distances of x, w and y (in the backward dy), where they are not
     contiguous; unaligned names those of "x", "w" and "y" whose address is not a
     multiple of 16 bytes."""
-    return _dense_sizes("linear", rows, d_in, d_out, dtype, act, grad_dtype, ldx, ldw, ldy, unaligned)
+    return _dense_plan("linear", *_dense_key("moe_linear_workspace_size", rows, d_in, d_out, dtype, act, grad_dtype, ldx, ldw,
+                                             ldy, unaligned))[1:]
 
 
 def moe_glu_workspace_size(rows: int, d_in: int, d_out: int, dtype: str = "bf16", act: str = "silu",
@@ -962,7 +966,32 @@ def moe_glu_workspace_size(rows: int, d_in: int, d_out: int, dtype: str = "bf16"
                            ldy: Optional[int] = None, unaligned=()):
     """Bytes of workspace for (moe_glu_fwd, moe_glu_bwd); ldx, ldw (of wg and wu),
     ldy (of a, in the backward da) and unaligned as in moe_linear_workspace_size."""
-    return _dense_sizes("glu", rows, d_in, d_out, dtype, act, grad_dtype, ldx, ldw, ldy, unaligned)
+    return _dense_plan("glu", *_dense_key("moe_glu_workspace_size", rows, d_in, d_out, dtype, act, grad_dtype, ldx, ldw, ldy,
+                                          unaligned))[1:]
+
+
+def _dense_names(kind, call, *key):
+    what = f"moe_{kind}_stage_names"
+    b = ctypes.create_string_buffer(256)
+    c = _dense_plan(kind, *_dense_key(what, *key))[0]
+    _check(getattr(load_library(), what)(ctypes.byref(c), call, b, len(b)), what)
+    return b.value.decode().split(",") if b.value else []
+
+
+def moe_linear_stage_names(rows: int, d_in: int, d_out: int, call: int, dtype: str = "bf16", act: str = "none",
+                           grad_dtype: Optional[str] = "f32", ldx: Optional[int] = None, ldw: Optional[int] = None,
+                           ldy: Optional[int] = None, unaligned=()):
+    """Names of the kernels that a call enqueues, with the tile and the number of
+    chunks of each product: call 0 moe_linear_fwd, 1 moe_linear_bwd, 2 the same
+    without db; the other arguments as in moe_linear_workspace_size."""
+    return _dense_names("linear", call, rows, d_in, d_out, dtype, act, grad_dtype, ldx, ldw, ldy, unaligned)
+
+
+def moe_glu_stage_names(rows: int, d_in: int, d_out: int, call: int, dtype: str = "bf16", act: str = "silu",
+                        grad_dtype: Optional[str] = "f32", ldx: Optional[int] = None, ldw: Optional[int] = None,
+                        ldy: Optional[int] = None, unaligned=()):
+    """The same for moe_glu_fwd (call 0) and moe_glu_bwd (1)."""
+    return _dense_names("glu", call, rows, d_in, d_out, dtype, act, grad_dtype, ldx, ldw, ldy, unaligned)
 
 
 def _dense_ws(nbytes: int, ws, like):

@@ -196,6 +196,11 @@ struct DenseShape {
 };
 constexpr int kDenseBf16Tiles = 4, kDenseF32Tiles = 2;
 DenseShape dense_shape(int form, bool bf16, int tile);
+// Variants of a tile: the 64-row bf16 tile's short ring (at most two slices a
+// workgroup), and the float32 tiles' loads of four columns (each operand's
+// contiguous direction is whole groups of four).
+bool dense_short(const DenseParams& P, int form);
+bool dense_v4(const DenseParams& P, int form);
 
 // bf16 matrices [rows][cols] (row distance ld) into [rows][ldo], zeros past cols
 struct DensePackParams {

@@ -1352,6 +1352,15 @@ DenseShape dense_shape(int form, bool bf16, int tile) {
   return s;
 }
 
+bool dense_short(const DenseParams& P, int form) {
+  const int64_t steps = (P.K + dn::SBK - 1) / dn::SBK * (form == kFormDx ? P.nseg : 1);
+  return steps <= 2 * (int64_t)P.S;
+}
+bool dense_v4(const DenseParams& P, int form) {
+  const bool ka = form != kFormDw, kb = form == kFormDx;   // K-contiguous operands
+  return (ka ? P.K : P.M) % 4 == 0 && (kb ? P.K : P.N) % 4 == 0;
+}
+
 template <int FORM, bool V4>
 static void dense_f32_launch(const DenseParams& P, int tile, int64_t grid, hipStream_t st) {
   if (tile == 0)
@@ -1363,10 +1372,7 @@ static void dense_f32_launch(const DenseParams& P, int tile, int64_t grid, hipSt
 template <int FORM>
 static void dense_gemm_launch(const DenseParams& P, bool bf16, int tile, int64_t grid, hipStream_t st) {
   if (!bf16) {
-    // whole groups of four along each operand's contiguous direction
-    const bool ka = FORM != kFormDw, kb = FORM == kFormDx;
-    const bool v4 = (ka ? P.K : P.M) % 4 == 0 && (kb ? P.K : P.N) % 4 == 0;
-    if (v4)
+    if (dense_v4(P, FORM))
       dense_f32_launch<FORM, true>(P, tile, grid, st);
     else
       dense_f32_launch<FORM, false>(P, tile, grid, st);
@@ -1378,8 +1384,7 @@ static void dense_gemm_launch(const DenseParams& P, bool bf16, int tile, int64_t
     case 2: dense_bf16_small_kernel<FORM, 2, 2, false><<<grid, 256, 0, st>>>(P); break;
     default: {
       constexpr int NB = FORM == kFormGlu ? 2 : 1;
-      const int64_t steps = (P.K + dn::SBK - 1) / dn::SBK * (FORM == kFormDx ? P.nseg : 1);
-      if (steps <= 2 * (int64_t)P.S)
+      if (dense_short(P, FORM))
         dense_bf16_small_kernel<FORM, 1, NB, true><<<grid, 256, 0, st>>>(P);
       else
         dense_bf16_small_kernel<FORM, 1, NB, false><<<grid, 256, 0, st>>>(P);

@@ -1,6 +1,9 @@
 // Host side of the dense operators' C ABI (declared in include/moedet.h):
 // argument checks, workspace layout, and the choice of kernel and split from
 // sizes alone.
+#include <cstdarg>
+#include <cstdio>
+
 #include "../../include/moedet.h"
 #include "dense.h"
 
@@ -272,6 +275,80 @@ moe_status workspace_size(const moe_dense* p, int nm, size_t* fwd, size_t* bwd) 
   if (fwd) *fwd = fwd_plan(p, d).total;
   if (bwd) *bwd = bwd_plan(p, d).total;
   return MOE_OK;
+}
+
+// ------------------------------------------------------------------ kernel names
+struct Names {
+  char* at;
+  size_t left;
+  bool fits = true;
+  void add(const char* format, ...) {
+    va_list v;
+    va_start(v, format);
+    const int n = vsnprintf(at, left, format, v);
+    va_end(v);
+    fits = fits && n >= 0 && (size_t)n < left;
+    if (fits) {
+      at += n;
+      left -= n;
+    }
+  }
+};
+
+void add_product(Names& o, const char* name, const Dense& d, int form, const Choice& c, int64_t M, int64_t N, int nseg, int64_t K) {
+  DenseParams P{};
+  P.M = M;
+  P.N = (int)N;
+  P.K = K;
+  P.nseg = nseg;
+  P.S = c.S;
+  static const char* const kBf16[kDenseBf16Tiles] = {"256x256", "128x256", "128x128", "64x64"};
+  static const char* const kF32[kDenseF32Tiles] = {"128x128_parts", "64x64_f32"};
+  o.add("%s_%s", name, d.bf16 ? kBf16[c.tile] : kF32[c.tile]);
+  if (d.bf16 && c.tile == kDenseBf16Tiles - 1 && dense_short(P, form)) o.add("_short");
+  if (!d.bf16 && !dense_v4(P, form)) o.add("_odd");
+  if (c.S > 1) o.add("_split%d", c.S);
+}
+
+moe_status stage_names(const moe_dense* p, int nm, int call, char* names, size_t bytes) {
+  Dense d;
+  const moe_status s = check(p, nm, &d);
+  if (s != MOE_OK) return s;
+  if (call < 0 || call > 2) return MOE_ERR_MODE;
+  if (!names) return MOE_ERR_NULL;
+  if (bytes < 1) return MOE_ERR_WORKSPACE;
+  Names o{names, bytes};
+  o.add("");
+  const bool db = nm == 1 && call == 1;
+  if (d.T == 0) {
+    if (call) o.add(nm == 2 ? "zero,zero" : db ? "zero,zero" : "zero");
+  } else if (call == 0) {
+    const FwdPlan f = fwd_plan(p, d);
+    if (!f.ch.S) return MOE_ERR_SHAPE;
+    const int form = nm == 2 ? kFormGlu : kFormLinear;
+    const char* name = nm == 2 ? "glu" : "linear";
+    if (f.pack_x || f.pack_w) o.add("copy,");
+    if (f.few) {
+      o.add("%s_few%d", name, (int)up(d.T, 16));
+      if (f.ch.S > 1) o.add("_split%d", f.ch.S);
+    } else {
+      add_product(o, name, d, form, f.ch, d.T, d.F, 1, d.D);
+    }
+    if (f.ch.S > 1) o.add(",join");
+  } else {
+    const BwdPlan b = bwd_plan(p, d);
+    if (!b.dx.S || !b.dw.S) return MOE_ERR_SHAPE;
+    const bool copies = b.pack_x || b.pack_w;
+    if (b.make_dz || db)
+      o.add(!copies ? "%s," : "%s_copy,", b.make_dz ? "dz" : "sums");
+    else if (copies)
+      o.add("copy,");
+    add_product(o, "dx", d, kFormDx, b.dx, d.T, d.D, nm, d.F);
+    o.add(",");
+    add_product(o, "dw", d, kFormDw, b.dw, d.D, d.F, nm, d.T);
+    if (b.dx.S > 1 || b.dw.S > 1 || db) o.add(",join");
+  }
+  return o.fits ? MOE_OK : MOE_ERR_WORKSPACE;
 }
 
 moe_status check_ws(const void* ws, size_t have, size_t need) {
@@ -558,6 +635,14 @@ MOE_API moe_status moe_linear_workspace_size(const moe_dense* p, size_t* fwd_byt
 
 MOE_API moe_status moe_glu_workspace_size(const moe_dense* p, size_t* fwd_bytes, size_t* bwd_bytes) {
   return workspace_size(p, 2, fwd_bytes, bwd_bytes);
+}
+
+MOE_API moe_status moe_linear_stage_names(const moe_dense* p, int call, char* names, size_t bytes) {
+  return stage_names(p, 1, call, names, bytes);
+}
+
+MOE_API moe_status moe_glu_stage_names(const moe_dense* p, int call, char* names, size_t bytes) {
+  return stage_names(p, 2, call, names, bytes);
 }
 
 MOE_API moe_status moe_linear_fwd(const moe_dense* p, const void* x, const void* w, const void* bias,

@@ -766,6 +766,16 @@ moe_status moe_linear_workspace_size(const moe_dense* p, size_t* fwd_bytes, size
 /* The same for the gated product. */
 moe_status moe_glu_workspace_size(const moe_dense* p, size_t* fwd_bytes, size_t* bwd_bytes);
 
+/* Names of the kernels that a call with this description enqueues, in order,
+ * comma-separated and ended by 0, in `names` (HOST, `bytes` long; 160 are
+ * enough): which tile each product takes, and in how many chunks of its
+ * contraction.  call: 0 = forward, 1 = backward with a bias gradient, 2 =
+ * backward without one (the gated product has none).  Errors: those of the
+ * description, MOE_ERR_MODE (call), MOE_ERR_NULL, MOE_ERR_WORKSPACE (bytes). */
+moe_status moe_linear_stage_names(const moe_dense* p, int call, char* names, size_t bytes);
+/* The same for the gated product. */
+moe_status moe_glu_stage_names(const moe_dense* p, int call, char* names, size_t bytes);
+
 /* Linear map with its epilogue: z = x w + bias, y = act(z) + residual.
  *   x [T, D], w [D, F]; bias [F] or NULL; residual [T, F] or NULL
  *   y        DEVICE [T, F] output

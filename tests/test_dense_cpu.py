@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import bitwise_deterministic_moe_amd as moe
+import dense_cases
 import oracle
 
 ACTS = list(moe.ACTIVATIONS)
@@ -314,3 +315,27 @@ def test_workspace_size_of_strided_and_unaligned_tensors(size):
                        (dict(ldx=511), "status 2"), (dict(act="tanh"), "act")):
         with pytest.raises(moe.MoeError, match=match):
             size(1000, 512, 768, **bad)
+
+
+# --------------------------------------------------------------------- kernels
+def test_cases_reach_every_kernel():
+    found = set().union(*[dense_cases.kernels(*c) for c in dense_cases.CASES])
+    assert found == dense_cases.every_kernel()
+
+
+def test_stage_names():
+    names = moe.moe_linear_stage_names
+    assert names(0, 64, 96, 0) == [] and names(0, 64, 96, 1) == ["zero", "zero"] and names(0, 64, 96, 2) == ["zero"]
+    assert names(1, 64, 96, 0) == ["linear_few16"]
+    assert names(1500, 1001, 517, 1, act="gelu")[0] == "dz_copy" and names(1500, 1001, 517, 0)[0] == "copy"
+    assert names(1500, 1024, 512, 0, unaligned=("x",))[0] == "copy" and names(1500, 1024, 512, 0)[0].startswith("linear_")
+    assert names(4096, 8192, 2048, 1)[0] == "sums" and names(4096, 8192, 2048, 2)[0].startswith("dx_")
+    assert names(4096, 8192, 2048, 1)[-1] == "join"
+    assert moe.moe_glu_stage_names(4096, 2048, 8192, 0) == ["glu_256x256"]
+    lib, c = moe.load_library(), _desc()
+    b = ctypes.create_string_buffer(64)
+    assert lib.moe_linear_stage_names(c, 3, b, 64) == MODE and lib.moe_linear_stage_names(c, 0, None, 64) == NULL
+    assert lib.moe_linear_stage_names(c, 0, b, 8) == WORKSPACE and lib.moe_linear_stage_names(None, 0, b, 64) == NULL
+    assert lib.moe_glu_stage_names(_desc(act=9), 0, b, 64) == MODE
+    with pytest.raises(moe.MoeError, match="status 5"):
+        names(4, 8, 8, 3)
