@@ -178,13 +178,24 @@ struct DenseParams {
   uint64_t seed;
 };
 
-// Rows of the few-row kernels (weights streamed once), by the number of matrices.
-// bf16 against the 64-row tiles, us: one matrix 2048 x 8192, 33 rows 10.9 and 12.9,
-// 64 rows 13.8 and 13.0; 2048^2, 33 rows 8.5 and 8.3, 64 rows 11.5 and 9.8;
-// gated 2048 x 8192, 48 rows 16.4 and 19.0, 64 rows 18.2 and 19.3; 4096^2, 64 rows
-// 29.8 and 20.4.  Operands that the tiles would have to copy first are streamed up to
-// 64 rows.  float32, one matrix 2048^2, 32 rows 12.5 and 13.9, 48 rows 17.7 and 15.6.
+// Rows of the few-row kernels (weights streamed once), by the number of matrices and
+// whether tiles would have to copy the weights first.  Against the tiles, us (kernels
+// alone, in a graph):
+//   bf16, one matrix  32 rows: 2048^2 9.7 and 9.4, 2048 x 8192 10.6 and 12.5, 1024^2 5.3 and
+//                     6.5, 4096^2 16.5 and 12.3; 64 rows: 12.7 and 10.7, 13.2 and 12.5, 7.0 and
+//                     6.6, 21.7 and 13.0
+//   bf16, gated       48 rows: 15.1 and 14.1, 16.5 and 20.0, 7.1 and 9.0, 28.4 and 19.9
+//   bf16, weights to copy, 64 rows: one matrix 13.7 and 18.0, 15.0 and 25.1, 7.7 and 10.2,
+//                     23.8 and 24.9; gated 17.7 and 21.1, 23.6 and 45.1, 10.7 and 13.8, 33.6 and 45.9
+//   float32           32 rows: one matrix 13.4 and 14.1, 26.2 and 27.1, 8.7 and 9.2, 24.2 and
+//                     27.0; gated 17.6 and 21.9, 54.1 and 46.8, 13.5 and 15.1, 49.1 and 50.8
 constexpr int few_rows(bool bf16, int nm, bool copies) { return !bf16 ? 32 : copies ? 64 : nm == 2 ? 48 : 32; }
+// Rows from which these kernels read a copy of an x whose bf16 rows do not all start on
+// 16 bytes: every workgroup reads all of x, and its loads then straddle lines.  In
+// place and with the copy, us, one matrix: 12 rows 4096^2 17.4 and 15.6, 2048 x 8192 10.9 and
+// 11.7; 16 rows 19.3 and 16.1, 11.7 and 11.8; 32 rows 31.0 and 19.2, 18.0 and 13.5; weights to copy
+// too, 64 rows 57.1 and 26.6, 30.8 and 18.0.
+constexpr int kFewCopyRows = 13;
 
 // tile: as in dense_shape
 hipError_t launch_dense_gemm(const DenseParams& P, int form, bool bf16, int tile, hipStream_t st);

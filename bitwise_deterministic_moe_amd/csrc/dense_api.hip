@@ -170,7 +170,7 @@ int few_chunks(const Dense& d) {
   return tS < t1 ? (int)S : 1;
 }
 bool few(const Dense& d, const moe_dense* p) {
-  return d.T <= few_rows(d.bf16, d.nm, !direct_x(d, p) || !direct_w(d, p));
+  return d.T <= few_rows(d.bf16, d.nm, !direct_w(d, p));
 }
 
 // ------------------------------------------------------------- workspace layout
@@ -191,22 +191,23 @@ FwdPlan fwd_plan(const moe_dense* p, const Dense& d) {
   size_t o = 0;
   if (d.T == 0) return f;
   if (f.few) {
+    f.pack_x = d.bf16 && d.T >= kFewCopyRows && (p->ldx % 8 || (d.any & MOE_ANY_X));
     f.ch = Choice{0, few_chunks(d)};
   } else {
     f.pack_x = !direct_x(d, p);
     f.pack_w = !direct_w(d, p);
     f.ch = choose(d, form, d.T, d.F, 1, d.D, 0);
-    if (f.pack_x) {
-      f.ldx = up(d.D, 8);
-      if (!copies_fit(d, f.ldx)) f.ch.S = 0;
-      f.x = o;
-      o += align_up((size_t)d.T * f.ldx * 2);
-    }
-    if (f.pack_w) {
-      f.ldw = up(d.F, 8);
-      f.w = o;
-      o += align_up((size_t)d.nm * d.D * f.ldw * 2);
-    }
+  }
+  if (f.pack_x) {
+    f.ldx = up(d.D, 8);
+    if (!copies_fit(d, f.ldx)) f.ch.S = 0;
+    f.x = o;
+    o += align_up((size_t)d.T * f.ldx * 2);
+  }
+  if (f.pack_w) {
+    f.ldw = up(d.F, 8);
+    f.w = o;
+    o += align_up((size_t)d.nm * d.D * f.ldw * 2);
   }
   f.part_seg = up(d.F, 4);
   f.part_ld = d.nm * f.part_seg;

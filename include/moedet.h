@@ -649,7 +649,7 @@ moe_status moe_mfma_rate(int64_t blocks, int64_t iters, float value, float* sink
  *     description says so (moe_any).  bfloat16 matrices at a 16-byte base whose
  *     row length and ld are multiples of 8 are read in place; other x,
  *     weights and dy (da) are copied into the workspace first where tiles read
- *     them.
+ *     them, and such x also where more than a few rows stream the weights.
  *   - Sums are float32, every output is rounded once.  Large float32 products
  *     read each number as the exact sum of three bfloat16 numbers; a row or
  *     column with a number that is not such a sum (some below 2^-110, infinite
@@ -782,7 +782,7 @@ moe_status moe_glu_stage_names(const moe_dense* p, int call, char* names, size_t
  *   z        DEVICE [T, F] of z_dtype, output (the backward reads it), or NULL
  *   ws       moe_linear_workspace_size fwd_bytes, 256-byte aligned
  * Few rows stream the weights once: at most 32, in bfloat16 48 for the gated
- * product and 64 where tiles would have to copy an operand.
+ * product and 64 where tiles would have to copy the weights.
  * Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_MODE (act), MOE_ERR_NULL,
  * MOE_ERR_WORKSPACE before anything is enqueued; MOE_ERR_HIP for a launch
  * failure. */

@@ -339,3 +339,18 @@ def test_stage_names():
     assert lib.moe_glu_stage_names(_desc(act=9), 0, b, 64) == MODE
     with pytest.raises(moe.MoeError, match="status 5"):
         names(4, 8, 8, 3)
+
+
+def test_few_rows_of_an_unaligned_input():
+    """An x whose rows do not start on 16 bytes is copied, for the weight-streaming
+    kernel as for the tiles, and does not keep more rows on that kernel."""
+    names = moe.moe_linear_stage_names
+    assert names(50, 512, 520, 0) == names(50, 512, 520, 0, ldx=513)[1:] and names(50, 512, 520, 0, ldx=513)[0] == "copy"
+    for rows in (13, 32):
+        assert names(rows, 512, 520, 0, ldx=513) == ["copy"] + names(rows, 512, 520, 0)
+        assert names(rows, 512, 520, 0, unaligned=("x",)) == ["copy"] + names(rows, 512, 520, 0)
+    assert names(12, 512, 520, 0, ldx=513) == ["linear_few16"]
+    assert names(20, 513, 520, 0, ldx=520) == ["linear_few32"]      # rows of 16-byte starts, whatever their length
+    assert names(64, 512, 521, 0) == ["linear_few64"] and names(64, 512, 521, 0, ldx=513) == ["copy", "linear_few64"]
+    assert moe.moe_glu_stage_names(49, 512, 520, 0, ldx=513)[1].startswith("glu_64x64")
+    assert names(20, 512, 520, 0, "f32", ldx=513) == ["linear_few32"]
