@@ -632,9 +632,9 @@ moe_status moe_mfma_rate(int64_t blocks, int64_t iters, float value, float* sink
 
 /* ------------------------------------------------------------------------
  * Dense operators around the expert layer: the layer norm in front of the
- * router and the experts, the gated feed-forward product of a shared expert
- * beside the routed ones, and the linear map (bias, activation, residual)
- * that takes it into the residual stream.  The pages describe none of them;
+ * experts, the gated feed-forward product of a shared expert beside the routed
+ * ones, and the linear map (bias, activation, residual) that adds its output
+ * to theirs.  The pages describe none of them;
  * the definitions below are this library's, under the pages' general rule
  * (every reduction in an order fixed by indices and shapes): there is one
  * mode, without atomics, and the output bits are a function of the input
