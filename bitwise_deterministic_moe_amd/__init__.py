@@ -782,8 +782,6 @@ def _act_code(act: str, what: str) -> int:
 def _any_code(x: int, w: int, y: int, rest: int) -> int:
     """The moe_any bits of a call: which addresses (of several matrices, their
     or) are no multiples of 16 bytes."""
-    if not (x | w | y | rest) & 15:
-        return 0
     return (x & 15 and _ANY["x"]) | (w & 15 and _ANY["w"]) | (y & 15 and _ANY["y"]) | (rest & 15 and _ANY["rest"])
 
 
@@ -1040,7 +1038,9 @@ def moe_linear_fwd(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, a
     elif save_z:
         z = _new(x, f, torch.float32)
     px, pw, py, pr, pz = x.data_ptr(), w.data_ptr(), y.data_ptr(), _ptr(residual), _ptr(z)
-    a |= _any_code(px, pw, py, (pr or 0) | (pz or 0))
+    rest = (pr or 0) | (pz or 0)
+    if (px | pw | py | rest) & 15:
+        a |= _any_code(px, pw, py, rest)
     c, need, _ = _dense_plan("linear", rows, d, f, code, code, zc, a, ldx, ldw, ldy, ldz, ldr, shuffle_seed)
     ws, nb = _dense_ws(need, ws, x)
     _run(what, lib.moe_linear_fwd, (c, px, pw, _ptr(bias), pr, py, pz, _ptr(ws), nb), x, w, bias, residual, y, z, ws)
@@ -1082,7 +1082,9 @@ def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z=None, a
         db = _flat(x, (f,), (1,), grad_dtype)
     py, px, pw, pz, pa, pdx, pdw = (dy.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(z), _ptr(dx_add), dx.data_ptr(),
                                     dw.data_ptr())
-    a |= _any_code(px, pw, py, (pz or 0) | (pa or 0) | pdx | pdw)
+    rest = (pz or 0) | (pa or 0) | pdx | pdw
+    if (px | pw | py | rest) & 15:
+        a |= _any_code(px, pw, py, rest)
     c, _, need = _dense_plan("linear", rows, d, f, code, g, zc, a, ldx, ldw, ldy, ldz, ldr, shuffle_seed)
     ws, nb = _dense_ws(need, ws, x)
     _run(what, lib.moe_linear_bwd, (c, py, px, pw, pz, pa, pdx, pdw, _ptr(db), _ptr(ws), nb), x, dy, w, z, dx_add, dx, dw,
@@ -1117,7 +1119,9 @@ def moe_glu_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, act: str = 
         g = _new(x, f, torch.float32)
         u = _new(x, f, torch.float32)
     px, pg, pu, pa, zg, zu = x.data_ptr(), wg.data_ptr(), wu.data_ptr(), a.data_ptr(), _ptr(g), _ptr(u)
-    ac |= _any_code(px, pg | pu, pa, (zg or 0) | (zu or 0))
+    rest = (zg or 0) | (zu or 0)
+    if (px | pg | pu | pa | rest) & 15:
+        ac |= _any_code(px, pg | pu, pa, rest)
     c, need, _ = _dense_plan("glu", rows, d, f, code, code, zc, ac, ldx, ldw, ldy, ldz, 0, shuffle_seed)
     ws, nb = _dense_ws(need, ws, x)
     _run(what, lib.moe_glu_fwd, (c, px, pg, pu, pa, zg, zu, _ptr(ws), nb), x, wg, wu, a, g, u, ws)
@@ -1157,7 +1161,9 @@ def moe_glu_bwd(da: torch.Tensor, x: torch.Tensor, wg: torch.Tensor, wu: torch.T
     py, px, pg, pu, zg, zu, pa = (da.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), g.data_ptr(), u.data_ptr(),
                                   _ptr(dx_add))
     pdx, dg, du = dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr()
-    ac |= _any_code(px, pg | pu, py, zg | zu | (pa or 0) | pdx | dg | du)
+    rest = zg | zu | (pa or 0) | pdx | dg | du
+    if (px | pg | pu | py | rest) & 15:
+        ac |= _any_code(px, pg | pu, py, rest)
     c, _, need = _dense_plan("glu", rows, d, f, code, gc, zc, ac, ldx, ldw, ldy, ldz, ldr, shuffle_seed)
     ws, nb = _dense_ws(need, ws, x)
     _run(what, lib.moe_glu_bwd, (c, py, px, pg, pu, zg, zu, pa, pdx, dg, du, _ptr(ws), nb), x, da, wg, wu, g, u, dx_add, dx,
