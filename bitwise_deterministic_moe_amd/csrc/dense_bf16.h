@@ -263,7 +263,7 @@ DEV void mainloop(uint32_t ring, int nsteps, Issue issue, f32x16_t (&acc)[4][4],
 // that hold one 32 x 32 block of each 64 x 64 part.  For products with too few
 // tiles of 128 x 256 to fill the device: more workgroups, a short first slice and a
 // short epilogue, paid for with more reads of the caches, which bound them
-// (2048^3 with 128 x 128: 24 us, 720 TF, 16 TB/s into LDS; 512^3 with 64 x 64: 5.9 us,
+// (2048^3 with 128 x 128: 24 us, 720 TF, 0.3 GB through the L2s, 13 TB/s; 512^3 with 64 x 64: 5.9 us,
 // of it 4.5 us launch, first slice and epilogue).
 // One barrier a slice: the reads of the slot that is filled next were waited for
 // before it.  More slots are no faster (1024^3: 8.2 us with 4, 8.4 with 5, 8.6 with
