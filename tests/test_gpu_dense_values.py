@@ -76,6 +76,30 @@ def test_small_times_large_float32_numbers(n, d, f):
     assert torch.equal(y1[:, keep], y[:, keep])
 
 
+@pytest.mark.parametrize("n,d,f", [(5, 264, 136), (200, 264, 136), (2048, 512, 2048), (600, 2048, 1100)])
+def test_small_times_large_bf16_numbers(n, d, f):
+    """The same in bf16: numbers below its normal ones count too."""
+    rng = np.random.default_rng(n)
+    b = lambda a: torch.from_numpy(a).bfloat16()  # noqa: E731
+    x = b(_spread(rng, (n, d), (0, 2, 3, 4, n - 1), (1, 64, 100, 127, d - 1)))
+    w = b(_spread(rng, (d, f), (2, 33, 66, 128, d - 2), (0, 63, 65, 131, f - 1)))
+    dy = b(_spread(rng, (n, f), (1, 2, 3, 4, n - 1), (2, 61, 67, 132, f - 3)))
+    hx, hw, hdy = B.host(x), B.host(w), B.host(dy)
+    x, w, dy = x.to(DEV), w.to(DEV), dy.to(DEV)
+
+    def check(got, a, c, what):
+        ref, tol = a @ c, B.prod_err(a.shape[1], np.abs(a), np.abs(c)) + a.shape[1] * 2.0 ** -148
+        B.check(got, ref, B.rounded(tol, ref, B.U["bf16" if got.dtype == torch.bfloat16 else "f32"]) + 2.0 ** -134, what)
+
+    check(moe.moe_linear_fwd(x, w)[0], hx, hw, "y")
+    dx, dw, _ = moe.moe_linear_bwd(dy, x, w, need_db=False)
+    check(dx, hdy, hw.T, "dx")
+    check(dw, hx.T, hdy, "dw")
+    _, g, u = moe.moe_glu_fwd(x, w, w, "none", save=True)
+    check(g, hx, hw, "g")
+    assert torch.equal(g, u)
+
+
 # ----------------------------------------------------------------- activations
 def _truth(name, z):
     """Value and derivative in float64, and the magnitudes of the derivative's two
