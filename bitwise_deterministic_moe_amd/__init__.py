@@ -24,7 +24,8 @@ __all__ = [
     "moe_mx_wgrad_rows", "moe_mx_quantize_wgrad", "moe_mx_wgrad", "MXW_TOKEN", "MXW_ROW", "MXW_ACT_P",
     "moe_route", "moe_layernorm_fwd", "moe_layernorm_bwd", "moe_linear_fwd", "moe_linear_bwd", "moe_glu_fwd",
     "moe_glu_bwd", "moe_layernorm_workspace_size", "moe_linear_workspace_size", "moe_glu_workspace_size", "ACTIVATIONS",
-    "moe_linear_stage_names", "moe_glu_stage_names",
+    "moe_linear_stage_names", "moe_glu_stage_names", "moe_sort", "moe_sort_workspace_size", "moe_permute_fwd",
+    "moe_permute_bwd", "moe_unpermute_fwd", "moe_unpermute_bwd", "moe_dropout_fwd", "moe_dropout_bwd",
 ]
 
 DETERMINISTIC = 0
@@ -41,7 +42,9 @@ EXPORTED_SYMBOLS = ("moe_abi_version", "moe_status_string", "moe_rows_cap", "moe
                     "moe_mx_fwd_fc2", "moe_mx_wgrad_rows", "moe_mx_quantize_wgrad", "moe_mx_wgrad", "moe_route",
                     "moe_source_hash", "moe_layernorm_workspace_size", "moe_layernorm_fwd", "moe_layernorm_bwd",
                     "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd", "moe_glu_workspace_size",
-                    "moe_glu_fwd", "moe_glu_bwd", "moe_linear_stage_names", "moe_glu_stage_names")
+                    "moe_glu_fwd", "moe_glu_bwd", "moe_linear_stage_names", "moe_glu_stage_names",
+                    "moe_sort_workspace_size", "moe_sort", "moe_permute_fwd", "moe_permute_bwd", "moe_unpermute_fwd",
+                    "moe_unpermute_bwd", "moe_dropout_fwd", "moe_dropout_bwd")
 # activations of the dense operators (moe_act)
 ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4}
 # matrices of a dense call that may start at any element (moe_any)
@@ -161,6 +164,18 @@ def load_library() -> ctypes.CDLL:
     for f in ("moe_layernorm_fwd", "moe_layernorm_workspace_size", "moe_layernorm_bwd", "moe_linear_fwd",
               "moe_linear_bwd", "moe_glu_fwd", "moe_glu_bwd"):
         getattr(lib, f).restype = ctypes.c_int
+    ci, i32 = ctypes.c_int, ctypes.c_int32
+    lib.moe_sort_workspace_size.argtypes = [i64, i32, i32, ctypes.POINTER(sz)]
+    lib.moe_sort.argtypes = [vp, ci, i64, i32, i32, i32, vp, vp, vp, vp, sz, u64, vp]
+    lib.moe_permute_fwd.argtypes = [vp, ci, i64, i32, i32, i64, vp, i64, vp, u64, vp]
+    lib.moe_permute_bwd.argtypes = [vp, ci, i64, i32, i32, vp, i64, vp, i64, vp, u64, vp]
+    lib.moe_unpermute_fwd.argtypes = [vp, ci, i64, i32, i32, vp, i64, vp, vp, i64, vp, u64, vp]
+    lib.moe_unpermute_bwd.argtypes = [vp, i64, vp, ci, i64, i32, i32, vp, i64, vp, vp, vp, u64, vp]
+    lib.moe_dropout_fwd.argtypes = [vp, vp, ci, i64, i64, i64, i64, ctypes.c_double, vp, vp, u64, vp]
+    lib.moe_dropout_bwd.argtypes = [vp, ci, i64, i64, i64, ctypes.c_double, vp, vp, u64, vp]
+    for f in ("moe_sort_workspace_size", "moe_sort", "moe_permute_fwd", "moe_permute_bwd", "moe_unpermute_fwd",
+              "moe_unpermute_bwd", "moe_dropout_fwd", "moe_dropout_bwd"):
+        getattr(lib, f).restype = ci
     for f in ("moe_route", "moe_mx_wgrad_rows", "moe_mx_quantize_wgrad", "moe_mx_wgrad", "moe_rows_cap",
               "moe_sched_elems", "moe_workspace_size", "moe_fwd", "moe_bwd_dgrad_dprob",
               "moe_bwd_dgrad_dprob_noalloc", "moe_mx_quantize_t", "moe_mx_fwd_fc1", "moe_mx_fwd_fc2",
@@ -1169,3 +1184,210 @@ def moe_glu_bwd(da: torch.Tensor, x: torch.Tensor, wg: torch.Tensor, wu: torch.T
     _run(what, lib.moe_glu_bwd, (c, py, px, pg, pu, zg, zu, pa, pdx, dg, du, _ptr(ws), nb), x, da, wg, wu, g, u, dx_add, dx,
          dwg, dwu, ws)
     return dx, dwg, dwu
+
+
+# ------------------------------------------------- pieces of an expert layer
+# element types of moe_permute_fwd's rows
+_ROW_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.uint8: 3, torch.int8: 6}
+
+
+@functools.lru_cache(maxsize=4096)
+def moe_sort_workspace_size(tokens: int, top_k: int, num_local: int) -> int:
+    """Workspace bytes of moe_sort."""
+    n = ctypes.c_size_t()
+    _check(load_library().moe_sort_workspace_size(tokens, top_k, num_local, ctypes.byref(n)), "moe_sort_workspace_size")
+    return n.value
+
+
+def moe_sort(topk_idx: torch.Tensor, num_local: int, expert_begin: int = 0, slot_row=None, offsets=None, row_src=None,
+             need_row_src: bool = False, ws=None, shuffle_seed: int = 0):
+    """Stable sort of the slots of topk_idx [T, k] (int32 or int64 expert
+    numbers) by expert, for the experts expert_begin .. expert_begin +
+    num_local - 1; a slot with any other number has no row.  Returns
+    (slot_row int32 [T, k], offsets int32 [num_local + 1], row_src): each slot's
+    row or -1, each expert's first row, and (given, or with need_row_src, else
+    None) each row's flat slot, int32 [T * k], written for the rows there are."""
+    lib, what = load_library(), "moe_sort"
+    if topk_idx.dim() != 2 or topk_idx.dtype not in (torch.int32, torch.int64) or not topk_idx.is_contiguous():
+        raise MoeError(f"{what}: topk_idx must be a contiguous int32 or int64 tensor [tokens, top_k], got "
+                       f"{topk_idx.dtype} {tuple(topk_idx.shape)}")
+    tokens, k = topk_idx.shape
+    if not 0 <= expert_begin < 1 << 31 or not 0 <= num_local < 1 << 31:
+        raise MoeError(f"{what}: experts {expert_begin} .. {expert_begin + num_local - 1}")
+    if k < 1 or tokens * k >= 1 << 31:
+        raise MoeError(f"{what}: {tokens} tokens of {k} slots")
+    i32 = torch.int32
+    if slot_row is None:
+        slot_row = _flat(topk_idx, (tokens, k), (k, 1), i32)
+    else:
+        _need(slot_row, tokens * k, i32, what + " slot_row")
+    if offsets is None:
+        offsets = _flat(topk_idx, (num_local + 1,), (1,), i32)
+    else:
+        _need(offsets, num_local + 1, i32, what + " offsets")
+    if row_src is not None:
+        _need(row_src, tokens * k, i32, what + " row_src")
+    elif need_row_src:
+        row_src = _flat(topk_idx, (tokens * k,), (1,), i32)
+    ws, nb = _dense_ws(moe_sort_workspace_size(tokens, k, num_local), ws, topk_idx)
+    _run(what, lib.moe_sort,
+         (_ptr(topk_idx), _TORCH_TO_CODE[topk_idx.dtype], tokens, k, expert_begin, num_local, _ptr(slot_row),
+          offsets.data_ptr(), _ptr(row_src), _ptr(ws), nb, shuffle_seed), topk_idx, slot_row, offsets, row_src, ws)
+    return slot_row, offsets, row_src
+
+
+def _slots(slot_row: torch.Tensor, tokens: int, what: str) -> int:
+    """Slots of a token in slot_row, [T, k] or flat."""
+    if slot_row.dtype is not torch.int32 or not slot_row.is_contiguous():
+        raise MoeError(f"{what}: slot_row must be a contiguous int32 tensor, got {slot_row.dtype} {tuple(slot_row.shape)}")
+    if slot_row.dim() == 2:
+        n, k = slot_row.shape
+        if n != tokens or k < 1:
+            raise MoeError(f"{what}: slot_row {tuple(slot_row.shape)} for {tokens} tokens")
+        return k
+    n = slot_row.numel()
+    if slot_row.dim() != 1 or (n % tokens if tokens else n) or (tokens and n < tokens):
+        raise MoeError(f"{what}: slot_row {tuple(slot_row.shape)} for {tokens} tokens")
+    return n // tokens if tokens else 1
+
+
+def _row_matrix(rows: torch.Tensor, cols: int, dtype, what: str) -> int:
+    """Rows of a contiguous matrix [rows, cols]."""
+    if rows.dim() != 2 or rows.dtype is not dtype or rows.shape[1] != cols or not rows.is_contiguous():
+        raise MoeError(f"{what}: need a contiguous {dtype} matrix of {cols} columns, got {rows.dtype} {tuple(rows.shape)}")
+    return rows.shape[0]
+
+
+def moe_permute_fwd(x: torch.Tensor, slot_row: torch.Tensor, rows=None, shuffle_seed: int = 0):
+    """rows[slot_row[t, j]] = x[t] for x [T, D] (float32, bf16, int8 or uint8;
+    any row distance) and slot_row [T, k] (or flat) of moe_sort or a Routing.
+    Returns rows, the matrix given or a new one of T * k rows; rows that no slot
+    names stay as they are."""
+    lib, what = load_library(), "moe_permute_fwd"
+    code = _ROW_CODE.get(x.dtype)
+    if code is None or x.dim() != 2 or x.shape[1] < 1:
+        raise MoeError(f"{what}: x must be a float32, bf16, int8 or uint8 matrix, got {x.dtype} {tuple(x.shape)}")
+    cols = x.shape[1]
+    tokens, ldx = _mat(x, cols, x.dtype, what + " x")
+    k = _slots(slot_row, tokens, what)
+    if rows is None:
+        n = tokens * k
+        rows = _flat(x, (n, cols), (cols, 1), x.dtype)
+    else:
+        n = _row_matrix(rows, cols, x.dtype, what + " rows")
+    _run(what, lib.moe_permute_fwd, (_ptr(x), code, tokens, k, cols, ldx, _ptr(slot_row), n, _ptr(rows), shuffle_seed), x,
+         slot_row, rows)
+    return rows
+
+
+def _sum_rows(what: str, fn, rows, slot_row, tokens, prob, add, out, seed):
+    code = _storage(rows, what)
+    if rows.dim() != 2 or rows.shape[1] < 1:
+        raise MoeError(f"{what}: rows must be a matrix, got {tuple(rows.shape)}")
+    cols = rows.shape[1]
+    n = _row_matrix(rows, cols, rows.dtype, what + " rows")
+    if slot_row.dim() == 2:
+        tokens = slot_row.shape[0]
+    elif add is not None:
+        tokens = add.numel() // cols
+    elif out is not None:
+        tokens = out.numel() // cols
+    elif tokens is None:
+        raise MoeError(f"{what}: a flat slot_row leaves the number of tokens open: reshape it to [tokens, top_k]")
+    k = _slots(slot_row, tokens, what)
+    if prob is not None:
+        _need(prob, tokens * k, torch.float32, what + " prob")
+    ldadd = _mat(add, cols, rows.dtype, what + " residual", tokens)[1] if add is not None else cols
+    if out is None:
+        out = _flat(rows, (tokens, cols), (cols, 1), rows.dtype)
+    else:
+        _need(out, tokens * cols, rows.dtype, what + " output")
+    args = (_ptr(rows), code, tokens, k, cols, _ptr(slot_row), n)
+    if prob is not None or what == "moe_unpermute_fwd":
+        args += (_ptr(prob),)
+    _run(what, fn, args + (_ptr(add), ldadd, _ptr(out), seed), rows, slot_row, prob, add, out)
+    return out
+
+
+def moe_permute_bwd(drows: torch.Tensor, slot_row: torch.Tensor, dx_add=None, dx=None, shuffle_seed: int = 0):
+    """Gradient of moe_permute_fwd: dx[t] = sum over j of drows[slot_row[t, j]]
+    (+ dx_add[t]), slots in order, in float32.  Returns dx [T, D], which may be
+    dx_add itself."""
+    return _sum_rows("moe_permute_bwd", load_library().moe_permute_bwd, drows, slot_row, None, None, dx_add, dx, shuffle_seed)
+
+
+def moe_unpermute_fwd(rows: torch.Tensor, slot_row: torch.Tensor, prob=None, residual=None, y=None, shuffle_seed: int = 0):
+    """y[t] = sum over j of prob[t, j] rows[slot_row[t, j]] (+ residual[t]) for
+    rows [R, D] sorted by expert (float32 or bf16), prob float32 [T, k] (None:
+    1), slots in order, in float32.  Returns y [T, D], which may be the residual
+    itself."""
+    tokens = prob.shape[0] if prob is not None and prob.dim() == 2 else None
+    return _sum_rows("moe_unpermute_fwd", load_library().moe_unpermute_fwd, rows, slot_row, tokens, prob, residual, y,
+                     shuffle_seed)
+
+
+def moe_unpermute_bwd(dy: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tensor, prob: torch.Tensor, drows=None,
+                      dprob=None, shuffle_seed: int = 0):
+    """Gradients of moe_unpermute_fwd from dy [T, D]: drows[slot_row[t, j]] =
+    prob[t, j] dy[t] (rows that no slot names stay as they are; drows may be rows
+    itself) and dprob[t, j] = <dy[t], rows[slot_row[t, j]]>, 0 for a slot
+    without a row.  Returns (drows [R, D], dprob float32 [T, k])."""
+    lib, what = load_library(), "moe_unpermute_bwd"
+    code = _storage(dy, what)
+    if dy.dim() != 2 or dy.shape[1] < 1:
+        raise MoeError(f"{what}: dy must be a matrix, got {tuple(dy.shape)}")
+    cols = dy.shape[1]
+    tokens, lddy = _mat(dy, cols, dy.dtype, what + " dy")
+    k = _slots(slot_row, tokens, what)
+    n = _row_matrix(rows, cols, dy.dtype, what + " rows")
+    _need(prob, tokens * k, torch.float32, what + " prob")
+    if drows is None:
+        drows = _flat(dy, (n, cols), (cols, 1), dy.dtype)
+    elif _row_matrix(drows, cols, dy.dtype, what + " drows") != n:
+        raise MoeError(f"{what}: drows has {drows.shape[0]} rows, rows {n}")
+    if dprob is None:
+        dprob = _flat(dy, (tokens, k), (k, 1), torch.float32)
+    else:
+        _need(dprob, tokens * k, torch.float32, what + " dprob")
+    _run(what, lib.moe_unpermute_bwd,
+         (_ptr(dy), lddy, _ptr(rows), code, tokens, k, cols, _ptr(slot_row), n, _ptr(prob), _ptr(drows), _ptr(dprob),
+          shuffle_seed), dy, rows, slot_row, prob, drows, dprob)
+    return drows, dprob
+
+
+def _dropout(what: str, fn, x, p, rng, residual, y, seed):
+    code = _storage(x, what)
+    if x.dim() == 0 or x.shape[-1] < 1:
+        raise MoeError(f"{what}: a tensor [..., D] with columns is needed, got {tuple(x.shape)}")
+    cols = x.shape[-1]
+    rows, ldx = _mat(x, cols, x.dtype, what + " x")
+    if not (0.0 <= p <= 1.0):
+        raise MoeError(f"{what}: p must be in 0..1, got {p}")
+    if rng.dtype is not torch.int64 or rng.numel() != 2 or not rng.is_contiguous():
+        raise MoeError(f"{what}: rng must be a contiguous int64 tensor of 2 numbers, got {rng.dtype} {tuple(rng.shape)}")
+    if y is None:
+        y = _like(x)
+    else:
+        _need(y, rows * cols, x.dtype, what + " output")
+    if what == "moe_dropout_fwd":
+        ldr = _mat(residual, cols, x.dtype, what + " residual", rows)[1] if residual is not None else cols
+        args = (_ptr(x), _ptr(residual), code, rows, cols, ldx, ldr, p, rng.data_ptr(), _ptr(y), seed)
+    else:
+        args = (_ptr(x), code, rows, cols, ldx, p, rng.data_ptr(), _ptr(y), seed)
+    _run(what, fn, args, x, residual, rng, y)
+    return y
+
+
+def moe_dropout_fwd(x: torch.Tensor, p: float, rng: torch.Tensor, residual=None, y=None, shuffle_seed: int = 0):
+    """y = residual + dropout(x) for x [..., D] (float32 or bf16): each element
+    dropped with probability p, the others times 1 / (1 - p).  rng, int64 [2] on the
+    GPU, holds the key and the first counter of the numbers (Philox 4x32-10); the
+    call uses ceil(x.numel() / 4) counters, after which the next call starts
+    (rng[1] += ...).  y may be x or the residual."""
+    return _dropout("moe_dropout_fwd", load_library().moe_dropout_fwd, x, p, rng, residual, y, shuffle_seed)
+
+
+def moe_dropout_bwd(dy: torch.Tensor, p: float, rng: torch.Tensor, dx=None, shuffle_seed: int = 0):
+    """Gradient of moe_dropout_fwd with respect to x, from its p and rng (the
+    residual's is dy)."""
+    return _dropout("moe_dropout_bwd", load_library().moe_dropout_bwd, dy, p, rng, None, dx, shuffle_seed)

@@ -79,7 +79,8 @@ typedef enum moe_dtype {
   MOE_I32 = 2,
   MOE_U8 = 3,
   MOE_I64 = 4,
-  MOE_F64 = 5
+  MOE_F64 = 5,
+  MOE_I8 = 6
 } moe_dtype;
 
 typedef enum moe_mode { MOE_DETERMINISTIC = 0, MOE_ATOMIC = 1 } moe_mode;
@@ -824,6 +825,120 @@ moe_status moe_glu_fwd(const moe_dense* p, const void* x, const void* wg, const 
 moe_status moe_glu_bwd(const moe_dense* p, const void* da, const void* x, const void* wg, const void* wu,
                        const void* g, const void* u, const void* dx_add, void* dx, void* dwg, void* dwu, void* ws,
                        size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Pieces of an expert layer, for a caller with a router or experts of its own:
+ * rows sorted by expert, copied for their experts and summed back with
+ * weights, forward and backward.  moe_fwd does the same inside, from its own
+ * router's choice.  The pages' general rule holds: one mode, no
+ * floating-point atomics, every sum in an order fixed by indices and sizes.
+ *
+ * Flat slot index i = t*k + j of token t's j-th choice.  slot_row [T,k] gives
+ * a slot's row among the rows sorted by expert, -1 for a slot without one; it
+ * is moe_sort's or a moe_routing's.  A slot whose row is not in [0, nrows) has
+ * none in the calls below: nothing is read or written for it.
+ * Conventions beyond those at the top of this file: base addresses are
+ * multiples of the element size; token matrices have a row distance (ld, in
+ * elements, at least cols) where a call says so; row matrices are contiguous
+ * [nrows, cols], and rows that no slot names stay as they are.  tokens * top_k
+ * is below 2^31, cols at most 2^24, every matrix at most 2^40 elements.
+ * Outputs must not overlap inputs, but where a call says so. */
+
+/* Workspace bytes of moe_sort (0 for few slots).  Errors: MOE_ERR_SHAPE, MOE_ERR_NULL. */
+moe_status moe_sort_workspace_size(int64_t tokens, int32_t top_k, int32_t num_local, size_t* bytes);
+
+/* Stable sort of the slots by expert, for the experts expert_begin ..
+ * expert_begin + num_local - 1 (1..1024 of them).
+ *   topk_idx  DEVICE [T,k] MOE_I32 or MOE_I64: expert numbers, in any order and
+ *             repeated at will; any other number (-1, say) is a slot without a row
+ *   slot_row  DEVICE int32 [T,k] output: row of each slot, or -1
+ *   offsets   DEVICE int32 [num_local + 1] output: each expert's first row;
+ *             offsets[num_local] = R.  Rows of an expert ascend in i
+ *   row_src   DEVICE int32 [T*k] output, or NULL: row -> flat slot; written
+ *             for rows < R
+ *   ws        moe_sort_workspace_size bytes, 256-byte aligned
+ * Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_WORKSPACE before
+ * anything is enqueued; MOE_ERR_HIP for a launch failure. */
+moe_status moe_sort(const void* topk_idx, moe_dtype idx_dtype, int64_t tokens, int32_t top_k, int32_t expert_begin,
+                    int32_t num_local, int32_t* slot_row, int32_t* offsets, int32_t* row_src, void* ws,
+                    size_t ws_bytes, uint64_t debug_shuffle_seed, void* stream);
+
+/* rows[slot_row[t,j]] = x[t].
+ *   x         DEVICE [T,cols], row distance ldx: MOE_F32, MOE_BF16, MOE_I8 or
+ *             MOE_U8 (encoded tokens; their scales are a MOE_F32 matrix of one column)
+ *   rows      DEVICE [nrows,cols] output
+ * Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_NULL before anything is
+ * enqueued; MOE_ERR_HIP for a launch failure. */
+moe_status moe_permute_fwd(const void* x, moe_dtype dtype, int64_t tokens, int32_t top_k, int32_t cols, int64_t ldx,
+                           const int32_t* slot_row, int64_t nrows, void* rows, uint64_t debug_shuffle_seed,
+                           void* stream);
+
+/* Its gradient: dx[t] = sum over j of drows[slot_row[t,j]] (+ dx_add[t]),
+ * slots ascending, float32 from 0, rounded once; a token without rows gets
+ * dx_add or zeros.
+ *   drows     DEVICE [nrows,cols], MOE_F32 or MOE_BF16
+ *   dx_add    DEVICE [T,cols], row distance ldadd, or NULL: another branch's gradient
+ *   dx        DEVICE [T,cols] contiguous, output; may be dx_add (ldadd = cols)
+ * Errors: as moe_permute_fwd. */
+moe_status moe_permute_bwd(const void* drows, moe_dtype dtype, int64_t tokens, int32_t top_k, int32_t cols,
+                           const int32_t* slot_row, int64_t nrows, const void* dx_add, int64_t ldadd, void* dx,
+                           uint64_t debug_shuffle_seed, void* stream);
+
+/* y[t] = sum over j of prob[t,j] rows[slot_row[t,j]] (+ residual[t]), as
+ * moe_permute_bwd adds.
+ *   rows      DEVICE [nrows,cols], MOE_F32 or MOE_BF16
+ *   prob      DEVICE float [T,k], or NULL for 1
+ *   residual  DEVICE [T,cols], row distance ldr, or NULL
+ *   y         DEVICE [T,cols] contiguous, output; may be the residual (ldr = cols)
+ * Errors: as moe_permute_fwd. */
+moe_status moe_unpermute_fwd(const void* rows, moe_dtype dtype, int64_t tokens, int32_t top_k, int32_t cols,
+                             const int32_t* slot_row, int64_t nrows, const float* prob, const void* residual,
+                             int64_t ldr, void* y, uint64_t debug_shuffle_seed, void* stream);
+
+/* Its gradients: drows[slot_row[t,j]] = prob[t,j] dy[t], rounded once, and
+ * dprob[t,j] = <dy[t], rows[slot_row[t,j]]> in float32 (0 for a slot without a
+ * row), in an order fixed by cols.  The residual's gradient is dy itself.
+ *   dy        DEVICE [T,cols], row distance lddy
+ *   rows      DEVICE [nrows,cols], as given to the forward (unread without dprob)
+ *   prob      DEVICE float [T,k]
+ *   drows     DEVICE [nrows,cols] output; may be rows itself
+ *   dprob     DEVICE float [T,k] output, or NULL
+ * No two slots of slot_row may name one row.  Errors: as moe_permute_fwd. */
+moe_status moe_unpermute_bwd(const void* dy, int64_t lddy, const void* rows, moe_dtype dtype, int64_t tokens,
+                             int32_t top_k, int32_t cols, const int32_t* slot_row, int64_t nrows, const float* prob,
+                             void* drows, float* dprob, uint64_t debug_shuffle_seed, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Dropout on the way into the residual stream, with numbers from a counter:
+ * no mask is stored, and the backward, a rerun or a resumed run finds the same
+ * one (the pages' guarantees for runs from the same state, and for a run
+ * resumed from a checkpoint, need such a mask).
+ *
+ * Element i = row * cols + column takes word i mod 4 of Philox 4x32 with 10
+ * rounds (Salmon, Moraes, Dror, Shaw, 2011) for the 64-bit counter rng[1] + i / 4
+ * (its upper 64 bits 0) under the key rng[0].  It is dropped where the word
+ * is below round(p 2^32).  A call uses ceil(rows * cols / 4) counters: the next
+ * one starts there.
+ *   y = residual + (dropped ? 0 : x * scale), scale = 1 / (1 - p) in float32,
+ *   one rounding
+ *   x         DEVICE [rows,cols], row distance ldx, MOE_F32 or MOE_BF16
+ *   residual  DEVICE [rows,cols], row distance ldr, or NULL for 0
+ *   p         0..1 (1 drops all)
+ *   rng       DEVICE uint64[2]: key and first counter.  They are read when the
+ *             kernel runs, so a captured graph takes new ones at each replay
+ *   y         DEVICE [rows,cols] contiguous, output; may be x or the residual
+ *             (with a row distance of cols)
+ * rows * ld is at most 2^40.  Base addresses are multiples of the element size.
+ * Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_NULL before anything is
+ * enqueued; MOE_ERR_HIP for a launch failure. */
+moe_status moe_dropout_fwd(const void* x, const void* residual, moe_dtype dtype, int64_t rows, int64_t cols,
+                           int64_t ldx, int64_t ldr, double p, const uint64_t* rng, void* y,
+                           uint64_t debug_shuffle_seed, void* stream);
+
+/* dx = dropped ? 0 : dy * scale, with the forward's p and rng.  The
+ * residual's gradient is dy itself.  Errors: as moe_dropout_fwd. */
+moe_status moe_dropout_bwd(const void* dy, moe_dtype dtype, int64_t rows, int64_t cols, int64_t lddy, double p,
+                           const uint64_t* rng, void* dx, uint64_t debug_shuffle_seed, void* stream);
 
 #ifdef __cplusplus
 }

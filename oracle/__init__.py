@@ -22,3 +22,6 @@ from .nvfp4 import e2m1_decode, e2m1_encode, nvfp4_quantize, nvfp4_dequantize  #
 from .dense import (  # noqa: F401,E402
     act, layernorm_forward, layernorm_backward, linear_forward, linear_backward, glu_forward, glu_backward,
 )
+from .rows import (  # noqa: F401,E402
+    sort_slots, permute_rows, sum_rows, sum_rows_backward, philox4x32, dropout_mask,
+)
