@@ -11,6 +11,7 @@ namespace moedet {
 constexpr int kSortMaxLocal = 1024;   // experts of a sort
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
 constexpr int kSortMaxChunks = 256;   // workgroups of a sort: one a CU
+constexpr int kSortMaxHist = 16384;   // counts that each of them adds up
 // Slots that one workgroup sorts in one launch; more take a launch that counts
 // the experts of each chunk and one that places the slots.
 constexpr int64_t kSortOne = 8192;
@@ -28,15 +29,17 @@ struct SortParams {
   int32_t* row_src;      // or null
   uint64_t seed;
 };
-// Chunks of n slots (a function of n alone).
-inline void sort_chunks(int64_t n, int64_t* chunk, int* chunks) {
+// Chunks of n slots (a function of n and local alone).
+inline void sort_chunks(int64_t n, int local, int64_t* chunk, int* chunks) {
   if (n <= kSortOne) {
     *chunk = kSortOne;
     *chunks = 1;
     return;
   }
+  int most = kSortMaxHist / local;
+  if (most > kSortMaxChunks) most = kSortMaxChunks;
   const int64_t step = kSortThreads;
-  *chunk = ((n + kSortMaxChunks - 1) / kSortMaxChunks + step - 1) / step * step;
+  *chunk = ((n + most - 1) / most + step - 1) / step * step;
   *chunks = (int)((n + *chunk - 1) / *chunk);
 }
 hipError_t launch_sort(const SortParams& P, hipStream_t st);

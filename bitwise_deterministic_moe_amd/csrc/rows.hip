@@ -12,6 +12,8 @@
 // registers or the L1 for its k slots, and no row -> slot table is read.  All are
 // bound by HBM.  Each output element is written by one thread: no atomics.
 // A slot whose row is outside [0, nrows) has none: it is not read or written.
+#include <type_traits>
+
 #include "rows.h"
 
 namespace moedet {
@@ -20,11 +22,35 @@ namespace {
 
 typedef uint32_t u32x4_b_t __attribute__((ext_vector_type(4), aligned(1)));
 
+// Rows that the last-level cache cannot hold are stored past it: otherwise the next
+// kernel's reads wait for their write-back.  4096 tokens of 22 slots, 2048 bf16 (369 MB of
+// rows): copied and summed back 177 us through the caches, 150 past them, gradients
+// 161 and 167 us alone but 246 and 218 behind the forward.  180 MB copied and summed back:
+// 37 and 42 us.
+constexpr int64_t kLastLevelBytes = (int64_t)256 << 20;
+bool past_cache(const RowsParams& P, int es) {
+  const int64_t slots = P.tokens * P.k;
+  return (P.nrows < slots ? P.nrows : slots) * P.cols * es > kLastLevelBytes;
+}
+
+// Such rows are loaded past it as well (the 369 MB summed back: 72.6 us through the
+// caches, 67.8 past them; 6 MB of rows that the backward reads again: 4.3 and 5.2 us).
+DEV u32x4_t load_past(const uint16_t* p) { return __builtin_nontemporal_load((const u32x4_any_t*)p); }
+DEV f32x4_t load_past(const float* p) { return __builtin_nontemporal_load((const f32x4_any_t*)p); }
+
+DEV void store_past(uint16_t* p, const float* v) {
+  __builtin_nontemporal_store(u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])},
+                              (u32x4_any_t*)p);
+}
+DEV void store_past(float* p, const float* v) {
+  __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, (f32x4_any_t*)p);
+}
+
 // A workgroup of 256 threads takes 256 / L tokens, L threads each (a power of two
 // up to 256, the row's 16-byte vectors where they are fewer).
-inline int row_threads(int64_t vecs) {
+int row_threads(int64_t vecs, int most) {
   int L = 8;
-  while (L < 256 && L < vecs) L <<= 1;
+  while (L < most && L < vecs) L <<= 1;
   return L;
 }
 
@@ -51,8 +77,30 @@ DEV bool place(const RowsParams& P, int L, int S, Place& p) {
 
 }  // namespace
 
-// WHOLE: L >= 64, so a wave has one token and its slots' rows are scalars.
-template <bool WHOLE>
+// The row of slot j of a token, -1 if it has none.
+DEV int32_t slot_at(const RowsParams& P, const int32_t* sr, int j, int end) {
+  const int32_t r = j < end ? sr[j] : -1;
+  return r < P.nrows ? r : -1;
+}
+
+// The slots that have a row, ascending, up to 64 at a time: the lanes read them
+// together and a ballot finds the ones with a row, so a rank with few of the
+// experts passes over the other slots at once.  f(lane of the slot, row) for each
+// in turn, where the wave has one token (WHOLE).
+template <class F>
+DEV void each_slot(uint64_t mask, int32_t r, F f) {
+  while (mask) {
+    const int b = (int)__builtin_ctzll(mask);
+    mask &= mask - 1;
+    f(b, __builtin_amdgcn_readlane(r, b));
+  }
+}
+
+// WHOLE: L >= 64, so a wave has one token.
+// 4096 tokens of 22 slots, 2048 bf16 (386 MB): 72 us, 5.4 TB/s.  16384 tokens of
+// which 2816 slots have a row: 42 us where every token's row was read and every
+// slot looked at in turn by four waves a token, 21 with the ballot, 10 with one wave.
+template <bool WHOLE, bool PAST>
 __global__ __launch_bounds__(256) void permute_kernel(RowsParams P, int es, int L, int S) {
   Place p;
   if (!place(P, L, S, p)) return;
@@ -61,81 +109,186 @@ __global__ __launch_bounds__(256) void permute_kernel(RowsParams P, int es, int 
   const int vecs = (int)((len + 15) / 16);
   const char* src = (const char*)P.x + t * P.ldx * es;
   const int32_t* sr = P.slot_row + t * P.k;
-  for (int v = p.v; v < vecs; v += L) {
-    const int64_t at = (int64_t)v * 16;
-    const int n = (int)(len - at < 16 ? len - at : 16);
-    u32x4_t x = {0u, 0u, 0u, 0u};
-    if (n == 16) x = *(const u32x4_b_t*)(src + at);
-    for (int j = p.j0; j < p.j1; ++j) {
-      const int32_t r = sr[j];
-      if (r < 0 || r >= P.nrows) continue;
-      char* dst = (char*)P.out + (int64_t)r * len + at;
-      if (n == 16) {
+  const int lane = threadIdx.x & 63;
+  auto put = [&](int32_t r, int64_t at, int n, const u32x4_t& x) __attribute__((always_inline)) {
+    char* dst = (char*)P.out + (int64_t)r * len + at;
+    if (n == 16) {
+      if constexpr (PAST)
+        __builtin_nontemporal_store(x, (u32x4_b_t*)dst);
+      else
         *(u32x4_b_t*)dst = x;
-      } else {
-        for (int b = 0; b < n; ++b) dst[b] = src[at + b];
+    } else {
+      for (int b = 0; b < n; ++b) dst[b] = src[at + b];
+    }
+  };
+  if constexpr (WHOLE) {
+    for (int j0 = p.j0; j0 < p.j1; j0 += 64) {
+      const int32_t r = slot_at(P, sr, j0 + lane, p.j1);
+      const uint64_t mask = __ballot(r >= 0);
+      if (!mask) continue;
+      for (int v = p.v; v < vecs; v += L) {
+        const int64_t at = (int64_t)v * 16;
+        const int n = (int)(len - at < 16 ? len - at : 16);
+        u32x4_t x = {0u, 0u, 0u, 0u};
+        if (n == 16) x = *(const u32x4_b_t*)(src + at);
+        each_slot(mask, r, [&](int, int32_t row) __attribute__((always_inline)) { put(row, at, n, x); });
+      }
+    }
+  } else {
+    for (int v = p.v; v < vecs; v += L) {
+      const int64_t at = (int64_t)v * 16;
+      const int n = (int)(len - at < 16 ? len - at : 16);
+      u32x4_t x = {0u, 0u, 0u, 0u};
+      if (n == 16) x = *(const u32x4_b_t*)(src + at);
+      for (int j = p.j0; j < p.j1; ++j) {
+        const int32_t r = slot_at(P, sr, j, p.j1);
+        if (r >= 0) put(r, at, n, x);
       }
     }
   }
 }
 
-template <typename T, bool WHOLE>
+// acc += w * the row's vector (or the vector itself without weights)
+template <typename T>
+DEV void add_row(float (&acc)[Vec<T>::N], const typename Vec<T>::raw& x, bool weighted, float w) {
+  float f[Vec<T>::N];
+  Vec<T>::get(x, f);
+#pragma unroll
+  for (int q = 0; q < Vec<T>::N; ++q) acc[q] = weighted ? __builtin_fmaf(w, f[q], acc[q]) : acc[q] + f[q];
+}
+
+DEV float get1(const uint16_t* p) { return bf16_to_f32(*p); }
+DEV float get1(const float* p) { return *p; }
+DEV void put1(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16(v); }
+DEV void put1(float* p, float v) { *p = v; }
+
+// Narrow rows, several tokens a wave.
+template <typename T>
+__global__ __launch_bounds__(256) void unpermute_narrow_kernel(RowsParams P, int L) {
+  constexpr int V = Vec<T>::N;
+  Place p;
+  if (!place(P, L, 1, p)) return;
+  const int64_t t = p.t;
+  const int32_t* sr = P.slot_row + t * P.k;
+  const float* pr = P.prob ? P.prob + t * P.k : nullptr;
+  const int col = p.v * V, n = P.cols - col;   // L threads hold the whole row
+  if (n <= 0) return;
+  float acc[V];
+#pragma unroll
+  for (int q = 0; q < V; ++q) acc[q] = 0.f;
+  // slots in groups whose numbers, then rows, are loaded together
+  constexpr int G = 4;
+  for (int j0 = 0; j0 < P.k; j0 += G) {
+    int32_t r[G];
+    typename Vec<T>::raw x[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) r[i] = slot_at(P, sr, j0 + i, P.k);
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      if (r[i] >= 0) x[i] = Vec<T>::load((const T*)P.rows + (int64_t)r[i] * P.cols + col, n);
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      if (r[i] >= 0) add_row<T>(acc, x[i], pr != nullptr, pr ? pr[j0 + i] : 1.f);
+  }
+  if (P.add) {
+    float a[V];
+    Vec<T>::get(Vec<T>::load((const T*)P.add + t * P.ldadd + col, n), a);
+#pragma unroll
+    for (int q = 0; q < V; ++q) acc[q] = acc[q] + a[q];
+  }
+  Vec<T>::store((T*)P.out + t * P.cols + col, acc, n);
+}
+
+// A wave has one token, and every loop and branch on the way to a load is the
+// same for its lanes: lanes past the row's last whole vector repeat it and
+// store nothing, and the columns behind it are summed one a lane by the token's
+// first wave.
+// 4096 tokens of 22 slots, 2048 bf16 (386 MB): 68 us, 5.7 TB/s; groups of 4 or 16
+// loads are no faster.
+template <typename T, bool PAST>
 __global__ __launch_bounds__(256) void unpermute_kernel(RowsParams P, int L) {
   constexpr int V = Vec<T>::N;
   Place p;
   if (!place(P, L, 1, p)) return;
-  const int64_t t = WHOLE ? (int64_t)__builtin_amdgcn_readfirstlane((int)p.t) : p.t;
-  const int vecs = (P.cols + V - 1) / V;
+  const int64_t t = __builtin_amdgcn_readfirstlane((int)p.t);
+  const int lane = threadIdx.x & 63, whole = P.cols / V;
   const int32_t* sr = P.slot_row + t * P.k;
-  const float* pr = P.prob ? P.prob + t * P.k : nullptr;
+  const bool weighted = P.prob != nullptr;
+  const float* pr = weighted ? P.prob + t * P.k : nullptr;
   const T* rows = (const T*)P.rows;
-  for (int v = p.v; v < vecs; v += L) {
-    const int col = v * V, n = P.cols - col;
+  // add(weight, element offset of the row) for the slots with a row, ascending, in
+  // groups of G whose loads go out together
+  constexpr int G = 8;
+  auto sum = [&](auto load, auto add) __attribute__((always_inline)) {
+    for (int j0 = 0; j0 < P.k; j0 += 64) {
+      const int32_t r = slot_at(P, sr, j0 + lane, P.k);
+      const float wl = weighted && j0 + lane < P.k ? pr[j0 + lane] : 0.f;
+      uint64_t mask = __ballot(r >= 0);
+      auto group = [&](int left, auto N) __attribute__((always_inline)) {
+        decltype(load((int64_t)0)) x[N.value];
+        float w[N.value];
+#pragma unroll
+        for (int i = 0; i < N.value; ++i) {
+          const int b = (int)__builtin_ctzll(mask);
+          if (i + 1 < left || left == N.value) mask &= mask - 1;   // past `left`: the last one again, not added
+          w[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wl), b));
+          x[i] = load((int64_t)__builtin_amdgcn_readlane(r, b) * P.cols);
+        }
+#pragma unroll
+        for (int i = 0; i < N.value; ++i)
+          if (i < left) add(x[i], w[i]);
+      };
+      int n = __popcll(mask);
+      for (; n >= G; n -= G) group(G, std::integral_constant<int, G>{});
+      if (n > G / 2)
+        group(n, std::integral_constant<int, G - 1>{});
+      else if (n > 0)
+        group(n, std::integral_constant<int, G / 2>{});
+    }
+  };
+  for (int v0 = __builtin_amdgcn_readfirstlane(p.v); v0 < whole; v0 += L) {
+    const int v = v0 + lane, col = min(v, whole - 1) * V;
     float acc[V];
 #pragma unroll
     for (int q = 0; q < V; ++q) acc[q] = 0.f;
-    // slots in groups whose loads are in flight together; added in slot order
-    constexpr int G = 8;
-    for (int j0 = 0; j0 < P.k; j0 += G) {
-      int32_t r[G];
-      typename Vec<T>::raw x[G];
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        r[i] = j0 + i < P.k ? sr[j0 + i] : -1;
-        if (r[i] >= P.nrows) r[i] = -1;
-      }
-#pragma unroll
-      for (int i = 0; i < G; ++i)
-        if (r[i] >= 0) x[i] = Vec<T>::load(rows + (int64_t)r[i] * P.cols + col, n);
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        if (r[i] < 0) continue;
-        float f[V];
-        Vec<T>::get(x[i], f);
-        const float w = pr ? pr[j0 + i] : 1.f;
-#pragma unroll
-        for (int q = 0; q < V; ++q) acc[q] = pr ? __builtin_fmaf(w, f[q], acc[q]) : acc[q] + f[q];
-      }
-    }
+    sum([&](int64_t at) __attribute__((always_inline)) {
+          if constexpr (PAST)
+            return load_past(rows + at + col);
+          else
+            return Vec<T>::load(rows + at + col, V);
+        },
+        [&](const typename Vec<T>::raw& x, float w) __attribute__((always_inline)) { add_row<T>(acc, x, weighted, w); });
     if (P.add) {
       float a[V];
-      Vec<T>::get(Vec<T>::load((const T*)P.add + t * P.ldadd + col, n), a);
+      Vec<T>::get(Vec<T>::load((const T*)P.add + t * P.ldadd + col, V), a);
 #pragma unroll
       for (int q = 0; q < V; ++q) acc[q] = acc[q] + a[q];
     }
-    Vec<T>::store((T*)P.out + t * P.cols + col, acc, n);
+    if (v < whole) Vec<T>::store((T*)P.out + t * P.cols + col, acc, V);
+  }
+  if (__builtin_amdgcn_readfirstlane(p.v) == 0 && whole * V < P.cols) {
+    const int c = whole * V + lane, col = min(c, P.cols - 1);
+    float acc = 0.f;
+    sum([&](int64_t at) __attribute__((always_inline)) { return get1(rows + at + col); },
+        [&](float x, float w) __attribute__((always_inline)) { acc = weighted ? __builtin_fmaf(w, x, acc) : acc + x; });
+    if (P.add) acc = acc + get1((const T*)P.add + t * P.ldadd + col);
+    if (c < P.cols) put1((T*)P.out + t * P.cols + c, acc);
   }
 }
 
-// A wave a slot; the four waves of a workgroup have neighbouring slots, mostly
-// of one token.
-template <typename T>
+// A wave a slot.  Rows that the caches cannot hold are taken in the order of the
+// slots, not in runs an XCD: rows of one expert that lie side by side are then
+// read and written at about the same time (369 MB of rows behind the forward:
+// 243 us in runs, 218 so; 6 MB of them 6.6 and 8.4 us).
+template <typename T, bool PAST>
 __global__ __launch_bounds__(256) void unpermute_bwd_kernel(RowsParams P) {
   constexpr int V = Vec<T>::N;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n = P.tokens * P.k;
-  const int64_t u = map_unit(blockIdx.x, (n + 3) / 4, P.seed);
-  if (u < 0) return;
+  const int64_t units = (n + 3) / 4;
+  int64_t u = blockIdx.x;
+  if (!PAST || P.seed) u = map_unit(u, units, P.seed);
+  if (u < 0 || u >= units) return;
   const int64_t i = u * 4 + w;
   if (i >= n) return;
   const int32_t r = P.slot_row[i];
@@ -143,7 +296,7 @@ __global__ __launch_bounds__(256) void unpermute_bwd_kernel(RowsParams P) {
     if (P.dprob && lane == 0) P.dprob[i] = 0.f;
     return;
   }
-  const T* dy = (const T*)P.x + i / P.k * P.ldx;
+  const T* dy = (const T*)P.x + (int64_t)((uint32_t)i / (uint32_t)P.k) * P.ldx;
   const T* row = (const T*)P.rows + (int64_t)r * P.cols;
   T* out = (T*)P.out + (int64_t)r * P.cols;
   const float p = P.prob[i];
@@ -162,7 +315,10 @@ __global__ __launch_bounds__(256) void unpermute_bwd_kernel(RowsParams P) {
     }
 #pragma unroll
     for (int q = 0; q < V; ++q) g[q] = p * g[q];
-    Vec<T>::store(out + col, g, m);
+    if (PAST && m >= V)
+      store_past(out + col, g);
+    else
+      Vec<T>::store(out + col, g, m);
   }
   if (!P.dprob) return;
 #pragma unroll
@@ -171,44 +327,48 @@ __global__ __launch_bounds__(256) void unpermute_bwd_kernel(RowsParams P) {
 }
 
 hipError_t launch_permute(const RowsParams& P, int es, hipStream_t st) {
-  const int L = row_threads(((int64_t)P.cols * es + 15) / 16);
+  const int L = row_threads(((int64_t)P.cols * es + 15) / 16, 64);
   const int64_t groups = (P.tokens + 256 / L - 1) / (256 / L);
   // too few tokens for the device: their slots are split too
   int64_t S = groups >= 512 ? 1 : (512 + groups - 1) / groups;
   if (S > P.k) S = P.k;
   const int64_t grid = grid_for_units(groups * S);
-  if (L >= 64)
-    permute_kernel<true><<<grid, 256, 0, st>>>(P, es, L, (int)S);
+  if (L < 64)
+    permute_kernel<false, false><<<grid, 256, 0, st>>>(P, es, L, (int)S);
+  else if (past_cache(P, es))
+    permute_kernel<true, true><<<grid, 256, 0, st>>>(P, es, L, (int)S);
   else
-    permute_kernel<false><<<grid, 256, 0, st>>>(P, es, L, (int)S);
+    permute_kernel<true, false><<<grid, 256, 0, st>>>(P, es, L, (int)S);
   return hipGetLastError();
 }
 
-hipError_t launch_unpermute(const RowsParams& P, bool bf16, hipStream_t st) {
-  const int V = bf16 ? 8 : 4;
-  const int L = row_threads((P.cols + V - 1) / V);
+template <typename T>
+static hipError_t launch_sum(const RowsParams& P, hipStream_t st) {
+  const int L = row_threads((P.cols + Vec<T>::N - 1) / Vec<T>::N, 256);
   const int64_t grid = grid_for_units((P.tokens + 256 / L - 1) / (256 / L));
-  if (bf16) {
-    if (L >= 64)
-      unpermute_kernel<uint16_t, true><<<grid, 256, 0, st>>>(P, L);
-    else
-      unpermute_kernel<uint16_t, false><<<grid, 256, 0, st>>>(P, L);
-  } else {
-    if (L >= 64)
-      unpermute_kernel<float, true><<<grid, 256, 0, st>>>(P, L);
-    else
-      unpermute_kernel<float, false><<<grid, 256, 0, st>>>(P, L);
-  }
+  if (L < 64)
+    unpermute_narrow_kernel<T><<<grid, 256, 0, st>>>(P, L);
+  else if (past_cache(P, sizeof(T)))
+    unpermute_kernel<T, true><<<grid, 256, 0, st>>>(P, L);
+  else
+    unpermute_kernel<T, false><<<grid, 256, 0, st>>>(P, L);
   return hipGetLastError();
 }
+hipError_t launch_unpermute(const RowsParams& P, bool bf16, hipStream_t st) {
+  return bf16 ? launch_sum<uint16_t>(P, st) : launch_sum<float>(P, st);
+}
 
-hipError_t launch_unpermute_bwd(const RowsParams& P, bool bf16, hipStream_t st) {
+template <typename T>
+static hipError_t launch_bwd(const RowsParams& P, hipStream_t st) {
   const int64_t grid = grid_for_units((P.tokens * P.k + 3) / 4);
-  if (bf16)
-    unpermute_bwd_kernel<uint16_t><<<grid, 256, 0, st>>>(P);
+  if (past_cache(P, sizeof(T)))
+    unpermute_bwd_kernel<T, true><<<grid, 256, 0, st>>>(P);
   else
-    unpermute_bwd_kernel<float><<<grid, 256, 0, st>>>(P);
+    unpermute_bwd_kernel<T, false><<<grid, 256, 0, st>>>(P);
   return hipGetLastError();
+}
+hipError_t launch_unpermute_bwd(const RowsParams& P, bool bf16, hipStream_t st) {
+  return bf16 ? launch_bwd<uint16_t>(P, st) : launch_bwd<float>(P, st);
 }
 
 }  // namespace moedet

@@ -41,7 +41,7 @@ moe_status check_sort(int64_t tokens, int32_t top_k, int32_t num_local) {
 size_t sort_ws(int64_t n, int local) {
   int64_t chunk;
   int chunks;
-  sort_chunks(n, &chunk, &chunks);
+  sort_chunks(n, local, &chunk, &chunks);
   if (chunks == 1) return 0;
   return ((size_t)chunks * local * 4 + kWsAlign - 1) / kWsAlign * kWsAlign;
 }
@@ -144,7 +144,7 @@ MOE_API moe_status moe_sort(const void* topk_idx, moe_dtype idx_dtype, int64_t t
   P.n = n;
   P.begin = expert_begin;
   P.local = num_local;
-  sort_chunks(n, &P.chunk, &P.chunks);
+  sort_chunks(n, num_local, &P.chunk, &P.chunks);
   P.hist = (int32_t*)ws;
   P.slot_row = slot_row;
   P.offsets = offsets;

@@ -77,11 +77,18 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams P) 
     const int e = tid & (span - 1), part = tid / span, parts = kSortThreads / span;
     if (e < El) {
       int tot = 0, before = 0;
-#pragma unroll 8
-      for (int q = part; q < P.chunks; q += parts) {
-        const int h = P.hist[(int64_t)q * El + e];
-        tot += h;
-        before += q < c ? h : 0;
+      // loads in batches without branches: past the end they repeat the last one
+      constexpr int B = 8;
+      for (int q0 = part; q0 < P.chunks; q0 += B * parts) {
+        int h[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) h[i] = P.hist[min(q0 + i * parts, P.chunks - 1) * El + e];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+          const int q = q0 + i * parts;
+          tot += q < P.chunks ? h[i] : 0;
+          before += q < c ? h[i] : 0;
+        }
       }
       atomicAdd(&s_tot[e], tot);
       atomicAdd(&s_before[e], before);
