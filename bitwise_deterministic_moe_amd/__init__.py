@@ -26,6 +26,7 @@ __all__ = [
     "moe_glu_bwd", "moe_layernorm_workspace_size", "moe_linear_workspace_size", "moe_glu_workspace_size", "ACTIVATIONS",
     "moe_linear_stage_names", "moe_glu_stage_names", "moe_sort", "moe_sort_workspace_size", "moe_permute_fwd",
     "moe_permute_bwd", "moe_unpermute_fwd", "moe_unpermute_bwd", "moe_dropout_fwd", "moe_dropout_bwd",
+    "moe_int8_quantize", "moe_int8_quantize_t", "moe_int8_workspace_size", "moe_int8_linear", "moe_int8_experts",
 ]
 
 DETERMINISTIC = 0
@@ -44,7 +45,8 @@ EXPORTED_SYMBOLS = ("moe_abi_version", "moe_status_string", "moe_rows_cap", "moe
                     "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd", "moe_glu_workspace_size",
                     "moe_glu_fwd", "moe_glu_bwd", "moe_linear_stage_names", "moe_glu_stage_names",
                     "moe_sort_workspace_size", "moe_sort", "moe_permute_fwd", "moe_permute_bwd", "moe_unpermute_fwd",
-                    "moe_unpermute_bwd", "moe_dropout_fwd", "moe_dropout_bwd")
+                    "moe_unpermute_bwd", "moe_dropout_fwd", "moe_dropout_bwd", "moe_int8_quantize", "moe_int8_quantize_t",
+                    "moe_int8_workspace_size", "moe_int8_linear", "moe_int8_experts")
 # activations of the dense operators (moe_act)
 ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4}
 # matrices of a dense call that may start at any element (moe_any)
@@ -88,6 +90,13 @@ class _CDense(ctypes.Structure):
                 ("act", ctypes.c_int32),
                 ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldz", ctypes.c_int64),
                 ("ldr", ctypes.c_int64), ("debug_shuffle_seed", ctypes.c_uint64)]
+
+
+class _CInt8(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32),
+                ("num_local", ctypes.c_int32), ("x_dtype", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldr", ctypes.c_int64),
+                ("debug_shuffle_seed", ctypes.c_uint64)]
 
 
 def library_path() -> str:
@@ -173,7 +182,14 @@ def load_library() -> ctypes.CDLL:
     lib.moe_unpermute_bwd.argtypes = [vp, i64, vp, ci, i64, i32, i32, vp, i64, vp, vp, vp, u64, vp]
     lib.moe_dropout_fwd.argtypes = [vp, vp, ci, i64, i64, i64, i64, ctypes.c_double, vp, vp, u64, vp]
     lib.moe_dropout_bwd.argtypes = [vp, ci, i64, i64, i64, ctypes.c_double, vp, vp, u64, vp]
-    for f in ("moe_sort_workspace_size", "moe_sort", "moe_permute_fwd", "moe_permute_bwd", "moe_unpermute_fwd",
+    Q = ctypes.POINTER(_CInt8)
+    lib.moe_int8_quantize.argtypes = [vp, ci, i64, i64, i64, vp, vp, u64, vp]
+    lib.moe_int8_quantize_t.argtypes = [vp, ci, i64, i64, i64, vp, vp, u64, vp]
+    lib.moe_int8_workspace_size.argtypes = [Q, ctypes.POINTER(sz)]
+    lib.moe_int8_linear.argtypes = [Q] + [vp] * 8 + [sz, vp]
+    lib.moe_int8_experts.argtypes = [Q] + [vp] * 8 + [sz, vp]
+    for f in ("moe_int8_quantize", "moe_int8_quantize_t", "moe_int8_workspace_size", "moe_int8_linear", "moe_int8_experts",
+              "moe_sort_workspace_size", "moe_sort", "moe_permute_fwd", "moe_permute_bwd", "moe_unpermute_fwd",
               "moe_unpermute_bwd", "moe_dropout_fwd", "moe_dropout_bwd"):
         getattr(lib, f).restype = ci
     for f in ("moe_route", "moe_mx_wgrad_rows", "moe_mx_quantize_wgrad", "moe_mx_wgrad", "moe_rows_cap",
@@ -1353,6 +1369,152 @@ def moe_unpermute_bwd(dy: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tens
          (_ptr(dy), lddy, _ptr(rows), code, tokens, k, cols, _ptr(slot_row), n, _ptr(prob), _ptr(drows), _ptr(dprob),
           shuffle_seed), dy, rows, slot_row, prob, drows, dprob)
     return drows, dprob
+
+
+# ------------------------------------------------- products in 8-bit integers
+def _up16(n: int) -> int:
+    return (n + 15) // 16 * 16
+
+
+def moe_int8_quantize(x: torch.Tensor, codes=None, scales=None, shuffle_seed: int = 0):
+    """8-bit codes and scales of the rows of x [..., K] (float32 or bf16): scale =
+    max |x| / 127, code = 127 x / max |x| to the nearest, ties to even.  Returns
+    (codes int8 [..., K up to a multiple of 16], scales float32 [...]), the codes
+    zero past K."""
+    lib, what = load_library(), "moe_int8_quantize"
+    code = _storage(x, what)
+    if x.dim() == 0 or x.shape[-1] < 1:
+        raise MoeError(f"{what}: a tensor [..., K] with columns is needed, got {tuple(x.shape)}")
+    cols = x.shape[-1]
+    rows, ldx = _mat(x, cols, x.dtype, what + " x")
+    wide = _up16(cols)
+    if codes is None:
+        codes = x.new_empty(x.shape[:-1] + (wide,), dtype=torch.int8)
+    else:
+        _need(codes, rows * wide, torch.int8, what + " codes")
+    if scales is None:
+        scales = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    else:
+        _need(scales, rows, torch.float32, what + " scales")
+    _run(what, lib.moe_int8_quantize, (_ptr(x), code, rows, cols, ldx, _ptr(codes), _ptr(scales), shuffle_seed), x, codes,
+         scales)
+    return codes, scales
+
+
+def moe_int8_quantize_t(w: torch.Tensor, codes=None, scales=None, shuffle_seed: int = 0):
+    """8-bit codes and scales of the columns (output channels) of the weights w
+    [..., K, F] (float32 or bf16), as moe_int8_linear and moe_int8_experts read
+    them.  Returns (codes int8 [..., F, K up to a multiple of 16], scales float32
+    [..., F])."""
+    lib, what = load_library(), "moe_int8_quantize_t"
+    code = _storage(w, what)
+    if w.dim() < 2 or w.shape[-1] < 1 or w.shape[-2] < 1 or not w.is_contiguous():
+        raise MoeError(f"{what}: w must be contiguous matrices [..., K, F], got {tuple(w.shape)}")
+    k, f = w.shape[-2:]
+    batch, wide = w.numel() // (k * f), _up16(k)
+    if codes is None:
+        codes = w.new_empty(w.shape[:-2] + (f, wide), dtype=torch.int8)
+    else:
+        _need(codes, batch * f * wide, torch.int8, what + " codes")
+    if scales is None:
+        scales = w.new_empty(w.shape[:-2] + (f,), dtype=torch.float32)
+    else:
+        _need(scales, batch * f, torch.float32, what + " scales")
+    _run(what, lib.moe_int8_quantize_t, (_ptr(w), code, batch, k, f, _ptr(codes), _ptr(scales), shuffle_seed), w, codes, scales)
+    return codes, scales
+
+
+@functools.lru_cache(maxsize=4096)
+def _int8_plan(rows: int, d_in: int, d_out: int, num_local: int, x_dtype: int, dtype: int, act: int, ldx: int, ldy: int,
+               ldr: int, seed: int):
+    """The C description of a product (read-only) and its workspace bytes."""
+    what = "moe_int8_workspace_size"
+    if max(rows, d_in, d_out, ldx, ldy, ldr) >= 1 << 31:
+        raise MoeError(f"{what}: sizes beyond 2^31")
+    c = _CInt8(rows, d_in, d_out, num_local, x_dtype, dtype, act, ldx, ldy, ldr, seed & 0xFFFFFFFFFFFFFFFF)
+    n = ctypes.c_size_t()
+    _check(load_library().moe_int8_workspace_size(ctypes.byref(c), ctypes.byref(n)), what)
+    return c, n.value
+
+
+def moe_int8_workspace_size(rows: int, d_in: int, d_out: int, num_local: int = 0, dtype: str = "bf16") -> int:
+    """Workspace bytes of moe_int8_linear (num_local 0) or moe_int8_experts with
+    x of dtype; none is needed where x holds codes."""
+    if dtype not in ("f32", "bf16"):
+        raise MoeError(f"moe_int8_workspace_size: dtypes are f32 and bf16, got {dtype!r}")
+    code = DTYPE_CODE[dtype]
+    return _int8_plan(rows, d_in, d_out, num_local, code, code, 0, d_in, d_out, 0, 0)[1]
+
+
+def _int8(what, fn, x, w_codes, w_scales, x_scales, bias, residual, offsets, act, out_dtype, y, ws, seed):
+    a = _act_code(act, what)
+    codes = x.dtype is torch.int8
+    xc = 6 if codes else _storage(x, what)
+    if x.dim() == 0 or x.shape[-1] < 1:
+        raise MoeError(f"{what}: x needs columns, got {tuple(x.shape)}")
+    if codes != (x_scales is not None):
+        raise MoeError(f"{what}: int8 codes x and x_scales are given together")
+    d = x.shape[-1]
+    rows, ldx = _mat(x, d, x.dtype, what + " x")
+    if w_codes.dtype is not torch.int8 or w_codes.dim() != (2 if offsets is None else 3) or not w_codes.is_contiguous() \
+            or w_codes.shape[-1] != _up16(d) or w_codes.shape[-2] < 1:
+        raise MoeError(f"{what}: w_codes must be contiguous int8 {'' if offsets is None else 'experts, '}"
+                       f"[d_out, {_up16(d)}], got {w_codes.dtype} {tuple(w_codes.shape)}")
+    f = w_codes.shape[-2]
+    local = 0
+    if offsets is not None:
+        local = w_codes.shape[0]
+        if local < 1:
+            raise MoeError(f"{what}: w_codes without experts")
+        _need(offsets, local + 1, torch.int32, what + " offsets")
+        if x.dim() != 2:
+            raise MoeError(f"{what}: x must be a matrix of rows sorted by expert, got {tuple(x.shape)}")
+    _need(w_scales, (local or 1) * f, torch.float32, what + " w_scales")
+    if codes:
+        _need(x_scales, rows, torch.float32, what + " x_scales")
+        dt = out_dtype or (y.dtype if y is not None else torch.bfloat16)
+    else:
+        dt = out_dtype or (y.dtype if y is not None else x.dtype)
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise MoeError(f"{what}: the output is float32 or bfloat16, not {dt}")
+    if bias is not None:
+        _need(bias, (local or 1) * f, dt, what + " bias")
+    ldr = _mat(residual, f, dt, what + " residual", rows)[1] if residual is not None else 0
+    if y is None:
+        y, ldy = _new(x, f, dt), f
+    else:
+        ldy = _mat(y, f, dt, what + " y", rows)[1]
+    c, need = _int8_plan(rows, d, f, local, xc, _TORCH_TO_CODE[dt], a, ldx, ldy, ldr, seed)
+    ws, nb = _dense_ws(need, ws, x)
+    last = _ptr(residual) if offsets is None else _ptr(offsets)
+    _run(what, fn, (c, _ptr(x), _ptr(x_scales), _ptr(w_codes), _ptr(w_scales), _ptr(bias), last, _ptr(y), _ptr(ws), nb), x,
+         x_scales, w_codes, w_scales, bias, residual, offsets, y, ws)
+    return y
+
+
+def moe_int8_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, x_scales=None, bias=None, residual=None,
+                    act: str = "none", out_dtype=None, y=None, ws=None, shuffle_seed: int = 0):
+    """y = act(x w + bias) + residual in 8-bit integers, for weights encoded by
+    moe_int8_quantize_t (w_codes int8 [F, K16], w_scales float32 [F]) and x [..., K]
+    of float32 or bf16, which the call quantises itself, or int8 codes
+    [..., K16] with their x_scales [...] (moe_int8_quantize).  y [..., F], bias
+    [F] and residual [..., F] are of out_dtype, by default y's, else x's, bf16
+    for codes.  y may be the residual itself."""
+    return _int8("moe_int8_linear", load_library().moe_int8_linear, x, w_codes, w_scales, x_scales, bias, residual, None, act,
+                 out_dtype, y, ws, shuffle_seed)
+
+
+def moe_int8_experts(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, offsets: torch.Tensor, x_scales=None,
+                     bias=None, act: str = "none", out_dtype=None, y=None, ws=None, shuffle_seed: int = 0):
+    """moe_int8_linear for rows x [R, K] sorted by expert: the rows offsets[e] ..
+    offsets[e + 1] - 1 (offsets int32 [El + 1], moe_sort's or a Routing's) with
+    expert e's weights (w_codes int8 [El, F, K16], w_scales float32 [El, F], bias
+    [El, F]).  Rows behind the last expert's are not read, and theirs of y [R, F]
+    stay as they are."""
+    if offsets is None:
+        raise MoeError("moe_int8_experts: offsets are needed")
+    return _int8("moe_int8_experts", load_library().moe_int8_experts, x, w_codes, w_scales, x_scales, bias, None, offsets, act,
+                 out_dtype, y, ws, shuffle_seed)
 
 
 def _dropout(what: str, fn, x, p, rng, residual, y, seed):

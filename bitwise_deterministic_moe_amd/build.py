@@ -13,7 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 HEADER = os.path.join(HERE, "..", "include", "moedet.h")
 LIB = os.path.join(HERE, "libmoedet.so")
 SOURCES = ["moedet.hip", "route.hip", "gemm.hip", "combine.hip", "fingerprint.hip", "mfma_rate.hip", "router.hip", "train.hip", "mx.hip", "nvfp4.hip",
-           "layernorm.hip", "dense.hip", "dense_api.hip", "sort.hip", "rows.hip", "dropout.hip", "rows_api.hip"]
+           "layernorm.hip", "dense.hip", "dense_api.hip", "sort.hip", "rows.hip", "dropout.hip", "rows_api.hip", "int8.hip",
+           "int8_api.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

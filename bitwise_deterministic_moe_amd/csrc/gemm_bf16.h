@@ -49,14 +49,13 @@ struct BoolC {
   static constexpr bool value = B;
 };
 
+using ::i32x4_t;
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 
 DEV int kc_swz(int r) { return (r >> 2) & 3; }
 DEV int mnc_swz(int k) { return (k & 7) << 2; }
 DEV int kc_off(int r, int c) { return r * 32 + ((c ^ kc_swz(r)) << 3); }
 DEV int mnc_off(int k, int mn) { return k * 256 + (((mn >> 3) ^ mnc_swz(k)) << 3) + (mn & 7); }
-
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 // Raw buffer descriptor: base, stride 0, num_records = bytes, default format.
 DEV i32x4_t make_rsrc(const void* base, uint32_t bytes) {

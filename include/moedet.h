@@ -909,6 +909,95 @@ moe_status moe_unpermute_bwd(const void* dy, int64_t lddy, const void* rows, moe
                              void* drows, float* dprob, uint64_t debug_shuffle_seed, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Products in 8-bit integers with a scale per token and per output channel, for
+ * serving: the linear map, and the experts' products on rows sorted by expert.
+ *
+ * Encoding of a vector v (a token's row of x, an output channel's column of w): with
+ * a = max |v_i|, scale = a / 127 rounded to float32, and code_i is the whole
+ * number nearest to 127 v_i / a, ties to the even one, decided exactly.
+ * A vector with a < 2^-100 has scale 0 and codes 0; one with a number that is not
+ * finite has a NaN scale and codes 0, so that its outputs are NaN.  Codes
+ * are stored K16 = K rounded up to a multiple of 16 to a vector, zeros past K.
+ * K is at most 131072, so that every sum of products is exact in int32.
+ * Every output depends on the inputs alone (there is nothing to reorder). */
+
+/* Codes and scales of the rows of x.
+ *   x        DEVICE [rows, cols], row distance ldx, MOE_F32 or MOE_BF16
+ *   codes    DEVICE int8 [rows, K16] output, 16-byte aligned;  scales  DEVICE float[rows] output
+ * Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_NULL before anything is
+ * enqueued; MOE_ERR_HIP for a launch failure. */
+moe_status moe_int8_quantize(const void* x, moe_dtype dtype, int64_t rows, int64_t cols, int64_t ldx, int8_t* codes,
+                             float* scales, uint64_t debug_shuffle_seed, void* stream);
+
+/* Codes and scales of the columns of each matrix w [rows, cols] of a batch (the
+ * weights' layout, rows = the contraction), the codes transposed.
+ *   w        DEVICE [batch, rows, cols] contiguous, MOE_F32 or MOE_BF16
+ *   codes    DEVICE int8 [batch, cols, K16] output (K = rows), 16-byte aligned
+ *   scales   DEVICE float[batch, cols] output
+ * cols is below 2^20.  Errors: as moe_int8_quantize. */
+moe_status moe_int8_quantize_t(const void* w, moe_dtype dtype, int64_t batch, int64_t rows, int64_t cols, int8_t* codes,
+                               float* scales, uint64_t debug_shuffle_seed, void* stream);
+
+/* One product.
+ *   rows       T >= 0 (below 2^31)
+ *   d_in       K;  d_out  F (below 2^20)
+ *   num_local  0 for one matrix, El (1..1024) for the experts' products
+ *   x_dtype    MOE_F32 or MOE_BF16: the call quantises x itself, into the workspace;
+ *              MOE_I8: x holds codes (d_in = K16, ldx multiples of 16, base 16-byte aligned)
+ *   dtype      MOE_F32 or MOE_BF16: y, bias and residual
+ *   act        moe_act
+ *   ldx, ldy, ldr  row distances of x, y and the residual (unread without
+ *              one), below 2^20
+ *   debug_shuffle_seed  0, or a test-only seed that shuffles the launch order
+ * A call whose launch could take more than 2^24 workgroups is refused (MOE_ERR_SHAPE). */
+typedef struct moe_int8 {
+  int64_t rows;
+  int32_t d_in;
+  int32_t d_out;
+  int32_t num_local;
+  int32_t x_dtype;
+  int32_t dtype;
+  int32_t act;
+  int64_t ldx;
+  int64_t ldy;
+  int64_t ldr;
+  uint64_t debug_shuffle_seed;
+} moe_int8;
+
+/* Workspace bytes of a product (0 where x holds codes).  Errors: those of the
+ * description, MOE_ERR_NULL. */
+moe_status moe_int8_workspace_size(const moe_int8* p, size_t* bytes);
+
+/* y[t, n] = act(x_scale[t] w_scale[n] sum over k of x_code[t, k] w_code[n, k] + bias[n])
+ * (+ residual[t, n]).  The sum is exact; it is rounded to float32 once, its
+ * product with x_scale once, and y once after float32 arithmetic.
+ *   x         DEVICE [T, K] of x_dtype
+ *   x_scales  DEVICE float[T] with MOE_I8, else unread
+ *   w_codes   DEVICE int8 [F, K16], 16-byte aligned;  w_scales  DEVICE float[F]
+ *   bias      DEVICE [F] or NULL;  residual  DEVICE [T, F] or NULL
+ *   y         DEVICE [T, F] output; may be the residual, with its row distance
+ *   ws        moe_int8_workspace_size bytes, 256-byte aligned
+ * Base addresses are multiples of the element size.  Errors: MOE_ERR_DTYPE,
+ * MOE_ERR_SHAPE, MOE_ERR_MODE (act), MOE_ERR_NULL, MOE_ERR_WORKSPACE before
+ * anything is enqueued; MOE_ERR_HIP for a launch failure. */
+moe_status moe_int8_linear(const moe_int8* p, const void* x, const float* x_scales, const int8_t* w_codes,
+                           const float* w_scales, const void* bias, const void* residual, void* y, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* The same for rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 with
+ * matrix e.  Rows from offsets[El] on are not read, and theirs of y stay as they
+ * are.
+ *   x         DEVICE [rows, K];  y  DEVICE [rows, F]
+ *   w_codes   DEVICE int8 [El, F, K16];  w_scales  DEVICE float[El, F]
+ *   bias      DEVICE [El, F] or NULL
+ *   offsets   DEVICE int32 [El + 1], ascending from 0: moe_sort's or a
+ *             moe_routing's
+ * Errors: as moe_int8_linear. */
+moe_status moe_int8_experts(const moe_int8* p, const void* x, const float* x_scales, const int8_t* w_codes,
+                            const float* w_scales, const void* bias, const int32_t* offsets, void* y, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Dropout on the way into the residual stream, with numbers from a counter:
  * no mask is stored, and the backward, a rerun or a resumed run finds the same
  * one (the pages' guarantees for runs from the same state, and for a run

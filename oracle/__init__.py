@@ -25,3 +25,4 @@ from .dense import (  # noqa: F401,E402
 from .rows import (  # noqa: F401,E402
     sort_slots, permute_rows, sum_rows, sum_rows_backward, philox4x32, dropout_mask,
 )
+from .int8 import int8_quantize, int8_code_exact, int8_product, int8_experts  # noqa: F401,E402

@@ -1,0 +1,172 @@
+"""The oracle of the products in 8-bit integers, and what their entry points
+refuse (before any GPU call, so this runs without a GPU)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import bitwise_deterministic_moe_amd as moe
+import oracle
+
+
+def test_codes_against_exact_fractions():
+    rng = np.random.default_rng(0)
+    for bits in (8, 24):
+        x = rng.standard_normal((20, 64)).astype(np.float32)
+        if bits == 8:
+            x = (x.view(np.uint32) & np.uint32(0xFFFF0000)).view(np.float32)
+        # ties: half of the largest, and odd multiples of a largest number of 254 units
+        x[3, :4], x[4, :3] = (2.0, 1.0, -1.0, 0.5), (254.0, 3.0, -125.0)
+        x[4, 3:] = rng.integers(-127, 128, 61) * 2 + 1
+        x[4, 3:] = np.clip(x[4, 3:], -253, 253)
+        codes, scales = oracle.int8_quantize(x)
+        for i in range(20):
+            top = np.abs(x[i]).max()
+            assert scales[i] == np.float32(top) / np.float32(127)
+            assert [oracle.int8_code_exact(v, top) for v in x[i]] == codes[i].tolist()
+    assert oracle.int8_quantize(np.array([[2.0, 1.0, -1.0]]))[0].tolist() == [[127, 64, -64]]
+
+
+def test_codes_of_zeros_and_numbers_that_are_not_finite():
+    tiny = 2.0 ** -101
+    codes, scales = oracle.int8_quantize(np.array([[0.0, 0.0], [tiny, -tiny], [2.0 ** -100, 0], [np.inf, 1], [np.nan, 1]]))
+    assert codes.tolist() == [[0, 0], [0, 0], [127, 0], [0, 0], [0, 0]]
+    assert scales[0] == scales[1] == 0 and scales[2] > 0 and np.isnan(scales[3:]).all()
+
+
+def test_product_of_the_codes_is_near_the_product():
+    rng = np.random.default_rng(1)
+    x, w = rng.standard_normal((9, 50)), rng.standard_normal((50, 7))
+    cx, sx = oracle.int8_quantize(x)
+    cw, sw = oracle.int8_quantize(w.T)
+    y, z, s = oracle.int8_product(cx, sx, cw, sw)
+    # each factor is off by at most half a step, its scale by its rounding
+    ex, ew = 0.5001 * sx[:, None].astype(float), 0.5001 * sw.astype(float)
+    bound = ex * np.abs(w).sum(0) + (np.abs(x) + ex).sum(1)[:, None] * ew
+    assert (np.abs(y - x @ w) <= bound).all()
+    parts = oracle.int8_experts(cx, sx, np.stack([cw, cw[::-1]]), np.stack([sw, sw[::-1]]), [0, 4, 9])
+    assert np.array_equal(parts[0][2], y[:4]) and np.array_equal(parts[1][2], y[4:, ::-1])
+
+
+# ------------------------------------------------------------------- refusals
+def _t(*s, dtype=torch.bfloat16):
+    return torch.zeros(s, dtype=dtype)
+
+
+I8, F32, I32 = torch.int8, torch.float32, torch.int32
+W, S = (lambda *s: _t(*s, dtype=I8)), (lambda *s: _t(*s, dtype=F32))
+BAD = [
+    (lambda: moe.moe_int8_quantize(_t(4, 8, dtype=torch.float16)), "float32 or bfloat16"),
+    (lambda: moe.moe_int8_quantize(torch.zeros(())), "columns"),
+    (lambda: moe.moe_int8_quantize(_t(8, 4).t()), "unit stride"),
+    (lambda: moe.moe_int8_quantize(_t(4, 8), codes=W(4, 8)), "codes"),
+    (lambda: moe.moe_int8_quantize(_t(4, 8), scales=S(3)), "scales"),
+    (lambda: moe.moe_int8_quantize(S(1, (1 << 17) + 1)), "GPU|status 2"),
+    (lambda: moe.moe_int8_quantize(_t(4, 8)), "GPU"),
+    (lambda: moe.moe_int8_quantize_t(_t(8)), "matrices"),
+    (lambda: moe.moe_int8_quantize_t(_t(8, 4).t()), "matrices"),
+    (lambda: moe.moe_int8_quantize_t(_t(2, 8, 4), codes=W(2, 4, 8)), "codes"),
+    (lambda: moe.moe_int8_quantize_t(_t(2, 8, 4), scales=S(4)), "scales"),
+    (lambda: moe.moe_int8_quantize_t(_t(2, 8, 4)), "GPU"),
+    (lambda: moe.moe_int8_linear(_t(4, 20), W(6, 20), S(6)), "w_codes"),
+    (lambda: moe.moe_int8_linear(_t(4, 20), S(6, 32), S(6)), "w_codes"),
+    (lambda: moe.moe_int8_linear(_t(4, 20), W(32, 6).t(), S(6)), "w_codes"),
+    (lambda: moe.moe_int8_linear(_t(4, 20), W(1, 6, 32), S(6)), "w_codes"),
+    (lambda: moe.moe_int8_linear(_t(4, 20), W(6, 32), S(5)), "w_scales"),
+    (lambda: moe.moe_int8_linear(_t(4, 20, dtype=torch.float16), W(6, 32), S(6)), "float32 or bfloat16"),
+    (lambda: moe.moe_int8_linear(_t(4, 20), W(6, 32), S(6), x_scales=S(4)), "together"),
+    (lambda: moe.moe_int8_linear(W(4, 32), W(6, 32), S(6)), "together"),
+    (lambda: moe.moe_int8_linear(W(4, 32), W(6, 32), S(6), x_scales=S(3)), "x_scales"),
+    (lambda: moe.moe_int8_linear(W(4, 20), W(6, 32), S(6), x_scales=S(4)), "status 2"),
+    (lambda: moe.moe_int8_linear(W(4, 40)[:, :32], W(6, 32), S(6), x_scales=S(4)), "status 2"),
+    (lambda: moe.moe_int8_linear(_t(4, 20), W(6, 32), S(6), bias=S(6)), "bias"),
+    (lambda: moe.moe_int8_linear(_t(4, 20), W(6, 32), S(6), residual=_t(4, 5)), "residual"),
+    (lambda: moe.moe_int8_linear(_t(4, 20), W(6, 32), S(6), y=_t(4, 5)), "y"),
+    (lambda: moe.moe_int8_linear(_t(4, 20), W(6, 32), S(6), act="tanh"), "act"),
+    (lambda: moe.moe_int8_linear(_t(4, 20), W(6, 32), S(6), out_dtype=torch.float16), "output"),
+    (lambda: moe.moe_int8_linear(_t(4, 20), W(6, 32), S(6)), "GPU"),
+    (lambda: moe.moe_int8_experts(_t(4, 20), W(3, 6, 32), S(3, 6), None), "offsets"),
+    (lambda: moe.moe_int8_experts(_t(4, 20), W(6, 32), S(6), _t(2, dtype=I32)), "w_codes"),
+    (lambda: moe.moe_int8_experts(_t(4, 20), W(0, 6, 32), S(0, 6), _t(1, dtype=I32)), "w_codes"),
+    (lambda: moe.moe_int8_experts(_t(4, 20), W(3, 6, 32), S(3, 6), _t(3, dtype=I32)), "offsets"),
+    (lambda: moe.moe_int8_experts(_t(4, 20), W(3, 6, 32), S(3, 6), _t(4, dtype=torch.int64)), "offsets"),
+    (lambda: moe.moe_int8_experts(_t(4, 20), W(3, 6, 32), S(2, 6), _t(4, dtype=I32)), "w_scales"),
+    (lambda: moe.moe_int8_experts(_t(2, 2, 20), W(3, 6, 32), S(3, 6), _t(4, dtype=I32)), "matrix"),
+    (lambda: moe.moe_int8_experts(_t(4, 20), W(1025, 6, 32), S(1025, 6), _t(1026, dtype=I32)), "status 2"),
+    (lambda: moe.moe_int8_experts(_t(4, 20), W(3, 6, 32), S(3, 6), _t(4, dtype=I32)), "GPU"),
+]
+
+
+@pytest.mark.parametrize("i", range(len(BAD)))
+def test_refusals(i):
+    call, says = BAD[i]
+    with pytest.raises(moe.MoeError, match=says):
+        call()
+
+
+OK, NULL, SHAPE, DTYPE, WS, MODE = 0, 1, 2, 3, 4, 5
+A = 0x10000   # an address that is not followed: the calls return before any launch
+
+
+def _product(experts=False, **o):
+    a = dict(rows=4, d_in=32, d_out=6, num_local=3 if experts else 0, x_dtype=1, dtype=1, act=0, ldx=32, ldy=6, ldr=6, x=A, xs=None,
+             w=A, ws_=A, bias=None, res=None, off=A, y=A, wk=A, nb=1 << 20)
+    a.update(o)
+    c = moe._CInt8(a["rows"], a["d_in"], a["d_out"], a["num_local"], a["x_dtype"], a["dtype"], a["act"], a["ldx"], a["ldy"], a["ldr"], 0)
+    lib = moe.load_library()
+    if experts:
+        return lib.moe_int8_experts(ctypes.byref(c), a["x"], a["xs"], a["w"], a["ws_"], a["bias"], a["off"], a["y"], a["wk"], a["nb"], None)
+    return lib.moe_int8_linear(ctypes.byref(c), a["x"], a["xs"], a["w"], a["ws_"], a["bias"], a["res"], a["y"], a["wk"], a["nb"], None)
+
+
+CASES = [
+    (DTYPE, dict(x_dtype=2)), (DTYPE, dict(x_dtype=3)), (DTYPE, dict(dtype=6)), (MODE, dict(act=5)), (MODE, dict(act=-1)),
+    (SHAPE, dict(rows=-1)), (SHAPE, dict(rows=1 << 31)), (SHAPE, dict(d_in=0)), (SHAPE, dict(d_in=(1 << 17) + 1, ldx=1 << 18)),
+    (SHAPE, dict(d_out=0)), (SHAPE, dict(d_out=1 << 20, ldy=1 << 20)), (SHAPE, dict(ldx=31)), (SHAPE, dict(ldy=5)),
+    (SHAPE, dict(ldx=1 << 20)), (SHAPE, dict(ldr=-1)), (SHAPE, dict(x_dtype=6, xs=A, d_in=20)), (SHAPE, dict(x_dtype=6, xs=A, ldx=40)),
+    (SHAPE, dict(x_dtype=6, xs=A, x=A + 8)), (NULL, dict(x_dtype=6)), (NULL, dict(x=None)), (NULL, dict(w=None)), (NULL, dict(ws_=None)),
+    (NULL, dict(y=None)), (NULL, dict(wk=None)), (WS, dict(nb=16)), (WS, dict(wk=A + 16)), (SHAPE, dict(x=A + 1)), (SHAPE, dict(w=A + 8)),
+    (SHAPE, dict(ws_=A + 2)), (SHAPE, dict(y=A + 1)), (SHAPE, dict(bias=A + 1)), (OK, dict(rows=0, x=None, w=None, y=None, wk=None)),
+    (SHAPE, dict(rows=(1 << 31) - 1, d_out=(1 << 20) - 1, ldy=(1 << 20) - 1, nb=1 << 50)),
+]
+
+
+@pytest.mark.parametrize("experts", [False, True])
+@pytest.mark.parametrize("status,o", CASES)
+def test_product_status(experts, status, o):
+    assert _product(experts, **o) == status
+
+
+def test_product_status_of_one_kind():
+    assert _product(num_local=3) == SHAPE and _product(True, num_local=0) == SHAPE and _product(True, num_local=1025) == SHAPE
+    assert _product(True, off=None) == NULL and _product(True, off=A + 2) == SHAPE
+    assert _product(res=A, ldr=5) == SHAPE and _product(res=A + 1) == SHAPE
+    lib = moe.load_library()
+    assert lib.moe_int8_linear(None, A, None, A, A, None, None, A, A, 1 << 20, None) == NULL
+    assert lib.moe_int8_workspace_size(None, None) == NULL
+    assert moe.moe_int8_workspace_size(5, 100, 7) >= 5 * 112 + 5 * 4
+    with pytest.raises(moe.MoeError, match="dtypes"):
+        moe.moe_int8_workspace_size(5, 100, 7, dtype="i8")
+
+
+@pytest.mark.parametrize("status,o", [
+    (DTYPE, dict(dt=6)), (SHAPE, dict(rows=-1)), (SHAPE, dict(rows=1 << 31)), (SHAPE, dict(cols=0)), (SHAPE, dict(cols=(1 << 17) + 1, ld=1 << 18)),
+    (SHAPE, dict(ld=7)), (NULL, dict(x=None)), (NULL, dict(c=None)), (NULL, dict(s=None)), (SHAPE, dict(x=A + 1)), (SHAPE, dict(c=A + 8)),
+    (SHAPE, dict(s=A + 2)), (SHAPE, dict(rows=1 << 30, ld=1 << 20)), (OK, dict(rows=0, x=None)),
+])
+def test_quantize_status(status, o):
+    a = dict(x=A, dt=1, rows=4, cols=8, ld=8, c=A, s=A)
+    a.update(o)
+    assert moe.load_library().moe_int8_quantize(a["x"], a["dt"], a["rows"], a["cols"], a["ld"], a["c"], a["s"], 0, None) == status
+
+
+@pytest.mark.parametrize("status,o", [
+    (DTYPE, dict(dt=2)), (SHAPE, dict(batch=-1)), (SHAPE, dict(rows=0)), (SHAPE, dict(rows=(1 << 17) + 1)), (SHAPE, dict(cols=0)),
+    (SHAPE, dict(cols=1 << 20)), (SHAPE, dict(batch=1 << 30)), (NULL, dict(x=None)), (NULL, dict(c=None)), (NULL, dict(s=None)),
+    (SHAPE, dict(x=A + 1)), (SHAPE, dict(c=A + 4)), (SHAPE, dict(s=A + 1)), (OK, dict(batch=0, x=None)),
+])
+def test_quantize_t_status(status, o):
+    a = dict(x=A, dt=1, batch=2, rows=8, cols=8, c=A, s=A)
+    a.update(o)
+    assert moe.load_library().moe_int8_quantize_t(a["x"], a["dt"], a["batch"], a["rows"], a["cols"], a["c"], a["s"], 0, None) == status
