@@ -21,40 +21,56 @@ namespace moedet {
 // ------------------------------------------------------------------ quantising
 namespace {
 
-// The code of x, r about 127 / top.  With m = floor(|x| r), off by at most one where
+// Codes of bf16 numbers: fma(x, r, 1.5 2^23) is the whole number nearest to x r, ties to
+// even, in its low bits, and for r = 127 / top rounded up it is the nearest to
+// 127 x / top, as x = X u and top = A 2^d u with X, A of 8 bits show:
+//   a quotient that is no tie is at least 1 / (254 X) > 2^-16 of its value away from
+//   one, and x r is off by at most 2^-23 of it;
+//   a tie is 254 X = (2 m + 1) A 2^d, and 127 divides 2 m + 1 or A.  In the first case
+//   x = top / 2, whose code is 64: x r >= 63.5 gives that.  In the second A = 254, r
+//   is a power of two, and x r is exact.
+//
+// Codes of float32 numbers: with m = floor(|x| r), off by at most one where
 // |x| r is next to a whole number, the code is m or m + 1 as 127 |x| - (m + 1/2) top is
-// negative or positive, and the even one where it is 0 (x = top / 2 is such a
-// tie: an ordinary value).  That difference is exact: 15 + 8 bits in float32 for
-// bf16, 31 + 32 bits in float64 for float32.
-template <typename T>
-DEV int code_of(float x, float top, float r) {
+// negative or positive, and the even one where it is 0; the difference is exact in
+// float64 (31 + 32 bits).
+DEV int code_f32(float x, float top, float r) {
   const float a = __builtin_fabsf(x), m = __builtin_floorf(a * r), h = m + 0.5f;
-  int up, tie;
-  if constexpr (sizeof(T) == 2) {
-    const float d = __builtin_fmaf(-h, top, 127.f * a);
-    up = d > 0.f;
-    tie = d == 0.f;
-  } else {
-    const double d = __builtin_fma(-(double)h, (double)top, 127.0 * (double)a);
-    up = d > 0.0;
-    tie = d == 0.0;
-  }
-  const int i = (int)m, c = i + (up | (tie & i));
+  const double d = __builtin_fma(-(double)h, (double)top, 127.0 * (double)a);
+  const int up = d > 0.0, tie = d == 0.0, i = (int)m, c = i + (up | (tie & i));
   return x < 0.f ? -c : c;
 }
 template <typename T>
+DEV uint32_t code_bits(float x, float top, float r) {   // the code in the low byte
+  if constexpr (sizeof(T) == 2) return __float_as_uint(__builtin_fmaf(x, r, 0x1.8p23f));
+  return (uint32_t)code_f32(x, top, r);
+}
+template <typename T>
 DEV uint32_t pack4(const float* v, float top, float r) {
-  uint32_t p = 0u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) p |= ((uint32_t)code_of<T>(v[i], top, r) & 0xffu) << (8 * i);
-  return p;
+  const uint32_t lo = __builtin_amdgcn_perm(code_bits<T>(v[1], top, r), code_bits<T>(v[0], top, r), 0x0c0c0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(code_bits<T>(v[3], top, r), code_bits<T>(v[2], top, r), 0x04000c0cu);
+  return lo | hi;
 }
 DEV uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Scale and reciprocal of a row whose largest magnitude has the bits `top`:
-// a row with a number that is not finite gets a NaN scale and codes 0.
+// Largest magnitude of a vector, as float32 bits.
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+DEV uint32_t magnitude(const u32x4_t& v) {
+  u16x2_t m = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, v[i] & 0x7fff7fffu));
+  return (uint32_t)max(m[0], m[1]) << 16;
+}
+DEV uint32_t magnitude(const f32x4_t& v) {
+  return max(max(magnitude(v[0]), magnitude(v[1])), max(magnitude(v[2]), magnitude(v[3])));
+}
+
+// Scale and reciprocal (rounded up) of a row whose largest magnitude has the bits
+// `top`.  A row of zeros, of numbers below kInt8Tiny, or with one that is not finite
+// has r = 0, which makes every code 0 if its numbers are taken as 0 (clean).
 struct RowScale {
   float top, r, scale;
+  DEV float clean(float v) const { return r == 0.f ? 0.f : v; }
 };
 DEV RowScale row_scale(uint32_t bits) {
   const float t = __uint_as_float(bits);
@@ -64,9 +80,23 @@ DEV RowScale row_scale(uint32_t bits) {
   } else if (t >= kInt8Tiny) {
     s.top = t;
     s.r = 127.f / t;
+    if (__builtin_fmaf(s.r, t, -127.f) < 0.f) s.r = __uint_as_float(__float_as_uint(s.r) + 1u);
     s.scale = t / 127.f;
   }
   return s;
+}
+
+// The codes of a vector.
+template <typename T>
+DEV void put_codes(int8_t* out, const typename Vec<T>::raw& v, const RowScale& s) {
+  float f[Vec<T>::N];
+  Vec<T>::get(v, f);
+#pragma unroll
+  for (int q = 0; q < Vec<T>::N; ++q) f[q] = s.clean(f[q]);
+  if constexpr (sizeof(T) == 2)
+    *(u32x2_t*)out = u32x2_t{pack4<T>(f, s.top, s.r), pack4<T>(f + 4, s.top, s.r)};
+  else
+    *(uint32_t*)out = pack4<T>(f, s.top, s.r);
 }
 
 }  // namespace
@@ -94,19 +124,13 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(Int8QuantParams P) {
     const int n = P.cols - v * V;
     return n > 0 ? Vec<T>::load(x + (int64_t)v * V, n) : typename Vec<T>::raw{};
   };
-  auto most = [&](const typename Vec<T>::raw& r) __attribute__((always_inline)) {
-    float f[V];
-    Vec<T>::get(r, f);
-#pragma unroll
-    for (int q = 0; q < V; ++q) top = max(top, magnitude(f[q]));
-  };
 #pragma unroll
   for (int i = 0; i < kQuantKeep; ++i)
     if (v0 + i * L < vecs) keep[i] = load(v0 + i * L);
 #pragma unroll
   for (int i = 0; i < kQuantKeep; ++i)
-    if (v0 + i * L < vecs) most(keep[i]);
-  for (int v = v0 + kQuantKeep * L; v < vecs; v += L) most(load(v));
+    if (v0 + i * L < vecs) top = max(top, magnitude(keep[i]));
+  for (int v = v0 + kQuantKeep * L; v < vecs; v += L) top = max(top, magnitude(load(v)));
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
   if constexpr (L == 256) {
@@ -116,24 +140,12 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(Int8QuantParams P) {
   }
   const RowScale s = row_scale(top);
   int8_t* out = P.codes + row * P.cols16;
-  auto put = [&](int v, const typename Vec<T>::raw& r) __attribute__((always_inline)) {
-    float f[V];
-    Vec<T>::get(r, f);
-    if (s.r == 0.f) {
-#pragma unroll
-      for (int q = 0; q < V; ++q) f[q] = 0.f;
-    }
-    if constexpr (V == 8)
-      *(u32x2_t*)(out + (int64_t)v * 8) = u32x2_t{pack4<T>(f, s.top, s.r), pack4<T>(f + 4, s.top, s.r)};
-    else
-      *(uint32_t*)(out + (int64_t)v * 4) = pack4<T>(f, s.top, s.r);
-  };
 #pragma unroll
   for (int i = 0; i < kQuantKeep; ++i) {
-    if (v0 + i * L < vecs) put(v0 + i * L, keep[i]);
+    if (v0 + i * L < vecs) put_codes<T>(out + (int64_t)(v0 + i * L) * V, keep[i], s);
     __builtin_amdgcn_sched_barrier(0);   // one vector's registers at a time
   }
-  for (int v = v0 + kQuantKeep * L; v < vecs; v += L) put(v, load(v));
+  for (int v = v0 + kQuantKeep * L; v < vecs; v += L) put_codes<T>(out + (int64_t)v * V, load(v), s);
   if (v0 == 0) P.scales[row] = s.scale;
 }
 
@@ -208,7 +220,7 @@ __global__ __launch_bounds__(512) void int8_quantize_t_kernel(Int8QuantTParams P
       for (int q = 0; q < V; ++q) f[q] = 0.f;
       if (n > 0 && rt + r < P.rows) Vec<T>::get(Vec<T>::load(w + (int64_t)(rt + r) * P.cols + vc, n), f);
 #pragma unroll
-      for (int q = 0; q < V; ++q) s_codes[vc + q][r] = (int8_t)code_of<T>(s[q].r == 0.f ? 0.f : f[q], s[q].top, s[q].r);
+      for (int q = 0; q < V; ++q) s_codes[vc + q][r] = (int8_t)code_bits<T>(s[q].clean(f[q]), s[q].top, s[q].r);
     }
     __syncthreads();
     const int c = tid >> 2, k = (tid & 3) * 16;
@@ -235,25 +247,84 @@ struct Int8Tile {
   int64_t m0;       // first row
   int rows;         // rows of the tile that exist
   int n0;
+  int chunk;        // one group: the chunk of the contraction
 };
 
-// The tile of this workgroup, BM x bn.  One group: bands of four tile rows, down the
-// band before across, so that the consecutive units of an XCD share both operands.
-// Groups: one after the other, down the group's tile rows before across, so that the
-// units that read one strip of weights follow each other; each workgroup
-// counts the groups' tiles itself from the offsets, which costs less than a launch.
+// The group and tile row of unit L of a launch, by one wave for itself: lane l counts
+// the tile rows of groups PER l .. PER l + PER - 1.
 // Offsets are clamped to 0..M, and a launch that they would make larger than ascending
 // ones can does nothing, so that no row outside the matrices is touched whatever
-// they hold.  NT threads; s: 8 + NT / 64 words of LDS.
-template <bool GROUPS, int NT>
-DEV bool int8_tile(const Int8Params& P, int bm, int bn, int* s, Int8Tile& t) {
+// they hold.
+template <int PER>
+DEV bool group_tile(const Int8Params& P, int bm, int bn, uint32_t nT, Int8Tile& t) {
+  const int lane = threadIdx.x & 63, g0 = lane * PER;
+  int at[PER + 1];
+  uint32_t n[PER], own = 0;
+#pragma unroll
+  for (int i = 0; i <= PER; ++i) at[i] = P.offsets[min(g0 + i, P.groups)];
+#pragma unroll
+  for (int i = 0; i <= PER; ++i) at[i] = (int)min((int64_t)max(at[i], 0), P.d.M);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const uint32_t rows = g0 + i < P.groups ? (uint32_t)max(at[i + 1] - at[i], 0) : 0u;
+    n[i] = min((rows + bm - 1) / bm, 1u << 24);
+    own += n[i];
+  }
+  own = min(own, 1u << 25);   // 64 lanes stay below 2^32; ascending offsets below 2^24
+  uint32_t incl = own;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += o;
+  }
+  const uint32_t total = (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
+  if ((uint64_t)total * nT > gridDim.x) return false;
+  const int64_t unit = map_unit(blockIdx.x, (int64_t)total * nT, P.d.seed);
+  if (unit < 0) return false;
+  const uint32_t L = (uint32_t)unit / nT;
+  // the lane whose groups hold tile row L, and the group among its own
+  const int who = __popcll(__ballot(incl <= L));
+  uint32_t pre = incl - own, h = 0;
+  int g = 0, first = 0, rows = 0;
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (!found && L < pre + n[i]) {
+      found = true;
+      g = g0 + i;
+      first = at[i];
+      rows = at[i + 1] - at[i];
+      h = n[i];
+    }
+    if (!found) pre += n[i];
+  }
+  t.g = __builtin_amdgcn_readlane(g, who);
+  const uint32_t hh = (uint32_t)__builtin_amdgcn_readlane((int)h, who);
+  const uint32_t in = (uint32_t)unit - (uint32_t)__builtin_amdgcn_readlane((int)pre, who) * nT;
+  const int m = (int)(in % hh) * bm;
+  t.m0 = __builtin_amdgcn_readlane(first, who) + m;
+  t.n0 = (int)(in / hh) * bn;
+  t.rows = min(__builtin_amdgcn_readlane(rows, who) - m, bm);
+  t.chunk = 0;
+  return true;
+}
+
+// The tile of this workgroup, BM x bn.  One group: bands of four tile rows, down the
+// band before across, so that the consecutive units of an XCD share both operands,
+// and all chunks of a tile one after the other.  Groups: one after the other, down the
+// group's tile rows before across, so that the units that read one strip of
+// weights follow each other; every wave finds its group from the offsets itself, which
+// costs less than a launch, and without a barrier less than once a workgroup.
+template <bool GROUPS>
+DEV bool int8_tile(const Int8Params& P, int bm, int bn, Int8Tile& t) {
   const uint32_t nT = (uint32_t)((P.d.N + bn - 1) / bn);
   if constexpr (!GROUPS) {
     constexpr uint32_t kBand = 4;
-    const uint32_t mT = (uint32_t)((P.d.M + bm - 1) / bm);
-    const int64_t unit = map_unit(blockIdx.x, (int64_t)mT * nT, P.d.seed);
+    const uint32_t mT = (uint32_t)((P.d.M + bm - 1) / bm), S = (uint32_t)P.d.S;
+    const int64_t unit = map_unit(blockIdx.x, (int64_t)mT * nT * S, P.d.seed);
     if (unit < 0) return false;
-    const uint32_t L = (uint32_t)unit;
+    const uint32_t L = (uint32_t)unit / S;
+    t.chunk = (int)((uint32_t)unit - L * S);
     const uint32_t band = L / (kBand * nT), in = L - band * kBand * nT;
     const uint32_t left = mT - band * kBand, h = left < kBand ? left : kBand;
     t.g = 0;
@@ -262,64 +333,9 @@ DEV bool int8_tile(const Int8Params& P, int bm, int bn, int* s, Int8Tile& t) {
     t.rows = (int)(P.d.M - t.m0 < bm ? P.d.M - t.m0 : bm);
     return true;
   } else {
-    constexpr int PER = (kInt8MaxGroups + NT - 1) / NT;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const int g0 = tid * PER;
-    const int64_t M = P.d.M;
-    int at[PER + 1], n[PER];
-    uint32_t own = 0;
-#pragma unroll
-    for (int i = 0; i <= PER; ++i) at[i] = P.offsets[min(g0 + i, P.groups)];
-#pragma unroll
-    for (int i = 0; i <= PER; ++i) at[i] = (int)min((int64_t)max(at[i], 0), M);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int rows = g0 + i < P.groups ? max(at[i + 1] - at[i], 0) : 0;
-      n[i] = min((int)(((uint32_t)rows + bm - 1) / bm), (1 << 24) - 1);   // sums over a wave stay below 2^32
-      own += n[i];
-    }
-    uint32_t incl = own;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint32_t o = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += o;
-    }
-    if (lane == 63) s[8 + w] = (int)incl;
-    __syncthreads();
-    uint64_t base = 0, total = 0;
-#pragma unroll
-    for (int i = 0; i < NT / 64; ++i) {
-      const uint32_t v = (uint32_t)s[8 + i];
-      base += i < w ? v : 0u;
-      total += v;
-    }
-    if (total * nT > gridDim.x) return false;
-    const int64_t unit = map_unit(blockIdx.x, (int64_t)(total * nT), P.d.seed);
-    if (unit < 0) return false;            // uniform
-    const int L = (int)((uint32_t)unit / nT);
-    int pre = (int)((uint32_t)base + incl - own);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (L >= pre && L < pre + n[i]) {
-        s[0] = g0 + i;
-        s[1] = at[i];
-        s[2] = at[i + 1] - at[i];
-        s[3] = pre;
-        s[4] = n[i];
-      }
-      pre += n[i];
-    }
-    __syncthreads();
-    t.g = __builtin_amdgcn_readfirstlane(s[0]);
-    const int first = __builtin_amdgcn_readfirstlane(s[1]), rows = __builtin_amdgcn_readfirstlane(s[2]);
-    const uint32_t in = (uint32_t)unit - (uint32_t)__builtin_amdgcn_readfirstlane(s[3]) * nT;
-    const uint32_t h = (uint32_t)__builtin_amdgcn_readfirstlane(s[4]);
-    const int m = (int)(in % h) * bm;
-    t.m0 = first + m;
-    t.n0 = (int)(in / h) * bn;
-    t.rows = min(rows - m, bm);
-    __syncthreads();                       // s may be the main loop's LDS
-    return true;
+    if (P.groups <= 64) return group_tile<1>(P, bm, bn, nT, t);
+    if (P.groups <= 256) return group_tile<4>(P, bm, bn, nT, t);
+    return group_tile<kInt8MaxGroups / 64>(P, bm, bn, nT, t);
   }
 }
 
@@ -342,13 +358,34 @@ struct Cols4 {
 // ----------------------------------------------------------------------- tiles
 constexpr int kInt8StageRow = 260;
 
+// Row scales, column scales and bias of a tile of up to 256 x 256: thread i holds
+// those of row i and column i from before the main loop, and puts them into LDS
+// behind it.  (Loaded where they are used, they cost the 4096 x 2048 x 8192 product 20 us
+// a tile between the last slice and the end, against 11.)
+struct TileScales {
+  float sa, sb, bias;
+  template <typename T>
+  DEV void load(const Int8Params& P, const Int8Tile& t, int tid) {
+    sa = P.sa[t.m0 + min(tid, t.rows - 1)];
+    const int64_t col = (int64_t)t.g * P.d.N + min(t.n0 + tid, P.d.N - 1);
+    sb = P.sb[col];
+    bias = 0.f;
+    if (P.d.bias) bias = sizeof(T) == 2 ? bf16_to_f32(((const uint16_t*)P.d.bias)[col]) : ((const float*)P.d.bias)[col];
+  }
+  DEV void put(float* s, int tid) const {
+    s[tid] = sa;
+    s[256 + tid] = sb;
+    s[512 + tid] = bias;
+  }
+};
+
 template <typename T, int WTM, bool GROUPS>
 __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Params P) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[dn::kRingBytes<WTM> / 2];
   constexpr int BM = 2 * WTM;
-  static_assert(64 * kInt8StageRow * 4 <= dn::kRingBytes<WTM>, "epilogue stage must fit in the ring");
+  static_assert(64 * kInt8StageRow * 4 + 768 * 4 <= dn::kRingBytes<WTM>, "epilogue stage must fit in the ring");
   Int8Tile t;
-  if (!int8_tile<GROUPS, 256>(P, BM, 256, (int*)lds, t)) return;
+  if (!int8_tile<GROUPS>(P, BM, 256, t)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, half = lane >> 5;
   const uint32_t ring = bf::lds_base(lds);
@@ -363,6 +400,8 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Params P) {
   dn::KcOp<4> ob;
   oa.init(P.a + t.m0 * P.lda, ((t.rows - 1) * lda + K2) * 2, wave, lane, t.rows, lda);
   ob.init(P.b + ((int64_t)t.g * P.d.N + t.n0) * P.d.K, ((nvalid - 1) * K2 + K2) * 2, wave, lane, nvalid, K2);
+  TileScales ts;
+  ts.load<T>(P, t, tid);
   i32x16_t acc[4][4];
   dn::mainloop<dn::KC, dn::KC, WTM>(ring, nsteps, [&](int s, uint32_t st, int i) {
     const bool live = s < nsteps;
@@ -373,14 +412,15 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Params P) {
     else
       ob.issue(st + AB, wave, i - LA, ok, (uint32_t)ks * 64u);
   }, acc, wm, wn, lane);
-  Cols4<T> c4;
-  const int col = t.n0 + lane * 4;
-  c4.load(P, t.g, col);
   // The sums go through LDS in passes of 64 rows, so that a wave writes whole rows
   // (and a row's scale is a scalar).  They are converted behind it: in front, the
   // compiler converts all of them at once and spills.
   int* stage = (int*)lds;
+  float* scales = (float*)(stage + 64 * kInt8StageRow);
+  ts.put(scales, tid);
   const int64_t end = t.m0 + t.rows;
+  const int col = t.n0 + lane * 4;
+  f32x4_t sb, bias;
 #pragma unroll 1
   for (int p = 0; 64 * p < t.rows; ++p) {
 #pragma unroll
@@ -401,6 +441,10 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Params P) {
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (p == 0) {
+      sb = *(const f32x4_t*)(scales + 256 + lane * 4);
+      bias = *(const f32x4_t*)(scales + 512 + lane * 4);
+    }
 #pragma unroll
     for (int st = 0; st < 16; st += 4) {
       float v[16];
@@ -408,9 +452,9 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Params P) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const i32x4_t sv = *(const i32x4_t*)(stage + (m + 4 * i) * kInt8StageRow + lane * 4);
-        const float sa = P.sa[min(t.m0 + 64 * p + m + 4 * i, end - 1)];
+        const float sa = scales[64 * p + m + 4 * i];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[4 * i + q] = __builtin_fmaf((float)sv[q] * sa, c4.sb[q], c4.bias[q]);
+        for (int q = 0; q < 4; ++q) v[4 * i + q] = __builtin_fmaf((float)sv[q] * sa, sb[q], bias[q]);
       }
       if (col >= P.d.N) continue;
       emit<T, kFormLinear, 4, true, true>(P.d, 0, AtRows{t.m0 + 64 * p + m, end, 4, col}, v);
@@ -419,29 +463,42 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Params P) {
   }
 }
 
-template <typename T, int MB, int NB, bool GROUPS>
+// Small tiles, 64 MB x 64 NB.  SHORT: a ring of two slots, so that two to five workgroups
+// share a CU and one's first loads and epilogue run beside another's slices.
+// A contraction split into S chunks (one group only): each workgroup leaves its sums in
+// the workspace, and int8_join_kernel adds them and runs the epilogue.  (The last workgroup
+// of a tile doing that, by a ticket, needs a fence across the XCDs in each: 37 x 2048 x
+// 8192 73 us, against 8 unsplit.)
+template <typename T, int MB, int NB, bool SHORT, bool GROUPS>
 __global__ __launch_bounds__(256) void int8_small_kernel(Int8Params P) {
-  using S = dn::Small<MB, NB, false>;
+  using S = dn::Small<MB, NB, SHORT>;
   constexpr int BM = 64 * MB, BN = 64 * NB, ROW = 64 * NB + 4;
-  static_assert(BM * ROW * 4 <= S::RING, "epilogue stage must fit in the ring");
-  __shared__ __attribute__((aligned(16))) uint16_t lds[S::RING / 2];
+  constexpr int STAGE = (BM * ROW + 768) * 4;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[(S::RING > STAGE ? S::RING : STAGE) / 2];
   Int8Tile t;
-  if (!int8_tile<GROUPS, 256>(P, BM, BN, (int*)lds, t)) return;
+  if (!int8_tile<GROUPS>(P, BM, BN, t)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const uint32_t ring = bf::lds_base(lds), own = (uint32_t)wave * 1024u;
   const int nvalid = P.d.N - t.n0 < BN ? P.d.N - t.n0 : BN;
   const int64_t K2 = P.d.K / 2, lda = P.lda / 2;
-  const int nsteps = (int)((K2 + dn::SBK - 1) / dn::SBK);
+  int s0 = 0, nsteps = (int)((K2 + dn::SBK - 1) / dn::SBK);
+  if constexpr (!GROUPS) {
+    const int all = nsteps, chunks = P.d.S;
+    s0 = (int)((int64_t)t.chunk * all / chunks);
+    nsteps = (int)((int64_t)(t.chunk + 1) * all / chunks) - s0;
+  }
   const int kc = dn::KcOp<1>::chunk(lane) * 8;
   dn::KcPart<MB> oa;
   dn::KcPart<NB> ob;
   oa.init(P.a + t.m0 * P.lda, ((t.rows - 1) * lda + K2) * 2, wave, lane, t.rows, lda);
   ob.init(P.b + ((int64_t)t.g * P.d.N + t.n0) * P.d.K, nvalid * K2 * 2, wave, lane, nvalid, K2);
+  TileScales ts;
+  ts.load<T>(P, t, tid);
   i32x16_t acc[MB][NB];
-  dn::small_mainloop<dn::KC, dn::KC, MB, NB, false>(ring, nsteps, [&](int h, uint32_t at, int i) {
+  dn::small_mainloop<dn::KC, dn::KC, MB, NB, SHORT>(ring, nsteps, [&](int h, uint32_t at, int i) {
     const bool live = h < 2 * nsteps;
-    const int ks = live ? h : 0;
+    const int ks = live ? 2 * s0 + h : 0;
     const bool ok = live && ks * dn::BK + kc < K2;
     if (i < MB)
       bf::dma16(oa.rs, at + own, ok ? oa.voff[i < MB ? i : 0] : dn::kOOB, (uint32_t)ks * 64u);
@@ -449,146 +506,198 @@ __global__ __launch_bounds__(256) void int8_small_kernel(Int8Params P) {
       bf::dma16(ob.rs, at + own, ok ? ob.voff[i < MB ? 0 : i - MB] : dn::kOOB, (uint32_t)ks * 64u);
   }, acc, wm, wn, lane);
   // through LDS, so that 16 lanes write 64 columns of a row
-  float* stage = (float*)lds;
+  int* stage = (int*)lds;
+  float* scales = (float*)(stage + BM * ROW);
+  ts.put(scales, tid);
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    const int m = mb * 64 + wm * 32 + (lane & 31);
-    const float sa = P.sa[t.m0 + min(m, t.rows - 1)];
+  for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const i32x16_t& a = acc[mb][n];
-        *(f32x4_t*)(stage + m * ROW + 64 * n + wn * 32 + 8 * i + 4 * (lane >> 5)) =
-            f32x4_t{(float)a[4 * i] * sa, (float)a[4 * i + 1] * sa, (float)a[4 * i + 2] * sa, (float)a[4 * i + 3] * sa};
+        *(i32x4_t*)(stage + (mb * 64 + wm * 32 + (lane & 31)) * ROW + 64 * n + wn * 32 + 8 * i + 4 * (lane >> 5)) =
+            i32x4_t{a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]};
       }
-  }
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   const int c = (lane & 15) * 4, m = 4 * wave + (lane >> 4);
 #pragma unroll 1
-  for (int n = 0; n < NB; ++n) {
-    const int col = t.n0 + 64 * n + c;
+  for (int p = 0; p < MB * NB; ++p) {
+    const int mb = p / NB, n = p % NB, col = t.n0 + 64 * n + c;
     if (col >= P.d.N) continue;
-    Cols4<T> c4;
-    c4.load(P, t.g, col);
-#pragma unroll 1
-    for (int mb = 0; mb < MB; ++mb) {
-      float v[16];
+    if constexpr (!GROUPS) {
+      if (P.d.S > 1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4_t sv = *(const f32x4_t*)(stage + (mb * 64 + m + 16 * i) * ROW + 64 * n + c);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[4 * i + q] = __builtin_fmaf(sv[q], c4.sb[q], c4.bias[q]);
+        for (int i = 0; i < 4; ++i) {
+          const int row = mb * 64 + m + 16 * i;
+          if (row < t.rows)
+            *(i32x4_t*)(P.part + ((int64_t)t.chunk * P.d.M + t.m0 + row) * P.part_ld + col) = *(const i32x4_t*)(stage + row * ROW + 64 * n + c);
+        }
+        continue;
       }
-      emit<T, kFormLinear, 4, false, true>(P.d, 0, AtRows{t.m0 + mb * 64 + m, t.m0 + t.rows, 16, col}, v);
     }
+    const f32x4_t sb = *(const f32x4_t*)(scales + 256 + 64 * n + c), bias = *(const f32x4_t*)(scales + 512 + 64 * n + c);
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const i32x4_t sv = *(const i32x4_t*)(stage + (mb * 64 + m + 16 * i) * ROW + 64 * n + c);
+      const float sa = scales[mb * 64 + m + 16 * i];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[4 * i + q] = __builtin_fmaf((float)sv[q] * sa, sb[q], bias[q]);
+    }
+    emit<T, kFormLinear, 4, false, true>(P.d, 0, AtRows{t.m0 + mb * 64 + m, t.m0 + t.rows, 16, col}, v);
   }
 }
 
-// -------------------------------------------------------------------- few rows
-// A workgroup streams 16 weight rows: its 8 waves take steps of 64 codes in turn,
-// so that together they read 512 bytes of a row, and multiply each with MT
-// blocks of 16 rows of x (v_mfma_i32_16x16x64_i8; a lane's 16 bytes of both operands
-// come straight from memory, those of x from the caches).  The waves' sums meet in
-// LDS.  A lane ends with four neighbouring columns of one row.
-constexpr int kFewWaves = 8, kFewDepth = 4;
-template <typename T, int MT, bool GROUPS>
-__global__ __launch_bounds__(64 * kFewWaves) void int8_few_kernel(Int8Params P) {
-  __shared__ __attribute__((aligned(16))) i32x4_t s_acc[kFewWaves * MT * 64];
-  Int8Tile t;
-  if (!int8_tile<GROUPS, 64 * kFewWaves>(P, 16 * MT, 16, (int*)s_acc, t)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int i16 = lane & 15, g = lane >> 4;
-  const int K = (int)P.d.K, steps = (K + 63) / 64;
-  const int8_t* w = P.b + ((int64_t)t.g * P.d.N + min(t.n0 + i16, P.d.N - 1)) * P.d.K;
-  const int8_t* x[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) x[m] = P.a + (t.m0 + min(16 * m + i16, t.rows - 1)) * P.lda;
-  i32x4_t acc[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = i32x4_t{0, 0, 0, 0};
-  struct Step {
-    i32x4_t w, x[MT];
-  };
-  // past the end of the rows: their last 16 codes again, and zeros for x
-  auto load = [&](Step& f, int s) __attribute__((always_inline)) {
-    const int k = 64 * s + 16 * g, kk = min(k, K - 16);
-    f.w = *(const i32x4_t*)(w + kk);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) f.x[m] = *(const i32x4_t*)(x[m] + kk);
-  };
-  auto mul = [&](const Step& f, int s) __attribute__((always_inline)) {
-    const bool in = 64 * s + 16 * g < K;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      i32x4_t v = f.x[m];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = in ? v[q] : 0;
-      acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w, v, acc[m], 0, 0, 0);
-    }
-  };
-  // rounds of kFewDepth steps, the next round's loads in flight
-  Step st[kFewDepth];
-#pragma unroll
-  for (int d = 0; d < kFewDepth; ++d) load(st[d], wave + d * kFewWaves);
-#pragma unroll 1
-  for (int s = wave; s < steps; s += kFewDepth * kFewWaves) {
-#pragma unroll
-    for (int d = 0; d < kFewDepth; ++d) {
-      mul(st[d], s + d * kFewWaves);
-      load(st[d], s + (kFewDepth + d) * kFewWaves);
-    }
-  }
-#pragma unroll
-  for (int m = 0; m < MT; ++m) s_acc[(wave * MT + m) * 64 + lane] = acc[m];
-  __syncthreads();
-  if (tid >= 64 * MT) return;
-  i32x4_t a = s_acc[tid];
-#pragma unroll
-  for (int v = 1; v < kFewWaves; ++v) a = a + s_acc[v * MT * 64 + tid];
-  const int row = (tid >> 6) * 16 + i16, col = t.n0 + 4 * g;
-  if (row >= t.rows || col >= P.d.N) return;
-  const float sa = P.sa[t.m0 + row];
+// The chunks' sums of four columns a thread, then the epilogue.
+template <typename T>
+__global__ __launch_bounds__(256) void int8_join_kernel(Int8Params P) {
+  const uint32_t quads = ((uint32_t)P.d.N + 3) / 4;
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;   // a split product has few elements
+  if (i >= (uint32_t)P.d.M * quads) return;
+  const int64_t row = i / quads;
+  const int col = (int)(i - (uint32_t)row * quads) * 4;
+  const int32_t* p = P.part + row * P.part_ld + col;
+  i32x4_t a = *(const i32x4_t*)p;
+#pragma unroll 4
+  for (int s = 1; s < P.d.S; ++s) a = a + *(const i32x4_t*)(p + (int64_t)s * P.d.M * P.part_ld);
+  const float sa = P.sa[row];
   Cols4<T> c4;
-  c4.load(P, t.g, col);
+  c4.load(P, 0, col);
   float v[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf((float)a[q] * sa, c4.sb[q], c4.bias[q]);
-  emit<T, kFormLinear, 1, false, true>(P.d, 0, AtRows{t.m0 + row, t.m0 + row + 1, 1, col}, v);
+  emit<T, kFormLinear, 1, false, true>(P.d, 0, AtRows{row, row + 1, 1, col}, v);
+}
+
+// -------------------------------------------------------------------- few rows
+// A wave streams 16 weight rows in steps of 64 codes, and multiplies each with 16 rows
+// of x (v_mfma_i32_16x16x64_i8; a lane's 16 bytes of the weights come straight from
+// memory).  A workgroup's four waves are 4 / ks neighbouring blocks of weight rows, each
+// streamed by ks waves that take its steps in turn and whose sums meet in LDS.  A
+// lane ends with four neighbouring columns of one row.
+// FUSED: x is not yet quantised; every workgroup does that itself, into LDS, while its
+// first weights are on the way (1 x 2048 x 2048: a launch of 3.9 us saved).
+constexpr int kFewWaves = 4, kFewDepth = 8;
+template <typename T, bool GROUPS, bool FUSED>
+__global__ __launch_bounds__(64 * kFewWaves) void int8_few_kernel(Int8Params P, int ks) {
+  static_assert(!(GROUPS && FUSED), "rows to quantise are those of one matrix");
+  constexpr int NT = 64 * kFewWaves;
+  __shared__ __attribute__((aligned(16))) i32x4_t s_acc[NT];
+  __shared__ __attribute__((aligned(16))) int8_t s_x[FUSED ? kInt8FusedBytes : 16];
+  __shared__ uint32_t s_top[kInt8FusedRows];
+  Int8Tile t;
+  if (!int8_tile<GROUPS>(P, 16, 16 * kFewWaves / ks, t)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i16 = lane & 15, g = lane >> 4;
+  const int part = wave & (ks - 1), n0 = t.n0 + 16 * (wave / ks);   // ks is a power of two
+  const int K = (int)P.d.K, steps = (K + 63) / 64;
+  const int8_t* w = P.b + ((int64_t)t.g * P.d.N + min(n0 + i16, P.d.N - 1)) * P.d.K;
+  const int xrow = min(i16, t.rows - 1);
+  const int8_t* x = FUSED ? s_x + xrow * K : P.a + (t.m0 + xrow) * P.lda;
+  i32x4_t acc = {0, 0, 0, 0};
+  // past the end of the rows: their last 16 codes again, and zeros for x
+  auto at = [&](int s) { return min(64 * s + 16 * g, K - 16); };
+  auto load_x = [&](int s) __attribute__((always_inline)) { return *(const i32x4_t*)(x + at(s)); };
+  struct Step {
+    i32x4_t w, x;
+  };
+  auto load = [&](Step& f, int s) __attribute__((always_inline)) {
+    f.w = *(const i32x4_t*)(w + at(s));
+    if constexpr (!FUSED) f.x = load_x(s);
+  };
+  auto mul = [&](const Step& f, int s) __attribute__((always_inline)) {
+    const bool in = 64 * s + 16 * g < K;
+    i32x4_t v = FUSED ? load_x(s) : f.x;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = in ? v[q] : 0;
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w, v, acc, 0, 0, 0);
+  };
+  // the steps part, part + ks, ... in rounds of kFewDepth, the next round's loads in
+  // flight; the last round loads nothing
+  const int n = steps > part ? (steps - part + ks - 1) / ks : 0;
+  Step st[kFewDepth];
+#pragma unroll
+  for (int d = 0; d < kFewDepth; ++d) load(st[d], part + min(d, max(n - 1, 0)) * ks);
+  // the epilogue's numbers, loaded beside the stream
+  const int col = n0 + 4 * g;
+  Cols4<T> c4;
+  c4.load(P, t.g, col);
+  float sa = 0.f;
+  if constexpr (FUSED) {
+    constexpr int V = Vec<T>::N;
+    const int per = K / V, vecs = t.rows * per;
+    if (tid < kInt8FusedRows) s_top[tid] = 0u;
+    __syncthreads();
+    auto get = [&](int v, int row) __attribute__((always_inline)) {
+      const int c = (v - row * per) * V, left = P.xcols - c;
+      return left > 0 ? Vec<T>::load((const T*)P.x + (t.m0 + row) * P.ldx + c, left) : typename Vec<T>::raw{};
+    };
+    for (int v = tid; v < vecs; v += NT) {
+      const int row = v / per;
+      atomicMax(&s_top[row], magnitude(get(v, row)));
+    }
+    __syncthreads();
+    for (int v = tid; v < vecs; v += NT) {
+      const int row = v / per;
+      put_codes<T>(s_x + v * V, get(v, row), row_scale(s_top[row]));
+    }
+    sa = row_scale(s_top[xrow]).scale;
+    __syncthreads();
+  } else {
+    sa = P.sa[t.m0 + xrow];
+  }
+  int i = 0;
+#pragma unroll 1
+  for (; i + kFewDepth < n; i += kFewDepth) {
+#pragma unroll
+    for (int d = 0; d < kFewDepth; ++d) {
+      mul(st[d], part + (i + d) * ks);
+      load(st[d], part + min(i + kFewDepth + d, n - 1) * ks);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < kFewDepth; ++d)
+    if (i + d < n) mul(st[d], part + (i + d) * ks);
+  if (ks > 1) {
+    s_acc[tid] = acc;
+    __syncthreads();
+    if (part != 0) return;
+    for (int v = 1; v < ks; ++v) acc = acc + s_acc[tid + 64 * v];
+  }
+  if (col >= P.d.N || i16 >= t.rows) return;
+  float v[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf((float)acc[q] * sa, c4.sb[q], c4.bias[q]);
+  emit<T, kFormLinear, 1, false, true>(P.d, 0, AtRows{t.m0 + i16, t.m0 + i16 + 1, 1, col}, v);
 }
 
 // --------------------------------------------------------------------- launches
 namespace {
 
-// Workgroups of a launch: with groups, as many as any offsets can need.
-int64_t int8_grid(const Int8Params& P, int bm, int bn) {
+// Workgroups of a launch: with groups, as many as ascending offsets can need.
+dim3 int8_grid(const Int8Params& P, int bm, int bn) {
   const int64_t nT = (P.d.N + bn - 1) / bn;
   int64_t mT = (P.d.M + bm - 1) / bm;
   if (P.offsets) {
     mT = P.d.M / bm + P.groups;
     if (mT > P.d.M) mT = P.d.M;
   }
-  return grid_for_units(mT * nT);
+  return dim3((uint32_t)grid_for_units(mT * nT * P.d.S));
 }
 
 template <typename T, bool GROUPS>
 void tiles(const Int8Params& P, int tile, hipStream_t st) {
-  const DenseShape sh = dense_shape(kFormLinear, true, tile);
-  const dim3 grid((uint32_t)int8_grid(P, sh.bm, sh.bn));
+  const Int8Shape sh = kInt8Shapes[tile];
+  const dim3 grid = int8_grid(P, sh.bm, sh.bn);
   switch (tile) {
     case 0: int8_tile_kernel<T, 128, GROUPS><<<grid, 256, 0, st>>>(P); break;
-    case 1: int8_tile_kernel<T, 64, GROUPS><<<grid, 256, 0, st>>>(P); break;
-    case 2: int8_small_kernel<T, 2, 2, GROUPS><<<grid, 256, 0, st>>>(P); break;
-    default: int8_small_kernel<T, 1, 1, GROUPS><<<grid, 256, 0, st>>>(P);
+    case 1: int8_small_kernel<T, 2, 2, true, GROUPS><<<grid, 256, 0, st>>>(P); break;
+    case 2: int8_small_kernel<T, 2, 1, true, GROUPS><<<grid, 256, 0, st>>>(P); break;
+    case 3: int8_small_kernel<T, 1, 1, true, GROUPS><<<grid, 256, 0, st>>>(P); break;
+    default: int8_small_kernel<T, 1, 1, false, GROUPS><<<grid, 256, 0, st>>>(P);
   }
-}
-template <typename T, bool GROUPS>
-void few(const Int8Params& P, int mt, hipStream_t st) {
-  const dim3 grid((uint32_t)int8_grid(P, 16 * mt, 16));
-  if (mt == 1)
-    int8_few_kernel<T, 1, GROUPS><<<grid, 64 * kFewWaves, 0, st>>>(P);
-  else
-    int8_few_kernel<T, 2, GROUPS><<<grid, 64 * kFewWaves, 0, st>>>(P);
+  if (!GROUPS && P.d.S > 1) int8_join_kernel<T><<<(uint32_t)((P.d.M * ((P.d.N + 3) / 4) + 255) / 256), 256, 0, st>>>(P);
 }
 
 }  // namespace
@@ -601,11 +710,24 @@ hipError_t launch_int8_tiles(const Int8Params& P, bool bf16, int tile, hipStream
   return hipGetLastError();
 }
 
-hipError_t launch_int8_few(const Int8Params& P, bool bf16, int mt, hipStream_t st) {
-  if (bf16)
-    P.offsets ? few<uint16_t, true>(P, mt, st) : few<uint16_t, false>(P, mt, st);
-  else
-    P.offsets ? few<float, true>(P, mt, st) : few<float, false>(P, mt, st);
+hipError_t launch_int8_few(const Int8Params& P, bool bf16, int ks, hipStream_t st) {
+  const dim3 grid = int8_grid(P, 16, 16 * kFewWaves / ks);
+  constexpr int NT = 64 * kFewWaves;
+  if (bf16) {
+    if (P.x)
+      int8_few_kernel<uint16_t, false, true><<<grid, NT, 0, st>>>(P, ks);
+    else if (P.offsets)
+      int8_few_kernel<uint16_t, true, false><<<grid, NT, 0, st>>>(P, ks);
+    else
+      int8_few_kernel<uint16_t, false, false><<<grid, NT, 0, st>>>(P, ks);
+  } else {
+    if (P.x)
+      int8_few_kernel<float, false, true><<<grid, NT, 0, st>>>(P, ks);
+    else if (P.offsets)
+      int8_few_kernel<float, true, false><<<grid, NT, 0, st>>>(P, ks);
+    else
+      int8_few_kernel<float, false, false><<<grid, NT, 0, st>>>(P, ks);
+  }
   return hipGetLastError();
 }
 

@@ -20,57 +20,81 @@ bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(byte
 int size_of(int dtype) { return dtype == MOE_F32 ? 4 : dtype == MOE_BF16 ? 2 : 1; }
 int up16(int64_t n) { return (int)((n + 15) / 16 * 16); }
 
-// A kernel of the product: few rows (mt > 0) or a tile.
-struct Choice {
-  int mt, tile;
-};
-
-// Tiles' costs as in the bf16 operators (choose in dense_api.hip), per slice of 64
-// codes (128 in the small tiles): alone while at most half of the CUs have one, busy when
-// all do.
-struct TileCost {
-  double alone, busy, fixed;
-  bool shares;
-};
-constexpr TileCost kTiles[kInt8Tiles] = {{0.7, 0.8, 9.0, false}, {0.36, 0.48, 8.0, false}, {0.38, 0.52, 5.8, false}, {0.2, 0.23, 4.5, true}};
 constexpr int kCUs = 256;
 
-Choice choose(int64_t rows, int64_t N, int64_t K, int64_t groups) {
-  // rows that share a matrix, were they spread evenly
-  const int64_t each = (rows + groups - 1) / groups;
-  if (each <= 16) return {1, 0};
-  if (each <= 32) return {2, 0};
-  Choice best{0, -1};
-  double least = 0;
+// The kernel of a product: few rows (ks > 0, fused: x is quantised by it), or a tile and the
+// chunks of its contraction.
+struct Choice {
+  int ks, tile, S;
+  bool fused;
+};
+
+// A tile's cost in microseconds, fitted to the times in int8.h: `each` a slice of each of
+// the workgroups that share a CU, `alone` one by itself, `fixed` the launch, first
+// slice and epilogue of a round.
+struct TileCost {
+  double alone, each, fixed;
+  int shares;               // workgroups a CU
+};
+constexpr TileCost kTiles[kInt8Tiles] = {{0.57, 0.84, 15.0, 1}, {0.75, 0.53, 9.7, 2}, {0.58, 0.36, 5.8, 3}, {0.52, 0.223, 4.0, 5}, {0.29, 0.22, 3.4, 2}};
+
+double estimate(int i, double tiles, double steps) {
+  const TileCost& c = kTiles[i];
+  const double per_cu = tiles / kCUs;
+  if (c.shares == 1) return (double)(int64_t)(per_cu + 0.999) * (c.fixed + steps * (per_cu <= 0.5 ? c.alone : c.each));
+  const double full = per_cu / c.shares;   // rounds of a full CU
+  const double slice = per_cu * c.each > c.alone ? per_cu * c.each : c.alone;
+  return c.fixed * (full < 1 ? 1 : 0.4 + 0.6 * full) + steps * slice;
+}
+
+Choice choose(const moe_int8* p, int64_t K) {
+  const int64_t rows = p->rows, N = p->d_out, groups = p->num_local ? p->num_local : 1;
+  Choice best{0, 0, 1, false};
+  // 16 rows and fewer of one matrix (16 x 2048 x 2048 5.3 us, with a tile 7.1), and experts
+  // of up to 3 rows were they spread evenly, stream the weights (4 tokens of 22 experts of 512, 352 MB:
+  // 60 us, with tiles 66; 16 tokens, 1079 MB: 178 and 205; but 800 rows of 64 experts 82 and 55).
+  if (p->num_local ? rows <= 3 * groups : rows <= 16) {
+    // a wave to 16 weight rows where that fills the device, else four (22 experts of
+    // 2048 x 2048: 17.8 and 19.8 us; 1 x 2048 x 2048: 8 and 4.5)
+    const int64_t waves = (N + 15) / 16 * (p->num_local ? rows : 1);
+    best.ks = waves >= 2048 ? 1 : 4;
+    best.fused = !p->num_local && p->x_dtype == p->dtype && rows <= kInt8FusedRows && rows * K <= kInt8FusedBytes;
+    return best;
+  }
+  double least = -1;
   for (int i = 0; i < kInt8Tiles; ++i) {
-    const TileCost& c = kTiles[i];
-    const DenseShape sh = dense_shape(kFormLinear, true, i);
-    const int64_t tiles = groups * ((each + sh.bm - 1) / sh.bm) * ((N + sh.bn - 1) / sh.bn);
-    const double steps = (double)((K / 2 + sh.bk - 1) / sh.bk);
-    const double per_cu = (double)((tiles + kCUs - 1) / kCUs);
-    double slice, t = c.fixed;
-    if (c.shares) {
-      slice = per_cu * c.busy > c.alone ? per_cu * c.busy : c.alone;
-    } else {
-      const double over = 2.0 * (double)tiles / kCUs - 1;
-      slice = per_cu * (over <= 0 ? c.alone : over >= 1 ? c.busy : c.alone + over * (c.busy - c.alone));
-      t += (per_cu - 1) * 0.6 * c.fixed;
-    }
-    t += steps * slice;
-    if (best.tile < 0 || t < least) {
-      best.tile = i;
-      least = t;
+    const Int8Shape& sh = kInt8Shapes[i];
+    const double nT = (double)((N + sh.bn - 1) / sh.bn);
+    // experts leave half a tile each on average
+    double mT = (double)((rows + sh.bm - 1) / sh.bm);
+    if (groups > 1) mT = (double)rows / sh.bm + 0.5 * (double)(groups < rows ? groups : rows);
+    const int64_t steps = (K + sh.bk - 1) / sh.bk;
+    for (int S = 1; S <= 8; S *= 2) {
+      // the 64 x 64 tile of one matrix may be split while workgroups are few
+      if (S > 1 && (i != kInt8Tiles - 1 || p->num_local || steps / S < 4 || mT * nT * S > 2 * kCUs)) break;
+      double t = estimate(i, mT * nT * S, (double)((steps + S - 1) / S));
+      // the sums written and read, and the join (64 x 2048 x 8192: 20 us whole, 12 in four chunks;
+      // 37 x 8192 x 2048: 8 and 10)
+      if (S > 1) t += 3.2 + (double)S * (double)rows * (double)N * 8.0 / 3e6;
+      // the weights at 5.2 TB/s; of tiles that reach that, the quickest
+      const double stream = (double)groups * (double)N * (double)K / 5.2e6;
+      t = (t > stream ? t : stream) + 0.1 * t;
+      if (least < 0 || t < least) {
+        best.tile = i;
+        best.S = S;
+        least = t;
+      }
     }
   }
   return best;
 }
 
 // Workgroups that a launch may need at most.
-int64_t units(const Choice& c, int64_t rows, int64_t N, int64_t groups) {
-  const DenseShape sh = c.mt ? DenseShape{16 * c.mt, 16, 64} : dense_shape(kFormLinear, true, c.tile);
-  int64_t mT = rows / sh.bm + groups;
-  if (mT > rows) mT = rows;
-  return mT * ((N + sh.bn - 1) / sh.bn);
+int64_t units(const moe_int8* p, const Choice& c) {
+  const int64_t bm = c.ks ? 16 : kInt8Shapes[c.tile].bm, bn = c.ks ? 64 / c.ks : kInt8Shapes[c.tile].bn;
+  int64_t mT = p->rows / bm + (p->num_local ? p->num_local : 1);
+  if (mT > p->rows) mT = p->rows;
+  return mT * ((p->d_out + bn - 1) / bn) * c.S;
 }
 
 moe_status check(const moe_int8* p) {
@@ -83,14 +107,35 @@ moe_status check(const moe_int8* p) {
   if (p->num_local < 0 || p->num_local > kInt8MaxGroups) return MOE_ERR_SHAPE;
   if (p->ldx < p->d_in || p->ldx >= kMaxLd || p->ldy < p->d_out || p->ldy >= kMaxLd || p->ldr < 0 || p->ldr >= kMaxLd) return MOE_ERR_SHAPE;
   if (p->x_dtype == MOE_I8 && (p->d_in % 16 || p->ldx % 16)) return MOE_ERR_SHAPE;
-  const int64_t groups = p->num_local ? p->num_local : 1;
-  if (units(choose(p->rows, p->d_out, up16(p->d_in), groups), p->rows, p->d_out, groups) > kMaxUnits) return MOE_ERR_SHAPE;
+  if (units(p, choose(p, up16(p->d_in))) > kMaxUnits) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 
-size_t codes_bytes(const moe_int8* p) { return align_up((size_t)p->rows * up16(p->d_in)); }
-size_t ws_need(const moe_int8* p) {
-  return p->x_dtype == MOE_I8 || p->rows == 0 ? 0 : codes_bytes(p) + align_up((size_t)p->rows * 4);
+// Workspace: codes and scales of x, then the sums of a split contraction.
+struct Plan {
+  Choice c;
+  int K;
+  int64_t part_ld;
+  size_t scales, part, total;   // byte offsets
+};
+Plan plan(const moe_int8* p) {
+  Plan w{};
+  w.K = up16(p->d_in);
+  w.c = choose(p, w.K);
+  if (p->rows == 0) return w;
+  size_t o = 0;
+  if (p->x_dtype != MOE_I8 && !w.c.fused) {
+    o = align_up((size_t)p->rows * w.K);
+    w.scales = o;
+    o += align_up((size_t)p->rows * 4);
+  }
+  if (w.c.S > 1) {
+    w.part_ld = ((int64_t)p->d_out + 3) / 4 * 4;
+    w.part = o;
+    o += align_up((size_t)w.c.S * p->rows * w.part_ld * 4);
+  }
+  w.total = o;
+  return w;
 }
 
 moe_status product(const moe_int8* p, const void* x, const float* x_scales, const int8_t* w_codes, const float* w_scales,
@@ -104,15 +149,16 @@ moe_status product(const moe_int8* p, const void* x, const float* x_scales, cons
       !aligned(bias, es) || !aligned(residual, es) || !aligned(y, es) || !aligned(offsets, 4))
     return MOE_ERR_SHAPE;
   if (residual && p->ldr < p->d_out) return MOE_ERR_SHAPE;
-  const size_t need = ws_need(p);
-  if (need && !ws) return MOE_ERR_NULL;
-  if (need && (ws_bytes < need || !aligned(ws, kWsAlign))) return MOE_ERR_WORKSPACE;
-  const int K = up16(p->d_in);
+  const Plan w = plan(p);
+  if (w.total && !ws) return MOE_ERR_NULL;
+  if (w.total && (ws_bytes < w.total || !aligned(ws, kWsAlign))) return MOE_ERR_WORKSPACE;
+  const int K = w.K;
   Int8Params P{};
   P.d.M = p->rows;
   P.d.N = p->d_out;
   P.d.K = K;
-  P.d.nseg = P.d.S = 1;
+  P.d.nseg = 1;
+  P.d.S = w.c.S;
   P.d.bias = bias;
   P.d.add = residual;
   P.d.ldadd = p->ldr;
@@ -127,7 +173,14 @@ moe_status product(const moe_int8* p, const void* x, const float* x_scales, cons
   P.sb = w_scales;
   P.offsets = offsets;
   P.groups = offsets ? p->num_local : 1;
-  if (!codes) {
+  const bool bf16 = p->dtype == MOE_BF16;
+  P.part = (int32_t*)((char*)ws + w.part);
+  P.part_ld = w.part_ld;
+  if (w.c.fused) {
+    P.x = x;
+    P.ldx = p->ldx;
+    P.xcols = p->d_in;
+  } else if (!codes) {
     Int8QuantParams Q{};
     Q.x = x;
     Q.rows = p->rows;
@@ -136,16 +189,14 @@ moe_status product(const moe_int8* p, const void* x, const float* x_scales, cons
     Q.cols16 = K;
     Q.limit = offsets ? offsets + p->num_local : nullptr;
     Q.codes = (int8_t*)ws;
-    Q.scales = (float*)((char*)ws + codes_bytes(p));
+    Q.scales = (float*)((char*)ws + w.scales);
     Q.seed = p->debug_shuffle_seed;
     if (launch_int8_quantize(Q, p->x_dtype == MOE_BF16, st) != hipSuccess) return MOE_ERR_HIP;
     P.a = Q.codes;
     P.lda = K;
     P.sa = Q.scales;
   }
-  const Choice c = choose(p->rows, p->d_out, K, P.groups);
-  const bool bf16 = p->dtype == MOE_BF16;
-  return hip_status(c.mt ? launch_int8_few(P, bf16, c.mt, st) : launch_int8_tiles(P, bf16, c.tile, st));
+  return hip_status(w.c.ks ? launch_int8_few(P, bf16, w.c.ks, st) : launch_int8_tiles(P, bf16, w.c.tile, st));
 }
 
 }  // namespace
@@ -198,7 +249,7 @@ MOE_API moe_status moe_int8_workspace_size(const moe_int8* p, size_t* bytes) {
   const moe_status s = check(p);
   if (s != MOE_OK) return s;
   if (!bytes) return MOE_ERR_NULL;
-  *bytes = ws_need(p);
+  *bytes = plan(p).total;
   return MOE_OK;
 }
 

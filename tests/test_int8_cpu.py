@@ -110,7 +110,7 @@ A = 0x10000   # an address that is not followed: the calls return before any lau
 
 
 def _product(experts=False, **o):
-    a = dict(rows=4, d_in=32, d_out=6, num_local=3 if experts else 0, x_dtype=1, dtype=1, act=0, ldx=32, ldy=6, ldr=6, x=A, xs=None,
+    a = dict(rows=40, d_in=32, d_out=6, num_local=3 if experts else 0, x_dtype=1, dtype=1, act=0, ldx=32, ldy=6, ldr=6, x=A, xs=None,
              w=A, ws_=A, bias=None, res=None, off=A, y=A, wk=A, nb=1 << 20)
     a.update(o)
     c = moe._CInt8(a["rows"], a["d_in"], a["d_out"], a["num_local"], a["x_dtype"], a["dtype"], a["act"], a["ldx"], a["ldy"], a["ldr"], 0)
@@ -145,7 +145,9 @@ def test_product_status_of_one_kind():
     lib = moe.load_library()
     assert lib.moe_int8_linear(None, A, None, A, A, None, None, A, A, 1 << 20, None) == NULL
     assert lib.moe_int8_workspace_size(None, None) == NULL
-    assert moe.moe_int8_workspace_size(5, 100, 7) >= 5 * 112 + 5 * 4
+    assert moe.moe_int8_workspace_size(50, 100, 7) >= 50 * 112 + 50 * 4
+    assert moe.moe_int8_workspace_size(2, 100, 7) == 0     # quantised by the product itself
+    assert moe.moe_int8_workspace_size(2, 100, 7, 3) > 0
     with pytest.raises(moe.MoeError, match="dtypes"):
         moe.moe_int8_workspace_size(5, 100, 7, dtype="i8")
 
