@@ -176,20 +176,13 @@ struct TileAddr {
   }
 };
 
-// The product of two fragments by the accumulator's type: bf16, or (the same 16 bytes a
-// lane, of which a K slice of 64 bytes a row holds twice as many) 8-bit integers.
-DEV f32x16_t mma(bf16x8_t b, bf16x8_t a, f32x16_t c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, a, c, 0, 0, 0); }
-DEV i32x16_t mma(bf16x8_t b, bf16x8_t a, i32x16_t c) {
-  return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, b), __builtin_bit_cast(i32x4_t, a), c, 0, 0, 0);
-}
-
 // One of the two products of group g (bf::mma2).
-template <int NMB, bool FIRST = false, class Acc>
-DEV void mma1(const bf::Frags& f, Acc (&acc)[4][4], int g, int j) {
+template <int NMB, bool FIRST = false>
+DEV void mma1(const bf::Frags& f, f32x16_t (&acc)[4][4], int g, int j) {
   const int mb = bf::kGrpM[g], nb = bf::kGrpN[g] + j;
   if (mb >= NMB) return;
-  const Acc zero = {};
-  acc[mb][nb] = mma(f.b[nb], f.a[mb], FIRST ? zero : acc[mb][nb]);
+  const f32x16_t zero = {};
+  acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[nb], f.a[mb], FIRST ? zero : acc[mb][nb], 0, 0, 0);
 }
 
 // nsteps >= 1 slices.  issue(s, slot, i): load i of slice s into the slot at
@@ -198,8 +191,8 @@ DEV void mma1(const bf::Frags& f, Acc (&acc)[4][4], int g, int j) {
 // in every step).  The order of waits and reads is bf::mainloop's: in step s the
 // B loads of slice s + NS - 2 go out while k-half 0 is multiplied; then slice
 // s + 1 has landed, and the A loads of slice s + NS - 1 go out while k-half 1 is.
-template <int AL, int BL, int WTM, class Issue, class Acc>
-DEV void mainloop(uint32_t ring, int nsteps, Issue issue, Acc (&acc)[4][4], int wm, int wn, int lane) {
+template <int AL, int BL, int WTM, class Issue>
+DEV void mainloop(uint32_t ring, int nsteps, Issue issue, f32x16_t (&acc)[4][4], int wm, int wn, int lane) {
   constexpr int LA = kALoads<WTM>, L = LA + 4, NMB = WTM / 32, SB = kSlot<WTM> * 2, NS = kSlots<WTM>;
   auto addr = [&](int sl) { return ring + (uint32_t)sl * SB; };
 #pragma unroll
@@ -336,8 +329,8 @@ struct KcPart {
 
 // issue(h, addr, i): load i (the parts of A, then those of B) of half slice h to
 // addr; half slices past 2 nsteps may hold anything.
-template <int AL, int BL, int MB, int NB, bool SHORT, class Issue, class Acc>
-DEV void small_mainloop(uint32_t ring, int nsteps, Issue issue, Acc (&acc)[MB][NB], int wm, int wn, int lane) {
+template <int AL, int BL, int MB, int NB, bool SHORT, class Issue>
+DEV void small_mainloop(uint32_t ring, int nsteps, Issue issue, f32x16_t (&acc)[MB][NB], int wm, int wn, int lane) {
   using S = Small<MB, NB, SHORT>;
   constexpr uint32_t HALF = S::HALF, SB = S::SLOT, END = S::NS * SB;
   constexpr int L = 2 * S::PARTS, NS = S::NS;
@@ -358,7 +351,7 @@ DEV void small_mainloop(uint32_t ring, int nsteps, Issue issue, Acc (&acc)[MB][N
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[m][n][r] = 0;
+      for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.f;
   struct Frag {
     bf16x8_t a[4][MB], b[4][NB];
   } f0, f1;
@@ -385,7 +378,7 @@ DEV void small_mainloop(uint32_t ring, int nsteps, Issue issue, Acc (&acc)[MB][N
 #pragma unroll
     for (int j = 0; j < NM; ++j) {
       const int q = j / (MB * NB), m = j / NB % MB, n = j % NB;
-      acc[m][n] = mma(f.b[q][n], f.a[q][m], acc[m][n]);
+      acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[q][n], f.a[q][m], acc[m][n], 0, 0, 0);
       if constexpr (S::AHEAD) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll

@@ -57,23 +57,27 @@ struct Int8Params {
   int64_t part_ld;
 };
 struct Int8Shape {
-  int bm, bn, bk;           // bk: codes of a K slice
+  int bm, bn;
 };
-// Tiles: 256 x 256 (one workgroup a CU), 128 x 128 (two), 128 x 64 (three), 64 x 64 (five), and 64
-// x 64 with a deeper ring (two) for products with a workgroup a CU or less.  Us
-// without activation (rows x columns x K), in this order:
-//   4096 x 8192 x 2048     92   96  111  128  144
-//   8192 x 2048 x 1024     29   33   35   39   48
-//   4096 x 2048 x 8192     87   79  111  122  128
-//   1000 x 8192 x 2048     34   26   34   37   40
-//   1024 x 4096 x 4096     47   35   29   35   36
-//   300 x 4096 x 4096      45   32   25   22   19
-//   64 x 2048 x 8192       66   55   42   36   20
-//   8 experts of 325..2456 rows, 2048 x 1024         51   41   39   44   55
-//   64 experts of 2400 rows, 2048 x 2048 (268 MB)    74   80   74   72   76
-//   64 experts of 800 rows                           68   60   66   55   60
-constexpr int kInt8Tiles = 5;
-constexpr Int8Shape kInt8Shapes[kInt8Tiles] = {{256, 256, 64}, {128, 128, 128}, {128, 64, 128}, {64, 64, 128}, {64, 64, 128}};
+constexpr int kInt8Slice = 128;   // codes of a tile's K slice
+// Tiles: 256 x 256 (one workgroup a CU), 128 x 128 (two), 128 x 64 with a ring of three slots
+// (two) and of two (three), 64 x 64 with two (five) and with four (two).  The deeper rings
+// are for products with few workgroups a CU.  Us without activation (rows x columns x
+// K), in this order:
+//   8192 x 8192 x 8192    468  552  696  681  843  863
+//   4096 x 8192 x 2048     81   83  102   97  120  131
+//   8192 x 2048 x 1024     29   28   33   32   35   41
+//   4096 x 2048 x 8192     84   70   84   93  105  107
+//   1000 x 8192 x 2048     35   23   28   29   32   34
+//   2048 x 2048 x 2048     34   17   16   15   17   18
+//   300 x 4096 x 4096      50   25   14   21   19   16
+//   512 x 2048 x 2048      33   15   10   13   11    7
+//   64 x 2048 x 8192       73   42   21   36   32   15
+//   8 experts of 325..2456 rows, 2048 x 1024          -   36   42   35   40   47
+//   64 experts of 2400 rows, 2048 x 2048 (268 MB)     -   71   68   65   64   61
+//   64 experts of 800 rows                            -   56   65   63   53   57
+constexpr int kInt8Tiles = 6;
+constexpr Int8Shape kInt8Shapes[kInt8Tiles] = {{256, 256}, {128, 128}, {128, 64}, {128, 64}, {64, 64}, {64, 64}};
 hipError_t launch_int8_tiles(const Int8Params& P, bool bf16, int tile, hipStream_t st);
 // ks: waves that share a contraction (1, 2 or 4)
 hipError_t launch_int8_few(const Int8Params& P, bool bf16, int ks, hipStream_t st);

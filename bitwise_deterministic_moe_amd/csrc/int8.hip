@@ -8,12 +8,10 @@
 // The sum is exact in int32, so its order and its split have no effect on the
 // bits.  It is rounded to float32 once, and its products with the two scales once each.
 //
-// Tiles for many rows use the main loops of the bf16 operators (dense_bf16.h): a K
-// slice of 64 bytes a row is 64 codes, the fragments are the same 16 bytes a
-// lane, and v_mfma_i32_32x32x32_i8 takes the place of the bf16 instruction.
-// Few rows stream the weights into registers.
-#include "dense_bf16.h"
+// Tiles for many rows copy both operands by DMA into a ring of LDS slots and feed
+// v_mfma_i32_32x32x32_i8; few rows stream the weights into registers.
 #include "dense_epilogue.h"
+#include "gemm_bf16.h"
 #include "int8.h"
 
 namespace moedet {
@@ -356,12 +354,136 @@ struct Cols4 {
 }  // namespace
 
 // ----------------------------------------------------------------------- tiles
-constexpr int kInt8StageRow = 260;
+// Tiles of 64 MB x 64 NB: 4 waves in a 2 x 2 grid, each 32 MB x 32 NB as blocks of
+// v_mfma_i32_32x32x32_i8.
+//
+// K slices are 128 codes, so that a row's slice is one whole 128-byte line: the L2s serve
+// requests, and lines asked for in halves cost two.  (Copies alone, every CU reading
+// panels of 128 and 256 rows of 2 to 8 KB: 17.6 TB/s in pieces of 64 bytes, 25 in lines.
+// 4096 x 2048 x 8192 in tiles of 128 x 128: 75 and 70 us.)
+// In LDS a row is 128 bytes, and its 16-byte chunk c sits at c ^ ((row >> 1) & 7): the 16
+// lanes that one cycle of a ds_read_b128 serves then cover all 64 banks (no bank
+// conflicts counted in the loop).
+//
+// A ring of NS slots.  A slice is multiplied in four quarters of 32 codes, the fragments
+// of the next quarter being read meanwhile; before the last one the wave waits for its own loads
+// of slice s + 1 and for its reads of slice s and meets the other waves, then reads the first
+// quarter of slice s + 1 and loads slice s + NS into the slot of slice s.
+namespace line {
+constexpr int BK = 128;
+template <int MB, int NB>
+constexpr uint32_t kSlot = (uint32_t)(MB + NB) * 8192u;   // bytes: A, then B
+
+DEV int swz(int row) { return (row >> 1) & 7; }
+
+// An operand's loads: load i of wave w covers tile rows 8 (w NL + i) .. + 7.
+template <int NL>
+struct Op {
+  bf::i32x4_t rs;
+  uint32_t voff[NL];
+  DEV void init(const void* base, int64_t extent, int wave, int lane, int valid, int64_t ld) {
+    rs = bf::make_rsrc(base, (uint32_t)extent);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int row = 8 * (wave * NL + i) + (lane >> 3);
+      voff[i] = row < valid ? (uint32_t)(row * ld) + (uint32_t)((lane & 7) ^ swz(row)) * 16u : bf::kOOB;
+    }
+  }
+};
+// First code of a slice that this lane loads in even and in odd loads (NL is even).
+DEV int first_code(int lane, int odd) { return ((lane & 7) ^ swz(8 * odd + (lane >> 3))) * 16; }
+
+// issue(s, addr, i): load i (those of A, then of B) of slice s into the slot at addr; slices
+// at or past nsteps must read zeros (their loads keep the count of outstanding ones).
+template <int MB, int NB, int NS, class Issue>
+DEV void mainloop(uint32_t ring, int nsteps, Issue issue, i32x16_t (&acc)[MB][NB], int wm, int wn, int lane) {
+  constexpr int L = 2 * (MB + NB), R = MB + NB, M = MB * NB;
+  constexpr uint32_t SB = kSlot<MB, NB>;
+  // Loads issued in the last quarter; the others in the first one of the next slice.  All of
+  // them at once are as good where a quarter is short (8192^3 in tiles of 256 x 256 474 us,
+  // 468 spread; 128 x 128 552 and 568).
+  constexpr int LAST = M >= 16 ? L / 2 : L;
+  uint32_t aa[4], ba[4];
+  {
+    const int ra = wm * 32 * MB + (lane & 31), rb = wn * 32 * NB + (lane & 31), half = lane >> 5;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      aa[q] = ring + (uint32_t)(ra * 128 + (((2 * q + half) ^ swz(ra)) << 4));
+      ba[q] = ring + (uint32_t)MB * 8192u + (uint32_t)(rb * 128 + (((2 * q + half) ^ swz(rb)) << 4));
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+#pragma unroll
+    for (int i = 0; i < L; ++i) issue(s, ring + s * SB, i);
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[m][n][r] = 0;
+  struct Frag {
+    i32x4_t a[MB], b[NB];
+  } f[2];
+  // fragment j (those of A, then of B) of quarter q in slot sl
+  auto read = [&](Frag& g, int q, int sl, int j) __attribute__((always_inline)) {
+    const bool isa = j < MB;
+    const LDS_AS char* p = (const LDS_AS char*)(uintptr_t)((isa ? aa[q] : ba[q]) + (uint32_t)sl * SB);
+    const i32x4_t v = *(const LDS_AS i32x4_t*)(p + (isa ? j : j - MB) * 4096);
+    if (isa)
+      g.a[isa ? j : 0] = v;
+    else
+      g.b[isa ? 0 : j - MB] = v;
+  };
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 1) * L) : "memory");
+#pragma unroll
+  for (int j = 0; j < R; ++j) read(f[0], 0, 0, j);
+  auto step = [&](int s, int sl) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (q == 3) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * L) : "memory");
+#pragma unroll
+      for (int j = 0; j < M; ++j) {
+#pragma unroll
+        for (int k = j * R / M; k < (j + 1) * R / M; ++k) {
+          if (q < 3)
+            read(f[(q + 1) & 1], q + 1, sl, k);
+          else
+            read(f[0], 0, (sl + 1) % NS, k);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        acc[j / NB][j % NB] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f[q & 1].b[j % NB], f[q & 1].a[j / NB], acc[j / NB][j % NB], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (q == 3) {
+#pragma unroll
+          for (int k = j * LAST / M; k < (j + 1) * LAST / M; ++k) issue(s + NS, ring + sl * SB, k);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (LAST < L && q == 0 && s > 0) {
+#pragma unroll
+          for (int k = j * (L - LAST) / M; k < (j + 1) * (L - LAST) / M; ++k)
+            issue(s - 1 + NS, ring + (sl + NS - 1) % NS * SB, LAST + k);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+  };
+  int s = 0;
+#pragma unroll 1
+  for (; s + NS <= nsteps; s += NS) {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) step(s + j, j);
+  }
+#pragma unroll
+  for (int j = 0; j < NS - 1; ++j)
+    if (s + j < nsteps) step(s + j, j);
+  bf::block_barrier();
+}
+}  // namespace line
 
 // Row scales, column scales and bias of a tile of up to 256 x 256: thread i holds
 // those of row i and column i from before the main loop, and puts them into LDS
-// behind it.  (Loaded where they are used, they cost the 4096 x 2048 x 8192 product 20 us
-// a tile between the last slice and the end, against 11.)
+// behind it.  (Loaded where they are used, they cost a 256 x 256 tile 3.5 us.)
 struct TileScales {
   float sa, sb, bias;
   template <typename T>
@@ -379,173 +501,101 @@ struct TileScales {
   }
 };
 
-template <typename T, int WTM, bool GROUPS>
-__global__ __launch_bounds__(256) void int8_tile_kernel(Int8Params P) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[dn::kRingBytes<WTM> / 2];
-  constexpr int BM = 2 * WTM;
-  static_assert(64 * kInt8StageRow * 4 + 768 * 4 <= dn::kRingBytes<WTM>, "epilogue stage must fit in the ring");
-  Int8Tile t;
-  if (!int8_tile<GROUPS>(P, BM, 256, t)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, half = lane >> 5;
-  const uint32_t ring = bf::lds_base(lds);
-  constexpr int LA = dn::kALoads<WTM>;
-  constexpr uint32_t AB = dn::kAOper<WTM> * 2;
-  const int nvalid = P.d.N - t.n0 < 256 ? P.d.N - t.n0 : 256;
-  // pairs of codes as 16-bit elements
-  const int64_t K2 = P.d.K / 2, lda = P.lda / 2;
-  const int nsteps = (int)((K2 + dn::BK - 1) / dn::BK);
-  const int kc = dn::KcOp<LA>::chunk(lane) * 8;
-  dn::KcOp<LA> oa;
-  dn::KcOp<4> ob;
-  oa.init(P.a + t.m0 * P.lda, ((t.rows - 1) * lda + K2) * 2, wave, lane, t.rows, lda);
-  ob.init(P.b + ((int64_t)t.g * P.d.N + t.n0) * P.d.K, ((nvalid - 1) * K2 + K2) * 2, wave, lane, nvalid, K2);
-  TileScales ts;
-  ts.load<T>(P, t, tid);
-  i32x16_t acc[4][4];
-  dn::mainloop<dn::KC, dn::KC, WTM>(ring, nsteps, [&](int s, uint32_t st, int i) {
-    const bool live = s < nsteps;
-    const int ks = live ? s : 0;
-    const bool ok = live && ks * dn::BK + kc < K2;
-    if (i < LA)
-      oa.issue(st, wave, i, ok, (uint32_t)ks * 64u);
-    else
-      ob.issue(st + AB, wave, i - LA, ok, (uint32_t)ks * 64u);
-  }, acc, wm, wn, lane);
-  // The sums go through LDS in passes of 64 rows, so that a wave writes whole rows
-  // (and a row's scale is a scalar).  They are converted behind it: in front, the
-  // compiler converts all of them at once and spills.
-  int* stage = (int*)lds;
-  float* scales = (float*)(stage + 64 * kInt8StageRow);
-  ts.put(scales, tid);
-  const int64_t end = t.m0 + t.rows;
-  const int col = t.n0 + lane * 4;
-  f32x4_t sb, bias;
-#pragma unroll 1
-  for (int p = 0; 64 * p < t.rows; ++p) {
-#pragma unroll
-    for (int q = 0; q < 2 * WTM / 64; ++q) {
-      if (p != q) continue;
-#pragma unroll
-      for (int mb = 0; mb < WTM / 32; ++mb) {
-        const int r0 = wm * WTM + mb * 32 - 64 * q;
-        if (r0 < 0 || r0 >= 64) continue;
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const i32x16_t& a = acc[mb][nb];
-            *(i32x4_t*)(stage + (r0 + r32) * kInt8StageRow + wn * 128 + nb * 32 + 8 * i + 4 * half) =
-                i32x4_t{a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]};
-          }
-      }
-    }
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (p == 0) {
-      sb = *(const f32x4_t*)(scales + 256 + lane * 4);
-      bias = *(const f32x4_t*)(scales + 512 + lane * 4);
-    }
-#pragma unroll
-    for (int st = 0; st < 16; st += 4) {
-      float v[16];
-      const int m = 4 * st + wave;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const i32x4_t sv = *(const i32x4_t*)(stage + (m + 4 * i) * kInt8StageRow + lane * 4);
-        const float sa = scales[64 * p + m + 4 * i];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[4 * i + q] = __builtin_fmaf((float)sv[q] * sa, sb[q], bias[q]);
-      }
-      if (col >= P.d.N) continue;
-      emit<T, kFormLinear, 4, true, true>(P.d, 0, AtRows{t.m0 + 64 * p + m, end, 4, col}, v);
-    }
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  }
-}
+DEV void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Small tiles, 64 MB x 64 NB.  SHORT: a ring of two slots, so that two to five workgroups
-// share a CU and one's first loads and epilogue run beside another's slices.
+// WGS: workgroups that share a CU (its registers and LDS), so that one's first loads and
+// epilogue run beside another's slices.
 // A contraction split into S chunks (one group only): each workgroup leaves its sums in
 // the workspace, and int8_join_kernel adds them and runs the epilogue.  (The last workgroup
-// of a tile doing that, by a ticket, needs a fence across the XCDs in each: 37 x 2048 x
-// 8192 73 us, against 8 unsplit.)
-template <typename T, int MB, int NB, bool SHORT, bool GROUPS>
-__global__ __launch_bounds__(256) void int8_small_kernel(Int8Params P) {
-  using S = dn::Small<MB, NB, SHORT>;
-  constexpr int BM = 64 * MB, BN = 64 * NB, ROW = 64 * NB + 4;
-  constexpr int STAGE = (BM * ROW + 768) * 4;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[(S::RING > STAGE ? S::RING : STAGE) / 2];
+// of a tile doing that, by a ticket, needs a fence across the XCDs in each: 37 x 8192 x
+// 2048 73 us, against 8 unsplit.)
+template <typename T, int MB, int NB, int NS, int WGS, bool GROUPS>
+__global__ __launch_bounds__(256, WGS) void int8_tile_kernel(Int8Params P) {
+  constexpr int BM = 64 * MB, BN = 64 * NB, LA = 2 * MB, LB = 2 * NB;
+  // The sums go through LDS, so that a wave writes whole pieces of rows, in passes of PR
+  // rows (one where the tile fits).  They are converted behind it: in front, the compiler
+  // converts all of them at once and spills.
+  constexpr int PR = BM * BN > 128 * 128 ? 64 : BM, ROW = BN + 4;
+  constexpr int RING = NS * line::kSlot<MB, NB>, STAGE = (PR * ROW + 768) * 4;
+  __shared__ __attribute__((aligned(16))) int8_t lds[RING > STAGE ? RING : STAGE];
   Int8Tile t;
   if (!int8_tile<GROUPS>(P, BM, BN, t)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
-  const uint32_t ring = bf::lds_base(lds), own = (uint32_t)wave * 1024u;
   const int nvalid = P.d.N - t.n0 < BN ? P.d.N - t.n0 : BN;
-  const int64_t K2 = P.d.K / 2, lda = P.lda / 2;
-  int s0 = 0, nsteps = (int)((K2 + dn::SBK - 1) / dn::SBK);
+  const int K = (int)P.d.K;
+  int s0 = 0, nsteps = (K + line::BK - 1) / line::BK;
   if constexpr (!GROUPS) {
     const int all = nsteps, chunks = P.d.S;
     s0 = (int)((int64_t)t.chunk * all / chunks);
     nsteps = (int)((int64_t)(t.chunk + 1) * all / chunks) - s0;
   }
-  const int kc = dn::KcOp<1>::chunk(lane) * 8;
-  dn::KcPart<MB> oa;
-  dn::KcPart<NB> ob;
-  oa.init(P.a + t.m0 * P.lda, ((t.rows - 1) * lda + K2) * 2, wave, lane, t.rows, lda);
-  ob.init(P.b + ((int64_t)t.g * P.d.N + t.n0) * P.d.K, nvalid * K2 * 2, wave, lane, nvalid, K2);
+  line::Op<LA> oa;
+  line::Op<LB> ob;
+  oa.init(P.a + t.m0 * P.lda, (t.rows - 1) * P.lda + K, wave, lane, t.rows, P.lda);
+  ob.init(P.b + ((int64_t)t.g * P.d.N + t.n0) * K, (int64_t)nvalid * K, wave, lane, nvalid, K);
+  const int k0 = line::first_code(lane, 0), k1 = line::first_code(lane, 1);
   TileScales ts;
   ts.load<T>(P, t, tid);
   i32x16_t acc[MB][NB];
-  dn::small_mainloop<dn::KC, dn::KC, MB, NB, SHORT>(ring, nsteps, [&](int h, uint32_t at, int i) {
-    const bool live = h < 2 * nsteps;
-    const int ks = live ? 2 * s0 + h : 0;
-    const bool ok = live && ks * dn::BK + kc < K2;
-    if (i < MB)
-      bf::dma16(oa.rs, at + own, ok ? oa.voff[i < MB ? i : 0] : dn::kOOB, (uint32_t)ks * 64u);
-    else
-      bf::dma16(ob.rs, at + own, ok ? ob.voff[i < MB ? 0 : i - MB] : dn::kOOB, (uint32_t)ks * 64u);
+  line::mainloop<MB, NB, NS>(bf::lds_base(lds), nsteps, [&](int s, uint32_t st, int i) {
+    const bool live = s < nsteps, isa = i < LA;
+    const int ks = live ? (s0 + s) * line::BK : 0, j = isa ? i : i - LA;
+    const bool ok = live && ks + ((i & 1) ? k1 : k0) < K;
+    bf::dma16(isa ? oa.rs : ob.rs, st + (isa ? 0u : (uint32_t)MB * 8192u) + (uint32_t)(wave * (isa ? LA : LB) + j) * 1024u,
+              ok ? (isa ? oa.voff[isa ? j : 0] : ob.voff[isa ? 0 : j]) : bf::kOOB, (uint32_t)ks);
   }, acc, wm, wn, lane);
-  // through LDS, so that 16 lanes write 64 columns of a row
   int* stage = (int*)lds;
-  float* scales = (float*)(stage + BM * ROW);
+  float* scales = (float*)(stage + PR * ROW);
   ts.put(scales, tid);
-#pragma unroll
-  for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const i32x16_t& a = acc[mb][n];
-        *(i32x4_t*)(stage + (mb * 64 + wm * 32 + (lane & 31)) * ROW + 64 * n + wn * 32 + 8 * i + 4 * (lane >> 5)) =
-            i32x4_t{a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]};
-      }
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   const int c = (lane & 15) * 4, m = 4 * wave + (lane >> 4);
 #pragma unroll 1
-  for (int p = 0; p < MB * NB; ++p) {
-    const int mb = p / NB, n = p % NB, col = t.n0 + 64 * n + c;
-    if (col >= P.d.N) continue;
-    if constexpr (!GROUPS) {
-      if (P.d.S > 1) {
+  for (int pass = 0; pass < BM / PR && pass * PR < t.rows; ++pass) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = mb * 64 + m + 16 * i;
-          if (row < t.rows)
-            *(i32x4_t*)(P.part + ((int64_t)t.chunk * P.d.M + t.m0 + row) * P.part_ld + col) = *(const i32x4_t*)(stage + row * ROW + 64 * n + c);
-        }
-        continue;
+    for (int q = 0; q < BM / PR; ++q) {
+      if (pass != q) continue;
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        const int r0 = (wm * MB + mb) * 32 - q * PR;
+        if (r0 < 0 || r0 >= PR) continue;
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const i32x16_t& a = acc[mb][n];
+            *(i32x4_t*)(stage + (r0 + (lane & 31)) * ROW + (wn * NB + n) * 32 + 8 * i + 4 * (lane >> 5)) =
+                i32x4_t{a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]};
+          }
       }
     }
-    const f32x4_t sb = *(const f32x4_t*)(scales + 256 + 64 * n + c), bias = *(const f32x4_t*)(scales + 512 + 64 * n + c);
-    float v[16];
+    lds_barrier();
+    // 16 lanes a row: 64 columns of 64 rows a step
+#pragma unroll 1
+    for (int p = 0; p < PR / 64 * NB; ++p) {
+      const int r0 = p / NB * 64 + m, n = p % NB, col = t.n0 + 64 * n + c, row0 = pass * PR + r0;
+      if (col >= P.d.N) continue;
+      if constexpr (!GROUPS) {
+        if (P.d.S > 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const i32x4_t sv = *(const i32x4_t*)(stage + (mb * 64 + m + 16 * i) * ROW + 64 * n + c);
-      const float sa = scales[mb * 64 + m + 16 * i];
+          for (int i = 0; i < 4; ++i)
+            if (row0 + 16 * i < t.rows)
+              *(i32x4_t*)(P.part + ((int64_t)t.chunk * P.d.M + t.m0 + row0 + 16 * i) * P.part_ld + col) =
+                  *(const i32x4_t*)(stage + (r0 + 16 * i) * ROW + 64 * n + c);
+          continue;
+        }
+      }
+      const f32x4_t sb = *(const f32x4_t*)(scales + 256 + 64 * n + c), bias = *(const f32x4_t*)(scales + 512 + 64 * n + c);
+      float v[16];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[4 * i + q] = __builtin_fmaf((float)sv[q] * sa, sb[q], bias[q]);
+      for (int i = 0; i < 4; ++i) {
+        const i32x4_t sv = *(const i32x4_t*)(stage + (r0 + 16 * i) * ROW + 64 * n + c);
+        const float sa = scales[row0 + 16 * i];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[4 * i + q] = __builtin_fmaf((float)sv[q] * sa, sb[q], bias[q]);
+      }
+      emit<T, kFormLinear, 4, true, true>(P.d, 0, AtRows{t.m0 + row0, t.m0 + t.rows, 16, col}, v);
     }
-    emit<T, kFormLinear, 4, false, true>(P.d, 0, AtRows{t.m0 + mb * 64 + m, t.m0 + t.rows, 16, col}, v);
+    if (BM > PR) lds_barrier();
   }
 }
 
@@ -690,12 +740,13 @@ template <typename T, bool GROUPS>
 void tiles(const Int8Params& P, int tile, hipStream_t st) {
   const Int8Shape sh = kInt8Shapes[tile];
   const dim3 grid = int8_grid(P, sh.bm, sh.bn);
-  switch (tile) {
-    case 0: int8_tile_kernel<T, 128, GROUPS><<<grid, 256, 0, st>>>(P); break;
-    case 1: int8_small_kernel<T, 2, 2, true, GROUPS><<<grid, 256, 0, st>>>(P); break;
-    case 2: int8_small_kernel<T, 2, 1, true, GROUPS><<<grid, 256, 0, st>>>(P); break;
-    case 3: int8_small_kernel<T, 1, 1, true, GROUPS><<<grid, 256, 0, st>>>(P); break;
-    default: int8_small_kernel<T, 1, 1, false, GROUPS><<<grid, 256, 0, st>>>(P);
+  switch (tile) {   // kInt8Shapes
+    case 0: int8_tile_kernel<T, 4, 4, 2, 1, GROUPS><<<grid, 256, 0, st>>>(P); break;
+    case 1: int8_tile_kernel<T, 2, 2, 2, 2, GROUPS><<<grid, 256, 0, st>>>(P); break;
+    case 2: int8_tile_kernel<T, 2, 1, 3, 2, GROUPS><<<grid, 256, 0, st>>>(P); break;
+    case 3: int8_tile_kernel<T, 2, 1, 2, 3, GROUPS><<<grid, 256, 0, st>>>(P); break;
+    case 4: int8_tile_kernel<T, 1, 1, 2, 4, GROUPS><<<grid, 256, 0, st>>>(P); break;
+    default: int8_tile_kernel<T, 1, 1, 4, 2, GROUPS><<<grid, 256, 0, st>>>(P);
   }
   if (!GROUPS && P.d.S > 1) int8_join_kernel<T><<<(uint32_t)((P.d.M * ((P.d.N + 3) / 4) + 255) / 256), 256, 0, st>>>(P);
 }

@@ -36,12 +36,15 @@ struct TileCost {
   double alone, each, fixed;
   int shares;               // workgroups a CU
 };
-constexpr TileCost kTiles[kInt8Tiles] = {{0.57, 0.84, 15.0, 1}, {0.75, 0.53, 9.7, 2}, {0.58, 0.36, 5.8, 3}, {0.52, 0.223, 4.0, 5}, {0.29, 0.22, 3.4, 2}};
+constexpr TileCost kTiles[kInt8Tiles] = {{1.0, 1.45, 18.0, 1}, {0.52, 0.47, 8.5, 2}, {0.26, 0.27, 5.5, 2}, {0.46, 0.286, 6.3, 3}, {0.44, 0.2, 4.0, 5}, {0.24, 0.18, 3.3, 2}};
 
-double estimate(int i, double tiles, double steps) {
+double estimate(int i, double tiles, double steps, int act) {
   const TileCost& c = kTiles[i];
   const double per_cu = tiles / kCUs;
-  if (c.shares == 1) return (double)(int64_t)(per_cu + 0.999) * (c.fixed + steps * (per_cu <= 0.5 ? c.alone : c.each));
+  // a SiLU or GELU epilogue has nothing beside it here (4096 x 8192 x 2048 with GELU 98.5 us, with
+  // tiles of 128 x 128 95; without 89.6 and 87)
+  if (c.shares == 1)
+    return (double)(int64_t)(per_cu + 0.999) * (c.fixed + (act >= MOE_ACT_SILU ? 4.0 : 0.0) + steps * (per_cu <= 0.5 ? c.alone : c.each));
   const double full = per_cu / c.shares;   // rounds of a full CU
   const double slice = per_cu * c.each > c.alone ? per_cu * c.each : c.alone;
   return c.fixed * (full < 1 ? 1 : 0.4 + 0.6 * full) + steps * slice;
@@ -68,13 +71,12 @@ Choice choose(const moe_int8* p, int64_t K) {
     // experts leave half a tile each on average
     double mT = (double)((rows + sh.bm - 1) / sh.bm);
     if (groups > 1) mT = (double)rows / sh.bm + 0.5 * (double)(groups < rows ? groups : rows);
-    const int64_t steps = (K + sh.bk - 1) / sh.bk;
+    const int64_t steps = (K + kInt8Slice - 1) / kInt8Slice;
     for (int S = 1; S <= 8; S *= 2) {
       // the 64 x 64 tile of one matrix may be split while workgroups are few
       if (S > 1 && (i != kInt8Tiles - 1 || p->num_local || steps / S < 4 || mT * nT * S > 2 * kCUs)) break;
-      double t = estimate(i, mT * nT * S, (double)((steps + S - 1) / S));
-      // the sums written and read, and the join (64 x 2048 x 8192: 20 us whole, 12 in four chunks;
-      // 37 x 8192 x 2048: 8 and 10)
+      double t = estimate(i, mT * nT * S, (double)((steps + S - 1) / S), p->act);
+      // the sums written and read, and the join
       if (S > 1) t += 3.2 + (double)S * (double)rows * (double)N * 8.0 / 3e6;
       // the weights at 5.2 TB/s; of tiles that reach that, the quickest
       const double stream = (double)groups * (double)N * (double)K / 5.2e6;
