@@ -75,7 +75,8 @@ struct DropoutParams {
   int64_t ldadd;
   void* y;                 // contiguous
   const uint64_t* rng;     // {key, first counter}
-  uint64_t limit;          // a 32-bit word below it drops its element (2^32: all)
+  uint32_t limit;          // a word below it drops its element
+  bool all;                // every element is dropped (a limit of 2^32)
   float scale;
   uint64_t seed;
 };

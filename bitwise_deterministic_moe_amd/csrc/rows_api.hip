@@ -105,7 +105,9 @@ moe_status dropout(const void* x, const void* add, int dtype, int64_t rows, int6
   P.ldadd = ldadd;
   P.y = y;
   P.rng = rng;
-  P.limit = (uint64_t)std::nearbyint(p * 4294967296.0);
+  const uint64_t limit = (uint64_t)std::nearbyint(p * 4294967296.0);
+  P.limit = (uint32_t)limit;
+  P.all = limit >> 32;
   P.scale = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.f;
   P.seed = seed;
   return hip_status(launch_dropout(P, dtype == MOE_BF16, (hipStream_t)stream));
