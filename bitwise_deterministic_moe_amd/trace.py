@@ -44,6 +44,12 @@ quantised along the routed rows (moe_mx_quantize_wgrad).  The op-level
 trace fingerprints every encoded tensor and its scale buffer, as the pages
 do for low-precision runs; it also records dh's NVFP4 encoding (codes,
 block scales, tensor scale).
+With dropout=p the layer's output is dropped with probability p:
+    y = moe_dropout_fwd(y, p, rng);  dy of the layer = moe_dropout_bwd(dy, p, rng)
+(with block=True the routed output ym, before the down projection adds to it).
+rng holds a seed and the first counter of the step, step * ceil(tokens * d_model
+/ 4): the mask is a function of the seed and the step, so that a resumed run
+finds the continuous run's.
 Metrics (loss, gradient norms) are summed on the host in float64 in a fixed
 order, so they are deterministic too.
 """
@@ -56,10 +62,11 @@ import numpy as np
 import torch
 
 from . import (MXW_ACT_P, MXW_ROW, MXW_TOKEN, MoeError, Problem, TORCH_DTYPE, moe_bwd_dgrad_dprob,
-               moe_bwd_wgrad, moe_fingerprint, moe_fwd, moe_glu_bwd, moe_glu_fwd, moe_layernorm_bwd, moe_layernorm_fwd,
-               moe_linear_bwd, moe_linear_fwd, moe_mx_dgrad_fc1, moe_mx_dgrad_fc2, moe_mx_fwd_fc1,
-               moe_mx_fwd_fc2, moe_mx_quantize, moe_mx_quantize_t, moe_mx_quantize_wgrad, moe_mx_wgrad,
-               moe_nvfp4_quantize, moe_route, moe_router_bwd, moe_router_fwd, moe_sgd_step)
+               moe_bwd_wgrad, moe_dropout_bwd, moe_dropout_fwd, moe_fingerprint, moe_fwd, moe_glu_bwd, moe_glu_fwd,
+               moe_layernorm_bwd, moe_layernorm_fwd, moe_linear_bwd, moe_linear_fwd, moe_mx_dgrad_fc1,
+               moe_mx_dgrad_fc2, moe_mx_fwd_fc1, moe_mx_fwd_fc2, moe_mx_quantize, moe_mx_quantize_t,
+               moe_mx_quantize_wgrad, moe_mx_wgrad, moe_nvfp4_quantize, moe_route, moe_router_bwd, moe_router_fwd,
+               moe_sgd_step)
 
 BLOCK_WEIGHTS = ("nw", "nb", "wg", "wu", "wd", "bd")   # the dense operators' masters (block=True)
 LEVELS = {"metrics": 0, "phases": 1, "ops": 2}
@@ -204,12 +211,21 @@ def _mx(t, rows: int, cols: int):
     return moe_mx_quantize(t.reshape(rows, cols))
 
 
+def dropout_rng(cfg, step: int, seed: int) -> torch.Tensor:
+    """Key and first counter of a step's dropout."""
+    first = step * ((cfg.tokens * cfg.d_model + 3) // 4)
+    return torch.from_numpy(np.array([seed & 0xFFFFFFFFFFFFFFFF, first], dtype=np.uint64).view(np.int64)).cuda()
+
+
 def train_step(cfg, st: TrainState, tracer: Tracer, hook: Optional[Callable] = None, mx: bool = False,
-               block: bool = False):
+               block: bool = False, dropout: float = 0.0, dropout_seed: int = 0):
     """One step at st.step; advances st.step.  ``hook(step, where, st)`` may
     change the state at "before_forward" (a fault injector for tests).  With
     ``mx`` every expert GEMM runs on MXFP8 operands; with ``block`` the dense
-    operators around the layer take part."""
+    operators around the layer take part; with ``dropout`` the layer's output is
+    dropped with that probability, under ``dropout_seed``."""
+    if not 0.0 <= dropout <= 1.0:
+        raise MoeError(f"dropout must be in 0..1, got {dropout}")
     if cfg.combine != 1 or cfg.num_local != cfg.num_experts:
         raise MoeError("the train step covers the full layer (token layout, all experts local)")
     if mx and (cfg.dtype != "bf16" or cfg.d_model > 2048 or cfg.d_ffn > 2048):
@@ -238,10 +254,14 @@ def train_step(cfg, st: TrainState, tracer: Tracer, hook: Optional[Callable] = N
         y = moe_mx_fwd_fc2(prob, routing, fwd_enc["act"], fwd_enc["w2t"])
     else:
         routing, h, y = moe_fwd(prob, logits, x, R["w1"], R["w2"])
+    ym, dy_block = y, dy
+    if dropout:
+        rng = dropout_rng(cfg, s, dropout_seed)
+        yd = y = moe_dropout_fwd(ym, dropout, rng)
+        dy = moe_dropout_bwd(dy, dropout, rng)         # of the layer's output from here on
     if block:
-        ym = y
         a, g, u = moe_glu_fwd(x, R["wg"], R["wu"], save=True)
-        y, _ = moe_linear_fwd(a, R["wd"], R["bd"], residual=ym)
+        y, _ = moe_linear_fwd(a, R["wd"], R["bd"], residual=y)
     if mx:
         el, D, F = cfg.num_local, cfg.d_model, cfg.d_ffn
         enc["dy"], enc["w2"] = _mx(dy, cfg.tokens, D), _mx(R["w2"], el * F, D)
@@ -258,7 +278,7 @@ def train_step(cfg, st: TrainState, tracer: Tracer, hook: Optional[Callable] = N
         dw1, dw2 = moe_bwd_wgrad(prob, routing, x, dy, h, dh)
     dlogits, dwr, dxr = moe_router_bwd(prob, routing, dprob, batch, R["wr"])
     if block:
-        da, dwd, dbd = moe_linear_bwd(dy, a, R["wd"])
+        da, dwd, dbd = moe_linear_bwd(dy_block, a, R["wd"])
         dxn, dwg, dwu = moe_glu_bwd(da, x, R["wg"], R["wu"], g, u, dx_add=dx)
         dxb, dnw, dnb = moe_layernorm_bwd(dxn, batch, R["nw"], mean, rstd, dx_add=dxr)
     torch.cuda.synchronize()
@@ -276,18 +296,23 @@ def train_step(cfg, st: TrainState, tracer: Tracer, hook: Optional[Callable] = N
         for n, op in (("act", "moe_mx_quantize"), ("w2t", "moe_mx_quantize_t")):
             T.tensor(s, "forward", op, f"{n}_codes", fwd_enc[n][0], 2)
             T.tensor(s, "forward", op, f"{n}_scales", fwd_enc[n][1], 2)
-        T.tensor(s, "forward", "moe_mx_fwd_fc2", "y", y, 1)
+        T.tensor(s, "forward", "moe_mx_fwd_fc2", "y", ym, 1)
     else:
         if block:
             for n, t in (("xn", x), ("mean", mean), ("rstd", rstd)):
                 T.tensor(s, "forward", "moe_layernorm_fwd", n, t, 2)
         T.tensor(s, "forward", "moe_fwd", "h", h, 2)
-        T.tensor(s, "forward", "moe_fwd", "y", ym if block else y, 1)
+        T.tensor(s, "forward", "moe_fwd", "y", ym, 1)
+    if dropout:
+        T.tensor(s, "forward", "moe_dropout_fwd", "y_dropped", yd, 1)
+    if not mx:
         if block:
             for n, t in (("g", g), ("u", u), ("a", a)):
                 T.tensor(s, "forward", "moe_glu_fwd", n, t, 2)
             T.tensor(s, "forward", "moe_linear_fwd", "y_block", y, 1)
     # backward
+    if dropout:
+        T.tensor(s, "backward", "moe_dropout_bwd", "dy_dropped", dy, 2)
     if mx:
         for n in ("dy", "w2"):
             T.tensor(s, "backward", "moe_mx_quantize", f"{n}_codes", enc[n][0], 2)
@@ -330,8 +355,8 @@ def train_step(cfg, st: TrainState, tracer: Tracer, hook: Optional[Callable] = N
         T.tensor(s, "backward", "moe_layernorm_bwd", "dnw", dnw, 1)
         T.tensor(s, "backward", "moe_layernorm_bwd", "dnb", dnb, 1)
     # end-to-end metrics of the step (host float64 in a fixed order)
-    yd = (y.double() * dy.double()).cpu().numpy().ravel()
-    T.metric(s, "loss", float(math.fsum(yd.tolist())) if yd.size < 1 << 21 else float(np.sum(yd)))
+    terms = (y.double() * dy_block.double()).cpu().numpy().ravel()
+    T.metric(s, "loss", float(math.fsum(terms.tolist())) if terms.size < 1 << 21 else float(np.sum(terms)))
     grads = {"w1": dw1, "w2": dw2, "wr": dwr}
     if block:
         grads.update(nw=dnw, nb=dnb, wg=dwg, wu=dwu, wd=dwd, bd=dbd)
@@ -347,12 +372,13 @@ def train_step(cfg, st: TrainState, tracer: Tracer, hook: Optional[Callable] = N
 
 
 def run(cfg, steps: int, level: str = "phases", window: Optional[range] = None, st: Optional[TrainState] = None,
-        hook: Optional[Callable] = None, lr: float = 0.05, mx: bool = False, block: bool = False):
+        hook: Optional[Callable] = None, lr: float = 0.05, mx: bool = False, block: bool = False, dropout: float = 0.0,
+        dropout_seed: int = 0):
     """Train from st (or the initial state) until st.step == steps."""
     st = st or initial_state(cfg, lr, block)
     tr = Tracer(level, window)
     while st.step < steps:
-        train_step(cfg, st, tr, hook, mx, block)
+        train_step(cfg, st, tr, hook, mx, block, dropout, dropout_seed)
     return st, tr
 
 
@@ -403,6 +429,8 @@ def main(argv=None):
     ap.add_argument("--mx", action="store_true", help="every expert GEMM on MXFP8 operands (bf16 layers)")
     ap.add_argument("--block", action="store_true", help="with the dense operators around the layer: norm, gated shared "
                     "expert, down projection")
+    ap.add_argument("--dropout", type=float, default=0.0, help="probability of dropping the layer's output elements")
+    ap.add_argument("--dropout-seed", type=int, default=0)
     a = ap.parse_args(argv)
     if a.compare:
         d = first_divergence(Tracer.load(a.compare[0]), Tracer.load(a.compare[1]))
@@ -410,7 +438,7 @@ def main(argv=None):
                                                  "b": d[2] and d[2].__dict__}))
         return
     from synth import CONFIGS
-    _, tr = run(CONFIGS[a.config], a.steps, a.level, mx=a.mx, block=a.block)
+    _, tr = run(CONFIGS[a.config], a.steps, a.level, mx=a.mx, block=a.block, dropout=a.dropout, dropout_seed=a.dropout_seed)
     if a.out:
         tr.save(a.out)
     print(json.dumps({"records": len(tr.records), "steps": a.steps, "level": a.level}))
