@@ -1448,34 +1448,37 @@ def moe_int8_workspace_size(rows: int, d_in: int, d_out: int, num_local: int = 0
 
 def _int8(what, fn, x, w_codes, w_scales, x_scales, bias, residual, offsets, act, out_dtype, y, ws, seed):
     a = _act_code(act, what)
-    codes = x.dtype is torch.int8
+    xd, xs, wsh = x.dtype, x.shape, w_codes.shape
+    codes = xd is torch.int8
     xc = 6 if codes else _storage(x, what)
-    if x.dim() == 0 or x.shape[-1] < 1:
-        raise MoeError(f"{what}: x needs columns, got {tuple(x.shape)}")
+    if not xs or xs[-1] < 1:
+        raise MoeError(f"{what}: x needs columns, got {tuple(xs)}")
     if codes != (x_scales is not None):
         raise MoeError(f"{what}: int8 codes x and x_scales are given together")
-    d = x.shape[-1]
-    rows, ldx = _mat(x, d, x.dtype, what + " x")
-    if w_codes.dtype is not torch.int8 or w_codes.dim() != (2 if offsets is None else 3) or not w_codes.is_contiguous() \
-            or w_codes.shape[-1] != _up16(d) or w_codes.shape[-2] < 1:
+    d = xs[-1]
+    rows, ldx = _mat(x, d, xd, what + " x")
+    if w_codes.dtype is not torch.int8 or len(wsh) != (2 if offsets is None else 3) or wsh[-1] != _up16(d) or wsh[-2] < 1 \
+            or not w_codes.is_contiguous():
         raise MoeError(f"{what}: w_codes must be contiguous int8 {'' if offsets is None else 'experts, '}"
-                       f"[d_out, {_up16(d)}], got {w_codes.dtype} {tuple(w_codes.shape)}")
-    f = w_codes.shape[-2]
-    local = 0
+                       f"[d_out, {_up16(d)}], got {w_codes.dtype} {tuple(wsh)}")
+    f = wsh[-2]
+    local, last = 0, residual
     if offsets is not None:
-        local = w_codes.shape[0]
+        local, last = wsh[0], offsets
         if local < 1:
             raise MoeError(f"{what}: w_codes without experts")
         _need(offsets, local + 1, torch.int32, what + " offsets")
-        if x.dim() != 2:
-            raise MoeError(f"{what}: x must be a matrix of rows sorted by expert, got {tuple(x.shape)}")
+        if len(xs) != 2:
+            raise MoeError(f"{what}: x must be a matrix of rows sorted by expert, got {tuple(xs)}")
     _need(w_scales, (local or 1) * f, torch.float32, what + " w_scales")
     if codes:
         _need(x_scales, rows, torch.float32, what + " x_scales")
-        dt = out_dtype or (y.dtype if y is not None else torch.bfloat16)
+    dt = out_dtype or (y.dtype if y is not None else torch.bfloat16 if codes else xd)
+    if dt is torch.bfloat16:
+        yc = 1
+    elif dt is torch.float32:
+        yc = 0
     else:
-        dt = out_dtype or (y.dtype if y is not None else x.dtype)
-    if dt is not torch.bfloat16 and dt is not torch.float32:
         raise MoeError(f"{what}: the output is float32 or bfloat16, not {dt}")
     if bias is not None:
         _need(bias, (local or 1) * f, dt, what + " bias")
@@ -1484,11 +1487,12 @@ def _int8(what, fn, x, w_codes, w_scales, x_scales, bias, residual, offsets, act
         y, ldy = _new(x, f, dt), f
     else:
         ldy = _mat(y, f, dt, what + " y", rows)[1]
-    c, need = _int8_plan(rows, d, f, local, xc, _TORCH_TO_CODE[dt], a, ldx, ldy, ldr, seed)
-    ws, nb = _dense_ws(need, ws, x)
-    last = _ptr(residual) if offsets is None else _ptr(offsets)
-    _run(what, fn, (c, _ptr(x), _ptr(x_scales), _ptr(w_codes), _ptr(w_scales), _ptr(bias), last, _ptr(y), _ptr(ws), nb), x,
-         x_scales, w_codes, w_scales, bias, residual, offsets, y, ws)
+    c, need = _int8_plan(rows, d, f, local, xc, yc, a, ldx, ldy, ldr, seed)
+    nb = 0
+    if ws is not None or need:
+        ws, nb = _dense_ws(need, ws, x)
+    _run(what, fn, (c, _ptr(x), _ptr(x_scales), _ptr(w_codes), _ptr(w_scales), _ptr(bias), _ptr(last), _ptr(y), _ptr(ws), nb), x,
+         x_scales, w_codes, w_scales, bias, last, y, ws)
     return y
 
 

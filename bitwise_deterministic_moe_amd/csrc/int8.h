@@ -34,7 +34,9 @@ struct Int8QuantTParams {
 };
 hipError_t launch_int8_quantize_t(const Int8QuantTParams& P, bool bf16, hipStream_t st);
 
-// Few rows that the product itself quantises, into LDS.
+// Rows that the few-row kernel quantises itself, into LDS: of one matrix up to this many (every
+// workgroup quantises all of them), of experts a workgroup's up to 16; their codes fit
+// kInt8FusedBytes, which leaves room for four workgroups a CU.
 constexpr int kInt8FusedRows = 4, kInt8FusedBytes = 32768;
 
 // y[m, n] = act(sa[m] sb[n] sum_k a[m, k] b[n, k] + bias[n]) + add[m, n], in

@@ -626,16 +626,16 @@ __global__ __launch_bounds__(256) void int8_join_kernel(Int8Params P) {
 // memory).  A workgroup's four waves are 4 / ks neighbouring blocks of weight rows, each
 // streamed by ks waves that take its steps in turn and whose sums meet in LDS.  A
 // lane ends with four neighbouring columns of one row.
-// FUSED: x is not yet quantised; every workgroup does that itself, into LDS, while its
-// first weights are on the way (1 x 2048 x 2048: a launch of 3.9 us saved).
+// FUSED: x is not yet quantised; every workgroup does that itself for its rows, into LDS,
+// while its first weights are on the way: a launch of 4 to 5 us saved (1 x 2048 x 2048 5.8
+// us, 3.9 and 4.4 in two launches).
 constexpr int kFewWaves = 4, kFewDepth = 8;
 template <typename T, bool GROUPS, bool FUSED>
 __global__ __launch_bounds__(64 * kFewWaves) void int8_few_kernel(Int8Params P, int ks) {
-  static_assert(!(GROUPS && FUSED), "rows to quantise are those of one matrix");
   constexpr int NT = 64 * kFewWaves;
   __shared__ __attribute__((aligned(16))) i32x4_t s_acc[NT];
   __shared__ __attribute__((aligned(16))) int8_t s_x[FUSED ? kInt8FusedBytes : 16];
-  __shared__ uint32_t s_top[kInt8FusedRows];
+  __shared__ uint32_t s_top[16];
   Int8Tile t;
   if (!int8_tile<GROUPS>(P, 16, 16 * kFewWaves / ks, t)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -677,7 +677,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void int8_few_kernel(Int8Params P, 
   if constexpr (FUSED) {
     constexpr int V = Vec<T>::N;
     const int per = K / V, vecs = t.rows * per;
-    if (tid < kInt8FusedRows) s_top[tid] = 0u;
+    if (tid < 16) s_top[tid] = 0u;
     __syncthreads();
     auto get = [&](int v, int row) __attribute__((always_inline)) {
       const int c = (v - row * per) * V, left = P.xcols - c;
@@ -751,6 +751,14 @@ void tiles(const Int8Params& P, int tile, hipStream_t st) {
   if (!GROUPS && P.d.S > 1) int8_join_kernel<T><<<(uint32_t)((P.d.M * ((P.d.N + 3) / 4) + 255) / 256), 256, 0, st>>>(P);
 }
 
+template <typename T, bool FUSED>
+void few(const Int8Params& P, dim3 grid, int ks, hipStream_t st) {
+  if (P.offsets)
+    int8_few_kernel<T, true, FUSED><<<grid, 64 * kFewWaves, 0, st>>>(P, ks);
+  else
+    int8_few_kernel<T, false, FUSED><<<grid, 64 * kFewWaves, 0, st>>>(P, ks);
+}
+
 }  // namespace
 
 hipError_t launch_int8_tiles(const Int8Params& P, bool bf16, int tile, hipStream_t st) {
@@ -763,22 +771,10 @@ hipError_t launch_int8_tiles(const Int8Params& P, bool bf16, int tile, hipStream
 
 hipError_t launch_int8_few(const Int8Params& P, bool bf16, int ks, hipStream_t st) {
   const dim3 grid = int8_grid(P, 16, 16 * kFewWaves / ks);
-  constexpr int NT = 64 * kFewWaves;
-  if (bf16) {
-    if (P.x)
-      int8_few_kernel<uint16_t, false, true><<<grid, NT, 0, st>>>(P, ks);
-    else if (P.offsets)
-      int8_few_kernel<uint16_t, true, false><<<grid, NT, 0, st>>>(P, ks);
-    else
-      int8_few_kernel<uint16_t, false, false><<<grid, NT, 0, st>>>(P, ks);
-  } else {
-    if (P.x)
-      int8_few_kernel<float, false, true><<<grid, NT, 0, st>>>(P, ks);
-    else if (P.offsets)
-      int8_few_kernel<float, true, false><<<grid, NT, 0, st>>>(P, ks);
-    else
-      int8_few_kernel<float, false, false><<<grid, NT, 0, st>>>(P, ks);
-  }
+  if (bf16)
+    P.x ? few<uint16_t, true>(P, grid, ks, st) : few<uint16_t, false>(P, grid, ks, st);
+  else
+    P.x ? few<float, true>(P, grid, ks, st) : few<float, false>(P, grid, ks, st);
   return hipGetLastError();
 }
 

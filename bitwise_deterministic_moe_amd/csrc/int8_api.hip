@@ -61,7 +61,7 @@ Choice choose(const moe_int8* p, int64_t K) {
     // 2048 x 2048: 17.8 and 19.8 us; 1 x 2048 x 2048: 8 and 4.5)
     const int64_t waves = (N + 15) / 16 * (p->num_local ? rows : 1);
     best.ks = waves >= 2048 ? 1 : 4;
-    best.fused = !p->num_local && p->x_dtype == p->dtype && rows <= kInt8FusedRows && rows * K <= kInt8FusedBytes;
+    best.fused = p->x_dtype == p->dtype && (p->num_local || rows <= kInt8FusedRows) && (p->num_local ? 16 : rows) * K <= kInt8FusedBytes;
     return best;
   }
   double least = -1;

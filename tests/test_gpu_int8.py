@@ -213,6 +213,7 @@ EXPERTS = [  # rows of each expert (cycled), experts, K, F, rows behind the last
     ([1], 22, 64, 48, 0), ([0, 1, 0, 3], 512, 96, 40, 5), ([0], 7, 64, 64, 9), ([5, 0, 17, 40], 9, 130, 70, 3), ([16], 33, 256, 257, 0),
     ([300, 2, 0, 65], 4, 200, 300, 20), ([64, 100, 1], 12, 64, 520, 1), ([1000, 24], 2, 320, 260, 0), ([31, 33], 1024, 32, 24, 2),
     ([700], 1, 100, 100, 7), ([129, 500, 0], 6, 1100, 140, 0), ([1], 3, 4096, 100, 0),
+    ([0, 20, 0, 0, 0, 0, 0, 1], 40, 2048, 72, 2), ([2, 0, 17], 30, 2040, 33, 1), ([3, 0], 9, 2064, 48, 1), ([1], 300, 64, 1500, 2),
 ]
 
 

@@ -147,7 +147,8 @@ def test_product_status_of_one_kind():
     assert lib.moe_int8_workspace_size(None, None) == NULL
     assert moe.moe_int8_workspace_size(50, 100, 7) >= 50 * 112 + 50 * 4
     assert moe.moe_int8_workspace_size(2, 100, 7) == 0     # quantised by the product itself
-    assert moe.moe_int8_workspace_size(2, 100, 7, 3) > 0
+    assert moe.moe_int8_workspace_size(2, 100, 7, 3) == 0
+    assert moe.moe_int8_workspace_size(2, 3000, 7, 3) > 0
     with pytest.raises(moe.MoeError, match="dtypes"):
         moe.moe_int8_workspace_size(5, 100, 7, dtype="i8")
 
