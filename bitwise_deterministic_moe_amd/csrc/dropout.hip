@@ -108,6 +108,7 @@ static hipError_t launch_form(const DropoutParams& P, hipStream_t st) {
   const int form = flat ? kFlat : P.cols % Vec<T>::N == 0 ? kRowVecs : kElements;
   const int64_t per = 256 * (form == kElements ? 4 : Vec<T>::N);
   const int64_t grid = (n + per - 1) / per;
+  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
   if (form == kFlat)
     dropout_kernel<T, kFlat><<<grid, 256, 0, st>>>(P, n);
   else if (form == kRowVecs)

@@ -148,16 +148,17 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(Int8QuantParams P) {
 }
 
 hipError_t launch_int8_quantize(const Int8QuantParams& P, bool bf16, hipStream_t st) {
-  const int V = bf16 ? 8 : 4;
-  // a wave a row while it keeps the row in registers
-  if (P.cols16 / V <= 64 * kQuantKeep) {
-    const int64_t grid = grid_for_units((P.rows + 3) / 4);
+  // a wave a row while it keeps the row in registers (several rows a wave are no faster: 4096 x
+  // 2048 bf16 7.3 us, 8.0 with four)
+  const bool wave = P.cols16 / (bf16 ? 8 : 4) <= 64 * kQuantKeep;
+  const int64_t grid = grid_for_units(wave ? (P.rows + 3) / 4 : P.rows);
+  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
+  if (wave) {
     if (bf16)
       int8_quantize_kernel<uint16_t, 64><<<grid, 256, 0, st>>>(P);
     else
       int8_quantize_kernel<float, 64><<<grid, 256, 0, st>>>(P);
   } else {
-    const int64_t grid = grid_for_units(P.rows);
     if (bf16)
       int8_quantize_kernel<uint16_t, 256><<<grid, 256, 0, st>>>(P);
     else

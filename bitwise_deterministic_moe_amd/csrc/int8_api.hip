@@ -12,9 +12,10 @@ namespace {
 constexpr size_t kWsAlign = 256;
 constexpr int64_t kMaxLd = (int64_t)1 << 20;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
-constexpr int64_t kMaxUnits = ((int64_t)1 << 24) - 8;
 
-moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+moe_status hip_status(hipError_t e) {
+  return e == hipSuccess ? MOE_OK : e == hipErrorInvalidConfiguration ? MOE_ERR_SHAPE : MOE_ERR_HIP;
+}
 size_t align_up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 int size_of(int dtype) { return dtype == MOE_F32 ? 4 : dtype == MOE_BF16 ? 2 : 1; }
@@ -109,7 +110,7 @@ moe_status check(const moe_int8* p) {
   if (p->num_local < 0 || p->num_local > kInt8MaxGroups) return MOE_ERR_SHAPE;
   if (p->ldx < p->d_in || p->ldx >= kMaxLd || p->ldy < p->d_out || p->ldy >= kMaxLd || p->ldr < 0 || p->ldr >= kMaxLd) return MOE_ERR_SHAPE;
   if (p->x_dtype == MOE_I8 && (p->d_in % 16 || p->ldx % 16)) return MOE_ERR_SHAPE;
-  if (units(p, choose(p, up16(p->d_in))) > kMaxUnits) return MOE_ERR_SHAPE;
+  if (units(p, choose(p, up16(p->d_in))) > kMaxGrid) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 
@@ -193,7 +194,8 @@ moe_status product(const moe_int8* p, const void* x, const float* x_scales, cons
     Q.codes = (int8_t*)ws;
     Q.scales = (float*)((char*)ws + w.scales);
     Q.seed = p->debug_shuffle_seed;
-    if (launch_int8_quantize(Q, p->x_dtype == MOE_BF16, st) != hipSuccess) return MOE_ERR_HIP;
+    const hipError_t e = launch_int8_quantize(Q, p->x_dtype == MOE_BF16, st);
+    if (e != hipSuccess) return hip_status(e);
     P.a = Q.codes;
     P.lda = K;
     P.sa = Q.scales;
@@ -230,7 +232,8 @@ MOE_API moe_status moe_int8_quantize_t(const void* w, moe_dtype dtype, int64_t b
                                        int8_t* codes, float* scales, uint64_t debug_shuffle_seed, void* stream) {
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_DTYPE;
   if (batch < 0 || rows < 1 || rows > kInt8MaxK || cols < 1 || cols >= kMaxLd) return MOE_ERR_SHAPE;
-  if (batch * (double)rows * (double)cols > (double)kMaxElems || batch * (double)((cols + 63) / 64) > (double)kMaxUnits)
+  if (batch * (double)rows * (double)cols > (double)kMaxElems ||
+      batch * (double)((cols + 63) / 64) > (double)(kMaxGrid / 2))   // workgroups of 512 threads
     return MOE_ERR_SHAPE;
   if (batch == 0) return MOE_OK;
   if (!w || !codes || !scales) return MOE_ERR_NULL;

@@ -14,6 +14,8 @@ constexpr int64_t kManyWgradTiles = 8192;  // weight-gradient tiles above which 
 
 // Grid size (a multiple of the 8 XCDs) for an upper bound on work units.
 inline int64_t grid_for_units(int64_t U_max) { return ((U_max + 7) / 8) * 8; }
+// Most workgroups of 256 threads that one launch takes (threads are counted in 32 bits).
+constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 8;
 // grid for map_unit_rounds
 inline int64_t grid_for_unit_rounds(int64_t U_max) { return grid_for_units(U_max) + 8; }
 

@@ -7,6 +7,9 @@
 
 namespace moedet {
 
+// The launchers below return hipErrorInvalidConfiguration, with nothing enqueued, for more
+// than kMaxGrid workgroups.
+
 // ---------------------------------------------------------------------- sort
 constexpr int kSortMaxLocal = 1024;   // experts of a sort
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;

@@ -333,6 +333,7 @@ hipError_t launch_permute(const RowsParams& P, int es, hipStream_t st) {
   int64_t S = groups >= 512 ? 1 : (512 + groups - 1) / groups;
   if (S > P.k) S = P.k;
   const int64_t grid = grid_for_units(groups * S);
+  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
   if (L < 64)
     permute_kernel<false, false><<<grid, 256, 0, st>>>(P, es, L, (int)S);
   else if (past_cache(P, es))
@@ -346,6 +347,7 @@ template <typename T>
 static hipError_t launch_sum(const RowsParams& P, hipStream_t st) {
   const int L = row_threads((P.cols + Vec<T>::N - 1) / Vec<T>::N, 256);
   const int64_t grid = grid_for_units((P.tokens + 256 / L - 1) / (256 / L));
+  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
   if (L < 64)
     unpermute_narrow_kernel<T><<<grid, 256, 0, st>>>(P, L);
   else if (past_cache(P, sizeof(T)))
@@ -361,6 +363,7 @@ hipError_t launch_unpermute(const RowsParams& P, bool bf16, hipStream_t st) {
 template <typename T>
 static hipError_t launch_bwd(const RowsParams& P, hipStream_t st) {
   const int64_t grid = grid_for_units((P.tokens * P.k + 3) / 4);
+  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
   if (past_cache(P, sizeof(T)))
     unpermute_bwd_kernel<T, true><<<grid, 256, 0, st>>>(P);
   else

@@ -14,7 +14,9 @@ constexpr size_t kWsAlign = 256;
 constexpr int64_t kMaxCols = (int64_t)1 << 24;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 
-moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+moe_status hip_status(hipError_t e) {
+  return e == hipSuccess ? MOE_OK : e == hipErrorInvalidConfiguration ? MOE_ERR_SHAPE : MOE_ERR_HIP;
+}
 
 int elem_bytes(int dtype) {
   switch (dtype) {

@@ -841,7 +841,9 @@ moe_status moe_glu_bwd(const moe_dense* p, const void* da, const void* x, const 
  * multiples of the element size; token matrices have a row distance (ld, in
  * elements, at least cols) where a call says so; row matrices are contiguous
  * [nrows, cols], and rows that no slot names stay as they are.  tokens * top_k
- * is below 2^31, cols at most 2^24, every matrix at most 2^40 elements.
+ * is below 2^31, cols at most 2^24, every matrix at most 2^40 elements; a
+ * call that would take more than 2^24 workgroups is refused, MOE_ERR_SHAPE (none
+ * of fewer than 16 million tokens and 64 million slots does).
  * Outputs must not overlap inputs, but where a call says so. */
 
 /* Workspace bytes of moe_sort (0 for few slots).  Errors: MOE_ERR_SHAPE, MOE_ERR_NULL. */
@@ -924,7 +926,8 @@ moe_status moe_unpermute_bwd(const void* dy, int64_t lddy, const void* rows, moe
 /* Codes and scales of the rows of x.
  *   x        DEVICE [rows, cols], row distance ldx, MOE_F32 or MOE_BF16
  *   codes    DEVICE int8 [rows, K16] output, 16-byte aligned;  scales  DEVICE float[rows] output
- * Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_NULL before anything is
+ * A call that would take more than 2^24 workgroups (2^23 of moe_int8_quantize_t) is
+ * refused.  Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_NULL before anything is
  * enqueued; MOE_ERR_HIP for a launch failure. */
 moe_status moe_int8_quantize(const void* x, moe_dtype dtype, int64_t rows, int64_t cols, int64_t ldx, int8_t* codes,
                              float* scales, uint64_t debug_shuffle_seed, void* stream);
@@ -1017,7 +1020,8 @@ moe_status moe_int8_experts(const moe_int8* p, const void* x, const float* x_sca
  *             kernel runs, so a captured graph takes new ones at each replay
  *   y         DEVICE [rows,cols] contiguous, output; may be x or the residual
  *             (with a row distance of cols)
- * rows * ld is at most 2^40.  Base addresses are multiples of the element size.
+ * rows * ld is at most 2^40, and a call that would take more than 2^24 workgroups of
+ * 1024 elements is refused, MOE_ERR_SHAPE.  Base addresses are multiples of the element size.
  * Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_NULL before anything is
  * enqueued; MOE_ERR_HIP for a launch failure. */
 moe_status moe_dropout_fwd(const void* x, const void* residual, moe_dtype dtype, int64_t rows, int64_t cols,

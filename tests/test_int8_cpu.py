@@ -129,6 +129,7 @@ CASES = [
     (NULL, dict(y=None)), (NULL, dict(wk=None)), (WS, dict(nb=16)), (WS, dict(wk=A + 16)), (SHAPE, dict(x=A + 1)), (SHAPE, dict(w=A + 8)),
     (SHAPE, dict(ws_=A + 2)), (SHAPE, dict(y=A + 1)), (SHAPE, dict(bias=A + 1)), (OK, dict(rows=0, x=None, w=None, y=None, wk=None)),
     (SHAPE, dict(rows=(1 << 31) - 1, d_out=(1 << 20) - 1, ldy=(1 << 20) - 1, nb=1 << 50)),
+    (SHAPE, dict(rows=1 << 26, nb=1 << 50)),   # quantising them
 ]
 
 
@@ -157,6 +158,8 @@ def test_product_status_of_one_kind():
     (DTYPE, dict(dt=6)), (SHAPE, dict(rows=-1)), (SHAPE, dict(rows=1 << 31)), (SHAPE, dict(cols=0)), (SHAPE, dict(cols=(1 << 17) + 1, ld=1 << 18)),
     (SHAPE, dict(ld=7)), (NULL, dict(x=None)), (NULL, dict(c=None)), (NULL, dict(s=None)), (SHAPE, dict(x=A + 1)), (SHAPE, dict(c=A + 8)),
     (SHAPE, dict(s=A + 2)), (SHAPE, dict(rows=1 << 30, ld=1 << 20)), (OK, dict(rows=0, x=None)),
+    # more than 2^24 workgroups: four rows each, or one of many columns
+    (SHAPE, dict(rows=1 << 26)), (SHAPE, dict(rows=1 << 24, cols=8192, ld=8192)),
 ])
 def test_quantize_status(status, o):
     a = dict(x=A, dt=1, rows=4, cols=8, ld=8, c=A, s=A)
@@ -168,6 +171,7 @@ def test_quantize_status(status, o):
     (DTYPE, dict(dt=2)), (SHAPE, dict(batch=-1)), (SHAPE, dict(rows=0)), (SHAPE, dict(rows=(1 << 17) + 1)), (SHAPE, dict(cols=0)),
     (SHAPE, dict(cols=1 << 20)), (SHAPE, dict(batch=1 << 30)), (NULL, dict(x=None)), (NULL, dict(c=None)), (NULL, dict(s=None)),
     (SHAPE, dict(x=A + 1)), (SHAPE, dict(c=A + 4)), (SHAPE, dict(s=A + 1)), (OK, dict(batch=0, x=None)),
+    (SHAPE, dict(batch=1 << 23)),   # workgroups of 512 threads
 ])
 def test_quantize_t_status(status, o):
     a = dict(x=A, dt=1, batch=2, rows=8, cols=8, c=A, s=A)

@@ -200,6 +200,15 @@ def test_unpermute_bwd_status(status, o):
     assert _unpermute_bwd(**o) == status
 
 
+def test_launches_beyond_the_grid():
+    # more than 2^24 workgroups of 256 threads: 32 tokens of 8 columns each, one token of 2048 columns, 4 slots
+    assert _permute(t=1 << 30, k=1) == SHAPE
+    assert _permute(False, t=1 << 30, k=1) == SHAPE
+    assert _permute(False, t=1 << 24, k=1, cols=2048) == SHAPE
+    assert _unpermute_bwd(t=1 << 26, k=1) == SHAPE
+    assert _dropout(rows=1 << 32) == SHAPE
+
+
 def _dropout(**o):
     a = dict(x=A, res=None, dt=1, rows=4, cols=8, ldx=8, ldr=8, p=0.1, rng=A, y=A)
     a.update(o)
