@@ -1437,13 +1437,16 @@ def _int8_plan(rows: int, d_in: int, d_out: int, num_local: int, x_dtype: int, d
     return c, n.value
 
 
-def moe_int8_workspace_size(rows: int, d_in: int, d_out: int, num_local: int = 0, dtype: str = "bf16") -> int:
+def moe_int8_workspace_size(rows: int, d_in: int, d_out: int, num_local: int = 0, dtype: str = "bf16", act: str = "none",
+                            out_dtype: Optional[str] = None) -> int:
     """Workspace bytes of moe_int8_linear (num_local 0) or moe_int8_experts with
-    x of dtype; none is needed where x holds codes."""
-    if dtype not in ("f32", "bf16"):
-        raise MoeError(f"moe_int8_workspace_size: dtypes are f32 and bf16, got {dtype!r}")
-    code = DTYPE_CODE[dtype]
-    return _int8_plan(rows, d_in, d_out, num_local, code, code, 0, d_in, d_out, 0, 0)[1]
+    x of dtype ("i8": codes) and an output of out_dtype, by default dtype, bf16 for codes."""
+    what = "moe_int8_workspace_size"
+    if dtype not in ("f32", "bf16", "i8") or out_dtype not in (None, "f32", "bf16"):
+        raise MoeError(f"{what}: x is f32, bf16 or i8 and the output f32 or bf16, got {dtype!r} and {out_dtype!r}")
+    code = 6 if dtype == "i8" else DTYPE_CODE[dtype]
+    y = DTYPE_CODE[out_dtype or ("bf16" if dtype == "i8" else dtype)]
+    return _int8_plan(rows, d_in, d_out, num_local, code, y, _act_code(act, what), d_in, d_out, 0, 0)[1]
 
 
 def _int8(what, fn, x, w_codes, w_scales, x_scales, bias, residual, offsets, act, out_dtype, y, ws, seed):

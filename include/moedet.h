@@ -967,7 +967,8 @@ typedef struct moe_int8 {
   uint64_t debug_shuffle_seed;
 } moe_int8;
 
-/* Workspace bytes of a product (0 where x holds codes).  Errors: those of the
+/* Workspace bytes of a product, with the fields of the call (x_dtype, dtype and act
+ * among them).  Errors: those of the
  * description, MOE_ERR_NULL. */
 moe_status moe_int8_workspace_size(const moe_int8* p, size_t* bytes);
 

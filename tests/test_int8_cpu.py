@@ -150,8 +150,27 @@ def test_product_status_of_one_kind():
     assert moe.moe_int8_workspace_size(2, 100, 7) == 0     # quantised by the product itself
     assert moe.moe_int8_workspace_size(2, 100, 7, 3) == 0
     assert moe.moe_int8_workspace_size(2, 3000, 7, 3) > 0
-    with pytest.raises(moe.MoeError, match="dtypes"):
-        moe.moe_int8_workspace_size(5, 100, 7, dtype="i8")
+    for bad in (dict(dtype="u8"), dict(out_dtype="i8")):
+        with pytest.raises(moe.MoeError, match="x is f32, bf16 or i8"):
+            moe.moe_int8_workspace_size(5, 100, 7, **bad)
+    with pytest.raises(moe.MoeError, match="act must be"):
+        moe.moe_int8_workspace_size(5, 100, 7, act="tanh")
+    assert moe.moe_int8_workspace_size(5, 112, 7, dtype="i8") == 0
+
+
+@pytest.mark.parametrize("x_dtype,out_dtype", [("bf16", None), ("bf16", "f32"), ("f32", None), ("f32", "bf16"), ("i8", None), ("i8", "f32")])
+def test_workspace_size_of_every_call(x_dtype, out_dtype):
+    """The size asked for is the one that the call needs, for every type and activation."""
+    code = {"f32": 0, "bf16": 1, "i8": 6}
+    out = code[out_dtype or ("bf16" if x_dtype == "i8" else x_dtype)]
+    lib, n = moe.load_library(), ctypes.c_size_t()
+    for rows, k, f, local in ((1, 64, 8, 0), (4, 2048, 2048, 0), (17, 8192, 64, 0), (64, 8192, 512, 0), (300, 4096, 4096, 0), (22, 2048, 2048, 512)):
+        for a, act in enumerate(("none", "relu", "relu2", "silu", "gelu")):
+            c = moe._CInt8(rows, k, f, local, code[x_dtype], out, a, k, f, 0, 0)
+            assert lib.moe_int8_workspace_size(ctypes.byref(c), ctypes.byref(n)) == OK
+            assert moe.moe_int8_workspace_size(rows, k, f, local, x_dtype, act, out_dtype) == n.value
+    # x of another type than the output is quantised by a launch of its own
+    assert (moe.moe_int8_workspace_size(1, 64, 8, 0, x_dtype, "none", out_dtype) > 0) == (x_dtype != "i8" and code[x_dtype] != out)
 
 
 @pytest.mark.parametrize("status,o", [
