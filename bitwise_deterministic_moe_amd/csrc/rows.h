@@ -2,6 +2,8 @@
 // rows sorted by expert, copied for their experts and summed back, and dropout.
 #pragma once
 
+#include <cmath>
+
 #include "dense.h"
 #include "kernels.h"
 
@@ -14,10 +16,11 @@ namespace moedet {
 constexpr int kSortMaxLocal = 1024;   // experts of a sort
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
 constexpr int kSortMaxChunks = 256;   // workgroups of a sort: one a CU
-constexpr int kSortMaxHist = 16384;   // counts that each of them adds up
 // Slots that one workgroup sorts in one launch; more take a launch that counts
-// the experts of each chunk and one that places the slots.
-constexpr int64_t kSortOne = 8192;
+// the experts of each chunk and one that places the slots (4096 slots of 8, 64 and 512 experts
+// 6.6, 7.2 and 8.3 us in one, 6.9, 7.2 and 8.4 in two; 8192: 9.2, 10.4 and 12.2, and 6.9, 7.7
+// and 8.5).
+constexpr int64_t kSortOne = 4096;
 
 struct SortParams {
   const void* idx;       // [n] expert numbers, int32 or int64
@@ -32,18 +35,19 @@ struct SortParams {
   int32_t* row_src;      // or null
   uint64_t seed;
 };
-// Chunks of n slots (a function of n and local alone).
+// Chunks of n slots (a function of n and local alone).  A workgroup walks its chunk, n /
+// chunks slots, and adds up chunks * local counts: the sum is least near the root of
+// n / local, times 3.2 as measured.  Us with about 30, 60, 120 and 240 chunks: 90112 slots of 512 experts
+// 11.5 and (88) 12.4, of 1024 13.7 and (88) 17.1; 360448 of 512 20.4, 16.4, 16.4, of 1024 23.4,
+// 20.5, 22.9; 1441792 of 512 58, 36, 27, 27, of 1024 63, 41, 35, 39, of 64 50, 29, 19, 14.
 inline void sort_chunks(int64_t n, int local, int64_t* chunk, int* chunks) {
-  if (n <= kSortOne) {
-    *chunk = kSortOne;
-    *chunks = 1;
-    return;
-  }
-  int most = kSortMaxHist / local;
-  if (most > kSortMaxChunks) most = kSortMaxChunks;
   const int64_t step = kSortThreads;
+  int64_t most = n <= kSortOne ? 1 : (int64_t)std::sqrt(10.0 * (double)n / local);
+  if (most < 1) most = 1;
+  if (most > kSortMaxChunks) most = kSortMaxChunks;
   *chunk = ((n + most - 1) / most + step - 1) / step * step;
-  *chunks = (int)((n + *chunk - 1) / *chunk);
+  if (*chunk < step) *chunk = step;
+  *chunks = n > *chunk ? (int)((n + *chunk - 1) / *chunk) : 1;
 }
 hipError_t launch_sort(const SortParams& P, hipStream_t st);
 

@@ -45,7 +45,8 @@ def _idx(t, k, experts, seed, dtype=torch.int32, low=0):
 # ------------------------------------------------------------------------ sort
 SORTS = [  # tokens, k, expert numbers, begin, local
     (0, 2, 4, 0, 4), (1, 1, 1, 0, 1), (1, 22, 512, 0, 512), (5, 3, 7, 0, 7), (64, 1, 3, 1, 1), (333, 5, 1024, 0, 1024),
-    (1000, 8, 64, 16, 8), (8192, 1, 64, 0, 64), (8193, 1, 64, 0, 64), (700, 22, 513, 5, 300), (4096, 22, 512, 0, 512),
+    (1000, 8, 64, 16, 8), (8192, 1, 64, 0, 64), (8193, 1, 64, 0, 64), (4096, 1, 64, 0, 64), (4097, 1, 1024, 0, 1024), (40000, 9, 1024, 0, 1024),
+    (30000, 40, 7, 1, 5), (700, 22, 513, 5, 300), (4096, 22, 512, 0, 512),
     (16384, 22, 512, 100, 4), (50000, 7, 2, 0, 2), (3000, 64, 1000, 0, 1000),
 ]
 
