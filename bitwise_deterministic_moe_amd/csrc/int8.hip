@@ -513,12 +513,14 @@ DEV void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "m
 template <typename T, int MB, int NB, int NS, int WGS, bool GROUPS>
 __global__ __launch_bounds__(256, WGS) void int8_tile_kernel(Int8Params P) {
   constexpr int BM = 64 * MB, BN = 64 * NB, LA = 2 * MB, LB = 2 * NB;
-  // The sums go through LDS, so that a wave writes whole pieces of rows, in passes of PR
-  // rows (one where the tile fits).  They are converted behind it: in front, the compiler
-  // converts all of them at once and spills.
-  constexpr int PR = BM * BN > 128 * 128 ? 64 : BM, ROW = BN + 4;
-  constexpr int RING = NS * line::kSlot<MB, NB>, STAGE = (PR * ROW + 768) * 4;
-  __shared__ __attribute__((aligned(16))) int8_t lds[RING > STAGE ? RING : STAGE];
+  // The sums go through LDS, so that a wave writes whole pieces of rows: each wave for itself,
+  // 32 rows at a time, the next ones stored before these are read.  They are converted behind it:
+  // in front, the compiler converts all of them at once and spills.
+  constexpr int ROW = 32 * NB + 4, STAGE = 32 * ROW, STAGES = MB > 1 ? 2 : 1;   // in words
+  constexpr int LR = NB > 1 ? 16 : 8;             // lanes on a row, four columns each
+  constexpr int HALVES = NB > 1 ? 2 : 1, STEPS = HALVES * 32 * NB / (4 * LR);   // 16 or 32 rows a step
+  constexpr int RING = NS * line::kSlot<MB, NB>, BEHIND = (4 * STAGES * STAGE + 768) * 4;
+  __shared__ __attribute__((aligned(16))) int8_t lds[RING > BEHIND ? RING : BEHIND];
   Int8Tile t;
   if (!int8_tile<GROUPS>(P, BM, BN, t)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -546,57 +548,51 @@ __global__ __launch_bounds__(256, WGS) void int8_tile_kernel(Int8Params P) {
     bf::dma16(isa ? oa.rs : ob.rs, st + (isa ? 0u : (uint32_t)MB * 8192u) + (uint32_t)(wave * (isa ? LA : LB) + j) * 1024u,
               ok ? (isa ? oa.voff[isa ? j : 0] : ob.voff[isa ? 0 : j]) : bf::kOOB, (uint32_t)ks);
   }, acc, wm, wn, lane);
-  int* stage = (int*)lds;
-  float* scales = (float*)(stage + PR * ROW);
+  float* scales = (float*)(lds + 4 * STAGES * STAGE * 4);
   ts.put(scales, tid);
-  const int c = (lane & 15) * 4, m = 4 * wave + (lane >> 4);
+  lds_barrier();
+  int* stage = (int*)lds + wave * STAGES * STAGE;
+  auto put = [&](int buf, const i32x16_t (&a)[NB]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(i32x4_t*)(stage + buf * STAGE + (lane & 31) * ROW + n * 32 + 8 * i + 4 * (lane >> 5)) =
+            i32x4_t{a[n][4 * i], a[n][4 * i + 1], a[n][4 * i + 2], a[n][4 * i + 3]};
+    asm volatile("" ::: "memory");
+  };
+  put(0, acc[0]);
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    if ((wm * MB + mb) * 32 >= t.rows) return;
+    if (mb + 1 < MB) put((mb + 1) % STAGES, acc[mb + 1]);
+    const int* src = stage + mb % STAGES * STAGE;
 #pragma unroll 1
-  for (int pass = 0; pass < BM / PR && pass * PR < t.rows; ++pass) {
-#pragma unroll
-    for (int q = 0; q < BM / PR; ++q) {
-      if (pass != q) continue;
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        const int r0 = (wm * MB + mb) * 32 - q * PR;
-        if (r0 < 0 || r0 >= PR) continue;
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const i32x16_t& a = acc[mb][n];
-            *(i32x4_t*)(stage + (r0 + (lane & 31)) * ROW + (wn * NB + n) * 32 + 8 * i + 4 * (lane >> 5)) =
-                i32x4_t{a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]};
-          }
-      }
-    }
-    lds_barrier();
-    // 16 lanes a row: 64 columns of 64 rows a step
-#pragma unroll 1
-    for (int p = 0; p < PR / 64 * NB; ++p) {
-      const int r0 = p / NB * 64 + m, n = p % NB, col = t.n0 + 64 * n + c, row0 = pass * PR + r0;
+    for (int p = 0; p < STEPS; ++p) {
+      const int r0 = p / (STEPS / HALVES) * 16 + lane / LR, c0 = p % (STEPS / HALVES) * 4 * LR + lane % LR * 4;
+      const int row0 = (wm * MB + mb) * 32 + r0, c = wn * 32 * NB + c0, col = t.n0 + c;
       if (col >= P.d.N) continue;
       if constexpr (!GROUPS) {
         if (P.d.S > 1) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (row0 + 16 * i < t.rows)
-              *(i32x4_t*)(P.part + ((int64_t)t.chunk * P.d.M + t.m0 + row0 + 16 * i) * P.part_ld + col) =
-                  *(const i32x4_t*)(stage + (r0 + 16 * i) * ROW + 64 * n + c);
+            if (row0 + i * (64 / LR) < t.rows)
+              *(i32x4_t*)(P.part + ((int64_t)t.chunk * P.d.M + t.m0 + row0 + i * (64 / LR)) * P.part_ld + col) =
+                  *(const i32x4_t*)(src + (r0 + i * (64 / LR)) * ROW + c0);
           continue;
         }
       }
-      const f32x4_t sb = *(const f32x4_t*)(scales + 256 + 64 * n + c), bias = *(const f32x4_t*)(scales + 512 + 64 * n + c);
+      const f32x4_t sb = *(const f32x4_t*)(scales + 256 + c), bias = *(const f32x4_t*)(scales + 512 + c);
       float v[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const i32x4_t sv = *(const i32x4_t*)(stage + (r0 + 16 * i) * ROW + 64 * n + c);
-        const float sa = scales[row0 + 16 * i];
+        const i32x4_t sv = *(const i32x4_t*)(src + (r0 + i * (64 / LR)) * ROW + c0);
+        const float sa = scales[row0 + i * (64 / LR)];
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[4 * i + q] = __builtin_fmaf((float)sv[q] * sa, sb[q], bias[q]);
       }
-      emit<T, kFormLinear, 4, true, true>(P.d, 0, AtRows{t.m0 + row0, t.m0 + t.rows, 16, col}, v);
+      emit<T, kFormLinear, 4, true, true>(P.d, 0, AtRows{t.m0 + row0, t.m0 + t.rows, 64 / LR, col}, v);
     }
-    if (BM > PR) lds_barrier();
   }
 }
 
