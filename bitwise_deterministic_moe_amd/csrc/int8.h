@@ -65,19 +65,19 @@ constexpr int kInt8Slice = 128;   // codes of a tile's K slice
 // Tiles: 256 x 256 (one workgroup a CU), 128 x 128 (two), 128 x 64 with a ring of three slots
 // (two) and of two (three), 64 x 64 with two (five) and with four (two).  The deeper rings
 // are for products with few workgroups a CU.  Us without activation (rows x columns x
-// K), in this order:
-//   8192 x 8192 x 8192    468  552  696  681  843  863
-//   4096 x 8192 x 2048     81   83  102   97  120  131
-//   8192 x 2048 x 1024     29   28   33   32   35   41
-//   4096 x 2048 x 8192     84   70   84   93  105  107
-//   1000 x 8192 x 2048     35   23   28   29   32   34
-//   2048 x 2048 x 2048     34   17   16   15   17   18
-//   300 x 4096 x 4096      50   25   14   21   19   16
-//   512 x 2048 x 2048      33   15   10   13   11    7
-//   64 x 2048 x 8192       73   42   21   36   32   15
-//   8 experts of 325..2456 rows, 2048 x 1024          -   36   42   35   40   47
-//   64 experts of 2400 rows, 2048 x 2048 (268 MB)     -   71   68   65   64   61
-//   64 experts of 800 rows                            -   56   65   63   53   57
+// K; experts with the squared ReLU), in this order:
+//   8192 x 8192 x 8192    450  551  703  690  845  864
+//   4096 x 8192 x 2048     73   84  100   98  119  127
+//   8192 x 2048 x 1024     23   26   33   31   34   41
+//   4096 x 2048 x 8192     79   71   84   93  104  106
+//   1000 x 8192 x 2048     33   23   28   29   31   34
+//   2048 x 2048 x 2048     28   16   16   15   17   18
+//   300 x 4096 x 4096      44   24   14   21   19   16
+//   512 x 2048 x 2048      27   15    9   13   11    7
+//   64 x 2048 x 8192       75   42   21   36   32   15
+//   8 experts of 325..2456 rows, 2048 x 1024         44   33   37   34   41   46
+//   64 experts of 2400 rows, 2048 x 2048 (268 MB)    71   58   68   66   63   59
+//   64 experts of 800 rows                           69   56   63   62   53   58
 constexpr int kInt8Tiles = 6;
 constexpr Int8Shape kInt8Shapes[kInt8Tiles] = {{256, 256}, {128, 128}, {128, 64}, {128, 64}, {64, 64}, {64, 64}};
 hipError_t launch_int8_tiles(const Int8Params& P, bool bf16, int tile, hipStream_t st);

@@ -10,6 +10,8 @@
 //
 // Tiles for many rows copy both operands by DMA into a ring of LDS slots and feed
 // v_mfma_i32_32x32x32_i8; few rows stream the weights into registers.
+#include <type_traits>
+
 #include "dense_epilogue.h"
 #include "gemm_bf16.h"
 #include "int8.h"
@@ -504,6 +506,42 @@ struct TileScales {
 
 DEV void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// The end of a tile: four columns, and CG of them COLS apart, of rows row, row + STEP, ... (four of
+// them, those below end): activation, residual, store.  FULL: all rows and columns are there,
+// so nothing is tested (a wave is alone on its SIMD, and branches around every store are
+// not hidden: 4096 x 8192 x 2048 in tiles of 256 x 256 82 us, 72 so).
+template <typename T, bool FULL, int CG, int COLS, int STEP>
+DEV void emit_rows(const DenseParams& P, int64_t row, int64_t end, int col, float (&v)[16 * CG]) {
+  float o[16 * CG];
+  if (P.add) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int g = 0; g < CG; ++g) {
+        const int n = P.N - (col + g * COLS);
+        if (!FULL && (row + i * STEP >= end || n <= 0)) continue;
+        float t[4];
+        get4((const T*)P.add + (row + i * STEP) * P.ldadd + col + g * COLS, FULL ? 4 : n, t);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[16 * g + 4 * i + q] = t[q];
+      }
+  }
+  act_n<sizeof(T) == 4, 16 * CG>(P.act, v);
+  if (P.add) {
+#pragma unroll
+    for (int i = 0; i < 16 * CG; ++i) v[i] = v[i] + o[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int g = 0; g < CG; ++g) {
+      const int n = P.N - (col + g * COLS);
+      if (!FULL && (row + i * STEP >= end || n <= 0)) continue;
+      const float* w = v + 16 * g + 4 * i;
+      put4<true>((T*)P.c[0] + (row + i * STEP) * P.ldc + col + g * COLS, FULL ? 4 : n, {w[0], w[1], w[2], w[3]});
+    }
+}
+
 // WGS: workgroups that share a CU (its registers and LDS), so that one's first loads and
 // epilogue run beside another's slices.
 // A contraction split into S chunks (one group only): each workgroup leaves its sums in
@@ -518,7 +556,7 @@ __global__ __launch_bounds__(256, WGS) void int8_tile_kernel(Int8Params P) {
   // in front, the compiler converts all of them at once and spills.
   constexpr int ROW = 32 * NB + 4, STAGE = 32 * ROW, STAGES = MB > 1 ? 2 : 1;   // in words
   constexpr int LR = NB > 1 ? 16 : 8;             // lanes on a row, four columns each
-  constexpr int HALVES = NB > 1 ? 2 : 1, STEPS = HALVES * 32 * NB / (4 * LR);   // 16 or 32 rows a step
+  constexpr int CG = 32 * NB / (4 * LR), STEPS = NB > 1 ? 2 : 1;   // groups of columns; 16 or 32 rows a step
   constexpr int RING = NS * line::kSlot<MB, NB>, BEHIND = (4 * STAGES * STAGE + 768) * 4;
   __shared__ __attribute__((aligned(16))) int8_t lds[RING > BEHIND ? RING : BEHIND];
   Int8Tile t;
@@ -562,38 +600,57 @@ __global__ __launch_bounds__(256, WGS) void int8_tile_kernel(Int8Params P) {
     asm volatile("" ::: "memory");
   };
   put(0, acc[0]);
+  const int lr = lane / LR, c0 = wn * 32 * NB + lane % LR * 4;
+  float sb[CG][4], bias[CG][4];
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    if ((wm * MB + mb) * 32 >= t.rows) return;
-    if (mb + 1 < MB) put((mb + 1) % STAGES, acc[mb + 1]);
-    const int* src = stage + mb % STAGES * STAGE;
+  for (int g = 0; g < CG; ++g)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      sb[g][q] = scales[256 + c0 + g * 4 * LR + q];
+      bias[g][q] = scales[512 + c0 + g * 4 * LR + q];
+    }
+  auto rows = [&](auto full) __attribute__((always_inline)) {
 #pragma unroll 1
-    for (int p = 0; p < STEPS; ++p) {
-      const int r0 = p / (STEPS / HALVES) * 16 + lane / LR, c0 = p % (STEPS / HALVES) * 4 * LR + lane % LR * 4;
-      const int row0 = (wm * MB + mb) * 32 + r0, c = wn * 32 * NB + c0, col = t.n0 + c;
-      if (col >= P.d.N) continue;
+    for (int s = 0; s < MB * STEPS; ++s) {
+      const int mb = s / STEPS;
+      if (s % STEPS == 0) {
+        if ((wm * MB + mb) * 32 >= t.rows) return;
+#pragma unroll
+        for (int q = 1; q < MB; ++q)
+          if (mb + 1 == q) put(q % STAGES, acc[q]);
+      }
+      const int r0 = s % STEPS * 16 + lr, row0 = (wm * MB + mb) * 32 + r0;
+      const int* src = stage + mb % STAGES * STAGE + r0 * ROW + lane % LR * 4;
       if constexpr (!GROUPS) {
         if (P.d.S > 1) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (row0 + i * (64 / LR) < t.rows)
-              *(i32x4_t*)(P.part + ((int64_t)t.chunk * P.d.M + t.m0 + row0 + i * (64 / LR)) * P.part_ld + col) =
-                  *(const i32x4_t*)(src + (r0 + i * (64 / LR)) * ROW + c0);
+#pragma unroll
+            for (int g = 0; g < CG; ++g)
+              if (row0 + i * (64 / LR) < t.rows && c0 + g * 4 * LR < nvalid)
+                *(i32x4_t*)(P.part + ((int64_t)t.chunk * P.d.M + t.m0 + row0 + i * (64 / LR)) * P.part_ld + t.n0 + c0 + g * 4 * LR) =
+                    *(const i32x4_t*)(src + i * (64 / LR) * ROW + g * 4 * LR);
           continue;
         }
       }
-      const f32x4_t sb = *(const f32x4_t*)(scales + 256 + c), bias = *(const f32x4_t*)(scales + 512 + c);
-      float v[16];
+      float v[16 * CG];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const i32x4_t sv = *(const i32x4_t*)(src + (r0 + i * (64 / LR)) * ROW + c0);
         const float sa = scales[row0 + i * (64 / LR)];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[4 * i + q] = __builtin_fmaf((float)sv[q] * sa, sb[q], bias[q]);
+        for (int g = 0; g < CG; ++g) {
+          const i32x4_t sv = *(const i32x4_t*)(src + i * (64 / LR) * ROW + g * 4 * LR);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[16 * g + 4 * i + q] = __builtin_fmaf((float)sv[q] * sa, sb[g][q], bias[g][q]);
+        }
       }
-      emit<T, kFormLinear, 4, true, true>(P.d, 0, AtRows{t.m0 + row0, t.m0 + t.rows, 64 / LR, col}, v);
+      emit_rows<T, full.value, CG, 4 * LR, 64 / LR>(P.d, t.m0 + row0, t.m0 + t.rows, t.n0 + c0, v);
     }
-  }
+  };
+  if (t.rows == BM && nvalid == BN)
+    rows(std::true_type{});
+  else
+    rows(std::false_type{});
 }
 
 // The chunks' sums of four columns a thread, then the epilogue.

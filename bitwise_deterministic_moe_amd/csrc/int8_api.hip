@@ -37,13 +37,13 @@ struct TileCost {
   double alone, each, fixed;
   int shares;               // workgroups a CU
 };
-constexpr TileCost kTiles[kInt8Tiles] = {{1.0, 1.45, 18.0, 1}, {0.52, 0.47, 8.5, 2}, {0.26, 0.27, 5.5, 2}, {0.46, 0.286, 6.3, 3}, {0.44, 0.2, 4.0, 5}, {0.24, 0.18, 3.3, 2}};
+constexpr TileCost kTiles[kInt8Tiles] = {{1.0, 1.45, 12.0, 1}, {0.52, 0.47, 8.5, 2}, {0.26, 0.27, 5.5, 2}, {0.46, 0.286, 6.3, 3}, {0.44, 0.2, 4.0, 5}, {0.24, 0.18, 3.3, 2}};
 
 double estimate(int i, double tiles, double steps, int act) {
   const TileCost& c = kTiles[i];
   const double per_cu = tiles / kCUs;
-  // a SiLU or GELU epilogue has nothing beside it here (4096 x 8192 x 2048 with GELU 98.5 us, with
-  // tiles of 128 x 128 95; without 89.6 and 87)
+  // a SiLU or GELU epilogue has nothing beside it here (8192 x 2048 x 1024 with GELU 31 us, with
+  // tiles of 128 x 128 31; without 23 and 27)
   if (c.shares == 1)
     return (double)(int64_t)(per_cu + 0.999) * (c.fixed + (act >= MOE_ACT_SILU ? 4.0 : 0.0) + steps * (per_cu <= 0.5 ? c.alone : c.each));
   const double full = per_cu / c.shares;   // rounds of a full CU
