@@ -279,7 +279,8 @@ __global__ __launch_bounds__(256) void unpermute_kernel(RowsParams P, int L) {
 // A wave a slot.  Rows that the caches cannot hold are taken in the order of the
 // slots, not in runs an XCD: rows of one expert that lie side by side are then
 // read and written at about the same time (369 MB of rows behind the forward:
-// 243 us in runs, 218 so; 6 MB of them 6.6 and 8.4 us).
+// 243 us in runs, 218 so; 6 MB of them 6.6 and 8.4 us).  4096 tokens of 22 slots, 2048 bf16:
+// 755 MB in 165 us, 4.6 TB/s.
 template <typename T, bool PAST>
 __global__ __launch_bounds__(256) void unpermute_bwd_kernel(RowsParams P) {
   constexpr int V = Vec<T>::N;

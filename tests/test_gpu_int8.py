@@ -249,6 +249,40 @@ def test_experts(counts, experts, k, f, behind, dtype):
         assert torch.equal(moe.moe_int8_linear(x[part], w[e].contiguous(), ws[e].contiguous(), bias=bias[e]), y[part])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,k,f", [(4076, 300, 4074), (4096, 256, 4096)])
+def test_largest_tiles(rows, k, f, dtype):
+    """Products that tiles of 256 x 256 take, whole tiles and ragged ones, of one matrix and of one expert."""
+    x = _values(rows, k, dtype, 8)
+    x = (x / x.abs().amax(1, keepdim=True).float()).to(TYPE[dtype])
+    w, ws, c, s = _weights(f, k, 4)
+    rng = np.random.default_rng(1)
+    bias = torch.from_numpy(rng.standard_normal(f).astype(np.float32)).to(DEV).to(TYPE[dtype])
+    wide = torch.randn((rows, f + 3), device=DEV).to(TYPE[dtype])
+    res = wide[:, 1:f + 1].clone()
+    off = torch.tensor([0, rows - 1], dtype=torch.int32, device=DEV)
+    some = np.r_[0:3, 120:136, 250:260, 2000:2002, rows - 70:rows]
+    cx, sx = oracle.int8_quantize(_f64(x[some]))
+    for act in ("gelu", "relu2"):
+        r = res if act == "gelu" else None
+        got = moe.moe_int8_linear(x, w, ws, bias=bias, residual=r, act=act)
+        want, z, scaled = oracle.int8_product(cx, sx, c, s, _f64(bias), act, None if r is None else _f64(r[some]))
+        _check_y(got[some], want, z, scaled, act, None if r is None else _f64(r[some]), dtype)
+        # in pieces, which other kernels take
+        for i in range(0, rows, 500):
+            piece = moe.moe_int8_linear(x[i:i + 500], w, ws, bias=bias, residual=None if r is None else r[i:i + 500], act=act)
+            assert torch.equal(got[i:i + 500], piece)
+        assert torch.equal(moe.moe_int8_linear(x, w, ws, bias=bias, residual=r, act=act, shuffle_seed=5), got)
+        if r is not None:   # y is the residual, between other columns
+            edge = wide[:, [0, -2, -1]].clone()
+            moe.moe_int8_linear(x, w, ws, bias=bias, residual=wide[:, 1:f + 1], act=act, y=wide[:, 1:f + 1])
+            assert torch.equal(wide[:, 1:f + 1], got) and torch.equal(wide[:, [0, -2, -1]], edge)
+        else:
+            y = torch.full((rows, f), 7.0, dtype=TYPE[dtype], device=DEV)
+            moe.moe_int8_experts(x, w[None], ws[None], off, bias=bias, act=act, y=y)
+            assert torch.equal(y[:-1], got[:-1]) and (y[-1] == 7).all()
+
+
 @pytest.mark.parametrize("rows", [6, 200])
 def test_offsets_out_of_range_touch_nothing_else(rows):
     """Offsets below 0, past the rows or descending: no row outside the matrices is touched."""
