@@ -836,7 +836,8 @@ moe_status moe_glu_bwd(const moe_dense* p, const void* da, const void* x, const 
  * Flat slot index i = t*k + j of token t's j-th choice.  slot_row [T,k] gives
  * a slot's row among the rows sorted by expert, -1 for a slot without one; it
  * is moe_sort's or a moe_routing's.  A slot whose row is not in [0, nrows) has
- * none in the calls below: nothing is read or written for it.
+ * none in the calls below: nothing is read or written for it.  Where rows are
+ * written (moe_permute_fwd, moe_unpermute_bwd) no two slots may name one row.
  * Conventions beyond those at the top of this file: base addresses are
  * multiples of the element size; token matrices have a row distance (ld, in
  * elements, at least cols) where a call says so; row matrices are contiguous
@@ -905,7 +906,7 @@ moe_status moe_unpermute_fwd(const void* rows, moe_dtype dtype, int64_t tokens, 
  *   prob      DEVICE float [T,k]
  *   drows     DEVICE [nrows,cols] output; may be rows itself
  *   dprob     DEVICE float [T,k] output, or NULL
- * No two slots of slot_row may name one row.  Errors: as moe_permute_fwd. */
+ * Errors: as moe_permute_fwd. */
 moe_status moe_unpermute_bwd(const void* dy, int64_t lddy, const void* rows, moe_dtype dtype, int64_t tokens,
                              int32_t top_k, int32_t cols, const int32_t* slot_row, int64_t nrows, const float* prob,
                              void* drows, float* dprob, uint64_t debug_shuffle_seed, void* stream);

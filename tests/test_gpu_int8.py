@@ -250,9 +250,10 @@ def test_experts(counts, experts, k, f, behind, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,k,f", [(4076, 300, 4074), (4096, 256, 4096)])
-def test_largest_tiles(rows, k, f, dtype):
-    """Products that tiles of 256 x 256 take, whole tiles and ragged ones, of one matrix and of one expert."""
+@pytest.mark.parametrize("rows,k,f", [(4076, 300, 4074), (4096, 256, 4096), (1813, 1804, 3139), (1999, 897, 1543), (2119, 794, 2577),
+                                      (519, 70, 5101)])
+def test_large_products(rows, k, f, dtype):
+    """Sizes that each of the larger tiles takes, whole tiles and ragged ones."""
     x = _values(rows, k, dtype, 8)
     x = (x / x.abs().amax(1, keepdim=True).float()).to(TYPE[dtype])
     w, ws, c, s = _weights(f, k, 4)
@@ -260,8 +261,7 @@ def test_largest_tiles(rows, k, f, dtype):
     bias = torch.from_numpy(rng.standard_normal(f).astype(np.float32)).to(DEV).to(TYPE[dtype])
     wide = torch.randn((rows, f + 3), device=DEV).to(TYPE[dtype])
     res = wide[:, 1:f + 1].clone()
-    off = torch.tensor([0, rows - 1], dtype=torch.int32, device=DEV)
-    some = np.r_[0:3, 120:136, 250:260, 2000:2002, rows - 70:rows]
+    some = np.r_[0:3, 120:136, 250:260, rows - 70:rows]
     cx, sx = oracle.int8_quantize(_f64(x[some]))
     for act in ("gelu", "relu2"):
         r = res if act == "gelu" else None
@@ -277,10 +277,24 @@ def test_largest_tiles(rows, k, f, dtype):
             edge = wide[:, [0, -2, -1]].clone()
             moe.moe_int8_linear(x, w, ws, bias=bias, residual=wide[:, 1:f + 1], act=act, y=wide[:, 1:f + 1])
             assert torch.equal(wide[:, 1:f + 1], got) and torch.equal(wide[:, [0, -2, -1]], edge)
-        else:
-            y = torch.full((rows, f), 7.0, dtype=TYPE[dtype], device=DEV)
-            moe.moe_int8_experts(x, w[None], ws[None], off, bias=bias, act=act, y=y)
-            assert torch.equal(y[:-1], got[:-1]) and (y[-1] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("experts,rows,k,f", [(1, 4076, 300, 4074), (3, 2878, 1155, 5053), (3, 2796, 658, 2631), (3, 2824, 909, 1105),
+                                              (3, 2999, 929, 1731), (3, 1016, 62, 2569)])
+def test_large_products_of_experts(experts, rows, k, f, dtype):
+    """The same by expert: the bits of the experts' products one by one, and nothing behind the last row."""
+    x = _values(rows, k, dtype, 9)
+    w, ws, _, _ = _weights(f, k, 6, experts)
+    bias = torch.randn((experts, f), device=DEV).to(TYPE[dtype])
+    cuts = [0, rows - 7] if experts == 1 else [0, rows // 3, rows // 3 + 1, rows - 7]
+    y = torch.full((rows, f), 7.0, dtype=TYPE[dtype], device=DEV)
+    moe.moe_int8_experts(x, w, ws, torch.tensor(cuts, dtype=torch.int32, device=DEV), bias=bias, act="relu2", y=y)
+    assert (y[cuts[-1]:] == 7).all()
+    for e in range(experts):
+        for i in range(cuts[e], cuts[e + 1], 500):
+            part = slice(i, min(i + 500, cuts[e + 1]))
+            assert torch.equal(y[part], moe.moe_int8_linear(x[part], w[e], ws[e], bias=bias[e], act="relu2"))
 
 
 @pytest.mark.parametrize("rows", [6, 200])
