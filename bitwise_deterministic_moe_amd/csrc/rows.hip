@@ -97,7 +97,7 @@ DEV void each_slot(uint64_t mask, int32_t r, F f) {
 }
 
 // WHOLE: L >= 64, so a wave has one token.
-// 4096 tokens of 22 slots, 2048 bf16 (386 MB): 72 us, 5.4 TB/s.  16384 tokens of
+// 4096 tokens of 22 slots, 2048 bf16 (386 MB): 70 us, 5.5 TB/s.  16384 tokens of
 // which 2816 slots have a row: 42 us where every token's row was read and every
 // slot looked at in turn by four waves a token, 21 with the ballot, 10 with one wave.
 template <bool WHOLE, bool PAST>
@@ -126,12 +126,23 @@ __global__ __launch_bounds__(256) void permute_kernel(RowsParams P, int es, int 
       const int32_t r = slot_at(P, sr, j0 + lane, p.j1);
       const uint64_t mask = __ballot(r >= 0);
       if (!mask) continue;
-      for (int v = p.v; v < vecs; v += L) {
-        const int64_t at = (int64_t)v * 16;
-        const int n = (int)(len - at < 16 ? len - at : 16);
-        u32x4_t x = {0u, 0u, 0u, 0u};
-        if (n == 16) x = *(const u32x4_b_t*)(src + at);
-        each_slot(mask, r, [&](int, int32_t row) __attribute__((always_inline)) { put(row, at, n, x); });
+      // 4 KB of the row at a time, stored whole for one slot after the other (4096 tokens of
+      // 22 slots, 2048 bf16, again and again: 85 us in pieces of 1 KB, 77 so)
+      constexpr int C = 4;
+      for (int v = p.v; v < vecs; v += C * 64) {
+        u32x4_t x[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const int64_t at = ((int64_t)v + c * 64) * 16;
+          if (at + 16 <= len) x[c] = *(const u32x4_b_t*)(src + at);
+        }
+        each_slot(mask, r, [&](int, int32_t row) __attribute__((always_inline)) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const int64_t at = ((int64_t)v + c * 64) * 16;
+            if (at < len) put(row, at, (int)(len - at < 16 ? len - at : 16), x[c]);
+          }
+        });
       }
     }
   } else {
@@ -276,55 +287,71 @@ __global__ __launch_bounds__(256) void unpermute_kernel(RowsParams P, int L) {
   }
 }
 
-// A wave a slot.  Rows that the caches cannot hold are taken in the order of the
+// A wave G slots: four where less than a third of many has a row (a rank with few of the experts;
+// those that have one are found by a ballot) or a row is one load of a wave, one otherwise.  By
+// one and by four, 16384 tokens of 22 slots, 2048 bf16, with 4, 64, 128 and 256 of 512 experts: 46
+// and 21 us, 144 and 104, 206 and 178, 336 and 328; 4096 tokens, 256 of 512: 92 and 95; all
+// slots with a row: 131072 of 512 columns 71 and 57, 65536 of 1024 63 and 76.
+// Rows that the caches cannot hold are taken in the order of the
 // slots, not in runs an XCD: rows of one expert that lie side by side are then
 // read and written at about the same time (369 MB of rows behind the forward:
 // 243 us in runs, 218 so; 6 MB of them 6.6 and 8.4 us).  4096 tokens of 22 slots, 2048 bf16:
-// 755 MB in 165 us, 4.6 TB/s.
-template <typename T, bool PAST>
+// 755 MB in 165 us, 4.6 TB/s; 5.7 were the rows in the slots' order.
+template <typename T, bool PAST, int G>
 __global__ __launch_bounds__(256) void unpermute_bwd_kernel(RowsParams P) {
   constexpr int V = Vec<T>::N;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n = P.tokens * P.k;
-  const int64_t units = (n + 3) / 4;
+  const int64_t units = (n + 4 * G - 1) / (4 * G);
   int64_t u = blockIdx.x;
   if (!PAST || P.seed) u = map_unit(u, units, P.seed);
   if (u < 0 || u >= units) return;
-  const int64_t i = u * 4 + w;
-  if (i >= n) return;
-  const int32_t r = P.slot_row[i];
-  if (r < 0 || r >= P.nrows) {
-    if (P.dprob && lane == 0) P.dprob[i] = 0.f;
-    return;
-  }
-  const T* dy = (const T*)P.x + (int64_t)((uint32_t)i / (uint32_t)P.k) * P.ldx;
-  const T* row = (const T*)P.rows + (int64_t)r * P.cols;
-  T* out = (T*)P.out + (int64_t)r * P.cols;
-  const float p = P.prob[i];
-  float dot = 0.f;
-  const int vecs = (P.cols + V - 1) / V;
+  const int64_t i0 = (u * 4 + w) * G;
+  if (i0 >= n) return;
+  auto slot = [&](int64_t i, int32_t r) __attribute__((always_inline)) {
+    const T* dy = (const T*)P.x + (int64_t)((uint32_t)i / (uint32_t)P.k) * P.ldx;
+    const T* row = (const T*)P.rows + (int64_t)r * P.cols;
+    T* out = (T*)P.out + (int64_t)r * P.cols;
+    const float p = P.prob[i];
+    float dot = 0.f;
+    const int vecs = (P.cols + V - 1) / V;
 #pragma unroll 4
-  for (int v = lane; v < vecs; v += 64) {
-    const int col = v * V, m = P.cols - col;
-    float g[V];
-    Vec<T>::get(Vec<T>::load(dy + col, m), g);
-    if (P.dprob) {
-      float f[V];
-      Vec<T>::get(Vec<T>::load(row + col, m), f);
+    for (int v = lane; v < vecs; v += 64) {
+      const int col = v * V, m = P.cols - col;
+      float g[V];
+      Vec<T>::get(Vec<T>::load(dy + col, m), g);
+      if (P.dprob) {
+        float f[V];
+        Vec<T>::get(Vec<T>::load(row + col, m), f);
 #pragma unroll
-      for (int q = 0; q < V; ++q) dot = __builtin_fmaf(g[q], f[q], dot);
+        for (int q = 0; q < V; ++q) dot = __builtin_fmaf(g[q], f[q], dot);
+      }
+#pragma unroll
+      for (int q = 0; q < V; ++q) g[q] = p * g[q];
+      if (PAST && m >= V)
+        store_past(out + col, g);
+      else
+        Vec<T>::store(out + col, g, m);
     }
+    if (!P.dprob) return;
 #pragma unroll
-    for (int q = 0; q < V; ++q) g[q] = p * g[q];
-    if (PAST && m >= V)
-      store_past(out + col, g);
-    else
-      Vec<T>::store(out + col, g, m);
+    for (int d = 1; d < 64; d <<= 1) dot = dot + __shfl_xor(dot, d, 64);
+    if (lane == 0) P.dprob[i] = dot;
+  };
+  if constexpr (G == 1) {
+    const int32_t r = P.slot_row[i0];
+    if (r >= 0 && r < P.nrows)
+      slot(i0, r);
+    else if (P.dprob && lane == 0)
+      P.dprob[i0] = 0.f;
+  } else {
+    const int64_t i = i0 + lane;
+    const bool mine = lane < G && i < n;
+    const int32_t r = mine ? P.slot_row[i] : -1;
+    const bool has = r >= 0 && r < P.nrows;
+    if (mine && !has && P.dprob) P.dprob[i] = 0.f;
+    each_slot(__ballot(has), r, [&](int b, int32_t row) __attribute__((always_inline)) { slot(i0 + b, row); });
   }
-  if (!P.dprob) return;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) dot = dot + __shfl_xor(dot, d, 64);
-  if (lane == 0) P.dprob[i] = dot;
 }
 
 hipError_t launch_permute(const RowsParams& P, int es, hipStream_t st) {
@@ -361,14 +388,23 @@ hipError_t launch_unpermute(const RowsParams& P, bool bf16, hipStream_t st) {
   return bf16 ? launch_sum<uint16_t>(P, st) : launch_sum<float>(P, st);
 }
 
+// Slots from which a wave may take four of them (below, waves are too few: 32768 slots of which
+// 2048 have a row 10.5 us by one, 11.8 by four).
+constexpr int64_t kManySlots = 65536;
 template <typename T>
 static hipError_t launch_bwd(const RowsParams& P, hipStream_t st) {
-  const int64_t grid = grid_for_units((P.tokens * P.k + 3) / 4);
+  const int64_t n = P.tokens * P.k;
+  const bool many = n >= kManySlots && (3 * P.nrows < n || P.cols <= 64 * Vec<T>::N), past = past_cache(P, sizeof(T));
+  const int64_t grid = grid_for_units(many ? (n + 15) / 16 : (n + 3) / 4);
   if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
-  if (past_cache(P, sizeof(T)))
-    unpermute_bwd_kernel<T, true><<<grid, 256, 0, st>>>(P);
+  if (many && past)
+    unpermute_bwd_kernel<T, true, 4><<<grid, 256, 0, st>>>(P);
+  else if (many)
+    unpermute_bwd_kernel<T, false, 4><<<grid, 256, 0, st>>>(P);
+  else if (past)
+    unpermute_bwd_kernel<T, true, 1><<<grid, 256, 0, st>>>(P);
   else
-    unpermute_bwd_kernel<T, false><<<grid, 256, 0, st>>>(P);
+    unpermute_bwd_kernel<T, false, 1><<<grid, 256, 0, st>>>(P);
   return hipGetLastError();
 }
 hipError_t launch_unpermute_bwd(const RowsParams& P, bool bf16, hipStream_t st) {

@@ -89,6 +89,7 @@ def test_sort_numbers_far_out():
 ROWS = [  # tokens, k, experts, local, columns
     (1, 1, 1, 1, 1), (1, 22, 512, 512, 2048), (3, 4, 8, 8, 7), (17, 2, 5, 3, 64), (130, 9, 20, 20, 257), (64, 3, 4, 1, 1000),
     (40, 6, 16, 16, 4096), (33, 2, 3, 3, 5001), (9, 65, 70, 70, 24), (2, 3, 4, 0, 40),
+    (3001, 22, 512, 30, 136), (9362, 7, 9, 9, 33),
 ]
 
 
@@ -369,6 +370,49 @@ def test_streams_and_graphs(t, k, cols):
             assert torch.equal(o[n], w[n]), n
         moe.moe_sort(inputs["idx"], 7)      # eager work between the replays
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t,k,experts,local,cols", [(20011, 7, 64, 64, 1032), (40003, 8, 64, 64, 505), (60000, 22, 512, 150, 700)])
+def test_rows_beyond_the_last_level_cache(t, k, experts, local, cols, dtype):
+    """More than 256 MB of rows, every element against float64 arithmetic on the GPU."""
+    g = torch.Generator(device=DEV).manual_seed(t)
+    mat = lambda n: torch.randn((n, cols), generator=g, device=DEV).to(dtype)  # noqa: E731
+    sr, off, _ = moe.moe_sort(torch.randint(0, experts, (t, k), generator=g, device=DEV, dtype=torch.int32), local)
+    n = int(off[-1])
+    assert n * cols * dtype.itemsize > 256 << 20
+    x, add, rows = mat(t), mat(t), mat(n + 3)
+    p = torch.rand((t, k), generator=g, device=DEV)
+    u = U[dtype]
+
+    def near(got, want, bound):
+        assert bool(((got.double() - want).abs() <= bound).all())
+
+    there = rows.clone()
+    moe.moe_permute_fwd(x, sr, rows=there)
+    assert torch.equal(there[n:], rows[n:])
+    y = moe.moe_unpermute_fwd(rows, sr, p, residual=add)
+    dx = moe.moe_permute_bwd(rows, sr)
+    drows = rows.clone()
+    _, dprob = moe.moe_unpermute_bwd(x, rows, sr, p, drows=drows)
+    assert torch.equal(drows[n:], rows[n:])
+    xd = x.double()
+    want, size, plain, whole = add.double(), add.double().abs(), torch.zeros_like(xd), torch.zeros_like(xd)
+    for j in range(k):
+        has = sr[:, j] >= 0
+        r = sr[:, j].long()[has]
+        assert torch.equal(there[r], x[has])
+        v, w = rows[r].double(), p[has, j:j + 1].double()
+        want[has] += v * w
+        size[has] += (v * w).abs()
+        plain[has] += v
+        whole[has] += v.abs()
+        near(drows[r], xd[has] * w, (u + 2 * E) * (xd[has] * w).abs())
+        dots = xd[has] * v
+        near(dprob[has, j], dots.sum(1), (cols + 1) * E * dots.abs().sum(1))
+        assert bool((dprob[~has, j] == 0).all())
+    near(y, want, (k + 2) * E * size + u * (want.abs() + (k + 2) * E * size))
+    near(dx, plain, (k + 2) * E * whole + u * (plain.abs() + (k + 2) * E * whole))
 
 
 def test_more_than_2_31_bytes_and_elements():
