@@ -373,14 +373,15 @@ def test_streams_and_graphs(t, k, cols):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("t,k,experts,local,cols", [(20011, 7, 64, 64, 1032), (40003, 8, 64, 64, 505), (60000, 22, 512, 150, 700)])
-def test_rows_beyond_the_last_level_cache(t, k, experts, local, cols, dtype):
-    """More than 256 MB of rows, every element against float64 arithmetic on the GPU."""
+@pytest.mark.parametrize("t,k,experts,local,cols,big", [(20011, 7, 64, 64, 1032, True), (40003, 8, 64, 64, 505, True),
+                                                        (60000, 22, 512, 150, 700, True), (5003, 22, 512, 20, 1033, False)])
+def test_many_rows(t, k, experts, local, cols, big, dtype):
+    """More than 256 MB of rows (big), or few rows of many slots: every element against float64 arithmetic on the GPU."""
     g = torch.Generator(device=DEV).manual_seed(t)
     mat = lambda n: torch.randn((n, cols), generator=g, device=DEV).to(dtype)  # noqa: E731
     sr, off, _ = moe.moe_sort(torch.randint(0, experts, (t, k), generator=g, device=DEV, dtype=torch.int32), local)
     n = int(off[-1])
-    assert n * cols * dtype.itemsize > 256 << 20
+    assert big == (n * cols * dtype.itemsize > 256 << 20)
     x, add, rows = mat(t), mat(t), mat(n + 3)
     p = torch.rand((t, k), generator=g, device=DEV)
     u = U[dtype]
