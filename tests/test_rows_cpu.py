@@ -201,13 +201,14 @@ def test_unpermute_bwd_status(status, o):
 
 
 def test_launches_beyond_the_grid():
-    # more than 2^24 workgroups of 256 threads: 32 tokens of 8 columns each, one token of 2048 columns, 4 slots, 16 of short rows
-    assert _permute(t=1 << 30, k=1) == SHAPE
-    assert _permute(False, t=1 << 30, k=1) == SHAPE
-    assert _permute(False, t=1 << 24, k=1, cols=2048) == SHAPE
-    assert _unpermute_bwd(t=1 << 26, k=1, n=1 << 26, cols=1000, ld=1000) == SHAPE
-    assert _unpermute_bwd(t=1 << 28, k=1) == SHAPE
-    assert _dropout(rows=1 << 32) == SHAPE
+    # far more than 2^24 workgroups, whichever kernel takes them
+    t = (1 << 31) - 1
+    assert _permute(t=t, k=1) == SHAPE
+    assert _permute(False, t=t, k=1) == SHAPE
+    assert _permute(False, t=t, k=1, cols=500) == SHAPE
+    assert _unpermute_bwd(t=t, k=1) == SHAPE
+    assert _unpermute_bwd(t=t, k=1, n=t, cols=500, ld=500) == SHAPE
+    assert _dropout(rows=1 << 36) == SHAPE
 
 
 def _dropout(**o):
