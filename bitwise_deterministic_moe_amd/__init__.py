@@ -1296,7 +1296,15 @@ def moe_permute_fwd(x: torch.Tensor, slot_row: torch.Tensor, rows=None, shuffle_
     return rows
 
 
-def _sum_rows(what: str, fn, rows, slot_row, tokens, prob, add, out, seed):
+def _per_slot(t: torch.Tensor, tokens: int, k: int, what: str):
+    """A float32 number per slot in the slots' order: [tokens, k], or any shape that is not a matrix."""
+    _need(t, tokens * k, torch.float32, what)
+    shape = t.shape
+    if len(shape) == 2 and shape[1] != k and min(shape) > 1:
+        raise MoeError(f"{what}: need [{tokens}, {k}], got {tuple(shape)}")
+
+
+def _sum_rows(what: str, fn, rows, slot_row, prob, add, out, seed):
     code = _storage(rows, what)
     if rows.dim() != 2 or rows.shape[1] < 1:
         raise MoeError(f"{what}: rows must be a matrix, got {tuple(rows.shape)}")
@@ -1304,15 +1312,19 @@ def _sum_rows(what: str, fn, rows, slot_row, tokens, prob, add, out, seed):
     n = _row_matrix(rows, cols, rows.dtype, what + " rows")
     if slot_row.dim() == 2:
         tokens = slot_row.shape[0]
+    elif prob is not None and prob.dim() == 2 and min(prob.shape) > 1:
+        tokens = prob.shape[0]
     elif add is not None:
         tokens = add.numel() // cols
     elif out is not None:
         tokens = out.numel() // cols
-    elif tokens is None:
+    elif prob is not None and prob.dim() == 2:
+        tokens = prob.shape[0]
+    else:
         raise MoeError(f"{what}: a flat slot_row leaves the number of tokens open: reshape it to [tokens, top_k]")
     k = _slots(slot_row, tokens, what)
     if prob is not None:
-        _need(prob, tokens * k, torch.float32, what + " prob")
+        _per_slot(prob, tokens, k, what + " prob")
     ldadd = _mat(add, cols, rows.dtype, what + " residual", tokens)[1] if add is not None else cols
     if out is None:
         out = _flat(rows, (tokens, cols), (cols, 1), rows.dtype)
@@ -1329,7 +1341,7 @@ def moe_permute_bwd(drows: torch.Tensor, slot_row: torch.Tensor, dx_add=None, dx
     """Gradient of moe_permute_fwd: dx[t] = sum over j of drows[slot_row[t, j]]
     (+ dx_add[t]), slots in order, in float32.  Returns dx [T, D], which may be
     dx_add itself."""
-    return _sum_rows("moe_permute_bwd", load_library().moe_permute_bwd, drows, slot_row, None, None, dx_add, dx, shuffle_seed)
+    return _sum_rows("moe_permute_bwd", load_library().moe_permute_bwd, drows, slot_row, None, dx_add, dx, shuffle_seed)
 
 
 def moe_unpermute_fwd(rows: torch.Tensor, slot_row: torch.Tensor, prob=None, residual=None, y=None, shuffle_seed: int = 0):
@@ -1337,9 +1349,7 @@ def moe_unpermute_fwd(rows: torch.Tensor, slot_row: torch.Tensor, prob=None, res
     rows [R, D] sorted by expert (float32 or bf16), prob float32 [T, k] (None:
     1), slots in order, in float32.  Returns y [T, D], which may be the residual
     itself."""
-    tokens = prob.shape[0] if prob is not None and prob.dim() == 2 else None
-    return _sum_rows("moe_unpermute_fwd", load_library().moe_unpermute_fwd, rows, slot_row, tokens, prob, residual, y,
-                     shuffle_seed)
+    return _sum_rows("moe_unpermute_fwd", load_library().moe_unpermute_fwd, rows, slot_row, prob, residual, y, shuffle_seed)
 
 
 def moe_unpermute_bwd(dy: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tensor, prob: torch.Tensor, drows=None,
@@ -1356,7 +1366,7 @@ def moe_unpermute_bwd(dy: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tens
     tokens, lddy = _mat(dy, cols, dy.dtype, what + " dy")
     k = _slots(slot_row, tokens, what)
     n = _row_matrix(rows, cols, dy.dtype, what + " rows")
-    _need(prob, tokens * k, torch.float32, what + " prob")
+    _per_slot(prob, tokens, k, what + " prob")
     if drows is None:
         drows = _flat(dy, (n, cols), (cols, 1), dy.dtype)
     elif _row_matrix(drows, cols, dy.dtype, what + " drows") != n:
@@ -1364,7 +1374,7 @@ def moe_unpermute_bwd(dy: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tens
     if dprob is None:
         dprob = _flat(dy, (tokens, k), (k, 1), torch.float32)
     else:
-        _need(dprob, tokens * k, torch.float32, what + " dprob")
+        _per_slot(dprob, tokens, k, what + " dprob")
     _run(what, lib.moe_unpermute_bwd,
          (_ptr(dy), lddy, _ptr(rows), code, tokens, k, cols, _ptr(slot_row), n, _ptr(prob), _ptr(drows), _ptr(dprob),
           shuffle_seed), dy, rows, slot_row, prob, drows, dprob)

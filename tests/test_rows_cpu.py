@@ -127,6 +127,34 @@ def test_refusals(i):
         call()
 
 
+def test_numbers_per_slot_are_laid_out_by_token():
+    """prob and dprob as [tokens, top_k], and one number of tokens from all that tell it."""
+    flat, both = _t(8, dtype=I32), _t(4, 2, dtype=I32)
+    p, turned = _t(4, 2, dtype=F32), _t(2, 4, dtype=F32)
+    fwd, bwd = moe.moe_unpermute_fwd, moe.moe_unpermute_bwd
+    for call, says in (
+        (lambda: fwd(_t(8, 8), flat, p, residual=_t(2, 8)), "residual"),       # 4 tokens of 2 slots, and 2 of 4
+        (lambda: fwd(_t(8, 8), flat, p, y=_t(2, 8)), "output"),
+        (lambda: fwd(_t(8, 8), flat, turned, residual=_t(4, 8)), "residual"),
+        (lambda: fwd(_t(8, 8), flat, _t(3, 2, dtype=F32)), "tokens"),
+        (lambda: fwd(_t(8, 8), both, turned), "prob"),
+        (lambda: bwd(_t(4, 8), _t(8, 8), both, turned), "prob"),
+        (lambda: bwd(_t(4, 8), _t(8, 8), flat, turned), "prob"),
+        (lambda: bwd(_t(4, 8), _t(8, 8), both, p, dprob=turned), "dprob"),
+        # numbers that agree, in other shapes than a matrix too: refused only for want of a GPU
+        (lambda: fwd(_t(8, 8), flat, p, residual=_t(4, 8), y=_t(4, 8)), "GPU"),
+        (lambda: fwd(_t(8, 8), flat, _t(8, dtype=F32), residual=_t(2, 8)), "GPU"),
+        (lambda: fwd(_t(8, 8), both, _t(8, dtype=F32)), "GPU"),
+        (lambda: fwd(_t(8, 8), both, _t(8, 1, dtype=F32)), "GPU"),
+        (lambda: fwd(_t(8, 8), flat, _t(1, 8, dtype=F32), residual=_t(2, 8)), "GPU"),
+        (lambda: fwd(_t(8, 8), flat, _t(8, 1, dtype=F32)), "GPU"),
+        (lambda: fwd(_t(8, 8), both, _t(2, 2, 2, dtype=F32)), "GPU"),
+        (lambda: bwd(_t(4, 8), _t(8, 8), flat, p, dprob=p), "GPU"),
+    ):
+        with pytest.raises(moe.MoeError, match=says):
+            call()
+
+
 OK, NULL, SHAPE, DTYPE, WS = 0, 1, 2, 3, 4
 A = 0x10000   # an address that is not followed: the calls return before any launch
 
