@@ -129,7 +129,9 @@ __global__ __launch_bounds__(256) void permute_kernel(RowsParams P, int es, int 
       // 4 KB of the row at a time, stored whole for one slot after the other (4096 tokens of
       // 22 slots, 2048 bf16, again and again: 85 us in pieces of 1 KB, 77 so)
       constexpr int C = 4;
-      for (int v = p.v; v < vecs; v += C * 64) {
+      // The loop is the same for all lanes: each_slot reads r of lanes that have no vector left.
+      for (int v0 = 0; v0 < vecs; v0 += C * 64) {
+        const int v = v0 + lane;
         u32x4_t x[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) {

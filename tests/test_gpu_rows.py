@@ -176,6 +176,21 @@ def test_permute_of_codes_and_their_scales(t, k, cols, dtype):
     assert torch.equal(moe.moe_permute_fwd(scales, slot_row)[:r], scales[tok])
 
 
+@pytest.mark.parametrize("dtype", [torch.uint8, BF16, F32])
+@pytest.mark.parametrize("t,k", [(3, 70), (700, 64), (70, 130)])
+def test_permute_of_ragged_rows_and_many_slots(t, k, dtype):
+    """Rows whose last pieces leave most lanes without a vector, for slots of every lane (a wave a token)."""
+    size = torch.empty(0, dtype=dtype).element_size()
+    for length in (516, 1008, 1028, 2100, 4112, 4600, 8204, 9000):      # bytes: 33 vectors up, past 4 KB and past 8
+        cols = length // size
+        x = torch.randint(0, 100, (t, cols), device=DEV).to(dtype)
+        slot_row, offsets, row_src = moe.moe_sort(_idx(t, k, 5, length, low=-1), 5, need_row_src=True)
+        r = int(offsets[-1])
+        rows = torch.full((r + 3, cols), 7, dtype=dtype, device=DEV)
+        moe.moe_permute_fwd(x, slot_row, rows=rows)
+        assert torch.equal(rows[:r], x[row_src[:r].long() // k]) and (rows[r:] == 7).all(), length
+
+
 def test_slots_past_the_rows_have_none():
     """A slot that names a row past the matrix: nothing is read or written for it."""
     slot_row = torch.tensor([[0, 5], [1, 2 ** 31 - 1], [-7, 2]], dtype=torch.int32, device=DEV)
