@@ -26,7 +26,8 @@ __all__ = [
     "moe_glu_bwd", "moe_layernorm_workspace_size", "moe_linear_workspace_size", "moe_glu_workspace_size", "ACTIVATIONS",
     "moe_linear_stage_names", "moe_glu_stage_names", "moe_sort", "moe_sort_workspace_size", "moe_permute_fwd",
     "moe_permute_bwd", "moe_unpermute_fwd", "moe_unpermute_bwd", "moe_dropout_fwd", "moe_dropout_bwd",
-    "moe_int8_quantize", "moe_int8_quantize_t", "moe_int8_workspace_size", "moe_int8_linear", "moe_int8_experts",
+    "moe_int8_quantize", "moe_int8_quantize_t", "moe_int8_workspace_size", "moe_int8_stage_names", "moe_int8_linear",
+    "moe_int8_experts",
 ]
 
 DETERMINISTIC = 0
@@ -46,7 +47,7 @@ EXPORTED_SYMBOLS = ("moe_abi_version", "moe_status_string", "moe_rows_cap", "moe
                     "moe_glu_fwd", "moe_glu_bwd", "moe_linear_stage_names", "moe_glu_stage_names",
                     "moe_sort_workspace_size", "moe_sort", "moe_permute_fwd", "moe_permute_bwd", "moe_unpermute_fwd",
                     "moe_unpermute_bwd", "moe_dropout_fwd", "moe_dropout_bwd", "moe_int8_quantize", "moe_int8_quantize_t",
-                    "moe_int8_workspace_size", "moe_int8_linear", "moe_int8_experts")
+                    "moe_int8_workspace_size", "moe_int8_stage_names", "moe_int8_linear", "moe_int8_experts")
 # activations of the dense operators (moe_act)
 ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4}
 # matrices of a dense call that may start at any element (moe_any)
@@ -186,10 +187,11 @@ def load_library() -> ctypes.CDLL:
     lib.moe_int8_quantize.argtypes = [vp, ci, i64, i64, i64, vp, vp, u64, vp]
     lib.moe_int8_quantize_t.argtypes = [vp, ci, i64, i64, i64, vp, vp, u64, vp]
     lib.moe_int8_workspace_size.argtypes = [Q, ctypes.POINTER(sz)]
+    lib.moe_int8_stage_names.argtypes = [Q, ctypes.c_char_p, sz]
     lib.moe_int8_linear.argtypes = [Q] + [vp] * 8 + [sz, vp]
     lib.moe_int8_experts.argtypes = [Q] + [vp] * 8 + [sz, vp]
-    for f in ("moe_int8_quantize", "moe_int8_quantize_t", "moe_int8_workspace_size", "moe_int8_linear", "moe_int8_experts",
-              "moe_sort_workspace_size", "moe_sort", "moe_permute_fwd", "moe_permute_bwd", "moe_unpermute_fwd",
+    for f in ("moe_int8_quantize", "moe_int8_quantize_t", "moe_int8_workspace_size", "moe_int8_stage_names",
+              "moe_int8_linear", "moe_int8_experts", "moe_sort_workspace_size", "moe_sort", "moe_permute_fwd", "moe_permute_bwd", "moe_unpermute_fwd",
               "moe_unpermute_bwd", "moe_dropout_fwd", "moe_dropout_bwd"):
         getattr(lib, f).restype = ci
     for f in ("moe_route", "moe_mx_wgrad_rows", "moe_mx_quantize_wgrad", "moe_mx_wgrad", "moe_rows_cap",
@@ -1447,16 +1449,30 @@ def _int8_plan(rows: int, d_in: int, d_out: int, num_local: int, x_dtype: int, d
     return c, n.value
 
 
-def moe_int8_workspace_size(rows: int, d_in: int, d_out: int, num_local: int = 0, dtype: str = "bf16", act: str = "none",
-                            out_dtype: Optional[str] = None) -> int:
-    """Workspace bytes of moe_int8_linear (num_local 0) or moe_int8_experts with
-    x of dtype ("i8": codes) and an output of out_dtype, by default dtype, bf16 for codes."""
-    what = "moe_int8_workspace_size"
+def _int8_sizes(what, rows, d_in, d_out, num_local, dtype, act, out_dtype):
+    """The plan of a product of contiguous matrices."""
     if dtype not in ("f32", "bf16", "i8") or out_dtype not in (None, "f32", "bf16"):
         raise MoeError(f"{what}: x is f32, bf16 or i8 and the output f32 or bf16, got {dtype!r} and {out_dtype!r}")
     code = 6 if dtype == "i8" else DTYPE_CODE[dtype]
     y = DTYPE_CODE[out_dtype or ("bf16" if dtype == "i8" else dtype)]
-    return _int8_plan(rows, d_in, d_out, num_local, code, y, _act_code(act, what), d_in, d_out, 0, 0)[1]
+    return _int8_plan(rows, d_in, d_out, num_local, code, y, _act_code(act, what), d_in, d_out, 0, 0)
+
+
+def moe_int8_workspace_size(rows: int, d_in: int, d_out: int, num_local: int = 0, dtype: str = "bf16", act: str = "none",
+                            out_dtype: Optional[str] = None) -> int:
+    """Workspace bytes of moe_int8_linear (num_local 0) or moe_int8_experts with
+    x of dtype ("i8": codes) and an output of out_dtype, by default dtype, bf16 for codes."""
+    return _int8_sizes("moe_int8_workspace_size", rows, d_in, d_out, num_local, dtype, act, out_dtype)[1]
+
+
+def moe_int8_stage_names(rows: int, d_in: int, d_out: int, num_local: int = 0, dtype: str = "bf16", act: str = "none",
+                         out_dtype: Optional[str] = None):
+    """Names of the kernels that such a call enqueues, with the tile and the number
+    of chunks of the product; the arguments as in moe_int8_workspace_size."""
+    what = "moe_int8_stage_names"
+    c, b = _int8_sizes(what, rows, d_in, d_out, num_local, dtype, act, out_dtype)[0], ctypes.create_string_buffer(64)
+    _check(load_library().moe_int8_stage_names(c, b, len(b)), what)
+    return b.value.decode().split(",") if b.value else []
 
 
 def _int8(what, fn, x, w_codes, w_scales, x_scales, bias, residual, offsets, act, out_dtype, y, ws, seed):

@@ -1,6 +1,8 @@
 // Host side of the C ABI of the products in 8-bit integers (declared in
 // include/moedet.h): argument checks, workspace, and the choice of kernel from
 // sizes alone.
+#include <cstdio>
+
 #include "../../include/moedet.h"
 #include "int8.h"
 
@@ -256,6 +258,27 @@ MOE_API moe_status moe_int8_workspace_size(const moe_int8* p, size_t* bytes) {
   if (!bytes) return MOE_ERR_NULL;
   *bytes = plan(p).total;
   return MOE_OK;
+}
+
+MOE_API moe_status moe_int8_stage_names(const moe_int8* p, char* names, size_t bytes) {
+  const moe_status s = check(p);
+  if (s != MOE_OK) return s;
+  if (!names) return MOE_ERR_NULL;
+  if (bytes < 1) return MOE_ERR_WORKSPACE;
+  static const char* const kNames[kInt8Tiles] = {"256x256", "128x128", "128x64_deep", "128x64", "64x64", "64x64_deep"};   // kInt8Shapes
+  const Choice c = choose(p, up16(p->d_in));
+  const char* kind = p->num_local ? "experts" : "linear";
+  const char* first = p->x_dtype == MOE_I8 || c.fused ? "" : "quantize,";
+  int n;
+  if (p->rows == 0)
+    n = snprintf(names, bytes, "%s", "");
+  else if (c.ks)
+    n = snprintf(names, bytes, "%s%s_few%d%s", first, kind, c.ks, c.fused ? "_quantize" : "");
+  else if (c.S > 1)
+    n = snprintf(names, bytes, "%s%s_%s_split%d,join", first, kind, kNames[c.tile], c.S);
+  else
+    n = snprintf(names, bytes, "%s%s_%s", first, kind, kNames[c.tile]);
+  return n >= 0 && (size_t)n < bytes ? MOE_OK : MOE_ERR_WORKSPACE;
 }
 
 MOE_API moe_status moe_int8_linear(const moe_int8* p, const void* x, const float* x_scales, const int8_t* w_codes,

@@ -973,6 +973,14 @@ typedef struct moe_int8 {
  * description, MOE_ERR_NULL. */
 moe_status moe_int8_workspace_size(const moe_int8* p, size_t* bytes);
 
+/* Names of the kernels that a product with this description enqueues, in order,
+ * comma-separated and ended by 0, in `names` (HOST, `bytes` long; 64 are enough):
+ * whether x is quantised by a launch of its own, the weight stream with the waves that
+ * share a contraction, or the tile (deep: the one of two rings with more slots)
+ * and in how many chunks of the contraction.  Errors: those of the description, MOE_ERR_NULL,
+ * MOE_ERR_WORKSPACE (bytes). */
+moe_status moe_int8_stage_names(const moe_int8* p, char* names, size_t bytes);
+
 /* y[t, n] = act(x_scale[t] w_scale[n] sum over k of x_code[t, k] w_code[n, k] + bias[n])
  * (+ residual[t, n]).  The sum is exact; it is rounded to float32 once, its
  * product with x_scale once, and y once after float32 arithmetic.

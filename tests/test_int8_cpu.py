@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import bitwise_deterministic_moe_amd as moe
+import int8_cases
 import oracle
 
 
@@ -196,3 +197,48 @@ def test_quantize_t_status(status, o):
     a = dict(x=A, dt=1, batch=2, rows=8, cols=8, c=A, s=A)
     a.update(o)
     assert moe.load_library().moe_int8_quantize_t(a["x"], a["dt"], a["batch"], a["rows"], a["cols"], a["c"], a["s"], 0, None) == status
+
+
+# --------------------------------------------------------------------- kernels
+def test_cases_reach_every_kernel():
+    for kernel, *case in int8_cases.LINEAR:
+        assert int8_cases.linear_kernel(*case) == "linear_" + kernel
+    for kernel, *case in int8_cases.EXPERTS:
+        assert int8_cases.experts_kernel(*case) == "experts_" + kernel
+    want = {(k, t) for k in int8_cases.FEW + int8_cases.TILES for t in ("bf16", "f32")}
+    assert {c[:2] for c in int8_cases.EXPERTS} == want
+    assert {c[:2] for c in int8_cases.LINEAR} == want | {(k, t) for k in int8_cases.SPLITS for t in ("bf16", "f32")}
+    # more than the eight steps of 64 codes that a wave has in flight, on every weight stream of both kinds (but the
+    # one whose 2048 codes of a row are eight steps at most)
+    for cases, at in ((int8_cases.LINEAR, 3), (int8_cases.EXPERTS, 4)):
+        for kernel in int8_cases.FEW:
+            if cases is int8_cases.LINEAR or kernel != "few4_quantize":
+                assert any(c[0] == kernel and c[at] > 64 * 8 * int(kernel[3]) for c in cases), kernel
+    # chunks of uneven numbers of slices, the last slice not full
+    for kernel, _, _, k, _, _ in int8_cases.LINEAR:
+        if "_split" in kernel:
+            k16 = (k + 15) // 16 * 16
+            assert (k16 + 127) // 128 % int(kernel[-1]) and k16 % 128, (kernel, k)
+
+
+def test_stage_names():
+    names = moe.moe_int8_stage_names
+    assert names(0, 64, 96) == [] and names(0, 64, 96, 4, "i8") == []
+    assert names(1, 2048, 2048) == ["linear_few4_quantize"] and names(5, 2048, 2048) == ["quantize", "linear_few4"]
+    assert names(1, 2048, 2048, out_dtype="f32") == ["quantize", "linear_few4"] and names(1, 2048, 2048, dtype="i8") == ["linear_few4"]
+    assert names(37, 2048, 8192, act="silu") == ["quantize", "linear_64x64_deep"]
+    assert names(4096, 2048, 8192, act="gelu") == ["quantize", "linear_256x256"]
+    assert names(4096, 2048, 8192, dtype="i8", act="gelu") == ["linear_256x256"]
+    assert names(22, 2048, 2048, 512, act="relu2") == ["experts_few1_quantize"]
+    assert names(8192, 1024, 2048, 8, act="relu2") == ["quantize", "experts_128x128"]
+    assert names(110, 7513, 5499) == ["quantize", "linear_64x64_deep_split2", "join"]
+    lib, b = moe.load_library(), ctypes.create_string_buffer(64)
+    c = moe._CInt8(40, 32, 6, 0, 1, 1, 0, 32, 6, 0, 0)
+    assert lib.moe_int8_stage_names(c, None, 64) == NULL and lib.moe_int8_stage_names(None, b, 64) == NULL
+    assert lib.moe_int8_stage_names(c, b, 0) == WS and lib.moe_int8_stage_names(c, b, 8) == WS
+    n = len(",".join(names(40, 32, 6)))
+    assert lib.moe_int8_stage_names(c, b, n) == WS and lib.moe_int8_stage_names(c, b, n + 1) == OK
+    with pytest.raises(moe.MoeError, match="status 2"):
+        names(4, 8, 8, 1025)
+    with pytest.raises(moe.MoeError, match="moe_int8_stage_names: x is f32"):
+        names(4, 8, 8, dtype="u8")
