@@ -81,7 +81,7 @@ constexpr int kInt8Slice = 128;   // codes of a tile's K slice
 constexpr int kInt8Tiles = 6;
 constexpr Int8Shape kInt8Shapes[kInt8Tiles] = {{256, 256}, {128, 128}, {128, 64}, {128, 64}, {64, 64}, {64, 64}};
 hipError_t launch_int8_tiles(const Int8Params& P, bool bf16, int tile, hipStream_t st);
-// ks: waves that share a contraction (1, 2 or 4)
+// ks: waves that share a contraction, 1 or 4
 hipError_t launch_int8_few(const Int8Params& P, bool bf16, int ks, hipStream_t st);
 
 }  // namespace moedet
