@@ -101,14 +101,24 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutParams P, int64_t n
   }
 }
 
+static int dropout_form(const DropoutParams& P, int vec) {
+  const bool flat = P.rows == 1 || (P.ldx == P.cols && (!P.add || P.ldadd == P.cols));
+  return flat ? kFlat : P.cols % vec == 0 ? kRowVecs : kElements;
+}
+static int64_t form_grid(const DropoutParams& P, int form, int vec) {
+  const int64_t per = 256 * (form == kElements ? 4 : vec);
+  return (P.rows * P.cols + per - 1) / per;
+}
+int64_t dropout_grid(const DropoutParams& P, bool bf16) {
+  const int vec = bf16 ? Vec<uint16_t>::N : Vec<float>::N;
+  return form_grid(P, dropout_form(P, vec), vec);
+}
+
 template <typename T>
 static hipError_t launch_form(const DropoutParams& P, hipStream_t st) {
   const int64_t n = P.rows * P.cols;
-  const bool flat = P.rows == 1 || (P.ldx == P.cols && (!P.add || P.ldadd == P.cols));
-  const int form = flat ? kFlat : P.cols % Vec<T>::N == 0 ? kRowVecs : kElements;
-  const int64_t per = 256 * (form == kElements ? 4 : Vec<T>::N);
-  const int64_t grid = (n + per - 1) / per;
-  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
+  const int form = dropout_form(P, Vec<T>::N);
+  const int64_t grid = form_grid(P, form, Vec<T>::N);
   if (form == kFlat)
     dropout_kernel<T, kFlat><<<grid, 256, 0, st>>>(P, n);
   else if (form == kRowVecs)

@@ -22,6 +22,7 @@ struct Int8QuantParams {
   float* scales;            // [rows]
   uint64_t seed;
 };
+int64_t int8_quantize_grid(int64_t rows, int cols16, bool bf16);
 hipError_t launch_int8_quantize(const Int8QuantParams& P, bool bf16, hipStream_t st);
 
 struct Int8QuantTParams {
@@ -32,6 +33,7 @@ struct Int8QuantTParams {
   float* scales;            // [batch][cols]
   uint64_t seed;
 };
+int64_t int8_quantize_t_grid(int64_t batch, int cols);   // workgroups of 512 threads
 hipError_t launch_int8_quantize_t(const Int8QuantTParams& P, bool bf16, hipStream_t st);
 
 // Rows that the few-row kernel quantises itself, into LDS: of one matrix up to this many (every

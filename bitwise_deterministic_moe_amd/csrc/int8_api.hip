@@ -15,9 +15,7 @@ constexpr size_t kWsAlign = 256;
 constexpr int64_t kMaxLd = (int64_t)1 << 20;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 
-moe_status hip_status(hipError_t e) {
-  return e == hipSuccess ? MOE_OK : e == hipErrorInvalidConfiguration ? MOE_ERR_SHAPE : MOE_ERR_HIP;
-}
+moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 size_t align_up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 int size_of(int dtype) { return dtype == MOE_F32 ? 4 : dtype == MOE_BF16 ? 2 : 1; }
@@ -112,7 +110,9 @@ moe_status check(const moe_int8* p) {
   if (p->num_local < 0 || p->num_local > kInt8MaxGroups) return MOE_ERR_SHAPE;
   if (p->ldx < p->d_in || p->ldx >= kMaxLd || p->ldy < p->d_out || p->ldy >= kMaxLd || p->ldr < 0 || p->ldr >= kMaxLd) return MOE_ERR_SHAPE;
   if (p->x_dtype == MOE_I8 && (p->d_in % 16 || p->ldx % 16)) return MOE_ERR_SHAPE;
-  if (units(p, choose(p, up16(p->d_in))) > kMaxGrid) return MOE_ERR_SHAPE;
+  const Choice c = choose(p, up16(p->d_in));
+  if (units(p, c) > kMaxGrid) return MOE_ERR_SHAPE;
+  if (p->x_dtype != MOE_I8 && !c.fused && int8_quantize_grid(p->rows, up16(p->d_in), p->x_dtype == MOE_BF16) > kMaxGrid) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 
@@ -214,7 +214,7 @@ MOE_API moe_status moe_int8_quantize(const void* x, moe_dtype dtype, int64_t row
                                      int8_t* codes, float* scales, uint64_t debug_shuffle_seed, void* stream) {
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_DTYPE;
   if (rows < 0 || rows >= (int64_t)1 << 31 || cols < 1 || cols > kInt8MaxK || ldx < cols || ldx >= kMaxElems) return MOE_ERR_SHAPE;
-  if (rows * (double)ldx > (double)kMaxElems) return MOE_ERR_SHAPE;
+  if (rows * (double)ldx > (double)kMaxElems || int8_quantize_grid(rows, up16(cols), dtype == MOE_BF16) > kMaxGrid) return MOE_ERR_SHAPE;
   if (rows == 0) return MOE_OK;
   if (!x || !codes || !scales) return MOE_ERR_NULL;
   if (!aligned(x, size_of(dtype)) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_SHAPE;
@@ -234,9 +234,8 @@ MOE_API moe_status moe_int8_quantize_t(const void* w, moe_dtype dtype, int64_t b
                                        int8_t* codes, float* scales, uint64_t debug_shuffle_seed, void* stream) {
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_DTYPE;
   if (batch < 0 || rows < 1 || rows > kInt8MaxK || cols < 1 || cols >= kMaxLd) return MOE_ERR_SHAPE;
-  if (batch * (double)rows * (double)cols > (double)kMaxElems ||
-      batch * (double)((cols + 63) / 64) > (double)(kMaxGrid / 2))   // workgroups of 512 threads
-    return MOE_ERR_SHAPE;
+  if (batch * (double)rows * (double)cols > (double)kMaxElems) return MOE_ERR_SHAPE;
+  if (int8_quantize_t_grid(batch, (int)cols) > kMaxGrid / 2) return MOE_ERR_SHAPE;   // workgroups of 512 threads
   if (batch == 0) return MOE_OK;
   if (!w || !codes || !scales) return MOE_ERR_NULL;
   if (!aligned(w, size_of(dtype)) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_SHAPE;

@@ -9,9 +9,6 @@
 
 namespace moedet {
 
-// The launchers below return hipErrorInvalidConfiguration, with nothing enqueued, for more
-// than kMaxGrid workgroups.
-
 // ---------------------------------------------------------------------- sort
 constexpr int kSortMaxLocal = 1024;   // experts of a sort
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
@@ -68,6 +65,10 @@ struct RowsParams {
   float* dprob;            // [tokens k] or null
   uint64_t seed;
 };
+// Workgroups of a call (*_grid), from its sizes alone: the entry points refuse more than kMaxGrid.
+int64_t permute_grid(const RowsParams& P, int elem_bytes);
+int64_t unpermute_grid(const RowsParams& P, bool bf16);
+int64_t unpermute_bwd_grid(const RowsParams& P, bool bf16);
 hipError_t launch_permute(const RowsParams& P, int elem_bytes, hipStream_t st);
 hipError_t launch_unpermute(const RowsParams& P, bool bf16, hipStream_t st);
 hipError_t launch_unpermute_bwd(const RowsParams& P, bool bf16, hipStream_t st);
@@ -87,6 +88,7 @@ struct DropoutParams {
   float scale;
   uint64_t seed;
 };
+int64_t dropout_grid(const DropoutParams& P, bool bf16);
 hipError_t launch_dropout(const DropoutParams& P, bool bf16, hipStream_t st);
 
 }  // namespace moedet

@@ -356,39 +356,54 @@ __global__ __launch_bounds__(256) void unpermute_bwd_kernel(RowsParams P) {
   }
 }
 
-hipError_t launch_permute(const RowsParams& P, int es, hipStream_t st) {
+namespace {
+
+struct RowsPlan {
+  int L, S;        // threads of a token, parts of its slots
+  int64_t grid;
+};
+RowsPlan permute_plan(const RowsParams& P, int es) {
   const int L = row_threads(((int64_t)P.cols * es + 15) / 16, 64);
   const int64_t groups = (P.tokens + 256 / L - 1) / (256 / L);
   // too few tokens for the device: their slots are split too
   int64_t S = groups >= 512 ? 1 : (512 + groups - 1) / groups;
   if (S > P.k) S = P.k;
-  const int64_t grid = grid_for_units(groups * S);
-  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
-  if (L < 64)
-    permute_kernel<false, false><<<grid, 256, 0, st>>>(P, es, L, (int)S);
+  return {L, (int)S, grid_for_units(groups * S)};
+}
+
+}  // namespace
+
+int64_t permute_grid(const RowsParams& P, int es) { return permute_plan(P, es).grid; }
+hipError_t launch_permute(const RowsParams& P, int es, hipStream_t st) {
+  const RowsPlan p = permute_plan(P, es);
+  if (p.L < 64)
+    permute_kernel<false, false><<<p.grid, 256, 0, st>>>(P, es, p.L, p.S);
   else if (past_cache(P, es))
-    permute_kernel<true, true><<<grid, 256, 0, st>>>(P, es, L, (int)S);
+    permute_kernel<true, true><<<p.grid, 256, 0, st>>>(P, es, p.L, p.S);
   else
-    permute_kernel<true, false><<<grid, 256, 0, st>>>(P, es, L, (int)S);
+    permute_kernel<true, false><<<p.grid, 256, 0, st>>>(P, es, p.L, p.S);
   return hipGetLastError();
 }
 
-template <typename T>
-static hipError_t launch_sum(const RowsParams& P, hipStream_t st) {
+static RowsPlan sum_plan(const RowsParams& P, int vec) {
   // four waves a token, one where few tokens have any row (16384 tokens of 22 slots, 2048 bf16: 4 of
   // 512 experts 23 and 17.5 us, 64 of them 35 and 39; 4096 tokens, all 74 and 96)
   const bool few = P.tokens >= 4096 && 16 * P.nrows < P.tokens * P.k;
-  const int L = row_threads((P.cols + Vec<T>::N - 1) / Vec<T>::N, few ? 64 : 256);
-  const int64_t grid = grid_for_units((P.tokens + 256 / L - 1) / (256 / L));
-  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
-  if (L < 64)
-    unpermute_narrow_kernel<T><<<grid, 256, 0, st>>>(P, L);
+  const int L = row_threads((P.cols + vec - 1) / vec, few ? 64 : 256);
+  return {L, 1, grid_for_units((P.tokens + 256 / L - 1) / (256 / L))};
+}
+template <typename T>
+static hipError_t launch_sum(const RowsParams& P, hipStream_t st) {
+  const RowsPlan p = sum_plan(P, Vec<T>::N);
+  if (p.L < 64)
+    unpermute_narrow_kernel<T><<<p.grid, 256, 0, st>>>(P, p.L);
   else if (past_cache(P, sizeof(T)))
-    unpermute_kernel<T, true><<<grid, 256, 0, st>>>(P, L);
+    unpermute_kernel<T, true><<<p.grid, 256, 0, st>>>(P, p.L);
   else
-    unpermute_kernel<T, false><<<grid, 256, 0, st>>>(P, L);
+    unpermute_kernel<T, false><<<p.grid, 256, 0, st>>>(P, p.L);
   return hipGetLastError();
 }
+int64_t unpermute_grid(const RowsParams& P, bool bf16) { return sum_plan(P, bf16 ? Vec<uint16_t>::N : Vec<float>::N).grid; }
 hipError_t launch_unpermute(const RowsParams& P, bool bf16, hipStream_t st) {
   return bf16 ? launch_sum<uint16_t>(P, st) : launch_sum<float>(P, st);
 }
@@ -396,12 +411,19 @@ hipError_t launch_unpermute(const RowsParams& P, bool bf16, hipStream_t st) {
 // Slots from which a wave may take four of them (below, waves are too few: 32768 slots of which
 // 2048 have a row 10.5 us by one, 11.8 by four).
 constexpr int64_t kManySlots = 65536;
+static bool many_slots(const RowsParams& P, int vec) {
+  const int64_t n = P.tokens * P.k;
+  return n >= kManySlots && (3 * P.nrows < n || P.cols <= 64 * vec);
+}
+static int64_t bwd_grid(const RowsParams& P, bool many) {
+  const int64_t n = P.tokens * P.k;
+  return grid_for_units(many ? (n + 15) / 16 : (n + 3) / 4);
+}
+int64_t unpermute_bwd_grid(const RowsParams& P, bool bf16) { return bwd_grid(P, many_slots(P, bf16 ? Vec<uint16_t>::N : Vec<float>::N)); }
 template <typename T>
 static hipError_t launch_bwd(const RowsParams& P, hipStream_t st) {
-  const int64_t n = P.tokens * P.k;
-  const bool many = n >= kManySlots && (3 * P.nrows < n || P.cols <= 64 * Vec<T>::N), past = past_cache(P, sizeof(T));
-  const int64_t grid = grid_for_units(many ? (n + 15) / 16 : (n + 3) / 4);
-  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
+  const bool many = many_slots(P, Vec<T>::N), past = past_cache(P, sizeof(T));
+  const int64_t grid = bwd_grid(P, many);
   if (many && past)
     unpermute_bwd_kernel<T, true, 4><<<grid, 256, 0, st>>>(P);
   else if (many)

@@ -14,9 +14,7 @@ constexpr size_t kWsAlign = 256;
 constexpr int64_t kMaxCols = (int64_t)1 << 24;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 
-moe_status hip_status(hipError_t e) {
-  return e == hipSuccess ? MOE_OK : e == hipErrorInvalidConfiguration ? MOE_ERR_SHAPE : MOE_ERR_HIP;
-}
+moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 int elem_bytes(int dtype) {
   switch (dtype) {
@@ -71,7 +69,6 @@ moe_status sum_rows(const void* rows, int dtype, int64_t tokens, int32_t top_k, 
   if (add && (ldadd < cols || ldadd > kMaxElems || tokens * (double)ldadd > (double)kMaxElems)) return MOE_ERR_SHAPE;
   if (!aligned(rows, es) || !aligned(prob, 4) || !aligned(add, es)) return MOE_ERR_SHAPE;
   if (tokens == 0) return MOE_OK;
-  if (nrows > 0 && !rows) return MOE_ERR_NULL;
   RowsParams P{};
   P.tokens = tokens;
   P.k = top_k;
@@ -84,6 +81,8 @@ moe_status sum_rows(const void* rows, int dtype, int64_t tokens, int32_t top_k, 
   P.ldadd = ldadd;
   P.out = y;
   P.seed = seed;
+  if (unpermute_grid(P, dtype == MOE_BF16) > kMaxGrid) return MOE_ERR_SHAPE;
+  if (nrows > 0 && !rows) return MOE_ERR_NULL;
   return hip_status(launch_unpermute(P, dtype == MOE_BF16, (hipStream_t)stream));
 }
 
@@ -96,8 +95,6 @@ moe_status dropout(const void* x, const void* add, int dtype, int64_t rows, int6
   if (ldx > kMaxElems || rows * (double)ldx > (double)kMaxElems) return MOE_ERR_SHAPE;
   if (add && (ldadd > kMaxElems || rows * (double)ldadd > (double)kMaxElems)) return MOE_ERR_SHAPE;
   if (rows == 0) return MOE_OK;
-  if (!x || !y || !rng) return MOE_ERR_NULL;
-  if (!aligned(x, es) || !aligned(y, es) || !aligned(add, es) || !aligned(rng, 8)) return MOE_ERR_SHAPE;
   DropoutParams P{};
   P.rows = rows;
   P.cols = (int)cols;
@@ -112,6 +109,9 @@ moe_status dropout(const void* x, const void* add, int dtype, int64_t rows, int6
   P.all = limit >> 32;
   P.scale = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.f;
   P.seed = seed;
+  if (dropout_grid(P, dtype == MOE_BF16) > kMaxGrid) return MOE_ERR_SHAPE;
+  if (!x || !y || !rng) return MOE_ERR_NULL;
+  if (!aligned(x, es) || !aligned(y, es) || !aligned(add, es) || !aligned(rng, 8)) return MOE_ERR_SHAPE;
   return hip_status(launch_dropout(P, dtype == MOE_BF16, (hipStream_t)stream));
 }
 
@@ -165,7 +165,6 @@ MOE_API moe_status moe_permute_fwd(const void* x, moe_dtype dtype, int64_t token
   const int es = elem_bytes(dtype);
   if (!aligned(rows, es)) return MOE_ERR_SHAPE;
   if (tokens == 0 || nrows == 0) return MOE_OK;
-  if (!rows) return MOE_ERR_NULL;
   RowsParams P{};
   P.tokens = tokens;
   P.k = top_k;
@@ -176,6 +175,8 @@ MOE_API moe_status moe_permute_fwd(const void* x, moe_dtype dtype, int64_t token
   P.ldx = ldx;
   P.out = rows;
   P.seed = debug_shuffle_seed;
+  if (permute_grid(P, es) > kMaxGrid) return MOE_ERR_SHAPE;
+  if (!rows) return MOE_ERR_NULL;
   return hip_status(launch_permute(P, es, (hipStream_t)stream));
 }
 
@@ -200,7 +201,6 @@ MOE_API moe_status moe_unpermute_bwd(const void* dy, int64_t lddy, const void* r
   const int es = elem_bytes(dtype);
   if (!aligned(rows, es) || !aligned(drows, es) || !aligned(prob, 4) || !aligned(dprob, 4)) return MOE_ERR_SHAPE;
   if (tokens == 0) return MOE_OK;
-  if (!prob || (nrows > 0 && (!drows || (dprob && !rows)))) return MOE_ERR_NULL;
   RowsParams P{};
   P.tokens = tokens;
   P.k = top_k;
@@ -214,6 +214,8 @@ MOE_API moe_status moe_unpermute_bwd(const void* dy, int64_t lddy, const void* r
   P.out = drows;
   P.dprob = dprob;
   P.seed = debug_shuffle_seed;
+  if (unpermute_bwd_grid(P, dtype == MOE_BF16) > kMaxGrid) return MOE_ERR_SHAPE;
+  if (!prob || (nrows > 0 && (!drows || (dprob && !rows)))) return MOE_ERR_NULL;
   return hip_status(launch_unpermute_bwd(P, dtype == MOE_BF16, (hipStream_t)stream));
 }
 

@@ -843,7 +843,7 @@ moe_status moe_glu_bwd(const moe_dense* p, const void* da, const void* x, const 
  * elements, at least cols) where a call says so; row matrices are contiguous
  * [nrows, cols], and rows that no slot names stay as they are.  tokens * top_k
  * is below 2^31, cols at most 2^24, every matrix at most 2^40 elements; a
- * call that would take more than 2^24 workgroups is refused, MOE_ERR_SHAPE (none
+ * call that would take more than 2^24 - 8 workgroups is refused, MOE_ERR_SHAPE (none
  * of fewer than 16 million tokens and 64 million slots does).
  * Outputs must not overlap inputs, but where a call says so. */
 
@@ -927,7 +927,8 @@ moe_status moe_unpermute_bwd(const void* dy, int64_t lddy, const void* rows, moe
 /* Codes and scales of the rows of x.
  *   x        DEVICE [rows, cols], row distance ldx, MOE_F32 or MOE_BF16
  *   codes    DEVICE int8 [rows, K16] output, 16-byte aligned;  scales  DEVICE float[rows] output
- * A call that would take more than 2^24 workgroups (2^23 of moe_int8_quantize_t) is
+ * A call that would take more than 2^24 - 8 workgroups (2^23 - 8 of moe_int8_quantize_t, 64
+ * columns of a matrix each) is
  * refused.  Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_NULL before anything is
  * enqueued; MOE_ERR_HIP for a launch failure. */
 moe_status moe_int8_quantize(const void* x, moe_dtype dtype, int64_t rows, int64_t cols, int64_t ldx, int8_t* codes,
@@ -953,7 +954,7 @@ moe_status moe_int8_quantize_t(const void* w, moe_dtype dtype, int64_t batch, in
  *   ldx, ldy, ldr  row distances of x, y and the residual (unread without
  *              one), below 2^20
  *   debug_shuffle_seed  0, or a test-only seed that shuffles the launch order
- * A call whose launch could take more than 2^24 workgroups is refused (MOE_ERR_SHAPE). */
+ * A call of which a launch could take more than 2^24 - 8 workgroups is refused (MOE_ERR_SHAPE). */
 typedef struct moe_int8 {
   int64_t rows;
   int32_t d_in;
@@ -1030,8 +1031,8 @@ moe_status moe_int8_experts(const moe_int8* p, const void* x, const float* x_sca
  *             kernel runs, so a captured graph takes new ones at each replay
  *   y         DEVICE [rows,cols] contiguous, output; may be x or the residual
  *             (with a row distance of cols)
- * rows * ld is at most 2^40, and a call that would take more than 2^24 workgroups of
- * 1024 elements is refused, MOE_ERR_SHAPE.  Base addresses are multiples of the element size.
+ * rows * ld is at most 2^40, and a call that would take more than 2^24 - 8 workgroups of 1024
+ * elements (2048 of bf16 in contiguous matrices or rows of a multiple of 8) is refused, MOE_ERR_SHAPE.  Base addresses are multiples of the element size.
  * Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_NULL before anything is
  * enqueued; MOE_ERR_HIP for a launch failure. */
 moe_status moe_dropout_fwd(const void* x, const void* residual, moe_dtype dtype, int64_t rows, int64_t cols,

@@ -409,3 +409,22 @@ def test_expert_layer_from_its_pieces(tokens, k, experts, d, f):
     kept = oracle.dropout_mask(tokens * d, 0.1, 5, 0).reshape(tokens, d)
     want = np.where(kept, _f64(y) / 0.9, 0) + _f64(x)
     assert (np.abs(_f64(z) - want) <= 2.0 ** -8 * np.abs(want) + 4 * E * (np.abs(_f64(y)) / 0.9 + np.abs(_f64(x)))).all()
+
+
+def test_the_largest_grids():
+    """The most rows and matrices that the quantisers take: 2^24 - 8 workgroups of four rows, 2^23 - 8 of a matrix."""
+    rows = 4 * ((1 << 24) - 8)
+    x = torch.ones((rows, 1), dtype=torch.bfloat16, device=DEV)
+    x[-1], x[rows // 2] = -2, 0
+    codes, scales = moe.moe_int8_quantize(x)
+    assert int((codes[:, 0] == 127).sum()) == rows - 2 and int(codes[-1, 0]) == -127 and int(codes[rows // 2, 0]) == 0
+    assert not codes[:, 1:].any() and scales[-1].item() == np.float32(2) / np.float32(127) and scales[rows // 2].item() == 0
+    del x, codes, scales
+    batch = (1 << 23) - 8
+    w = torch.ones((batch, 1, 2), dtype=torch.bfloat16, device=DEV)
+    w[-1, 0, 1], w[batch // 2, 0, 0] = -2, 0
+    codes, scales = moe.moe_int8_quantize_t(w)
+    assert int((codes[..., 0] == 127).sum()) == 2 * batch - 2 and int(codes[-1, 1, 0]) == -127 and int(codes[batch // 2, 0, 0]) == 0
+    assert not codes[..., 1:].any() and scales[-1, 1].item() == np.float32(2) / np.float32(127)
+    with pytest.raises(moe.MoeError, match="status 2"):
+        moe.moe_int8_quantize_t(torch.ones((batch + 1, 1, 2), dtype=torch.bfloat16, device=DEV))

@@ -449,3 +449,30 @@ def test_more_than_2_31_bytes_and_elements():
     y = moe.moe_dropout_fwd(torch.ones((n, cols), dtype=BF16, device=DEV), 0.5, _rng(2, 7))
     at = n * cols - 4096
     assert np.array_equal(_f64(y.reshape(-1)[at:]) != 0, oracle.dropout_mask(4096, 0.5, 2, 7 + at // 4))
+
+
+def test_the_largest_grids():
+    """The most tokens of one column that the calls take: 2^24 - 8 workgroups, the numbers of the last ones looked at."""
+    t = 32 * ((1 << 24) - 8)
+    slot_row = torch.full((t, 1), -1, dtype=torch.int32, device=DEV)
+    at = torch.tensor([0, 31, 32, t // 2, t - 33, t - 32, t - 1], device=DEV)
+    slot_row[at, 0] = torch.arange(7, dtype=torch.int32, device=DEV)
+    x = torch.zeros((t, 1), dtype=torch.uint8, device=DEV)
+    x[at, 0] = torch.arange(1, 8, dtype=torch.uint8, device=DEV)
+    assert moe.moe_permute_fwd(x, slot_row, rows=torch.zeros((7, 1), dtype=torch.uint8, device=DEV))[:, 0].tolist() == list(range(1, 8))
+    del x
+    rows = torch.arange(1, 8, device=DEV).to(BF16)[:, None].contiguous()
+    y = moe.moe_unpermute_fwd(rows, slot_row)
+    assert y[at, 0].tolist() == list(range(1, 8)) and int((y != 0).sum()) == 7
+    del y
+    n = t // 2                                    # 16 slots a workgroup
+    slot_row = slot_row[n:]
+    prob = torch.full((n, 1), 3.0, device=DEV)
+    drows, dprob = moe.moe_unpermute_bwd(torch.full((n, 1), 2.0, dtype=BF16, device=DEV), rows, slot_row, prob)
+    assert drows[3:, 0].tolist() == [6.0] * 4     # the named rows of this half
+    assert dprob[at[3:] - n, 0].tolist() == [8.0, 10.0, 12.0, 14.0] and int((dprob != 0).sum()) == 4
+    for tokens, call in ((t + 1, lambda s: moe.moe_unpermute_fwd(rows, s)),
+                         (n + 1, lambda s: moe.moe_unpermute_bwd(torch.empty((n + 1, 1), dtype=BF16, device=DEV), rows, s,
+                                                                 torch.empty((n + 1, 1), device=DEV)))):
+        with pytest.raises(moe.MoeError, match="status 2"):
+            call(torch.full((tokens, 1), -1, dtype=torch.int32, device=DEV))

@@ -199,6 +199,46 @@ def test_quantize_t_status(status, o):
     assert moe.load_library().moe_int8_quantize_t(a["x"], a["dt"], a["batch"], a["rows"], a["cols"], a["c"], a["s"], 0, None) == status
 
 
+# The last size inside the grid's limit and the first one outside; a pointer is missing, so that neither is launched.
+LIMIT = (1 << 24) - 8
+
+
+def test_grid_limits_of_the_quantisers():
+    lib = moe.load_library()
+    for rows, cols in ((4 * LIMIT, 8), (4 * LIMIT, 4096), (LIMIT, 4097)):      # four rows a workgroup, or one
+        assert lib.moe_int8_quantize(None, 1, rows, cols, cols, A, A, 0, None) == NULL
+        assert lib.moe_int8_quantize(None, 1, rows + 1, cols, cols, A, A, 0, None) == SHAPE
+    most = (1 << 23) - 8
+    for batch, cols in ((most, 64), (most // 8, 512)):                          # 64 columns a workgroup
+        assert lib.moe_int8_quantize_t(None, 1, batch, 8, cols, A, A, 0, None) == NULL
+        assert lib.moe_int8_quantize_t(None, 1, batch + 1, 8, cols, A, A, 0, None) == SHAPE
+
+
+@pytest.mark.parametrize("x_dtype", ["i8", "bf16"])
+@pytest.mark.parametrize("k,f,local", [(16, 16, 0), (2048, 2048, 0), (8192, 8192, 0), (16, 16, 8), (2048, 2048, 64)])
+def test_grid_limits_of_the_products(x_dtype, k, f, local):
+    def fits(rows):
+        try:
+            moe.moe_int8_workspace_size(rows, k, f, local, x_dtype)
+            return True
+        except moe.MoeError as e:
+            assert "status 2" in str(e)
+            return False
+
+    lo, hi = 1, (1 << 31) - 1
+    assert fits(lo) and not fits(hi)
+    while hi - lo > 1:
+        mid = (lo + hi) // 2
+        lo, hi = (mid, hi) if fits(mid) else (lo, mid)
+    name = moe.moe_int8_stage_names(lo, k, f, local, x_dtype)[-1]
+    bm, bn = (int(n) for n in name.split("_")[1].split("x"))
+    units = lambda rows: (rows // bm + max(local, 1)) * ((f + bn - 1) // bn)  # noqa: E731
+    # quantised four rows a workgroup, or one of more than 4096 columns
+    quantised = lambda rows: 0 if x_dtype == "i8" else (rows + 3) // 4 if k <= 4096 else rows  # noqa: E731
+    assert units(lo) <= LIMIT and quantised(lo) <= LIMIT
+    assert units(hi) > LIMIT or quantised(hi) > LIMIT
+
+
 # --------------------------------------------------------------------- kernels
 def test_cases_reach_every_kernel():
     for kernel, *case in int8_cases.LINEAR:

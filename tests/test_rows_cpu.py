@@ -239,6 +239,32 @@ def test_launches_beyond_the_grid():
     assert _dropout(rows=1 << 36) == SHAPE
 
 
+# The last size inside the grid's limit and the first one outside, with a pointer missing, so that neither is launched:
+# tokens of 32, 4 and 1 a workgroup, slots of 16 and 4, elements of 2048 and 1024.
+LIMIT = (1 << 24) - 8
+
+
+@pytest.mark.parametrize("call,tokens,o", [
+    (lambda **o: _permute(rows=None, **o), 32 * LIMIT, dict()), (lambda **o: _permute(rows=None, **o), 4 * LIMIT, dict(cols=2048, ld=2048)),
+    (lambda **o: _permute(False, rows=None, **o), 32 * LIMIT, dict()),
+    (lambda **o: _permute(False, rows=None, **o), 4 * LIMIT, dict(cols=2048, ld=2048)),
+    (lambda **o: _permute(False, rows=None, **o), LIMIT, dict(cols=2048, ld=2048, n=LIMIT)),
+    (lambda **o: _permute(False, rows=None, **o), LIMIT, dict(dt=0, cols=1000, n=LIMIT)),
+    (lambda **o: _unpermute_bwd(prob=None, **o), 16 * LIMIT, dict()),
+    (lambda **o: _unpermute_bwd(prob=None, **o), 4 * LIMIT, dict(cols=1000, ld=1000, n=4 * LIMIT)),
+])
+def test_grid_limits_of_the_rows(call, tokens, o):
+    assert call(k=1, t=tokens, **o) == NULL and call(k=1, t=tokens + 1, **o) == SHAPE
+
+
+@pytest.mark.parametrize("per,o", [(2048, dict()), (2048, dict(ldx=9)), (1024, dict(cols=1, ldx=2, ldr=1)), (1024, dict(dt=0)),
+                                   (1024, dict(dt=0, ldx=9))])
+def test_grid_limits_of_dropout(per, o):
+    cols = o.get("cols", 8)
+    rows = per * LIMIT // cols
+    assert _dropout(rows=rows, y=None, **o) == NULL and _dropout(rows=rows + 1, y=None, **o) == SHAPE
+
+
 def _dropout(**o):
     a = dict(x=A, res=None, dt=1, rows=4, cols=8, ldx=8, ldr=8, p=0.1, rng=A, y=A)
     a.update(o)
