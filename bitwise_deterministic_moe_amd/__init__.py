@@ -1280,7 +1280,8 @@ def moe_permute_fwd(x: torch.Tensor, slot_row: torch.Tensor, rows=None, shuffle_
     """rows[slot_row[t, j]] = x[t] for x [T, D] (float32, bf16, int8 or uint8;
     any row distance) and slot_row [T, k] (or flat) of moe_sort or a Routing.
     Returns rows, the matrix given or a new one of T * k rows; rows that no slot
-    names stay as they are."""
+    names stay as they are.  The calls on rows choose their kernels by the matrix's
+    size: give one of fewer rows where few slots can have one."""
     lib, what = load_library(), "moe_permute_fwd"
     code = _ROW_CODE.get(x.dtype)
     if code is None or x.dim() != 2 or x.shape[1] < 1:

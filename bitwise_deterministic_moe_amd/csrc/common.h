@@ -95,7 +95,7 @@ DEV int64_t map_unit(int64_t b, int64_t U, uint64_t seed) {
 
 // The same for kernels that stream through memory once and share nothing: unit b to
 // workgroup b, so that the XCDs read neighbouring addresses at about the same time
-// (dropout of 16384 x 2048 bf16 with its gradient 77.8 us in runs an XCD, 63.7 so).
+// (dropout of 16384 x 2048 bf16 with its gradient, in turn on one card, 77.8 us in runs an XCD, 63.7 so).
 DEV int64_t stream_unit(int64_t b, int64_t U, uint64_t seed) {
   if (b >= U) return -1;
   if (!seed) return b;

@@ -5,9 +5,10 @@
 // Philox 4x32 with 10 rounds (Salmon, Moraes, Dror, Shaw, "Parallel random
 // numbers: as easy as 1, 2, 3", 2011) at counter first + i / 4 under the key;
 // it is dropped where the word is below round(p 2^32).  y = x scale + add for
-// a kept element, add (or 0) for a dropped one, one rounding.
+// a kept element, add (or 0) for a dropped one: one fused multiply-add in float32 (where x scale
+// and add cancel, their difference keeps what a rounded product would lose), rounded to the type.
 //
-// Bound by HBM (16384 x 2048 bf16 with a residual and its gradient, 335 MB: 63.7 us, 5.3
+// Bound by HBM (16384 x 2048 bf16 with a residual and its gradient, 335 MB: 64 to 74 us, 4.5 to 5.3
 // TB/s): the 19 products of 64 bits behind four elements, quarter-rate instructions,
 // run beside the loads.
 #include "rows.h"

@@ -103,8 +103,8 @@ DEV void put_codes(int8_t* out, const typename Vec<T>::raw& v, const RowScale& s
 
 // L threads a row (64: four rows a workgroup; 256: one).  The first kQuantKeep
 // vectors of a thread stay in registers between the two passes, the others are read again.
-// Bound by HBM where rows are many: 16384 x 2048 bf16 24.7 us (4.1 TB/s), 4096 x 2048 7.3, of
-// it 2 the launch.
+// Bound by HBM where rows are many: 16384 x 2048 bf16 21.6 to 24.7 us (4.1 to 4.7 TB/s), 4096 x
+// 2048 7.3, of it 2 the launch.
 constexpr int kQuantKeep = 8;
 template <typename T, int L>
 __global__ __launch_bounds__(256) void int8_quantize_kernel(Int8QuantParams P) {
@@ -551,8 +551,8 @@ DEV void emit_rows(const DenseParams& P, int64_t row, int64_t end, int col, floa
 
 // WGS: workgroups that share a CU (its registers and LDS), so that one's first loads and
 // epilogue run beside another's slices.
-// 8192^3 450 us, 2.4 POP/s: matrix units busy 62% of the cycles, at the 1.5 to 1.8 GHz that
-// the power leaves.  4096 x 8192 x 2048 72 us: of each of its two rounds (256 x 256) 5 the launch and
+// 8192^3 436 to 450 us, 2.4 to 2.5 POP/s: matrix units busy 62 to 68% of the cycles, at the 1.5 to 1.8 GHz
+// that the power leaves.  4096 x 8192 x 2048 69 to 72 us: of each of its two rounds (256 x 256) 5 the launch and
 // first slice, 23 the slices, 8 the 33 MB stored; GELU adds 5 to 7, which nothing hides.
 // A contraction split into S chunks (one group only): each workgroup leaves its sums in
 // the workspace, and int8_join_kernel adds them and runs the epilogue.  (The last workgroup
@@ -694,7 +694,7 @@ __global__ __launch_bounds__(256) void int8_join_kernel(Int8Params P) {
 // while its first weights are on the way: a launch of 4 to 5 us saved (1 x 2048 x 2048 5.8
 // us, 3.9 and 4.4 in two launches).
 // Bound by the weights' stream where experts are many (a token's 22 experts of 2048 x 2048, 92
-// MB: 18.8 us, 4.9 TB/s), by latency below (4.2 MB: 5.8).
+// MB: 18.8 to 19.8 us, 4.6 to 4.9 TB/s), by latency below (4.2 MB: 4.9 to 6.0).
 constexpr int kFewWaves = 4, kFewDepth = 8;
 template <typename T, bool GROUPS, bool FUSED>
 __global__ __launch_bounds__(64 * kFewWaves) void int8_few_kernel(Int8Params P, int ks) {

@@ -24,7 +24,9 @@ int up16(int64_t n) { return (int)((n + 15) / 16 * 16); }
 constexpr int kCUs = 256;
 
 // The kernel of a product: few rows (ks > 0, fused: x is quantised by it), or a tile and the
-// chunks of its contraction.
+// chunks of its contraction.  Of experts, p->rows are the rows that x has room for: how many there are is
+// known on the GPU alone.  (About 2050 rows of 4 experts, 2048 x 2048, in an x of as many 28.6 us, of 65536
+// rows 39.9, of 360448 60: larger tiles, and workgroups without a tile.)
 struct Choice {
   int ks, tile, S;
   bool fused;

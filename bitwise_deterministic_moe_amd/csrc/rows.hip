@@ -4,7 +4,7 @@
 //  unpermute      y[t] = sum over j ascending of p[t, j] rows[slot_row[t, j]],
 //                 float32 from 0, then add[t], rounded once.  Without p it is
 //                 permute's backward.
-//  unpermute_bwd  drows[slot_row[t, j]] = p[t, j] dy[t], rounded once;
+//  unpermute_bwd  drows[slot_row[t, j]] = p[t, j] dy[t] in float32, rounded to the type;
 //                 dprob[t, j] = <dy[t], rows[slot_row[t, j]]> in float32, each
 //                 lane over its columns ascending, then a fixed tree over the lanes.
 //
@@ -26,7 +26,10 @@ typedef uint32_t u32x4_b_t __attribute__((ext_vector_type(4), aligned(1)));
 // kernel's reads wait for their write-back.  4096 tokens of 22 slots, 2048 bf16 (369 MB of
 // rows): copied and summed back 177 us through the caches, 150 past them, gradients
 // 161 and 167 us alone but 246 and 218 behind the forward.  180 MB copied and summed back:
-// 37 and 42 us.
+// 37 and 42 us.  How many slots have a row is known on the GPU alone, so the size of the matrix
+// decides, here and below: one that is larger than its rows need may be taken for one that the
+// cache cannot hold (16384 tokens of 22 slots with 4 of 512 experts here, 2048 bf16, about 2050 rows
+// summed back: 20.5 us in a matrix of 65536 rows, 25.6 past the cache in one of 360448).
 constexpr int64_t kLastLevelBytes = (int64_t)256 << 20;
 bool past_cache(const RowsParams& P, int es) {
   const int64_t slots = P.tokens * P.k;
@@ -97,7 +100,7 @@ DEV void each_slot(uint64_t mask, int32_t r, F f) {
 }
 
 // WHOLE: L >= 64, so a wave has one token.
-// 4096 tokens of 22 slots, 2048 bf16 (386 MB): 70 us, 5.5 TB/s.  16384 tokens of
+// 4096 tokens of 22 slots, 2048 bf16 (386 MB): 75 to 78 us, 5.0 to 5.2 TB/s.  16384 tokens of
 // which 2816 slots have a row: 42 us where every token's row was read and every
 // slot looked at in turn by four waves a token, 21 with the ballot, 10 with one wave.
 template <bool WHOLE, bool PAST>
@@ -289,16 +292,18 @@ __global__ __launch_bounds__(256) void unpermute_kernel(RowsParams P, int L) {
   }
 }
 
-// A wave G slots: four where less than a third of many has a row (a rank with few of the experts;
-// those that have one are found by a ballot) or a row is one load of a wave, one otherwise.  By
-// one and by four, 16384 tokens of 22 slots, 2048 bf16, with 4, 64, 128 and 256 of 512 experts: 46
+// A wave G slots: four where less than a third of many can have a row, by the rows of the matrix (a
+// rank with few of the experts; those that have one are found by a ballot), or a row is one load of
+// a wave, one otherwise.  By one and by four, 16384 tokens of 22 slots, 2048 bf16, with 4, 64, 128
+// and 256 of 512 experts in a matrix of as many rows as slots have one: 46
 // and 21 us, 144 and 104, 206 and 178, 336 and 328; 4096 tokens, 256 of 512: 92 and 95; all
-// slots with a row: 131072 of 512 columns 71 and 57, 65536 of 1024 63 and 76.
+// slots with a row: 131072 of 512 columns 71 and 57, 65536 of 1024 63 and 76.  The 4 of 512 in a
+// matrix of 65536 rows 19.3, of 360448, which could hold a row of every slot, 41.
 // Rows that the caches cannot hold are taken in the order of the
 // slots, not in runs an XCD: rows of one expert that lie side by side are then
 // read and written at about the same time (369 MB of rows behind the forward:
 // 243 us in runs, 218 so; 6 MB of them 6.6 and 8.4 us).  4096 tokens of 22 slots, 2048 bf16:
-// 755 MB in 165 us, 4.6 TB/s; 5.7 were the rows in the slots' order.
+// 755 MB in 158 to 169 us, 4.5 to 4.8 TB/s; 5.7 were the rows in the slots' order.
 template <typename T, bool PAST, int G>
 __global__ __launch_bounds__(256) void unpermute_bwd_kernel(RowsParams P) {
   constexpr int V = Vec<T>::N;
@@ -386,8 +391,9 @@ hipError_t launch_permute(const RowsParams& P, int es, hipStream_t st) {
 }
 
 static RowsPlan sum_plan(const RowsParams& P, int vec) {
-  // four waves a token, one where few tokens have any row (16384 tokens of 22 slots, 2048 bf16: 4 of
-  // 512 experts 23 and 17.5 us, 64 of them 35 and 39; 4096 tokens, all 74 and 96)
+  // four waves a token, one where few tokens can have any row, by the rows of the matrix (16384 tokens of
+  // 22 slots, 2048 bf16, as many rows as slots have one: 4 of 512 experts 23 and 17.5 us, 64 of them 35
+  // and 39; 4096 tokens, all 74 and 96).  The 4 of 512 in a matrix of tokens x 4 rows take four waves, 20.5.
   const bool few = P.tokens >= 4096 && 16 * P.nrows < P.tokens * P.k;
   const int L = row_threads((P.cols + vec - 1) / vec, few ? 64 : 256);
   return {L, 1, grid_for_units((P.tokens + 256 / L - 1) / (256 / L))};

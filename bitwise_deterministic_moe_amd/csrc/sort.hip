@@ -14,8 +14,9 @@
 //                     lane's rank among equal experts comes from ballots.
 //                     With one chunk it is the whole sort.
 //
-// Bound by latency: 22 slots of 512 experts 5.0 us in one launch, 90112 slots 11.4 in two
-// (1.1 MB), 1441792 slots 26 (most of it the ballots, one a bit of the expert's number).
+// Bound by latency: 22 slots of 512 experts 4.9 us in one launch, 90112 slots 11.3 in two
+// (1.1 MB), 1441792 slots 26 (most of it the ballots, one a bit of the expert's number), again and
+// again in a graph; 13.3 for the 90112 among other calls, whose indices come from memory.
 #include "common.h"
 #include "rows.h"
 

@@ -845,6 +845,9 @@ moe_status moe_glu_bwd(const moe_dense* p, const void* da, const void* x, const 
  * is below 2^31, cols at most 2^24, every matrix at most 2^40 elements; a
  * call that would take more than 2^24 - 8 workgroups is refused, MOE_ERR_SHAPE (none
  * of fewer than 16 million tokens and 64 million slots does).
+ * How many slots have a row is known on the GPU alone, so sizes decide which kernel takes a
+ * call, nrows among them (and, of moe_int8_experts, rows).  Results do not depend on it, but a matrix
+ * with many more rows than slots have one costs time where few slots have one.
  * Outputs must not overlap inputs, but where a call says so. */
 
 /* Workspace bytes of moe_sort (0 for few slots).  Errors: MOE_ERR_SHAPE, MOE_ERR_NULL. */
@@ -898,7 +901,7 @@ moe_status moe_unpermute_fwd(const void* rows, moe_dtype dtype, int64_t tokens, 
                              const int32_t* slot_row, int64_t nrows, const float* prob, const void* residual,
                              int64_t ldr, void* y, uint64_t debug_shuffle_seed, void* stream);
 
-/* Its gradients: drows[slot_row[t,j]] = prob[t,j] dy[t], rounded once, and
+/* Its gradients: drows[slot_row[t,j]] = prob[t,j] dy[t], in float32 and rounded to the type, and
  * dprob[t,j] = <dy[t], rows[slot_row[t,j]]> in float32 (0 for a slot without a
  * row), in an order fixed by cols.  The residual's gradient is dy itself.
  *   dy        DEVICE [T,cols], row distance lddy
@@ -1022,8 +1025,8 @@ moe_status moe_int8_experts(const moe_int8* p, const void* x, const float* x_sca
  * (its upper 64 bits 0) under the key rng[0].  It is dropped where the word
  * is below round(p 2^32).  A call uses ceil(rows * cols / 4) counters: the next
  * one starts there.
- *   y = residual + (dropped ? 0 : x * scale), scale = 1 / (1 - p) in float32,
- *   one rounding
+ *   y = residual + (dropped ? 0 : x * scale), scale = 1 / (1 - p) in float32, a fused
+ *   multiply-add in float32, rounded to the type
  *   x         DEVICE [rows,cols], row distance ldx, MOE_F32 or MOE_BF16
  *   residual  DEVICE [rows,cols], row distance ldr, or NULL for 0
  *   p         0..1 (1 drops all)
