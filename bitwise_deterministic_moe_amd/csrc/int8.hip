@@ -551,7 +551,7 @@ DEV void emit_rows(const DenseParams& P, int64_t row, int64_t end, int col, floa
 
 // WGS: workgroups that share a CU (its registers and LDS), so that one's first loads and
 // epilogue run beside another's slices.
-// 8192^3 436 to 450 us, 2.4 to 2.5 POP/s: matrix units busy 62 to 68% of the cycles, at the 1.5 to 1.8 GHz
+// 8192^3 432 to 450 us, 2.4 to 2.5 POP/s: matrix units busy 62 to 68% of the cycles, at the 1.5 to 1.8 GHz
 // that the power leaves.  4096 x 8192 x 2048 69 to 72 us: of each of its two rounds (256 x 256) 5 the launch and
 // first slice, 23 the slices, 8 the 33 MB stored; GELU adds 5 to 7, which nothing hides.
 // A contraction split into S chunks (one group only): each workgroup leaves its sums in
